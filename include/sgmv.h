@@ -410,6 +410,159 @@ sgmv_status sgmv_merge_adapter_ex(const void* w, int64_t ldw, void* w_out, int64
                                   const sgmv_pool* pool, int32_t adapter,
                                   const sgmv_launch_opts* opts, void* stream);
 
+/* ------------------------------------------------------------------------------------ *
+ * Paged key/value cache of one attention layer, quantised as it is written, the attention of
+ * a step's new tokens over it, and the check of drafted tokens: what a serving step does with
+ * the projections that the delta above completes. Not part of the source pages.
+ *
+ * Cache, all device memory: `pages` pages of `page_size` tokens, per page and head one block.
+ * In a block, tokens are stored in groups of SGMV_KV_GROUP = 16; with D = head_dim, c = 16
+ * bytes of elements (4 fp32, 8 bf16, 16 of the 8-bit formats), group g = t / 16, r = t % 16:
+ *   k        [pages][heads][page_size/16][D/c][16][c]   K[t][d] at (((g*(D/c) + d/c)*16 + r)*c + d%c
+ *   v        [pages][heads][page_size/16][D][16]        V[t][d] at (g*D + d)*16 + 8*(r/4%2) + 4*(r/8) + r%4
+ *   k_scale, v_scale  [pages][heads][page_size] fp32    8-bit formats only (else NULL)
+ * A value is code * scale. Pointers are 16-byte aligned. head_dim is a multiple of 16 up to
+ * SGMV_KV_MAX_HEAD_DIM; page_size a power of two from 16 to SGMV_KV_MAX_PAGE.
+ *
+ * Quantising a row (one token, one head), with F = 448 (E4M3) or 127 (I8): amax = max |x|,
+ * scale = amax / F in fp32, code = x * F / amax rounded to the format, ties to even. A row of
+ * zeros has scale 0 and codes 0. A row with a non-finite value has scale NaN and codes 0: it
+ * reads back as NaN.
+ * ------------------------------------------------------------------------------------ */
+typedef enum {
+  SGMV_KV_F32 = 0,  /* fp32 rows as they are       */
+  SGMV_KV_BF16 = 1, /* bf16 rows as they are       */
+  SGMV_KV_E4M3 = 2, /* fp8 e4m3 (finite, NaN) codes */
+  SGMV_KV_I8 = 3    /* int8 codes in [-127, 127]    */
+} sgmv_kv_format;
+
+#define SGMV_KV_GROUP 16
+#define SGMV_KV_MAX_PAGE 4096
+#define SGMV_KV_MAX_HEAD_DIM 256
+#define SGMV_KV_MAX_HEADS 1024
+#define SGMV_KV_MAX_B 65536
+#define SGMV_KV_MAX_SPLITS 64
+
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t pages, page_size, heads, head_dim;
+  int32_t format; /* sgmv_kv_format */
+} sgmv_kv_cache;
+
+/* Fill the dimensions of `cache` and report the byte sizes the caller must allocate for k and
+ * for v (data_bytes each) and for k_scale and v_scale (scale_bytes each, 0 for F32 and BF16).
+ * Pointers in `cache` are cleared. The contents need no initialisation: no call reads a token
+ * that was not written, except as bytes that it then discards.
+ * Errors: EINVAL (null pointer, a size < 1, unknown format); EUNSUPPORTED (limits above). */
+sgmv_status sgmv_kv_init(int32_t pages, int32_t page_size, int32_t heads, int32_t head_dim,
+                         int32_t format, sgmv_kv_cache* cache, size_t* data_bytes,
+                         size_t* scale_bytes);
+
+/* The sequences of a step. Device arrays:
+ *   q_start     [B + 1] int32, not decreasing: sequence b's new tokens are rows
+ *               q_start[b] .. q_start[b + 1) of the step's T rows (none is allowed)
+ *   kv_len      [B] int32: its length in tokens, the new ones included (they are its last)
+ *   page_table  [B][ldp] int32: page of its tokens [i * page_size, (i + 1) * page_size) for
+ *               i < table_pages
+ * New token i of sequence b stands at position kv_len[b] - n_b + i, n_b = q_start[b + 1] -
+ * q_start[b]; one at a negative position does not exist (it is not written, and attends to
+ * nothing). A page id outside [0, pages) (use -1) means that those tokens are not there: not
+ * written, not attended to, read back as zeros. Pages may be shared by sequences as long as
+ * no two tokens of one write call go to the same place. kv_len is cut to table_pages *
+ * page_size, q_start to [0, T]: no contents of these arrays lead outside the arrays.
+ * Host numbers: T rows, max_q >= every n_b, max_kv >= every kv_len (they choose the launch;
+ * rows of a sequence with more than max_q new tokens may stay unwritten). */
+typedef struct {
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  int64_t ldp;
+  int32_t table_pages;
+  int32_t B, T, max_q, max_kv;
+} sgmv_kv_batch;
+
+/* Write the step's new keys and values into the cache, quantised to its format.
+ *   k, v  device, row of token t and head h at t * ld_token + h * ld_head (elements of
+ *         `dtype`), head_dim contiguous elements; e.g. the k and v slices that a delta call
+ *         updates. ld_head >= head_dim, ld_token >= (heads - 1) * ld_head + head_dim.
+ * dtype is SGMV_F32 or SGMV_BF16; an F32 or BF16 cache takes rows of its own type only.
+ * Errors: EINVAL; EUNSUPPORTED; EHIP. */
+sgmv_status sgmv_kv_write(const void* k, int64_t ldk_token, int64_t ldk_head, const void* v,
+                          int64_t ldv_token, int64_t ldv_head, int32_t dtype,
+                          const sgmv_kv_batch* batch, const sgmv_kv_cache* cache, void* stream);
+
+/* Read tokens back (to move a sequence, or to check): with m_b = out_start[b + 1] -
+ * out_start[b], output rows out_start[b] .. are the last m_b tokens of sequence b, so
+ * out_start = q_start gives the step's new tokens and running sums of kv_len whole sequences.
+ *   out_start  [B + 1] int32 device, not decreasing, cut to [0, rows]
+ *   k, v       device, `rows` rows laid out as in sgmv_kv_write; code * scale rounded once
+ * Rows of tokens at negative positions are not written. q_start is not used.
+ * Errors: EINVAL; EUNSUPPORTED; EHIP. */
+sgmv_status sgmv_kv_read(const sgmv_kv_batch* batch, const sgmv_kv_cache* cache,
+                         const int32_t* out_start, int32_t rows, void* k, int64_t ldk_token,
+                         int64_t ldk_head, void* v, int64_t ldv_token, int64_t ldv_head,
+                         int32_t dtype, void* stream);
+
+/* Attention of the step's new tokens over the cache (which already holds them: write first).
+ * Query head g of `heads` reads key/value head g / (heads / cache heads). The token at
+ * position pos sees tokens t <= pos, with a window also t > pos - window, that are there:
+ *   s_t = scale * q . k_t,   out = sum_t e^(s_t - max s) v_t / sum_t e^(s_t - max s),
+ *   lse = log sum_t e^(s_t)  (so parts over disjoint tokens can be joined)
+ * A row that sees nothing gets out = 0 and lse = -inf. A value that is not finite reaches only
+ * the rows that see its token. Products are of bf16 or fp32 operands (the 8-bit formats'
+ * codes are exact in bf16), summed in fp32; with bf16 rows the probabilities (times the V
+ * scale) are rounded to bf16 for their product with V.
+ *   q, out  device rows [T][heads][head_dim] of `dtype` with token and head strides, as in
+ *           sgmv_kv_write; out must not overlap q
+ *   lse     device [T][heads] fp32, or NULL
+ *   scale   finite and > 0;  window  0 = none
+ *   n_split 0 = the library's choice, else 1..SGMV_KV_MAX_SPLITS ranges that a sequence's
+ *           tokens are split into
+ *   workspace  device, 16-byte aligned, of sgmv_kv_attention_workspace bytes (0: may be NULL)
+ * Errors: EINVAL; EUNSUPPORTED; ECAPACITY (workspace); EHIP. */
+typedef struct {
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t ldq_token, ldq_head, ldo_token, ldo_head;
+  int32_t heads, dtype;
+  float scale;
+  int32_t window, n_split;
+} sgmv_attention;
+
+sgmv_status sgmv_kv_attention_workspace(const sgmv_attention* attn, const sgmv_kv_batch* batch,
+                                        const sgmv_kv_cache* cache, size_t* bytes);
+sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* batch,
+                              const sgmv_kv_cache* cache, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* Check drafted tokens against the target's probabilities, from given random numbers.
+ * Sequence b has n_b = draft_start[b + 1] - draft_start[b] drafts (0 is allowed) at
+ * draft_start[b] .., and n_b + 1 target rows from draft_start[b] + b on. Draft i is taken
+ * while accept_u[i] * draft[i][id_i] < target[i'][id_i]; after the first that is not, the
+ * token is drawn from max(target row - draft row, 0) (from the target row where that is all
+ * zero), and where all are taken from the last target row. A row w is drawn from as the
+ * lowest j with w_0 + .. + w_j > sample_u * (w_0 + ..), summed in fp64.
+ *   target   device [N + B][ldt], draft device [N][ldd], probabilities of `dtype` (SGMV_F32 or
+ *            SGMV_BF16), vocab entries per row; they need not sum to 1, and entries that are
+ *            negative or not finite count as 0. draft = NULL: drafts are certain (probability
+ *            1 at the drafted id, as of a greedy drafter or a lookup).
+ *   draft_ids [N] int32, accept_u [N] fp32, sample_u [B] fp32 in [0, 1), draft_start [B + 1]
+ *            int32 not decreasing, all device. A draft outside [0, vocab) is not taken.
+ *   tokens   device [B][ldo >= max_drafts + 1] int32: the drafts taken, the drawn token, then
+ *            -1. The drawn token is -1 where its row has no positive entry.
+ *   accepted device [B] int32: drafts taken
+ * max_drafts >= every n_b (further drafts are not looked at).
+ * Errors: EINVAL; EHIP. */
+sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd,
+                               int32_t vocab, int32_t dtype, const int32_t* draft_ids,
+                               const int32_t* draft_start, int32_t B, int32_t N,
+                               int32_t max_drafts, const float* accept_u, const float* sample_u,
+                               int32_t* tokens, int64_t ldo, int32_t* accepted, void* stream);
+
 /* Human-readable name of a status code (static string). */
 const char* sgmv_status_string(sgmv_status s);
 

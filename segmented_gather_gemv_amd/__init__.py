@@ -10,6 +10,9 @@ those of the C-ABI in ``include/sgmv.h``:
     sgmv_expand(h, pool, seg, y | [slices])           -> None (y updated in place)
     sgmv_lora_delta(x, pool, seg, y | [slices])       -> None (y updated in place)
 
+and, for the attention of the same step, sgmv_kv_write, sgmv_kv_read, sgmv_kv_attention and
+sgmv_verify_drafts (_serving.py).
+
 The shared library is loaded from this package directory; importing raises if it is
 missing (build it with ``python -m segmented_gather_gemv_amd.build``).
 """
@@ -46,7 +49,8 @@ EXPORTED = [
     "sgmv_lora_delta_ids_ex", "sgmv_build_segments_cached", "sgmv_build_segments_cached_ex",
     "sgmv_pool_pack_ex", "sgmv_merge_adapter", "sgmv_merge_adapter_ex", "sgmv_status_string",
     "sgmv_version", "sgmv_chunk_size_for_batch", "sgmv_lora_delta_ids_noalloc",
-    "sgmv_exchange_placement",
+    "sgmv_exchange_placement", "sgmv_kv_init", "sgmv_kv_write", "sgmv_kv_read",
+    "sgmv_kv_attention_workspace", "sgmv_kv_attention", "sgmv_verify_drafts",
 ]
 
 
@@ -535,10 +539,18 @@ def sgmv_merge_adapter(w: torch.Tensor, pool: Pool, adapter: int,
     return out
 
 
+# the paged cache, its attention and the draft check
+from ._serving import (  # noqa: E402
+    KV_F32, KV_BF16, KV_E4M3, KV_I8, KV_GROUP, KV_MAX_PAGE, KV_MAX_HEAD_DIM, KV_MAX_HEADS, KV_MAX_B,
+    KV_MAX_SPLITS, KvCache, KvBatch, sgmv_kv_init, sgmv_kv_wrap, sgmv_kv_batch, sgmv_kv_write,
+    sgmv_kv_read, sgmv_kv_attention, sgmv_kv_attention_workspace, sgmv_verify_drafts)
+
 __all__ = [
     "LIB_PATH", "EXPORTED", "SgmvError", "Pool", "Segments", "LaunchOpts", "library",
     "sgmv_pool_init", "sgmv_pool_pack", "sgmv_segments_alloc", "sgmv_build_segments",
     "sgmv_shrink", "sgmv_expand", "sgmv_lora_delta", "sgmv_lora_delta_ids",
     "sgmv_lora_delta_ids_noalloc", "sgmv_segments_cache_alloc", "sgmv_build_segments_cached", "sgmv_merge_adapter",
     "sgmv_chunk_size_for_batch", "sgmv_exchange_placement",
+    "KvCache", "KvBatch", "sgmv_kv_init", "sgmv_kv_wrap", "sgmv_kv_batch", "sgmv_kv_write",
+    "sgmv_kv_read", "sgmv_kv_attention", "sgmv_kv_attention_workspace", "sgmv_verify_drafts",
 ]

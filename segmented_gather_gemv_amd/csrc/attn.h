@@ -1,0 +1,103 @@
+// Attention of a step's new tokens over the paged cache: arguments and the steps that the kernels
+// share. Row r of a sequence and key/value head is (new token r / G, query head r % G of the
+// group), so that the G query heads of a key/value head share its tiles.
+#pragma once
+
+#include "kv_common.h"
+
+namespace sgmv {
+
+constexpr int AT_ROWS = 32;   // rows of one 32x32 product
+constexpr int AT_TOKENS = 32; // tokens of one 32x32 product
+
+struct AttnArgs {
+  KvArgs kv;
+  const void* q;
+  void* out;
+  float* lse;  // [T][Hq], may be null
+  int64_t ldq_t, ldq_h, ldo_t, ldo_h;
+  int32_t Hq, G;
+  int32_t f32;         // q and out are fp32, else bf16
+  int32_t q_vec;       // q rows may be read 16 bytes at a time
+  int32_t o_vec;       // out rows may be written 8 bytes (bf16) or 16 (fp32) at a time
+  float scale_log2;    // scale * log2(e)
+  int32_t window;      // 0: none
+  // rows of one sequence up to which the direct kernel takes it (the tiled kernel takes the
+  // others); INT32_MAX: the direct kernel takes all
+  int32_t direct_rows;
+  int32_t one_tile;    // direct kernel: every sequence it takes has at most AT_ROWS rows
+  // split of a sequence's tokens over workgroups: `n_split` ranges of `chunk` tokens (a multiple
+  // of the tile), the last one to the end
+  int32_t chunk[2], n_split[2];  // [0] direct kernel, [1] tiled kernel
+  float* part_o;       // [max n_split][T][Hq][D]
+  float* part_ml;      // [max n_split][T][Hq][2]: maximum (of scores times log2(e)), sum
+};
+
+// Tokens that rows [row0, row0 + n) of a sequence look at: [begin, end), begin a multiple of 32.
+struct Span {
+  int begin, end;
+};
+
+__device__ __forceinline__ Span row_span(const AttnArgs& A, const KvSeq& s, int row0, int n) {
+  const int rows = s.q_len * A.G;
+  const int lo = row0 / A.G, hi = (min(row0 + n, rows) - 1) / A.G;
+  const int first = s.kv_len - s.q_len;
+  Span p;
+  p.end = max(first + hi + 1, 0);
+  p.begin = A.window ? max(first + lo - A.window + 1, 0) & ~(AT_TOKENS - 1) : 0;
+  return p;
+}
+
+// Ranges that the tokens of a span are split into, for the direct (0) or the tiled (1) kernel.
+__device__ __forceinline__ int span_splits(const AttnArgs& A, const Span& p, int kernel) {
+  const int chunk = A.chunk[kernel];
+  return min(max((p.end - p.begin + chunk - 1) / chunk, 1), A.n_split[kernel]);
+}
+
+__device__ __forceinline__ f32x16_t mfma_32x32_bf16(u32x4_t a, u32x4_t b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ f32x16_t mfma_32x32_f32(float a, float b, f32x16_t c) {
+  return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+}
+
+// Token of register i of a 32x32 product's lane in half h.
+__device__ __forceinline__ int reg_token(int i, int h) { return (i & 3) + 8 * (i >> 2) + 4 * h; }
+
+// Four values of one output row from element `at` on.
+template <bool F32>
+__device__ __forceinline__ void store_out(const AttnArgs& A, int64_t at, float a, float b, float c, float d) {
+  if constexpr (F32) {
+    float* p = static_cast<float*>(A.out) + at;
+    if (A.o_vec) {
+      *reinterpret_cast<f32x4_t*>(p) = f32x4_t{a, b, c, d};
+    } else {
+      p[0] = a; p[1] = b; p[2] = c; p[3] = d;
+    }
+  } else {
+    uint16_t* p = static_cast<uint16_t*>(A.out) + at;
+    const u32x2_t w = {pack_bf16x2(a, b), pack_bf16x2(c, d)};
+    if (A.o_vec) {
+      *reinterpret_cast<u32x2_t*>(p) = w;
+    } else {
+      p[0] = (uint16_t)w.x; p[1] = (uint16_t)(w.x >> 16);
+      p[2] = (uint16_t)w.y; p[3] = (uint16_t)(w.y >> 16);
+    }
+  }
+}
+
+constexpr int TILED_ROWS = 256;  // rows of one workgroup of the tiled kernel
+
+// Maximum of a value over the two halves of the wave, in both.
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+}  // namespace sgmv

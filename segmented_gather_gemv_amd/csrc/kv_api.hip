@@ -1,0 +1,244 @@
+// C-ABI of the paged cache, its attention and the draft check: argument validation, launch
+// geometry and dispatch. Stateless; every call runs on the caller's stream. Declarations and
+// contracts are in include/sgmv.h.
+#include <cmath>
+#include <cstring>
+
+#include "attn.h"
+#include "verify.h"
+
+namespace sgmv {
+hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
+hipError_t launch_kv_read(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
+hipError_t launch_attn_direct_bf16(const AttnArgs& A, int fmt, unsigned slots, hipStream_t stream);
+hipError_t launch_attn_direct_f32(const AttnArgs& A, int fmt, unsigned slots, hipStream_t stream);
+hipError_t launch_attn_combine(const AttnArgs& A, hipStream_t stream);
+
+namespace {
+
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool scaled(int fmt) { return fmt == SGMV_KV_E4M3 || fmt == SGMV_KV_I8; }
+inline int format_bytes(int fmt) { return fmt == SGMV_KV_F32 ? 4 : fmt == SGMV_KV_BF16 ? 2 : 1; }
+inline bool row_type_ok(int dtype) { return dtype == SGMV_F32 || dtype == SGMV_BF16; }
+// A cache that is not quantised holds rows of its own type only.
+inline bool types_fit(int dtype, int fmt) {
+  return scaled(fmt) || (fmt == SGMV_KV_F32) == (dtype == SGMV_F32);
+}
+constexpr int64_t MOST_GRID = 0x7fffffff;
+
+sgmv_status shape_ok(int32_t pages, int32_t page_size, int32_t heads, int32_t head_dim, int32_t fmt) {
+  if (pages < 1 || page_size < 1 || heads < 1 || head_dim < 1 || fmt < SGMV_KV_F32 || fmt > SGMV_KV_I8)
+    return SGMV_EINVAL;
+  if (page_size < SGMV_KV_GROUP || page_size > SGMV_KV_MAX_PAGE || (page_size & (page_size - 1)) ||
+      head_dim % 16 || head_dim > SGMV_KV_MAX_HEAD_DIM || heads > SGMV_KV_MAX_HEADS)
+    return SGMV_EUNSUPPORTED;
+  return SGMV_OK;
+}
+
+sgmv_status cache_ok(const sgmv_kv_cache* c) {
+  if (!c || !c->k || !c->v) return SGMV_EINVAL;
+  const sgmv_status s = shape_ok(c->pages, c->page_size, c->heads, c->head_dim, c->format);
+  if (s != SGMV_OK) return s;
+  if (scaled(c->format) && (!c->k_scale || !c->v_scale)) return SGMV_EINVAL;
+  if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16) || !aligned_to(c->k_scale, 16) ||
+      !aligned_to(c->v_scale, 16))
+    return SGMV_EINVAL;
+  return SGMV_OK;
+}
+
+// Fills the arguments of a cache and a batch. `empty`: nothing to do.
+sgmv_status fill(const sgmv_kv_batch* s, const sgmv_kv_cache* c, KvArgs& K, bool& empty) {
+  const sgmv_status st = cache_ok(c);
+  if (st != SGMV_OK) return st;
+  if (!s || s->B < 0 || s->T < 0 || s->max_q < 0 || s->max_kv < 0 || s->table_pages < 0 ||
+      s->ldp < s->table_pages)
+    return SGMV_EINVAL;
+  empty = s->B == 0;
+  if (!empty && (!s->q_start || !s->kv_len || (s->table_pages > 0 && !s->page_table))) return SGMV_EINVAL;
+  if (s->B > SGMV_KV_MAX_B) return SGMV_EUNSUPPORTED;
+  K = KvArgs{c->k, c->v, c->k_scale, c->v_scale, s->q_start, s->kv_len, s->page_table, s->ldp,
+             c->pages, __builtin_ctz((unsigned)c->page_size), s->table_pages, s->B, s->T, c->heads,
+             c->head_dim};
+  return SGMV_OK;
+}
+
+// Rows [n][heads][D] with a token and a head stride: rows must not overlap one another.
+bool rows_ok(const void* p, int64_t n, int64_t ld_t, int64_t ld_h, int heads, int D) {
+  return p && ld_h >= D && (n <= 1 || ld_t >= (int64_t)(heads - 1) * ld_h + D);
+}
+
+sgmv_status launched(hipError_t e) { return e == hipSuccess ? SGMV_OK : SGMV_EHIP; }
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Token ranges of a kernel whose launch has `base` workgroups before splitting: enough ranges
+// to reach `want` workgroups, each of at least `least` tokens, chunk a multiple of `unit`.
+void split_tokens(int64_t base, int64_t tokens, int64_t want, int64_t least, int unit, int forced,
+                  int32_t& n_split, int32_t& chunk) {
+  int64_t n = forced > 0 ? forced : ceil_div(want, base > 0 ? base : 1);
+  const int64_t most = forced > 0 ? n : ceil_div(tokens, least);
+  if (n > most) n = most;
+  if (n > SGMV_KV_MAX_SPLITS) n = SGMV_KV_MAX_SPLITS;
+  if (n < 1) n = 1;
+  int64_t c = ceil_div(ceil_div(tokens > 0 ? tokens : 1, n), unit) * unit;
+  chunk = (int32_t)(c < 0x40000000 ? c : 0x40000000);
+  n_split = (int32_t)n;
+}
+
+// Geometry of an attention call; everything but the pointers of its rows and workspace.
+sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_cache* c, AttnArgs& A,
+                 int64_t& slots, bool& empty) {
+  std::memset(&A, 0, sizeof(A));
+  if (!a) return SGMV_EINVAL;
+  const sgmv_status st = fill(s, c, A.kv, empty);
+  if (st != SGMV_OK) return st;
+  if (!row_type_ok(a->dtype) || !types_fit(a->dtype, c->format) || a->heads < 1 ||
+      a->heads % c->heads || !std::isfinite(a->scale) || a->scale <= 0.f || a->window < 0 ||
+      a->n_split < 0 || a->n_split > SGMV_KV_MAX_SPLITS)
+    return SGMV_EINVAL;
+  if (a->heads > SGMV_KV_MAX_HEADS) return SGMV_EUNSUPPORTED;
+  A.Hq = a->heads;
+  A.G = a->heads / c->heads;
+  A.f32 = a->dtype == SGMV_F32;
+  A.scale_log2 = a->scale * 1.44269504088896341f;
+  if (!std::isfinite(A.scale_log2)) return SGMV_EINVAL;
+  A.window = a->window;
+  A.direct_rows = INT32_MAX;
+  empty = empty || s->T == 0;
+  if ((int64_t)s->T * A.Hq > MOST_GRID) return SGMV_EUNSUPPORTED;
+  A.one_tile = (int64_t)s->max_q * A.G <= AT_ROWS;
+  slots = A.one_tile ? s->B : (int64_t)s->T * A.G / AT_ROWS + s->B;
+  int64_t tokens = s->max_kv;
+  if (a->window && tokens > (int64_t)a->window + s->max_q + AT_TOKENS) tokens = (int64_t)a->window + s->max_q + AT_TOKENS;
+  split_tokens(slots * c->heads, tokens, 1024, 256, 128, a->n_split, A.n_split[0], A.chunk[0]);
+  A.n_split[1] = 1;
+  A.chunk[1] = A.chunk[0];
+  if (slots * c->heads * A.n_split[0] > MOST_GRID) return SGMV_EUNSUPPORTED;
+  return SGMV_OK;
+}
+
+size_t part_bytes(const AttnArgs& A) {
+  const int n = A.n_split[0] > A.n_split[1] ? A.n_split[0] : A.n_split[1];
+  return n <= 1 ? 0 : (size_t)n * A.kv.T * A.Hq * (A.kv.D + 2) * sizeof(float);
+}
+
+}  // namespace
+}  // namespace sgmv
+
+using namespace sgmv;
+
+extern "C" {
+
+sgmv_status sgmv_kv_init(int32_t pages, int32_t page_size, int32_t heads, int32_t head_dim,
+                         int32_t format, sgmv_kv_cache* cache, size_t* data_bytes,
+                         size_t* scale_bytes) {
+  if (!cache || !data_bytes || !scale_bytes) return SGMV_EINVAL;
+  const sgmv_status s = shape_ok(pages, page_size, heads, head_dim, format);
+  if (s != SGMV_OK) return s;
+  *cache = sgmv_kv_cache{nullptr, nullptr, nullptr, nullptr, pages, page_size, heads, head_dim, format};
+  const size_t rows = (size_t)pages * page_size * heads;
+  *data_bytes = rows * head_dim * format_bytes(format);
+  *scale_bytes = scaled(format) ? rows * sizeof(float) : 0;
+  return SGMV_OK;
+}
+
+sgmv_status sgmv_kv_write(const void* k, int64_t ldk_token, int64_t ldk_head, const void* v,
+                          int64_t ldv_token, int64_t ldv_head, int32_t dtype,
+                          const sgmv_kv_batch* batch, const sgmv_kv_cache* cache, void* stream) {
+  KvArgs K;
+  bool empty;
+  const sgmv_status s = fill(batch, cache, K, empty);
+  if (s != SGMV_OK) return s;
+  if (!row_type_ok(dtype) || !types_fit(dtype, cache->format)) return SGMV_EINVAL;
+  if (empty || batch->T == 0) return SGMV_OK;
+  if (!rows_ok(k, K.T, ldk_token, ldk_head, K.H, K.D) || !rows_ok(v, K.T, ldv_token, ldv_head, K.H, K.D))
+    return SGMV_EINVAL;
+  const KvRows R{const_cast<void*>(k), const_cast<void*>(v), ldk_token, ldk_head, ldv_token, ldv_head,
+                 nullptr, 0, dtype == SGMV_F32};
+  return launched(launch_kv_write(K, R, cache->format, static_cast<hipStream_t>(stream)));
+}
+
+sgmv_status sgmv_kv_read(const sgmv_kv_batch* batch, const sgmv_kv_cache* cache,
+                         const int32_t* out_start, int32_t rows, void* k, int64_t ldk_token,
+                         int64_t ldk_head, void* v, int64_t ldv_token, int64_t ldv_head,
+                         int32_t dtype, void* stream) {
+  KvArgs K;
+  bool empty;
+  const sgmv_status s = fill(batch, cache, K, empty);
+  if (s != SGMV_OK) return s;
+  if (!row_type_ok(dtype) || !types_fit(dtype, cache->format) || rows < 0) return SGMV_EINVAL;
+  if (empty || rows == 0) return SGMV_OK;
+  if (!out_start || !rows_ok(k, rows, ldk_token, ldk_head, K.H, K.D) ||
+      !rows_ok(v, rows, ldv_token, ldv_head, K.H, K.D))
+    return SGMV_EINVAL;
+  const KvRows R{k, v, ldk_token, ldk_head, ldv_token, ldv_head, out_start, rows, dtype == SGMV_F32};
+  return launched(launch_kv_read(K, R, cache->format, static_cast<hipStream_t>(stream)));
+}
+
+sgmv_status sgmv_kv_attention_workspace(const sgmv_attention* attn, const sgmv_kv_batch* batch,
+                                        const sgmv_kv_cache* cache, size_t* bytes) {
+  if (!bytes) return SGMV_EINVAL;
+  AttnArgs A;
+  int64_t slots;
+  bool empty;
+  const sgmv_status s = plan(attn, batch, cache, A, slots, empty);
+  if (s != SGMV_OK) return s;
+  *bytes = empty ? 0 : part_bytes(A);
+  return SGMV_OK;
+}
+
+sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* batch,
+                              const sgmv_kv_cache* cache, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  AttnArgs A;
+  int64_t slots;
+  bool empty;
+  const sgmv_status s = plan(attn, batch, cache, A, slots, empty);
+  if (s != SGMV_OK) return s;
+  if (empty) return SGMV_OK;
+  const int D = A.kv.D;
+  if (!rows_ok(attn->q, A.kv.T, attn->ldq_token, attn->ldq_head, A.Hq, D) ||
+      !rows_ok(attn->out, A.kv.T, attn->ldo_token, attn->ldo_head, A.Hq, D))
+    return SGMV_EINVAL;
+  A.q = attn->q;
+  A.out = attn->out;
+  A.lse = attn->lse;
+  A.ldq_t = attn->ldq_token;
+  A.ldq_h = attn->ldq_head;
+  A.ldo_t = attn->ldo_token;
+  A.ldo_h = attn->ldo_head;
+  const int e = A.f32 ? 4 : 2;
+  A.q_vec = aligned_to(A.q, 16) && A.ldq_t * e % 16 == 0 && A.ldq_h * e % 16 == 0;
+  A.o_vec = aligned_to(A.out, 4 * e) && A.ldo_t % 4 == 0 && A.ldo_h % 4 == 0;
+  const size_t need = part_bytes(A);
+  if (need) {
+    if (!workspace || !aligned_to(workspace, 16)) return SGMV_EINVAL;
+    if (workspace_bytes < need) return SGMV_ECAPACITY;
+    const int n = A.n_split[0] > A.n_split[1] ? A.n_split[0] : A.n_split[1];
+    A.part_o = static_cast<float*>(workspace);
+    A.part_ml = A.part_o + (size_t)n * A.kv.T * A.Hq * D;
+  }
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  hipError_t err = A.f32 ? launch_attn_direct_f32(A, cache->format, (unsigned)slots, st)
+                         : launch_attn_direct_bf16(A, cache->format, (unsigned)slots, st);
+  if (err == hipSuccess && need) err = launch_attn_combine(A, st);
+  return launched(err);
+}
+
+sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd,
+                               int32_t vocab, int32_t dtype, const int32_t* draft_ids,
+                               const int32_t* draft_start, int32_t B, int32_t N,
+                               int32_t max_drafts, const float* accept_u, const float* sample_u,
+                               int32_t* tokens, int64_t ldo, int32_t* accepted, void* stream) {
+  if (B < 0 || N < 0 || vocab < 1 || max_drafts < 0 || !row_type_ok(dtype)) return SGMV_EINVAL;
+  if (B == 0) return SGMV_OK;
+  if (!target || !draft_start || !sample_u || !tokens || !accepted || ldt < vocab ||
+      (draft && ldd < vocab) || ldo < (int64_t)max_drafts + 1)
+    return SGMV_EINVAL;
+  if (N > 0 && max_drafts > 0 && (!draft_ids || !accept_u)) return SGMV_EINVAL;
+  const VerifyArgs A{target, draft, ldt, ldd, draft_ids, draft_start, accept_u, sample_u, tokens, ldo,
+                     accepted, B, vocab, N, max_drafts, dtype == SGMV_BF16};
+  return launched(launch_verify(A, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,24 @@
+// Arguments of the draft check (verify.hip).
+#pragma once
+
+#include "common.h"
+
+namespace sgmv {
+
+struct VerifyArgs {
+  const void* target;
+  const void* draft;  // null: point masses
+  int64_t ldt, ldd;
+  const int32_t* ids;
+  const int32_t* start;
+  const float* accept_u;
+  const float* sample_u;
+  int32_t* tokens;
+  int64_t ldo;
+  int32_t* accepted;
+  int32_t B, V, N, max_drafts, bf16;
+};
+
+hipError_t launch_verify(const VerifyArgs& A, hipStream_t stream);
+
+}  // namespace sgmv
