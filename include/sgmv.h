@@ -499,7 +499,7 @@ sgmv_status sgmv_kv_write(const void* k, int64_t ldk_token, int64_t ldk_head, co
  * out_start = q_start gives the step's new tokens and running sums of kv_len whole sequences.
  *   out_start  [B + 1] int32 device, not decreasing, cut to [0, rows]
  *   k, v       device, `rows` rows laid out as in sgmv_kv_write; code * scale rounded once
- * Rows of tokens at negative positions are not written. q_start is not used.
+ * Rows of tokens at negative positions, and of missing pages, are zeros. q_start is not used.
  * Errors: EINVAL; EUNSUPPORTED; EHIP. */
 sgmv_status sgmv_kv_read(const sgmv_kv_batch* batch, const sgmv_kv_cache* cache,
                          const int32_t* out_start, int32_t rows, void* k, int64_t ldk_token,

@@ -218,6 +218,11 @@ def _same_device(batch: KvBatch, cache: KvCache):
         raise ValueError("the batch must be on the cache's device")
 
 
+def _on_gpu(t: torch.Tensor):
+    if t.device.type != "cuda":
+        raise ValueError("the kernels run on GPU tensors")
+
+
 # ---------------------------------------------------------------------------------------
 # write, read, attention
 # ---------------------------------------------------------------------------------------
@@ -229,8 +234,10 @@ def sgmv_kv_write(k: torch.Tensor, v: torch.Tensor, batch: KvBatch, cache: KvCac
     vt, vh = _rows3(v, T, H, cache, "v")
     if v.dtype != k.dtype:
         raise TypeError("k and v must share a dtype")
+    dtype = _dtype_code(k.dtype)
     _same_device(batch, cache)
-    _check(_lib.sgmv_kv_write(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, _dtype_code(k.dtype),
+    _on_gpu(k)
+    _check(_lib.sgmv_kv_write(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dtype,
                               batch.ref, cache.ref, _stream(k.device)), "sgmv_kv_write")
 
 
@@ -254,6 +261,7 @@ def sgmv_kv_read(batch: KvBatch, cache: KvCache, out_start: torch.Tensor, rows: 
     if k.dtype != dtype or v.dtype != dtype:
         raise TypeError(f"k and v must be {dtype}")
     _same_device(batch, cache)
+    _on_gpu(k)
     _check(_lib.sgmv_kv_read(batch.ref, cache.ref, out_start.data_ptr(), rows, k.data_ptr(), kt,
                              kh, v.data_ptr(), vt, vh, _dtype_code(dtype), _stream(k.device)),
            "sgmv_kv_read")
@@ -289,6 +297,7 @@ def sgmv_kv_attention(q: torch.Tensor, batch: KvBatch, cache: KvCache,
     ref, need = ctypes.byref(a), ctypes.c_size_t()
     _check(_lib.sgmv_kv_attention_workspace(ref, batch.ref, cache.ref, ctypes.byref(need)),
            "sgmv_kv_attention")
+    _on_gpu(q)
     size = need.value
     if workspace is None and size:
         workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
@@ -356,6 +365,7 @@ def sgmv_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
     if accepted.dtype != torch.int32 or accepted.numel() != B or accepted.device != dev or (
             not accepted.is_contiguous()):
         raise ValueError("accepted must be B contiguous int32 entries on target's device")
+    _on_gpu(target)
     _check(_lib.sgmv_verify_drafts(
         target.data_ptr(), target.stride(0) if N + B > 1 else V,
         None if draft is None or N == 0 else draft.data_ptr(),
