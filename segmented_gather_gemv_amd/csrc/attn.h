@@ -33,6 +33,11 @@ struct AttnArgs {
   float* part_ml;      // [max n_split][T][Hq][2]: maximum (of scores times log2(e)), sum
 };
 
+// The tiled kernel: head dimensions it has instances of, waves and rows of its workgroups.
+constexpr bool tiled_dim(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
+constexpr int tiled_waves(int D) { return D <= 128 ? 8 : 4; }
+constexpr int tiled_rows(int D) { return tiled_waves(D) * AT_ROWS; }
+
 // Tokens that rows [row0, row0 + n) of a sequence look at: [begin, end), begin a multiple of 32.
 struct Span {
   int begin, end;
@@ -86,8 +91,6 @@ __device__ __forceinline__ void store_out(const AttnArgs& A, int64_t at, float a
     }
   }
 }
-
-constexpr int TILED_ROWS = 256;  // rows of one workgroup of the tiled kernel
 
 // Maximum of a value over the two halves of the wave, in both.
 __device__ __forceinline__ float half_max(float v) {

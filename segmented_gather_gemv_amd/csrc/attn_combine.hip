@@ -21,7 +21,7 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A) {
   const int tok = token - s.q0;
   if (tok < 0 || tok >= s.q_len) return;
   const int rows = s.q_len * A.G, row = tok * A.G + head % A.G;
-  const int kernel = rows > A.direct_rows, tile = kernel ? TILED_ROWS : AT_ROWS;
+  const int kernel = rows > A.direct_rows, tile = kernel ? tiled_rows(K.D) : AT_ROWS;
   const Span span = row_span(A, s, row / tile * tile, tile);
   const int used = span_splits(A, span, kernel);
   if (used == 1) return;

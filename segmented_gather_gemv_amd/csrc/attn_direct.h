@@ -96,39 +96,37 @@ __device__ __forceinline__ void keep_tokens(VRegs<4>& r, uint32_t keep) {
     if (!(keep >> i & 1)) r.w[i / 4][i % 4] = 0u;
 }
 
-// A value that is +inf or NaN counts in `up`, one that is -inf or NaN in `down` (as 1.0), and is
-// then zeroed. Returns whether there was any in this lane.
-__device__ __forceinline__ bool split_nonfinite(VRegs<2>& r, VRegs<2>& up, VRegs<2>& down) {
+// The places (16 bits, in V's order) of a group's first n tokens.
+__device__ __forceinline__ uint32_t places_below(int n) {
+  const uint32_t t = (1u << n) - 1u;  // tokens 4-7 and 8-11 change places
+  return (t & 0xf00fu) | (t & 0x00f0u) << 4 | (t & 0x0f00u) >> 4;
+}
+
+__device__ __forceinline__ bool has_nonfinite(const VRegs<2>& r) {
   bool any = false;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t w = r.w[i], u = 0, d = 0;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t x = w >> (16 * j) & 0xffffu;
-      if ((x & 0x7f80u) == 0x7f80u) {
-        any = true;
-        if (x != 0xff80u) u |= 0x3f80u << (16 * j);
-        if (x != 0x7f80u) d |= 0x3f80u << (16 * j);
-        w &= ~(0xffffu << (16 * j));
-      }
-    }
-    r.w[i] = w; up.w[i] = u; down.w[i] = d;
-  }
+  for (int i = 0; i < 4; ++i)
+    any |= (r.w[i] & 0x7f80u) == 0x7f80u || (r.w[i] & 0x7f800000u) == 0x7f800000u;
   return any;
 }
-__device__ __forceinline__ bool split_nonfinite(VRegs<4>& r, VRegs<4>& up, VRegs<4>& down) {
+__device__ __forceinline__ bool has_nonfinite(const VRegs<4>& r) {
   bool any = false;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t x = r.w[i / 4][i % 4];
-    const bool bad = (x & 0x7f800000u) == 0x7f800000u;
-    any |= bad;
-    up.w[i / 4][i % 4] = bad && x != 0xff800000u ? 0x3f800000u : 0u;
-    down.w[i / 4][i % 4] = bad && x != 0x7f800000u ? 0x3f800000u : 0u;
-    r.w[i / 4][i % 4] = bad ? 0u : x;
-  }
+  for (int i = 0; i < 8; ++i) any |= (r.w[i / 4][i % 4] & 0x7f800000u) == 0x7f800000u;
   return any;
+}
+
+__device__ __forceinline__ void drop_nonfinite(VRegs<2>& r) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if ((r.w[i] & 0x7f80u) == 0x7f80u) r.w[i] &= 0xffff0000u;
+    if ((r.w[i] & 0x7f800000u) == 0x7f800000u) r.w[i] &= 0x0000ffffu;
+  }
+}
+__device__ __forceinline__ void drop_nonfinite(VRegs<4>& r) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if ((r.w[i / 4][i % 4] & 0x7f800000u) == 0x7f800000u) r.w[i / 4][i % 4] = 0u;
 }
 
 // O^T += V^T P^T over one group of 16 tokens: p holds this lane's 8 probabilities
@@ -370,35 +368,35 @@ __global__ __launch_bounds__(256) void attn_direct_kernel(AttnArgs A) {
 #pragma unroll
         for (int g = 0; g < 2; ++g) keep_tokens(vr[n][g], there >> (8 * g) & 0xffu);
       if constexpr (!KvFormat<FMT>::scaled) {
-        // values that are not finite, in tokens that some of the rows do not see: 0 * inf would
-        // spoil those rows, so such values are counted over the rows that do see them instead
-        float seen[16];
+        // A V value that is not finite, in a tile that some rows see only part of: in the product,
+        // 0 * inf would spoil the rows that do not see it. It is left out of the product and added
+        // to the rows that see it, token by token. (8-bit codes are finite; their scales meet only
+        // probabilities that are not 0.)
+        bool odd = false;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) seen[j] = p[j] > 0.f ? 1.f : 0.f;
-        u32x4_t sb[2] = {};
-        if constexpr (!F32) {
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int g = 0; g < 2; ++g)
+          for (int g = 0; g < 2; ++g) odd |= has_nonfinite(vr[n][g]);
+        if (__any(odd)) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) sb[g][j] = pack_bf16x2(seen[8 * g + 2 * j], seen[8 * g + 2 * j + 1]);
-        }
+          for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          VRegs<X::bytes> up[2], down[2];
-          const bool a0 = split_nonfinite(vr[n][0], up[0], down[0]);
-          const bool a1 = split_nonfinite(vr[n][1], up[1], down[1]);
-          if (__any(a0 || a1)) {
-            f32x16_t u = {}, d = {};
+            for (int g = 0; g < 2; ++g) drop_nonfinite(vr[n][g]);
+#pragma unroll 1
+          for (int x = 0; x < AT_TOKENS; ++x) {
+            const int t = t0 + x;
+            if ((x < 16 ? p0 : p1) < 0 || t > pos || (A.window && t <= pos - A.window)) continue;
+            const int64_t at = (x < 16 ? g0 : g1) * D + 8 * ((x >> 2) & 1) + 4 * ((x >> 3) & 1) + (x & 3);
 #pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              u = pv<F32, FMT>(up[g], seen + 8 * g, sb[g], u);
-              d = pv<F32, FMT>(down[g], seen + 8 * g, sb[g], d);
-            }
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              if (u[j] > 0.f) o[n][j] += INFINITY;
-              if (d[j] > 0.f) o[n][j] -= INFINITY;
-            }
+              for (int j = 0; j < 16; ++j) {
+                const int d = 32 * n + reg_token(j, half);
+                if (!EXACT && d >= D) continue;
+                const float f = F32 ? static_cast<const float*>(K.v)[at + d * 16]
+                                    : bf16_bits_to_f32(static_cast<const uint16_t*>(K.v)[at + d * 16]);
+                if (!(fabsf(f) < INFINITY)) o[n][j] += f;
+              }
           }
         }
       }

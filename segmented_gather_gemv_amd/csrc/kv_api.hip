@@ -1,6 +1,7 @@
 // C-ABI of the paged cache, its attention and the draft check: argument validation, launch
 // geometry and dispatch. Stateless; every call runs on the caller's stream. Declarations and
 // contracts are in include/sgmv.h.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -12,6 +13,9 @@ hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, hipStream_
 hipError_t launch_kv_read(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
 hipError_t launch_attn_direct_bf16(const AttnArgs& A, int fmt, unsigned slots, hipStream_t stream);
 hipError_t launch_attn_direct_f32(const AttnArgs& A, int fmt, unsigned slots, hipStream_t stream);
+hipError_t launch_attn_tiled_bf16(const AttnArgs& A, unsigned slots, hipStream_t stream);
+hipError_t launch_attn_tiled_e4m3(const AttnArgs& A, unsigned slots, hipStream_t stream);
+hipError_t launch_attn_tiled_i8(const AttnArgs& A, unsigned slots, hipStream_t stream);
 hipError_t launch_attn_combine(const AttnArgs& A, hipStream_t stream);
 
 namespace {
@@ -85,12 +89,18 @@ void split_tokens(int64_t base, int64_t tokens, int64_t want, int64_t least, int
   n_split = (int32_t)n;
 }
 
-// Geometry of an attention call; everything but the pointers of its rows and workspace.
+// Geometry of an attention call; everything but the pointers of its rows and workspace. Slots: tiles
+// of rows that each kernel's grid has room for (0: not launched).
+struct Launch {
+  int64_t direct_slots = 0, tiled_slots = 0;
+  bool empty = true;
+};
+
 sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_cache* c, AttnArgs& A,
-                 int64_t& slots, bool& empty) {
+                 Launch& L) {
   std::memset(&A, 0, sizeof(A));
   if (!a) return SGMV_EINVAL;
-  const sgmv_status st = fill(s, c, A.kv, empty);
+  const sgmv_status st = fill(s, c, A.kv, L.empty);
   if (st != SGMV_OK) return st;
   if (!row_type_ok(a->dtype) || !types_fit(a->dtype, c->format) || a->heads < 1 ||
       a->heads % c->heads || !std::isfinite(a->scale) || a->scale <= 0.f || a->window < 0 ||
@@ -103,17 +113,23 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   A.scale_log2 = a->scale * 1.44269504088896341f;
   if (!std::isfinite(A.scale_log2)) return SGMV_EINVAL;
   A.window = a->window;
-  A.direct_rows = INT32_MAX;
-  empty = empty || s->T == 0;
+  L.empty = L.empty || s->T == 0;
   if ((int64_t)s->T * A.Hq > MOST_GRID) return SGMV_EUNSUPPORTED;
-  A.one_tile = (int64_t)s->max_q * A.G <= AT_ROWS;
-  slots = A.one_tile ? s->B : (int64_t)s->T * A.G / AT_ROWS + s->B;
+  // sequences of up to 32 rows go to the direct kernel; so do all where the tiled one has no instance
+  const bool tiled = !A.f32 && tiled_dim(c->head_dim) && (int64_t)s->max_q * A.G > AT_ROWS;
+  A.direct_rows = tiled ? AT_ROWS : INT32_MAX;
+  A.one_tile = tiled || (int64_t)s->max_q * A.G <= AT_ROWS;
+  L.direct_slots = A.one_tile ? s->B : (int64_t)s->T * A.G / AT_ROWS + s->B;
+  if (tiled && s->T == (int64_t)s->B * s->max_q) L.direct_slots = 0;  // no sequence is short
+  if (tiled) L.tiled_slots = (int64_t)s->T * A.G / tiled_rows(c->head_dim) + s->B;
   int64_t tokens = s->max_kv;
-  if (a->window && tokens > (int64_t)a->window + s->max_q + AT_TOKENS) tokens = (int64_t)a->window + s->max_q + AT_TOKENS;
-  split_tokens(slots * c->heads, tokens, 1024, 256, 128, a->n_split, A.n_split[0], A.chunk[0]);
-  A.n_split[1] = 1;
-  A.chunk[1] = A.chunk[0];
-  if (slots * c->heads * A.n_split[0] > MOST_GRID) return SGMV_EUNSUPPORTED;
+  if (a->window) tokens = std::min(tokens, (int64_t)a->window + s->max_q + AT_TOKENS);
+  split_tokens(L.direct_slots * c->heads, tokens, 1024, 256, 128, a->n_split, A.n_split[0], A.chunk[0]);
+  split_tokens(L.tiled_slots * c->heads, tokens, 256, 512, 64, a->n_split, A.n_split[1], A.chunk[1]);
+  if (!L.direct_slots) A.n_split[0] = 1;
+  if (!L.tiled_slots) A.n_split[1] = 1;
+  if (std::max(L.direct_slots * A.n_split[0], L.tiled_slots * A.n_split[1]) * c->heads > MOST_GRID)
+    return SGMV_EUNSUPPORTED;
   return SGMV_OK;
 }
 
@@ -179,11 +195,10 @@ sgmv_status sgmv_kv_attention_workspace(const sgmv_attention* attn, const sgmv_k
                                         const sgmv_kv_cache* cache, size_t* bytes) {
   if (!bytes) return SGMV_EINVAL;
   AttnArgs A;
-  int64_t slots;
-  bool empty;
-  const sgmv_status s = plan(attn, batch, cache, A, slots, empty);
+  Launch L;
+  const sgmv_status s = plan(attn, batch, cache, A, L);
   if (s != SGMV_OK) return s;
-  *bytes = empty ? 0 : part_bytes(A);
+  *bytes = L.empty ? 0 : part_bytes(A);
   return SGMV_OK;
 }
 
@@ -191,11 +206,10 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
                               const sgmv_kv_cache* cache, void* workspace, size_t workspace_bytes,
                               void* stream) {
   AttnArgs A;
-  int64_t slots;
-  bool empty;
-  const sgmv_status s = plan(attn, batch, cache, A, slots, empty);
+  Launch L;
+  const sgmv_status s = plan(attn, batch, cache, A, L);
   if (s != SGMV_OK) return s;
-  if (empty) return SGMV_OK;
+  if (L.empty) return SGMV_OK;
   const int D = A.kv.D;
   if (!rows_ok(attn->q, A.kv.T, attn->ldq_token, attn->ldq_head, A.Hq, D) ||
       !rows_ok(attn->out, A.kv.T, attn->ldo_token, attn->ldo_head, A.Hq, D))
@@ -219,8 +233,14 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
     A.part_ml = A.part_o + (size_t)n * A.kv.T * A.Hq * D;
   }
   hipStream_t st = static_cast<hipStream_t>(stream);
-  hipError_t err = A.f32 ? launch_attn_direct_f32(A, cache->format, (unsigned)slots, st)
-                         : launch_attn_direct_bf16(A, cache->format, (unsigned)slots, st);
+  hipError_t err = hipSuccess;
+  if (L.tiled_slots)
+    err = (cache->format == SGMV_KV_BF16   ? launch_attn_tiled_bf16
+           : cache->format == SGMV_KV_E4M3 ? launch_attn_tiled_e4m3
+                                           : launch_attn_tiled_i8)(A, (unsigned)L.tiled_slots, st);
+  if (err == hipSuccess && L.direct_slots)
+    err = (A.f32 ? launch_attn_direct_f32 : launch_attn_direct_bf16)(A, cache->format,
+                                                                     (unsigned)L.direct_slots, st);
   if (err == hipSuccess && need) err = launch_attn_combine(A, st);
   return launched(err);
 }
