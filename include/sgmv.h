@@ -442,6 +442,7 @@ typedef enum {
 #define SGMV_KV_MAX_HEADS 1024
 #define SGMV_KV_MAX_B 65536
 #define SGMV_KV_MAX_SPLITS 64
+#define SGMV_MAX_VOCAB 1073741824
 
 typedef struct {
   void* k;
@@ -556,12 +557,15 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
  *            -1. The drawn token is -1 where its row has no positive entry.
  *   accepted device [B] int32: drafts taken
  * max_drafts >= every n_b (further drafts are not looked at).
- * Errors: EINVAL; EHIP. */
+ *   workspace  device, 16-byte aligned, of sgmv_verify_drafts_workspace(B, vocab) bytes
+ * Errors: EINVAL; EUNSUPPORTED (B >= SGMV_KV_MAX_B, vocab > SGMV_MAX_VOCAB); ECAPACITY (workspace); EHIP. */
+size_t sgmv_verify_drafts_workspace(int32_t B, int32_t vocab);
 sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd,
                                int32_t vocab, int32_t dtype, const int32_t* draft_ids,
                                const int32_t* draft_start, int32_t B, int32_t N,
                                int32_t max_drafts, const float* accept_u, const float* sample_u,
-                               int32_t* tokens, int64_t ldo, int32_t* accepted, void* stream);
+                               int32_t* tokens, int64_t ldo, int32_t* accepted, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* sgmv_status_string(sgmv_status s);

@@ -50,7 +50,7 @@ EXPORTED = [
     "sgmv_pool_pack_ex", "sgmv_merge_adapter", "sgmv_merge_adapter_ex", "sgmv_status_string",
     "sgmv_version", "sgmv_chunk_size_for_batch", "sgmv_lora_delta_ids_noalloc",
     "sgmv_exchange_placement", "sgmv_kv_init", "sgmv_kv_write", "sgmv_kv_read",
-    "sgmv_kv_attention_workspace", "sgmv_kv_attention", "sgmv_verify_drafts",
+    "sgmv_kv_attention_workspace", "sgmv_kv_attention", "sgmv_verify_drafts", "sgmv_verify_drafts_workspace",
 ]
 
 

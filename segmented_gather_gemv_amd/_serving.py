@@ -65,10 +65,12 @@ def _bind():
         "sgmv_kv_attention_workspace": [A, S, C, P(sz)],
         "sgmv_kv_attention": [A, S, C, vp, sz, vp],
         "sgmv_verify_drafts": [vp, i64, vp, i64, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp,
-                               i64, vp, vp],
+                               i64, vp, vp, sz, vp],
     }.items():
         f = getattr(_lib, name)
         f.argtypes, f.restype = args, ctypes.c_int
+    _lib.sgmv_verify_drafts_workspace.argtypes = [i32, i32]
+    _lib.sgmv_verify_drafts_workspace.restype = sz
 
 
 _bind()
@@ -366,12 +368,15 @@ def sgmv_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
             not accepted.is_contiguous()):
         raise ValueError("accepted must be B contiguous int32 entries on target's device")
     _on_gpu(target)
+    size = _lib.sgmv_verify_drafts_workspace(B, V)
+    workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
     _check(_lib.sgmv_verify_drafts(
         target.data_ptr(), target.stride(0) if N + B > 1 else V,
         None if draft is None or N == 0 else draft.data_ptr(),
         V if draft is None or N <= 1 else draft.stride(0), V, _dtype_code(target.dtype),
         draft_ids.data_ptr(), draft_start.data_ptr(), B, N, int(max_drafts), accept_u.data_ptr(),
         sample_u.data_ptr(), tokens.data_ptr(),
-        tokens.stride(0) if B > 1 else max_drafts + 1, accepted.data_ptr(), _stream(dev)),
+        tokens.stride(0) if B > 1 else max_drafts + 1, accepted.data_ptr(),
+        workspace.data_ptr(), size, _stream(dev)),
         "sgmv_verify_drafts")
     return tokens, accepted

@@ -245,19 +245,32 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
   return launched(err);
 }
 
+size_t sgmv_verify_drafts_workspace(int32_t B, int32_t vocab) {
+  if (B < 1 || vocab < 1) return 0;
+  return (size_t)B * (size_t)ceil_div(vocab, VF_CHUNK) * 2 * sizeof(double);
+}
+
 sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd,
                                int32_t vocab, int32_t dtype, const int32_t* draft_ids,
                                const int32_t* draft_start, int32_t B, int32_t N,
                                int32_t max_drafts, const float* accept_u, const float* sample_u,
-                               int32_t* tokens, int64_t ldo, int32_t* accepted, void* stream) {
+                               int32_t* tokens, int64_t ldo, int32_t* accepted, void* workspace,
+                               size_t workspace_bytes, void* stream) {
   if (B < 0 || N < 0 || vocab < 1 || max_drafts < 0 || !row_type_ok(dtype)) return SGMV_EINVAL;
   if (B == 0) return SGMV_OK;
   if (!target || !draft_start || !sample_u || !tokens || !accepted || ldt < vocab ||
       (draft && ldd < vocab) || ldo < (int64_t)max_drafts + 1)
     return SGMV_EINVAL;
   if (N > 0 && max_drafts > 0 && (!draft_ids || !accept_u)) return SGMV_EINVAL;
+  if (B >= SGMV_KV_MAX_B || vocab > SGMV_MAX_VOCAB) return SGMV_EUNSUPPORTED;
+  if (!workspace || !aligned_to(workspace, 16)) return SGMV_EINVAL;
+  if (workspace_bytes < sgmv_verify_drafts_workspace(B, vocab)) return SGMV_ECAPACITY;
+  const int e = dtype == SGMV_F32 ? 4 : 2;
+  const bool vec = aligned_to(target, 4 * e) && ldt % 4 == 0 &&
+                   (!draft || (aligned_to(draft, 4 * e) && ldd % 4 == 0));
   const VerifyArgs A{target, draft, ldt, ldd, draft_ids, draft_start, accept_u, sample_u, tokens, ldo,
-                     accepted, B, vocab, N, max_drafts, dtype == SGMV_BF16};
+                     accepted, static_cast<double*>(workspace), B, vocab, N, max_drafts,
+                     dtype == SGMV_BF16, (int32_t)ceil_div(vocab, VF_CHUNK), vec};
   return launched(launch_verify(A, static_cast<hipStream_t>(stream)));
 }
 

@@ -5,6 +5,8 @@
 
 namespace sgmv {
 
+constexpr int VF_CHUNK = 4096;  // entries of a row that one workgroup sums
+
 struct VerifyArgs {
   const void* target;
   const void* draft;  // null: point masses
@@ -16,7 +18,9 @@ struct VerifyArgs {
   int32_t* tokens;
   int64_t ldo;
   int32_t* accepted;
-  int32_t B, V, N, max_drafts, bf16;
+  double* sums;  // [B][chunks][2]
+  int32_t B, V, N, max_drafts, bf16, chunks;
+  int32_t vec;  // rows may be read four entries at a time
 };
 
 hipError_t launch_verify(const VerifyArgs& A, hipStream_t stream);

@@ -7,22 +7,26 @@
 // p_{n+1}. A row is drawn from by its running sum: the lowest j whose sum passes r times the total.
 //
 // Sums are in fp64: with 2^17 entries a running sum in fp32 is off by more than an entry's own
-// weight. Bound by reading the one or two rows that are drawn from.
+// weight. Bound by reading the one or two rows that are drawn from, so a row is cut into chunks of
+// VF_CHUNK entries, one workgroup each: the first launch sums them (every one of a sequence's
+// workgroups looks at the drafts itself, a few loads), the second finds the chunk that r falls into
+// and the entry in it. One launch in which the last workgroup of a sequence does the second part would need
+// a cleared counter, which is a launch too.
 #include "verify.h"
 
 namespace sgmv {
 
 namespace {
 
-constexpr int VF_THREADS = 1024;
+constexpr int VF_THREADS = 256, VF_WAVES = VF_THREADS / WAVE;
+constexpr int VF_EACH = VF_CHUNK / VF_THREADS;  // entries of one thread
 
-template <class T> __device__ __forceinline__ float prob(const T* p);
-template <> __device__ __forceinline__ float prob(const float* p) { return *p; }
-template <> __device__ __forceinline__ float prob(const uint16_t* p) { return bf16_bits_to_f32(*p); }
+__device__ __forceinline__ float prob(const float* p) { return *p; }
+__device__ __forceinline__ float prob(const uint16_t* p) { return bf16_bits_to_f32(*p); }
 
 // What is not a weight (negative, NaN, infinite) counts as none.
-__device__ __forceinline__ double weight(double w) { return w > 0. && w < 1e300 ? w : 0.; }
 __device__ __forceinline__ float clean(float p) { return p > 0.f && p < INFINITY ? p : 0.f; }
+__device__ __forceinline__ double rest(double p, double q) { return p > q ? p - q : 0.; }
 
 __device__ __forceinline__ double wave_scan(double v) {  // inclusive
   const int lane = threadIdx.x & (WAVE - 1);
@@ -34,86 +38,217 @@ __device__ __forceinline__ double wave_scan(double v) {  // inclusive
   return v;
 }
 
+// Inclusive running sum over the workgroup's threads, the sum before this thread (the very value that the
+// thread before has as its own, so that neighbours leave no gap) and the total.
+__device__ __forceinline__ double block_scan(double v, double* s_sum, double& before, double& total) {
+  const int lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE;
+  const double up = wave_scan(v);
+  __syncthreads();
+  if (lane == WAVE - 1) s_sum[wv] = up;
+  __syncthreads();
+  double base = 0.;
+  total = 0.;
+  for (int i = 0; i < VF_WAVES; ++i) {
+    if (i < wv) base += s_sum[i];
+    total += s_sum[i];
+  }
+  const double left = __shfl_up(up, 1);
+  before = lane ? base + left : base;
+  return base + up;
+}
+
+// The row that sequence b is drawn from: target row p, draft row q (or none), entry left out (or -1).
+template <class T> struct Row {
+  const T* p;
+  const T* q;
+  int hole;
+};
+
+struct Drafts {
+  int first, n;
+};
+
+__device__ __forceinline__ Drafts drafts(const VerifyArgs& A, int b) {
+  const int first = min(max(A.start[b], 0), A.N);
+  return {first, max(min(min(max(A.start[b + 1], 0), A.N) - first, A.max_drafts), 0)};
+}
+
 template <class T>
-__global__ __launch_bounds__(VF_THREADS) void verify_kernel(VerifyArgs A) {
-  __shared__ double s_sum[VF_THREADS / WAVE];
-  __shared__ int s_at;
-  const int b = blockIdx.x, tid = threadIdx.x, lane = tid & (WAVE - 1), wv = tid / WAVE;
-  const int d0 = min(max(A.start[b], 0), A.N);
-  const int n = max(min(min(max(A.start[b + 1], 0), A.N) - d0, A.max_drafts), 0);
-  const T* target = static_cast<const T*>(A.target) + (int64_t)(d0 + b) * A.ldt;
-  const T* draft = static_cast<const T*>(A.draft) + (A.draft ? (int64_t)d0 * A.ldd : 0);
-  int taken = n;
-  for (int i0 = 0; i0 < n && taken == n; i0 += WAVE) {
+__device__ __forceinline__ Row<T> drawn_row(const VerifyArgs& A, int b, Drafts d, int taken) {
+  const bool out = taken < d.n;
+  return {static_cast<const T*>(A.target) + (int64_t)(d.first + b + taken) * A.ldt,
+          out && A.draft ? static_cast<const T*>(A.draft) + (int64_t)(d.first + taken) * A.ldd : nullptr,
+          out && !A.draft ? A.ids[d.first + taken] : -1};
+}
+
+// Entries [j, j + 4) of a row, j a multiple of 4; 0 past the end.
+template <class T, bool VEC>
+__device__ __forceinline__ void four(const T* row, int j, int V, float (&f)[4]) {
+  if (VEC && j + 4 <= V) {
+    if constexpr (sizeof(T) == 4) {
+      const u32x4_t v = load_u32x4(row + j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = clean(__uint_as_float(v[i]));
+    } else {
+      const u32x2_t v = *reinterpret_cast<const u32x2_t*>(row + j);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[2 * i] = clean(__uint_as_float(v[i] << 16));
+        f[2 * i + 1] = clean(__uint_as_float(v[i] & 0xffff0000u));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = j + i < V ? clean(prob(row + j + i)) : 0.f;
+  }
+}
+
+template <class T, bool VEC>
+__global__ __launch_bounds__(VF_THREADS) void verify_sum_kernel(VerifyArgs A) {
+  __shared__ double s_sum[2][VF_WAVES];
+  const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & (WAVE - 1), wv = tid / WAVE;
+  const Drafts d = drafts(A, b);
+  const T* target = static_cast<const T*>(A.target) + (int64_t)(d.first + b) * A.ldt;
+  const T* draft = static_cast<const T*>(A.draft) + (A.draft ? (int64_t)d.first * A.ldd : 0);
+  int taken = d.n;
+  for (int i0 = 0; i0 < d.n && taken == d.n; i0 += WAVE) {
     const int i = i0 + lane;
     bool ok = true;
-    if (i < n) {
-      const int id = A.ids[d0 + i];
+    if (i < d.n) {
+      const int id = A.ids[d.first + i];
       ok = false;
       if ((uint32_t)id < (uint32_t)A.V) {
         const double p = clean(prob(target + (int64_t)i * A.ldt + id));
         const double q = A.draft ? clean(prob(draft + (int64_t)i * A.ldd + id)) : 1.0;
-        ok = (double)A.accept_u[d0 + i] * q < p;
+        ok = (double)A.accept_u[d.first + i] * q < p;  // exact: 24 bits times 24
       }
     }
     const uint64_t bad = __ballot(!ok);
     if (bad) taken = i0 + __ffsll((unsigned long long)bad) - 1;
   }
-  int32_t* out = A.tokens + (int64_t)b * A.ldo;
-  for (int i = tid; i <= A.max_drafts; i += VF_THREADS)
-    if (i != taken) out[i] = i < taken ? A.ids[d0 + i] : -1;
-  if (tid == 0) A.accepted[b] = taken;
-
-  const T* p = target + (int64_t)taken * A.ldt;
-  const T* q = taken < n && A.draft ? draft + (int64_t)taken * A.ldd : nullptr;
-  const int hole = taken < n && !A.draft ? A.ids[d0 + taken] : -1;
-  const int per = (A.V + VF_THREADS - 1) / VF_THREADS;
-  const int j0 = min(tid * per, A.V), j1 = min(j0 + per, A.V);
-  if (tid == 0) s_at = -1;
-  for (int pass = 0; pass < 2; ++pass) {  // the second where the rest is all zero: p itself
-    auto w = [&](int j) {
-      const float a = clean(prob(p + j));
-      if (pass) return (double)a;
-      return weight(j == hole ? 0. : (double)a - (q ? (double)clean(prob(q + j)) : 0.));
-    };
-    double mine = 0.;
-    for (int j = j0; j < j1; ++j) mine += w(j);
-    const double upto = wave_scan(mine);
-    __syncthreads();
-    if (lane == WAVE - 1) s_sum[wv] = upto;
-    __syncthreads();
-    double before = 0., total = 0.;
-    for (int i = 0; i < VF_THREADS / WAVE; ++i) {
-      if (i < wv) before += s_sum[i];
-      total += s_sum[i];
+  if (c == 0) {
+    int32_t* out = A.tokens + (int64_t)b * A.ldo;
+    for (int i = tid; i <= A.max_drafts; i += VF_THREADS)
+      if (i != taken) out[i] = i < taken ? A.ids[d.first + i] : -1;
+    if (tid == 0) A.accepted[b] = taken;
+  }
+  const Row<T> row = drawn_row<T>(A, b, d, taken);
+  double sum = 0., all = 0.;  // of what is left of p, and of p itself
+#pragma unroll
+  for (int i = 0; i < VF_EACH / 4; ++i) {
+    const int j = c * VF_CHUNK + 4 * (i * VF_THREADS + tid);
+    float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
+    four<T, VEC>(row.p, j, A.V, p);
+    if (row.q) four<T, VEC>(row.q, j, A.V, q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      all += p[e];
+      sum += j + e == row.hole ? 0. : rest(p[e], q[e]);
     }
+  }
+#pragma unroll
+  for (int o = 32; o; o >>= 1) {
+    sum += __shfl_xor(sum, o);
+    all += __shfl_xor(all, o);
+  }
+  if (lane == 0) {
+    s_sum[0][wv] = sum;
+    s_sum[1][wv] = all;
+  }
+  __syncthreads();
+  if (tid < 2) {
+    double t = 0.;
+    for (int i = 0; i < VF_WAVES; ++i) t += s_sum[tid][i];
+    A.sums[((int64_t)b * A.chunks + c) * 2 + tid] = t;
+  }
+}
+
+template <class T, bool VEC>
+__global__ __launch_bounds__(VF_THREADS) void verify_draw_kernel(VerifyArgs A) {
+  __shared__ double s_sum[VF_WAVES], s_base;
+  __shared__ int s_chunk, s_token, s_last;
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int taken = A.accepted[b];
+  const Row<T> row = drawn_row<T>(A, b, drafts(A, b), taken);
+  if (tid == 0) s_chunk = s_token = s_last = -1;
+  // the chunk that r falls into; the second pass, over p itself, where nothing is left of it
+  const double* sums = A.sums + (int64_t)b * A.chunks * 2;
+  const int per = (A.chunks + VF_THREADS - 1) / VF_THREADS;
+  const int c0 = min(tid * per, A.chunks), c1 = min(c0 + per, A.chunks);
+  double at = 0.;
+  int pass = 0;
+  for (; pass < 2; ++pass) {
+    double mine = 0., before, total;
+    for (int c = c0; c < c1; ++c) mine += sums[2 * c + pass];
+    const double upto = block_scan(mine, s_sum, before, total);
     if (!(total > 0.)) continue;
-    const double at = (double)A.sample_u[b] * total;
-    // the same sums on both sides of a border, so that the intervals leave no gap
-    const double left = __shfl_up(upto, 1);
-    const double lo = lane ? before + left : before, hi = before + upto;
-    if (mine > 0. && lo <= at && at < hi) {
-      double c = lo;
-      int found = -1;
-      for (int j = j0; j < j1; ++j) {
-        const double x = w(j);
-        c += x;
-        if (x > 0.) found = j;
-        if (c > at) break;
+    at = (double)A.sample_u[b] * total;
+    if (before <= at && at < upto) {  // one thread
+      double base = before, last = before;
+      int chunk = -1;
+      for (int c = c0; c < c1; ++c) {
+        const double x = sums[2 * c + pass];
+        if (x > 0.) {
+          chunk = c;
+          last = base;
+        }
+        base += x;
+        if (base > at) break;
       }
-      atomicMax(&s_at, found);
+      s_chunk = chunk;
+      s_base = last;
     }
     break;
   }
   __syncthreads();
-  if (tid == 0) out[taken] = s_at;
+  int token = -1;
+  if (s_chunk >= 0) {
+    const int j0 = s_chunk * VF_CHUNK + tid * VF_EACH;
+    double w[VF_EACH], mine = 0.;
+#pragma unroll
+    for (int i = 0; i < VF_EACH / 4; ++i) {
+      float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
+      four<T, VEC>(row.p, j0 + 4 * i, A.V, p);
+      if (row.q && !pass) four<T, VEC>(row.q, j0 + 4 * i, A.V, q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[4 * i + e] = !pass && j0 + 4 * i + e == row.hole ? 0. : rest(p[e], q[e]);
+        mine += w[4 * i + e];
+      }
+    }
+    double before, total;
+    block_scan(mine, s_sum, before, total);
+    double sum = s_base + before;
+    // the lowest entry that passes; the last one with a weight if rounding leaves none (the chunk's sum was
+    // formed in another order)
+    int found = -1, last = -1;
+#pragma unroll
+    for (int i = 0; i < VF_EACH; ++i) {
+      sum += w[i];
+      if (w[i] > 0.) {
+        last = j0 + i;
+        if (found < 0 && sum > at) found = j0 + i;
+      }
+    }
+    if (last >= 0) atomicMax(&s_last, last);
+    if (found >= 0) atomicMin((unsigned*)&s_token, (unsigned)found);  // -1 is the largest
+    __syncthreads();
+    token = s_token >= 0 ? s_token : s_last;
+  }
+  if (tid == 0) A.tokens[(int64_t)b * A.ldo + taken] = token;
+}
+
+template <class T, bool VEC>
+void launch(const VerifyArgs& A, hipStream_t stream) {
+  verify_sum_kernel<T, VEC><<<dim3(A.chunks, A.B), VF_THREADS, 0, stream>>>(A);
+  verify_draw_kernel<T, VEC><<<dim3(A.B), VF_THREADS, 0, stream>>>(A);
 }
 
 }  // namespace
 
 hipError_t launch_verify(const VerifyArgs& A, hipStream_t stream) {
-  if (A.bf16) verify_kernel<uint16_t><<<dim3(A.B), dim3(VF_THREADS), 0, stream>>>(A);
-  else verify_kernel<float><<<dim3(A.B), dim3(VF_THREADS), 0, stream>>>(A);
+  if (A.bf16) A.vec ? launch<uint16_t, true>(A, stream) : launch<uint16_t, false>(A, stream);
+  else A.vec ? launch<float, true>(A, stream) : launch<float, false>(A, stream);
   return hipGetLastError();
 }
 

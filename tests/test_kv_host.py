@@ -225,19 +225,24 @@ def test_empty_calls_do_nothing():
         assert lib.sgmv_kv_attention_workspace(ctypes.byref(a), b, c, ctypes.byref(need)) == sg.SGMV_OK
         assert need.value == 0
     assert lib.sgmv_verify_drafts(None, 0, None, 0, 10, 0, None, None, 0, 0, 0, None, None, None, 0,
-                                  None, None) == sg.SGMV_OK
+                                  None, None, 0, None) == sg.SGMV_OK
 
 
 def test_verify_refuses():
     def call(target=0x1000, ldt=10, draft=0x2000, ldd=10, vocab=10, dtype=0, ids=0x3000, start=0x4000,
-             B=2, N=3, most=2, au=0x5000, su=0x6000, tokens=0x7000, ldo=3, accepted=0x8000):
+             B=2, N=3, most=2, au=0x5000, su=0x6000, tokens=0x7000, ldo=3, accepted=0x8000,
+             ws=0x9000, size=32):
         return sg.library().sgmv_verify_drafts(target, ldt, draft, ldd, vocab, dtype, ids, start, B, N,
-                                               most, au, su, tokens, ldo, accepted, None)
+                                               most, au, su, tokens, ldo, accepted, ws, size, None)
 
     for kw in (dict(target=None), dict(ldt=9), dict(ldd=9), dict(vocab=0), dict(dtype=2), dict(ids=None),
                dict(start=None), dict(B=-1), dict(N=-1), dict(most=-1), dict(au=None), dict(su=None),
-               dict(tokens=None), dict(ldo=2), dict(accepted=None)):
+               dict(tokens=None), dict(ldo=2), dict(accepted=None), dict(ws=None), dict(ws=0x9008)):
         assert call(**kw) == sg.SGMV_EINVAL, kw
+    assert sg.library().sgmv_verify_drafts_workspace(2, 10) == 32
+    assert call(size=31) == sg.SGMV_ECAPACITY
+    assert call(B=65536, size=1 << 30) == sg.SGMV_EUNSUPPORTED
+    assert call(vocab=(1 << 30) + 1, ldt=1 << 31, ldd=1 << 31, size=1 << 40) == sg.SGMV_EUNSUPPORTED
 
 
 # ---- refusals of the binding -----------------------------------------------------------
