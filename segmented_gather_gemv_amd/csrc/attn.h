@@ -7,8 +7,8 @@
 
 namespace sgmv {
 
-constexpr int AT_ROWS = 32;   // rows of one 32x32 product
-constexpr int AT_TOKENS = 32; // tokens of one 32x32 product
+constexpr int AT_ROWS = 32;   // rows of one wave of the tiled kernel
+constexpr int AT_TOKENS = 32; // granularity of a window's first token
 
 struct AttnArgs {
   KvArgs kv;
@@ -25,7 +25,8 @@ struct AttnArgs {
   // rows of one sequence up to which the direct kernel takes it (the tiled kernel takes the
   // others); INT32_MAX: the direct kernel takes all
   int32_t direct_rows;
-  int32_t one_tile;    // direct kernel: every sequence it takes has at most AT_ROWS rows
+  int32_t direct_tile; // rows of the direct kernel's workgroups: 16 or 32
+  int32_t one_tile;    // direct kernel: every sequence it takes has at most that many rows
   // split of a sequence's tokens over workgroups: `n_split` ranges of `chunk` tokens (a multiple
   // of the tile), the last one to the end
   int32_t chunk[2], n_split[2];  // [0] direct kernel, [1] tiled kernel
@@ -63,10 +64,6 @@ __device__ __forceinline__ f32x16_t mfma_32x32_bf16(u32x4_t a, u32x4_t b, f32x16
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(a), as_bf16x8(b), c, 0, 0, 0);
 }
 
-__device__ __forceinline__ f32x16_t mfma_32x32_f32(float a, float b, f32x16_t c) {
-  return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
-}
-
 // Token of register i of a 32x32 product's lane in half h.
 __device__ __forceinline__ int reg_token(int i, int h) { return (i & 3) + 8 * (i >> 2) + 4 * h; }
 
@@ -92,6 +89,10 @@ __device__ __forceinline__ void store_out(const AttnArgs& A, int64_t at, float a
   }
 }
 
+__device__ __forceinline__ f32x4_t mfma_16x16x4_f32(float a, float b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
+}
+
 // Maximum of a value over the two halves of the wave, in both.
 __device__ __forceinline__ float half_max(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -101,6 +102,17 @@ __device__ __forceinline__ float half_max(float v) {
 __device__ __forceinline__ float half_sum(float v) {
   const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Maximum and sum of a value over the lanes of equal lane % 16, in all of them.
+__device__ __forceinline__ float quad_max(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+
+__device__ __forceinline__ float quad_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
 }  // namespace sgmv

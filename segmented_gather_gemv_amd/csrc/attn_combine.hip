@@ -1,30 +1,34 @@
 // Joining the parts of rows whose tokens were split over workgroups: with each part's maximum m_i
 // (of scores times log2 e), sum l_i and unnormalised output o_i,
 //   m = max m_i,  out = sum 2^(m_i - m) o_i / sum 2^(m_i - m) l_i,  lse = (m + log2 of that sum) ln 2.
-// One wave per (token, query head); it reads what the parts wrote (4 (D + 2) bytes each, still in
-// the caches), and skips rows that were not split.
+// One launch for each kernel that may have split, one wave per row of its tiles; it reads what the
+// parts wrote (4 (D + 2) bytes each, still in the caches), and skips rows that were not split.
 #include "attn.h"
 
 namespace sgmv {
 
 namespace {
 
+constexpr int JOIN_ROWS = 4;  // of a workgroup
+
 template <bool F32>
-__global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A) {
+__global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A, int kernel) {
   const KvArgs& K = A.kv;
   const int lane = threadIdx.x & (WAVE - 1);
-  const int64_t at = (int64_t)blockIdx.x * (256 / WAVE) + threadIdx.x / WAVE;
-  const int token = (int)(at / A.Hq), head = (int)(at % A.Hq);
-  if (token >= K.T) return;
-  const int b = wave_find(K.B, token, [&](int i) { return min(max(K.q_start[i], 0), K.T); });
+  const int tile = kernel ? tiled_rows(K.D) : A.direct_tile, per_tile = tile / JOIN_ROWS;
+  const int kvh = blockIdx.x % K.H, rest = blockIdx.x / K.H;
+  const int slot = rest / per_tile;
+  const auto first_slot = [&](int i) { return (int)((int64_t)min(max(K.q_start[i], 0), K.T) * A.G / tile) + i; };
+  const bool one = !kernel && A.one_tile;
+  const int b = one ? slot : __builtin_amdgcn_readfirstlane(wave_find(K.B, slot, first_slot));
+  const int tile0 = one ? 0 : (slot - first_slot(b)) * tile;
   const KvSeq s = kv_seq(K, b);
-  const int tok = token - s.q0;
-  if (tok < 0 || tok >= s.q_len) return;
-  const int rows = s.q_len * A.G, row = tok * A.G + head % A.G;
-  const int kernel = rows > A.direct_rows, tile = kernel ? tiled_rows(K.D) : AT_ROWS;
-  const Span span = row_span(A, s, row / tile * tile, tile);
-  const int used = span_splits(A, span, kernel);
+  const int rows = s.q_len * A.G, row = tile0 + rest % per_tile * JOIN_ROWS + (int)threadIdx.x / WAVE;
+  if (tile0 < 0 || row >= rows || (rows > A.direct_rows) != (kernel == 1)) return;
+  const int used = span_splits(A, row_span(A, s, tile0, tile), kernel);
   if (used == 1) return;
+  const int token = s.q0 + row / A.G, head = kvh * A.G + row % A.G;
+  const int64_t at = (int64_t)token * A.Hq + head;
 
   const int64_t stride = (int64_t)K.T * A.Hq;
   float m = -INFINITY, l = 0.f;
@@ -36,7 +40,7 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A) {
   float top = m;
 #pragma unroll
   for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-  const float f = m == -INFINITY ? 0.f : exp2f(m - top);
+  const float f = m == -INFINITY ? 1.f : exp2f(m - top);  // l = 0 and o = 0, or NaN
   float sum = l * f;
 #pragma unroll
   for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
@@ -47,7 +51,7 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A) {
     if (d < K.D) {
       const f32x4_t v = *reinterpret_cast<const f32x4_t*>(A.part_o + (i * stride + at) * K.D + d);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] += w == 0.f ? 0.f : w * v[j];
+      for (int j = 0; j < 4; ++j) acc[j] += w * v[j];
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -60,11 +64,11 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A) {
 
 }  // namespace
 
-hipError_t launch_attn_combine(const AttnArgs& A, hipStream_t stream) {
-  const int64_t n = (int64_t)A.kv.T * A.Hq;
-  const dim3 g((unsigned)((n + 3) / 4)), b(256);
-  if (A.f32) attn_combine_kernel<true><<<g, b, 0, stream>>>(A);
-  else attn_combine_kernel<false><<<g, b, 0, stream>>>(A);
+hipError_t launch_attn_combine(const AttnArgs& A, int kernel, unsigned slots, hipStream_t stream) {
+  const int tile = kernel ? tiled_rows(A.kv.D) : A.direct_tile;
+  const dim3 g(slots * (unsigned)(tile / JOIN_ROWS) * (unsigned)A.kv.H), b(JOIN_ROWS * WAVE);
+  if (A.f32) attn_combine_kernel<true><<<g, b, 0, stream>>>(A, kernel);
+  else attn_combine_kernel<false><<<g, b, 0, stream>>>(A, kernel);
   return hipGetLastError();
 }
 

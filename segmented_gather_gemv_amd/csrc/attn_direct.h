@@ -1,170 +1,97 @@
 // Attention over the paged cache with keys and values loaded straight into matrix-core operands.
 //
-// For one (sequence, key/value head), a tile of 32 rows (new token, query head of the group) and a
-// range of tokens, each of the workgroup's 4 waves takes every fourth 32 tokens:
+// For one (sequence, key/value head), a tile of 16 R rows (new token, query head of the group) and a
+// range of tokens, each of the workgroup's waves takes every WAVES-th step of TOK tokens:
 //   S^T = K Q^T   (tokens x rows),  p = exp2(c s - m),  O^T += V^T P^T,   one running (m, l) per row.
-// A lane holds one row's scores in its registers (of tokens 8 (i / 4) + 4 half + i % 4), its
-// maximum needs one exchange with the other half, its sum none before the end, and its
-// probabilities are the next product's operand as they stand (kv_common.h). Nothing goes through
-// LDS but the four waves' sums at the end.
+// In a 16x16 product lane (r = lane % 16, quad = lane / 16) gives row r of the left operand, column r of
+// the right one and the inner indices 8 quad .. 8 quad + 7, and holds the result's rows 4 quad .. 4 quad
+// + 3 of column r. Which token is a product's row is free: tile x gives row 4 q + i the token at place
+// 4 x + i (V's order) of the piece that quad q loads of V, 16 bytes of one d. So a lane's probabilities
+// are the right operand of the next product as they stand, every load of K and V is 16 bytes wide, and
+// nothing goes through LDS but the waves' sums at the end. TOK is what makes those pieces whole:
+// 64 tokens of 8-bit codes (quad q: group q), 32 of wider ones (quad q: half q % 2 of group q / 2).
 //
-// Bound: the bytes of K and V, read once per tile of rows. 32x32 products on 8 rows waste three
-// quarters of the matrix cores, which does not matter: at 13 bytes per clock and CU (8 TB/s over 256
-// CUs) K and V of bf16 keep them 10% busy.
+// Bound: the bytes of K and V, read once per tile of rows. K and V of the next step are in flight
+// while this one is computed; 16 rows leave registers for three workgroups per CU at a head dimension
+// of 128, which is what hides the memory's latency.
 #pragma once
 
-#include "attn.h"
+#include "attn_operand.h"
 
 namespace sgmv {
 
-// Product of 32 rows of one operand with 32 of the other over one 16-byte chunk per lane and half.
-// bf16 operands: chunk = 8 values (bf16 cache) or 16 (8-bit, converted); fp32: the k = 2 product.
 template <bool F32, int FMT> struct Direct {
   static constexpr int bytes = KvFormat<FMT>::bytes;
-  static constexpr int C = 16 / bytes;                 // values of d in one K chunk
-  static constexpr int q_regs = F32 ? C : C / 2;       // registers of Q that go with one chunk
-  static constexpr int v_loads = bytes == 4 ? 2 : 1;   // 16-byte (8-byte for 8-bit) loads per V group
+  static constexpr int C = 16 / bytes;                // values of d in one piece of K
+  static constexpr int q_regs = F32 ? C : C / 2;      // registers of Q that go with one piece
+  static constexpr int tokens = bytes == 1 ? 64 : 32; // of one step
+  static constexpr int NT = tokens / 16;              // 16-token tiles of a step
+  static constexpr int v_loads = bytes == 4 ? 2 : 1;  // pieces of V per 16 values of d
 
-  // S^T += chunk of K times Q
-  static __device__ __forceinline__ f32x16_t qk(u32x4_t k, const uint32_t (&q)[q_regs], f32x16_t s) {
+  // A piece of K (or of V) as operands: codes in bf16, or the values of fp32 products.
+  struct Operand {
+    u32x4_t h[F32 ? 1 : C / 8];
+    float f[F32 ? C : 1];
+  };
+  static __device__ __forceinline__ Operand operand(u32x4_t w) {
+    Operand a;
     if constexpr (F32) {
-      float f[C];
-      if constexpr (bytes == 4) {
-        f[0] = __uint_as_float(k.x); f[1] = __uint_as_float(k.y);
-        f[2] = __uint_as_float(k.z); f[3] = __uint_as_float(k.w);
-      } else {
-        const uint32_t w[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (bytes == 4) {
+          a.f[i] = __uint_as_float(w[i]);
+        } else {
           float g[4];
           codes4<FMT>(w[i], g);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) f[4 * i + j] = g[j];
+          for (int j = 0; j < 4; ++j) a.f[4 * i + j] = g[j];
         }
       }
-#pragma unroll
-      for (int i = 0; i < C; ++i) s = mfma_32x32_f32(f[i], __uint_as_float(q[i]), s);
     } else if constexpr (bytes == 2) {
-      s = mfma_32x32_bf16(k, u32x4_t{q[0], q[1], q[2], q[3]}, s);
+      a.h[0] = w;
     } else {
-      s = mfma_32x32_bf16(codes8_bf16<FMT>(u32x2_t{k.x, k.y}), u32x4_t{q[0], q[1], q[2], q[3]}, s);
-      s = mfma_32x32_bf16(codes8_bf16<FMT>(u32x2_t{k.z, k.w}), u32x4_t{q[4], q[5], q[6], q[7]}, s);
+      a.h[0] = codes8_bf16<FMT>(u32x2_t{w.x, w.y});
+      a.h[1] = codes8_bf16<FMT>(u32x2_t{w.z, w.w});
+    }
+    return a;
+  }
+  // s += K piece times Q piece
+  static __device__ __forceinline__ f32x4_t qk(const Operand& k, const uint32_t (&q)[q_regs], f32x4_t s) {
+    if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) s = mfma_16x16x4_f32(k.f[i], __uint_as_float(q[i]), s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < C / 8; ++i)
+        s = mfma_16x16x32_bf16(as_bf16x8(k.h[i]), as_bf16x8(u32x4_t{q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]}), s);
     }
     return s;
   }
 };
 
-// A V operand: 8 tokens of one d, as stored.
-template <int BYTES> struct VRegs;
-template <> struct VRegs<1> { u32x2_t w; };
-template <> struct VRegs<2> { u32x4_t w; };
-template <> struct VRegs<4> { u32x4_t w[2]; };
-
-template <int BYTES>
-__device__ __forceinline__ VRegs<BYTES> load_v(const char* p) {
-  VRegs<BYTES> r;
-  if constexpr (BYTES == 1) r.w = *reinterpret_cast<const u32x2_t*>(p);
-  if constexpr (BYTES == 2) r.w = load_u32x4(p);
-  if constexpr (BYTES == 4) {
-    r.w[0] = load_u32x4(p);
-    r.w[1] = load_u32x4(p + 16);
-  }
-  return r;
+// Waves per SIMD to allocate registers for.
+constexpr int direct_waves(bool f32, int fmt, int DP, int R) {
+  if (f32) return DP <= 64 && R == 1 ? 2 : 1;
+  if (DP <= 64) return R == 1 ? 3 : 2;
+  if (DP <= 128) return 2;
+  return 1;
 }
 
-// Keep the tokens whose bit of `keep` (8 bits, one per stored element) is set, zero the others.
-__device__ __forceinline__ uint32_t keep_pair(uint32_t w, uint32_t two) {
-  return w & ((two & 1 ? 0x0000ffffu : 0u) | (two & 2 ? 0xffff0000u : 0u));
-}
-__device__ __forceinline__ void keep_tokens(VRegs<1>& r, uint32_t keep) {
-  const uint32_t b = keep & 15, c = keep >> 4;
-  auto bytes = [](uint32_t m) {
-    return (m & 1 ? 0xffu : 0u) | (m & 2 ? 0xff00u : 0u) | (m & 4 ? 0xff0000u : 0u) | (m & 8 ? 0xff000000u : 0u);
-  };
-  r.w.x &= bytes(b);
-  r.w.y &= bytes(c);
-}
-__device__ __forceinline__ void keep_tokens(VRegs<2>& r, uint32_t keep) {
-  r.w.x = keep_pair(r.w.x, keep);
-  r.w.y = keep_pair(r.w.y, keep >> 2);
-  r.w.z = keep_pair(r.w.z, keep >> 4);
-  r.w.w = keep_pair(r.w.w, keep >> 6);
-}
-__device__ __forceinline__ void keep_tokens(VRegs<4>& r, uint32_t keep) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (!(keep >> i & 1)) r.w[i / 4][i % 4] = 0u;
-}
-
-// The places (16 bits, in V's order) of a group's first n tokens.
-__device__ __forceinline__ uint32_t places_below(int n) {
-  const uint32_t t = (1u << n) - 1u;  // tokens 4-7 and 8-11 change places
-  return (t & 0xf00fu) | (t & 0x00f0u) << 4 | (t & 0x0f00u) >> 4;
-}
-
-__device__ __forceinline__ bool has_nonfinite(const VRegs<2>& r) {
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    any |= (r.w[i] & 0x7f80u) == 0x7f80u || (r.w[i] & 0x7f800000u) == 0x7f800000u;
-  return any;
-}
-__device__ __forceinline__ bool has_nonfinite(const VRegs<4>& r) {
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) any |= (r.w[i / 4][i % 4] & 0x7f800000u) == 0x7f800000u;
-  return any;
-}
-
-__device__ __forceinline__ void drop_nonfinite(VRegs<2>& r) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if ((r.w[i] & 0x7f80u) == 0x7f80u) r.w[i] &= 0xffff0000u;
-    if ((r.w[i] & 0x7f800000u) == 0x7f800000u) r.w[i] &= 0x0000ffffu;
-  }
-}
-__device__ __forceinline__ void drop_nonfinite(VRegs<4>& r) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if ((r.w[i / 4][i % 4] & 0x7f800000u) == 0x7f800000u) r.w[i / 4][i % 4] = 0u;
-}
-
-// O^T += V^T P^T over one group of 16 tokens: p holds this lane's 8 probabilities
-template <bool F32, int FMT>
-__device__ __forceinline__ f32x16_t pv(const VRegs<KvFormat<FMT>::bytes>& v, const float* p, u32x4_t pb,
-                                       f32x16_t o) {
-  if constexpr (F32) {
-    float f[8];
-    if constexpr (KvFormat<FMT>::bytes == 4) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v.w[i / 4][i % 4]);
-    } else {
-      float a[4], b[4];
-      codes4<FMT>(v.w.x, a);
-      codes4<FMT>(v.w.y, b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) { f[i] = a[i]; f[4 + i] = b[i]; }
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o = mfma_32x32_f32(f[i], p[i], o);
-    return o;
-  } else if constexpr (KvFormat<FMT>::bytes == 2) {
-    return mfma_32x32_bf16(v.w, pb, o);
-  } else {
-    return mfma_32x32_bf16(codes8_bf16<FMT>(v.w), pb, o);
-  }
-}
-
-// DP: head dimension rounded up to 64, 128 or 256; EXACT: it is that
-template <bool F32, int FMT, int DP, bool EXACT>
-__global__ __launch_bounds__(256) void attn_direct_kernel(AttnArgs A) {
+// DP: head dimension, or (not EXACT) an upper bound of it
+template <bool F32, int FMT, int DP, bool EXACT, int R, int WAVES>
+__global__ __launch_bounds__(WAVES* WAVE, direct_waves(F32, FMT, DP, R)) void attn_direct_kernel(AttnArgs A) {
   using X = Direct<F32, FMT>;
-  constexpr int WAVES = 4;
-  constexpr int NCH = DP / (2 * X::C);  // K chunks of one lane (its half's)
-  constexpr int NB = DP / 32;           // blocks of 32 values of d
+  constexpr int C = X::C, NT = X::NT, TOK = X::tokens, NG = TOK / 16, BYTES = X::bytes;
+  constexpr bool SCALED = KvFormat<FMT>::scaled;
+  constexpr int NCH = (DP / C + 3) / 4;  // pieces of K of one lane, per tile
+  constexpr int NB = DP / 16;            // blocks of 16 values of d
+  constexpr int VL = X::v_loads;
+  constexpr int ROWS = 16 * R, LD = DP + 4;
+  __shared__ float s_m[WAVES][ROWS], s_l[WAVES][ROWS];
+  __shared__ __align__(16) float s_o[WAVES][ROWS * LD];
   const KvArgs& K = A.kv;
   const int lane = threadIdx.x & (WAVE - 1), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-  const int col = lane & 31, half = lane >> 5;
+  const int r = lane & 15, quad = lane >> 4;
   const int D = EXACT ? DP : K.D;
 
   // this workgroup's piece
@@ -176,38 +103,59 @@ __global__ __launch_bounds__(256) void attn_direct_kernel(AttnArgs A) {
     b = slot;
     row0 = 0;
   } else {
-    // row tiles of sequence b take the slots from (rows before b) / 32 + b on
+    // row tiles of sequence b take the slots from (rows before b) / ROWS + b on
     b = wave_find(K.B, slot, [&](int i) {
-      return (int)((int64_t)min(max(K.q_start[i], 0), K.T) * A.G / AT_ROWS) + i;
+      return (int)((int64_t)min(max(K.q_start[i], 0), K.T) * A.G / ROWS) + i;
     });
     b = __builtin_amdgcn_readfirstlane(b);
-    row0 = (slot - ((int)((int64_t)min(max(K.q_start[b], 0), K.T) * A.G / AT_ROWS) + b)) * AT_ROWS;
+    row0 = (slot - ((int)((int64_t)min(max(K.q_start[b], 0), K.T) * A.G / ROWS) + b)) * ROWS;
   }
   const KvSeq s = kv_seq(K, b);
   const int rows = s.q_len * A.G;
   if (row0 < 0 || row0 >= rows || rows > A.direct_rows) return;
-  const Span span = row_span(A, s, row0, AT_ROWS);
+  const Span span = row_span(A, s, row0, ROWS);
   const int used = span_splits(A, span, 0);
   if (split >= used) return;
   const int t_begin = span.begin + split * A.chunk[0];
   const int t_end = split == used - 1 ? span.end : t_begin + A.chunk[0];
 
-  // Q: this lane's row, the chunks of d that its half meets
-  const int row = row0 + col;
-  const bool row_ok = row < rows;
-  const int tok = (row_ok ? row : 0) / A.G, head = kvh * A.G + (row_ok ? row : 0) % A.G;
-  uint32_t q[NCH][X::q_regs];
-  {
+  const int first = s.kv_len - s.q_len;
+  const int lo_pos = first + row0 / A.G;  // positions of the tile's first and last row
+  const int hi_pos = first + (min(row0 + ROWS, rows) - 1) / A.G;
+  const int ps = 1 << K.lps;
+  const int32_t* table = K.table + (int64_t)b * K.ldp;
+
+  // pages of this wave's next 64 / NG steps, lane NG i + g that of group g of step i, and of those
+  // that follow
+  constexpr int STEPS = WAVE / NG;
+  auto load_pages = [&](int i0) {
+    const int t = t_begin + TOK * (wv + WAVES * (i0 + lane / NG)) + 16 * (lane % NG);
+    return t < t_end ? kv_page(K, table, t) : -1;
+  };
+  const int n_steps = max((t_end - t_begin + TOK - 1) / TOK, 0);
+  const int mine = wv < n_steps ? (n_steps - wv + WAVES - 1) / WAVES : 0;
+  int pages = load_pages(0), pages_next = load_pages(STEPS);
+
+  // Q: rows r, 16 + r, .. of the tile; the pieces of d that this quad meets
+  int pos[R];  // position of each row
+  bool row_ok[R];
+  uint32_t q[R][NCH][X::q_regs];
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    const int row = row0 + 16 * t + r;
+    row_ok[t] = row < rows;
+    const int tok = (row_ok[t] ? row : 0) / A.G, head = kvh * A.G + (row_ok[t] ? row : 0) % A.G;
+    pos[t] = first + tok;
     const int64_t at = (int64_t)(s.q0 + tok) * A.ldq_t + (int64_t)head * A.ldq_h;
-    constexpr int NW = X::q_regs / 4;  // 16-byte pieces per chunk
-    constexpr int E = F32 ? 4 : 8;     // values of q per piece
+    constexpr int NW = X::q_regs / 4;  // 16-byte pieces of Q that go with one of K
+    constexpr int E = F32 ? 4 : 8;     // values in each
 #pragma unroll
     for (int c = 0; c < NCH; ++c)
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const int d = (2 * c + half) * X::C + w * E;
+        const int d = (4 * c + quad) * C + w * E;
         u32x4_t v = {0u, 0u, 0u, 0u};
-        if (row_ok && (EXACT || d < D)) {
+        if (row_ok[t] && d < D) {
           const char* p = static_cast<const char*>(A.q) + (at + d) * (F32 ? 4 : 2);
           if (A.q_vec) {
             v = load_u32x4(p);
@@ -222,153 +170,181 @@ __global__ __launch_bounds__(256) void attn_direct_kernel(AttnArgs A) {
           }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[c][4 * w + j] = v[j];
+        for (int j = 0; j < 4; ++j) q[t][c][4 * w + j] = v[j];
       }
   }
 
-  const int first = s.kv_len - s.q_len;
-  const int pos = first + tok;                      // this row's position
-  const int lo_pos = first + row0 / A.G;            // the tile's first and last
-  const int hi_pos = first + (min(row0 + AT_ROWS, rows) - 1) / A.G;
-  const int ps = 1 << K.lps;
-  const int32_t* table = K.table + (int64_t)b * K.ldp;
-
-  f32x16_t o[NB];
+  f32x4_t o[R][NB];
+  float m[R], l[R];
 #pragma unroll
-  for (int i = 0; i < NB; ++i) o[i] = f32x16_t{};
-  float m = -INFINITY, l = 0.f;
+  for (int t = 0; t < R; ++t) {
+#pragma unroll
+    for (int n = 0; n < NB; ++n) o[t][n] = f32x4_t{};
+    m[t] = -INFINITY;
+    l[t] = 0.f;
+  }
 
-  // pages of this wave's next 32 tiles: lane 2 i + g holds that of group g of tile i
-  int pages = -1;
-  auto load_pages = [&](int i0) {
-    const int t = t_begin + 32 * (wv + WAVES * (i0 + (lane >> 1))) + 16 * (lane & 1);
-    pages = t < t_end ? kv_page(K, table, t) : -1;
-  };
-  const int n_tiles = (t_end - t_begin + 31) / 32;
-  const int mine = wv < n_tiles ? (n_tiles - wv + WAVES - 1) / WAVES : 0;
-
-  u32x4_t kr[NCH];
-  float ks[16], vs[16];
-  (void)ks; (void)vs;
-  // block of group g of tile i: first token's index in [pages][H][ps]
-  auto group_at = [&](int i, int g) {
-    const int p = __builtin_amdgcn_readlane(pages, (2 * i + g) & 63);
-    const int t = t_begin + 32 * (wv + WAVES * i) + 16 * g;
+  // Groups that this lane loads from: of K as row r of a tile, of V as quad. Token of the lane's
+  // row i of tile x: 16 * group + tok0 + step(x) + i.
+  const int kg = BYTES == 1 ? r >> 2 : r >> 3, vg = BYTES == 1 ? quad : quad >> 1;
+  const int k_tok = BYTES == 1 ? r & 3 : 4 * ((r >> 2) & 1) + (r & 3);
+  const int v_half = BYTES == 1 ? 0 : quad & 1;
+  auto tile_tok = [](int x) { return BYTES == 1 ? 8 * (x & 1) + 4 * (x >> 1) : 8 * x; };
+  // [pages][H][page size] index of a group's first token
+  auto group_at = [&](int p, int i, int g) {
+    const int t = t_begin + TOK * (wv + WAVES * i) + 16 * g;
     return ((int64_t)max(p, 0) * K.H + kvh) * ps + (t & (ps - 1));
   };
+
+  u32x4_t kr[NT][NCH], vr[NB][VL];
+  f32x4_t ks[SCALED ? NT : 1], vs[SCALED ? NT : 1];
+  (void)ks; (void)vs;
+  bool missing;  // of the step whose K is loaded: some group is not there
+  int vpage;     // and the page of this lane's group of V
   auto load_k = [&](int i) {
-    const int64_t g0 = group_at(i, 0), g1 = group_at(i, 1);
-    const char* p = static_cast<const char*>(K.k) + (lane & 16 ? g1 : g0) * D * X::bytes + (lane & 15) * 16;
+    const int idx = (i & (STEPS - 1)) * NG;
+    const int p = __shfl(pages, idx + kg);
+    vpage = __shfl(pages, idx + vg);
+    missing = __any(p < 0);
+    const char* base = static_cast<const char*>(K.k) + group_at(p, i, kg) * D * BYTES + k_tok * 16;
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      int d = 2 * c + half;
-      if (!EXACT) d = min(d, D / X::C - 1);
-      kr[c] = load_u32x4(p + d * 256);
-    }
-    if constexpr (KvFormat<FMT>::scaled) {
+    for (int x = 0; x < NT; ++x)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f32x4_t a = *reinterpret_cast<const f32x4_t*>(K.k_scale + (j < 2 ? g0 : g1) + 8 * (j & 1) + 4 * half);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ks[4 * j + e] = a[e];
+      for (int c = 0; c < NCH; ++c) {
+        int piece = 4 * c + quad;
+        const bool whole = EXACT && DP / C % 4 == 0;
+        if (!whole) piece = min(piece, D / C - 1);
+        kr[x][c] = load_u32x4(base + piece * 256 + tile_tok(x) * 16);
+        if (!whole && 4 * c + quad >= D / C) kr[x][c] = u32x4_t{0u, 0u, 0u, 0u};
       }
+    if constexpr (SCALED) {
+      const float* at = K.k_scale + group_at(vpage, i, vg);
+#pragma unroll
+      for (int x = 0; x < NT; ++x) ks[x] = *reinterpret_cast<const f32x4_t*>(at + tile_tok(x));
+    }
+  };
+  auto load_v = [&](int i) {
+    const int64_t g = group_at(vpage, i, vg);
+    const char* base = static_cast<const char*>(K.v) + (g * D + r * 16 + 8 * v_half) * BYTES;
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int e = 0; e < VL; ++e)
+        if (EXACT || 16 * n < D) vr[n][e] = load_u32x4(base + n * 256 * BYTES + 16 * e);
+    if constexpr (SCALED) {
+#pragma unroll
+      for (int x = 0; x < NT; ++x) vs[x] = *reinterpret_cast<const f32x4_t*>(K.v_scale + g + tile_tok(x));
     }
   };
 
   if (mine > 0) {
-    load_pages(0);
     load_k(0);
+    load_v(0);
   }
   for (int i = 0; i < mine; ++i) {
-    const int t0 = t_begin + 32 * (wv + WAVES * i);
-    const int p0 = __builtin_amdgcn_readlane(pages, (2 * i) & 63);
-    const int p1 = __builtin_amdgcn_readlane(pages, (2 * i + 1) & 63);
-    const int64_t g0 = group_at(i, 0), g1 = group_at(i, 1);
-    VRegs<X::bytes> vr[NB][2];
-#pragma unroll
-    for (int n = 0; n < NB; ++n) {
-      int d = 32 * n + col;
-      if (!EXACT) d = min(d, D - 1);
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-        vr[n][g] = load_v<X::bytes>(static_cast<const char*>(K.v) + ((g ? g1 : g0) * D + d * 16 + 8 * half) * X::bytes);
-    }
-    if constexpr (KvFormat<FMT>::scaled) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const f32x4_t a = *reinterpret_cast<const f32x4_t*>(K.v_scale + (j < 2 ? g0 : g1) + 8 * (j & 1) + 4 * half);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) vs[4 * j + e] = a[e];
-      }
-    }
+    const int t0 = t_begin + TOK * (wv + WAVES * i);
+    const bool gap = missing;
+    const int page = vpage;  // of this lane's tokens
 
-    f32x16_t sc = {};
+    f32x4_t sc[R][NT];
 #pragma unroll
-    for (int c = 0; c < NCH; ++c)
-      if (EXACT || 2 * c * X::C < D) sc = X::qk(kr[c], q[c], sc);
-    if constexpr (KvFormat<FMT>::scaled) {
+    for (int x = 0; x < NT; ++x) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) sc[j] *= ks[j];
+      for (int t = 0; t < R; ++t) sc[t][x] = f32x4_t{};
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+        if (EXACT || 4 * c * C < D) {
+          const auto k = X::operand(kr[x][c]);
+#pragma unroll
+          for (int t = 0; t < R; ++t) sc[t][x] = X::qk(k, q[t][c], sc[t][x]);
+        }
+    }
+    if constexpr (SCALED) {
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sc[t][x][j] *= ks[x][j];
     }
     if (i + 1 < mine) {
-      if (((i + 1) & 31) == 0) load_pages(i + 1);
+      if (((i + 1) & (STEPS - 1)) == 0) {
+        pages = pages_next;
+        pages_next = load_pages(i + 1 + STEPS);
+      }
       load_k(i + 1);
     }
 
-    // a tile that some row sees only part of, or with tokens that are not there
-    const bool edge = t0 + 31 > lo_pos || (A.window && t0 <= hi_pos - A.window) || p0 < 0 || p1 < 0;
-    uint32_t there = 0xffffu;  // this lane's tokens that exist
+    // a step that some row sees only part of, or with tokens that are not there
+    const bool edge = t0 + TOK - 1 > lo_pos || (A.window && t0 <= hi_pos - A.window) || gap;
+    const int t_lane = t0 + 16 * vg + 4 * v_half;  // this lane's first token
     if (edge) {
-      there = 0;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int t = t0 + reg_token(j, half);
-        const bool has = t < s.kv_len && (j < 8 ? p0 : p1) >= 0;
-        there |= has ? 1u << j : 0u;
-        if (!has || t > pos || (A.window && t <= pos - A.window)) sc[j] = -INFINITY;
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int at = t_lane + tile_tok(x) + j;
+          const bool has = at < s.kv_len && page >= 0;
+#pragma unroll
+          for (int t = 0; t < R; ++t)
+            if (!has || at > pos[t] || (A.window && at <= pos[t] - A.window)) sc[t][x][j] = -INFINITY;
+        }
+    }
+
+    u32x4_t pb[R][NT / 2];  // probabilities in bf16
+    float pf[F32 ? R : 1][NT][4];
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      float top = sc[t][0][0];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = fmaxf(top, sc[t][x][j]);
+      top *= A.scale_log2;
+      // a stale maximum is as good as long as nothing grows past 2^8
+      if (__any(top > m[t] + 8.f)) {
+        const float now = fmaxf(m[t], quad_max(top));
+        const float f = m[t] == now ? 1.f : exp2f(m[t] - now);  // 0 from -inf on
+        m[t] = now;
+        l[t] *= f;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[t][n][j] *= f;
+      }
+      const float base = m[t] == -INFINITY ? 0.f : m[t];
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          p[j] = __builtin_amdgcn_exp2f(fmaf(sc[t][x][j], A.scale_log2, -base));
+          l[t] += p[j];
+        }
+        if constexpr (SCALED) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) p[j] = edge && p[j] == 0.f ? 0.f : p[j] * vs[x][j];
+        }
+        if constexpr (F32) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) pf[t][x][j] = p[j];
+        } else {
+          pb[t][x / 2][2 * (x & 1)] = pack_bf16x2(p[0], p[1]);
+          pb[t][x / 2][2 * (x & 1) + 1] = pack_bf16x2(p[2], p[3]);
+        }
       }
     }
 
-    float top = sc[0];
-#pragma unroll
-    for (int j = 1; j < 16; ++j) top = fmaxf(top, sc[j]);
-    top = half_max(top) * A.scale_log2;
-    // a stale maximum is as good as long as nothing grows past 2^8
-    if (__any(top > m + 8.f)) {
-      const float now = fmaxf(m, top);
-      const float f = m == now ? 1.f : exp2f(m - now);  // 0 from -inf on
-      m = now;
-      l *= f;
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[n][j] *= f;
-    }
-    const float base = m == -INFINITY ? 0.f : m;
-    float p[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      p[j] = __builtin_amdgcn_exp2f(fmaf(sc[j], A.scale_log2, -base));
-      l += p[j];
-    }
-    if constexpr (KvFormat<FMT>::scaled) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) p[j] = edge && p[j] == 0.f ? 0.f : p[j] * vs[j];
-    }
-    u32x4_t pb[2] = {};
-    if constexpr (!F32) {
-#pragma unroll
-      for (int g = 0; g < 2; ++g)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) pb[g][j] = pack_bf16x2(p[8 * g + 2 * j], p[8 * g + 2 * j + 1]);
-    }
     if (edge) {
+      uint32_t there = 0;  // this lane's places whose token exists
+      const int n_there = page >= 0 ? min(max(s.kv_len - (t0 + 16 * vg), 0), 16) : 0;
+      there = places_below(n_there) >> (8 * v_half);
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int g = 0; g < 2; ++g) keep_tokens(vr[n][g], there >> (8 * g) & 0xffu);
-      if constexpr (!KvFormat<FMT>::scaled) {
-        // A V value that is not finite, in a tile that some rows see only part of: in the product,
+        for (int e = 0; e < VL; ++e) vr[n][e] = keep_elements<BYTES>(vr[n][e], there >> (4 * e));
+      if constexpr (!SCALED) {
+        // A V value that is not finite, in a step that some rows see only part of: in the product,
         // 0 * inf would spoil the rows that do not see it. It is left out of the product and added
         // to the rows that see it, token by token. (8-bit codes are finite; their scales meet only
         // probabilities that are not 0.)
@@ -376,105 +352,150 @@ __global__ __launch_bounds__(256) void attn_direct_kernel(AttnArgs A) {
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-          for (int g = 0; g < 2; ++g) odd |= has_nonfinite(vr[n][g]);
+          for (int e = 0; e < VL; ++e)
+            if (EXACT || 16 * n < D) odd |= has_nonfinite<BYTES>(vr[n][e]);
         if (__any(odd)) {
 #pragma unroll
           for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) drop_nonfinite(vr[n][g]);
+            for (int e = 0; e < VL; ++e) vr[n][e] = drop_nonfinite<BYTES>(vr[n][e]);
 #pragma unroll 1
-          for (int x = 0; x < AT_TOKENS; ++x) {
-            const int t = t0 + x;
-            if ((x < 16 ? p0 : p1) < 0 || t > pos || (A.window && t <= pos - A.window)) continue;
-            const int64_t at = (x < 16 ? g0 : g1) * D + 8 * ((x >> 2) & 1) + 4 * ((x >> 3) & 1) + (x & 3);
+          for (int x = 0; x < TOK; ++x) {
+            const int at_t = t0 + x;
+            const int p = kv_page(K, table, at_t);
+            if (p < 0) continue;
+            const int64_t at = ((((int64_t)p * K.H + kvh) * ps + ((at_t & (ps - 1)) & ~15)) * D) +
+                               8 * ((x >> 2) & 1) + 4 * ((x >> 3) & 1) + (x & 3);
+#pragma unroll 1
+            for (int n = 0; n < D / 16; ++n) {
+              float f[4];
 #pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int d = 32 * n + reg_token(j, half);
-                if (!EXACT && d >= D) continue;
-                const float f = F32 ? static_cast<const float*>(K.v)[at + d * 16]
-                                    : bf16_bits_to_f32(static_cast<const uint16_t*>(K.v)[at + d * 16]);
-                if (!(fabsf(f) < INFINITY)) o[n][j] += f;
+              for (int j = 0; j < 4; ++j) {
+                const int64_t e = at + (16 * n + 4 * quad + j) * 16;
+                f[j] = F32 ? static_cast<const float*>(K.v)[e] : bf16_bits_to_f32(static_cast<const uint16_t*>(K.v)[e]);
               }
+#pragma unroll
+              for (int t = 0; t < R; ++t)
+                if (at_t <= pos[t] && !(A.window && at_t <= pos[t] - A.window)) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    if (!(fabsf(f[j]) < INFINITY)) {
+#pragma unroll
+                      for (int k = 0; k < NB; ++k)
+                        if (k == n) o[t][k][j] += f[j];
+                    }
+                }
+            }
           }
         }
       }
     }
 #pragma unroll
-    for (int n = 0; n < NB; ++n)
+    for (int n = 0; n < NB; ++n) {
+      if (!EXACT && 16 * n >= D) continue;
 #pragma unroll
-      for (int g = 0; g < 2; ++g) o[n] = pv<F32, FMT>(vr[n][g], p + 8 * g, pb[g], o[n]);
+      for (int e = 0; e < VL; ++e) {
+        const auto v = X::operand(vr[n][e]);
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+          if constexpr (F32) {
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+              o[t][n] = mfma_16x16x4_f32(v.f[j], pf[t][BYTES == 1 ? j / 4 : e][j % 4], o[t][n]);
+          } else {
+#pragma unroll
+            for (int h = 0; h < C / 8; ++h) o[t][n] = mfma_16x16x32_bf16(as_bf16x8(v.h[h]), as_bf16x8(pb[t][h]), o[t][n]);
+          }
+        }
+      }
+    }
+    if (i + 1 < mine) load_v(i + 1);
   }
 
-  // the four waves' sums: waves 2, 3 hand theirs to 0, 1, then 1 to 0
-  __shared__ float s_m[WAVES][32], s_l[WAVES][32];
-  __shared__ float s_o[2][NB * 16 * WAVE];
-  l = half_sum(l);
-  if (half == 0) {
-    s_m[wv][col] = m;
-    s_l[wv][col] = l;
+  // The waves' sums. A wave that saw nothing has m = -inf, l = 0, o = 0 (or NaN where all it saw
+  // was NaN, which has to stay).
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    l[t] = quad_sum(l[t]);
+    if (quad == 0) {
+      s_m[wv][16 * t + r] = m[t];
+      s_l[wv][16 * t + r] = l[t];
+    }
   }
   __syncthreads();
-  const float top = fmaxf(fmaxf(s_m[0][col], s_m[1][col]), fmaxf(s_m[2][col], s_m[3][col]));
-  float sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < WAVES; ++w) sum += s_m[w][col] == -INFINITY ? 0.f : s_l[w][col] * exp2f(s_m[w][col] - top);
-  const float f = m == -INFINITY ? 0.f : exp2f(m - top);
+  for (int t = 0; t < R; ++t) {
+    float top = -INFINITY;
 #pragma unroll
-  for (int n = 0; n < NB; ++n)
-#pragma unroll
-    for (int j = 0; j < 16; ++j) o[n][j] *= f;
-#pragma unroll
-  for (int step = 2; step >= 1; step >>= 1) {
-    if (wv >= step && wv < 2 * step) {
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) s_o[wv - step][(n * 16 + j) * WAVE + lane] = o[n][j];
-    }
-    __syncthreads();
-    if (wv < step) {
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int j = 0; j < 16; ++j) o[n][j] += s_o[wv][(n * 16 + j) * WAVE + lane];
-    }
-    __syncthreads();
-  }
-  if (wv != 0 || !row_ok) return;
-
-  const int64_t at = (int64_t)(s.q0 + tok) * A.Hq + head;
-  if (used > 1) {
-    const int64_t place = (int64_t)split * K.T * A.Hq + at;
-    if (half == 0) {
-      A.part_ml[2 * place] = top;
-      A.part_ml[2 * place + 1] = sum;
-    }
-    float* dst = A.part_o + place * D;
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, s_m[w][16 * t + r]);
+    const float f = m[t] == -INFINITY ? 1.f : exp2f(m[t] - top);
 #pragma unroll
     for (int n = 0; n < NB; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int d = 32 * n + 8 * j + 4 * half;
-        if (EXACT || d < D)
-          *reinterpret_cast<f32x4_t*>(dst + d) = f32x4_t{o[n][4 * j], o[n][4 * j + 1], o[n][4 * j + 2], o[n][4 * j + 3]};
-      }
-    return;
+      if (EXACT || 16 * n < D)
+        *reinterpret_cast<f32x4_t*>(&s_o[wv][(16 * t + r) * LD + 16 * n + 4 * quad]) =
+            f32x4_t{o[t][n][0] * f, o[t][n][1] * f, o[t][n][2] * f, o[t][n][3] * f};
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  if (A.lse && half == 0)
-    A.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
-  const int64_t oat = (int64_t)(s.q0 + tok) * A.ldo_t + (int64_t)head * A.ldo_h;
+  __syncthreads();
+  const int tile_rows = min(ROWS, rows - row0);
+  const int per_row = D / 4;
+  for (int e = threadIdx.x; e < tile_rows * per_row; e += WAVES * WAVE) {
+    const int lr = e / per_row, d = 4 * (e - lr * per_row);
+    f32x4_t sum_o = {0.f, 0.f, 0.f, 0.f};
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int n = 0; n < NB; ++n)
+    for (int w = 0; w < WAVES; ++w) {
+      top = fmaxf(top, s_m[w][lr]);
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(&s_o[w][lr * LD + d]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int d = 32 * n + 8 * j + 4 * half;
-      if (!EXACT && d >= D) continue;
-      store_out<F32>(A, oat + d, o[n][4 * j] * inv, o[n][4 * j + 1] * inv, o[n][4 * j + 2] * inv, o[n][4 * j + 3] * inv);
+      for (int j = 0; j < 4; ++j) sum_o[j] += v[j];
     }
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const float mw = s_m[w][lr];
+      sum += mw == -INFINITY ? s_l[w][lr] : s_l[w][lr] * exp2f(mw - top);
+    }
+    const int tok = (row0 + lr) / A.G, head = kvh * A.G + (row0 + lr) % A.G;
+    const int64_t at = (int64_t)(s.q0 + tok) * A.Hq + head;
+    if (used > 1) {
+      const int64_t place = (int64_t)split * K.T * A.Hq + at;
+      if (d == 0) {
+        A.part_ml[2 * place] = top;
+        A.part_ml[2 * place + 1] = sum;
+      }
+      *reinterpret_cast<f32x4_t*>(A.part_o + place * D + d) = sum_o;
+    } else {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      if (A.lse && d == 0) A.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
+      store_out<F32>(A, (int64_t)(s.q0 + tok) * A.ldo_t + (int64_t)head * A.ldo_h + d, sum_o[0] * inv,
+                     sum_o[1] * inv, sum_o[2] * inv, sum_o[3] * inv);
+    }
+  }
+}
+
+template <bool F32, int FMT, int DP, bool EXACT, int R, int WAVES>
+hipError_t launch_direct(const AttnArgs& A, unsigned slots, hipStream_t stream) {
+  const dim3 g(slots * (unsigned)A.n_split[0] * (unsigned)A.kv.H);
+  attn_direct_kernel<F32, FMT, DP, EXACT, R, WAVES><<<g, WAVES * WAVE, 0, stream>>>(A);
+  return hipGetLastError();
+}
+
+template <int FMT, int R>
+hipError_t launch_direct_dim(const AttnArgs& A, unsigned slots, hipStream_t stream) {
+  const int D = A.kv.D;
+  if (D == 64) return launch_direct<false, FMT, 64, true, R, 4>(A, slots, stream);
+  if (D == 96) return launch_direct<false, FMT, 96, true, R, 4>(A, slots, stream);
+  if (D == 128) return launch_direct<false, FMT, 128, true, R, 4>(A, slots, stream);
+  if (D == 192) return launch_direct<false, FMT, 192, true, R, 4>(A, slots, stream);
+  if (D == 256) return launch_direct<false, FMT, 256, true, R, 4>(A, slots, stream);
+  if (D < 64) return launch_direct<false, FMT, 64, false, R, 4>(A, slots, stream);
+  if (D < 128) return launch_direct<false, FMT, 128, false, R, 4>(A, slots, stream);
+  return launch_direct<false, FMT, 256, false, R, 4>(A, slots, stream);
+}
+
+template <int FMT>
+hipError_t launch_direct_bf16(const AttnArgs& A, unsigned slots, hipStream_t stream) {
+  return A.direct_tile == 16 ? launch_direct_dim<FMT, 1>(A, slots, stream)
+                             : launch_direct_dim<FMT, 2>(A, slots, stream);
 }
 
 }  // namespace sgmv
-

@@ -3,24 +3,27 @@
 
 namespace sgmv {
 
-template <int FMT>
-static void launch_fmt(const AttnArgs& A, dim3 g, hipStream_t stream) {
-  const dim3 b(256);
+// fp32 operands take twice the registers of bf16 ones: head dimensions past 128 get one tile of rows.
+template <int FMT, int R>
+static hipError_t launch_dim(const AttnArgs& A, unsigned slots, hipStream_t stream) {
   const int D = A.kv.D;
-  if (D == 64) attn_direct_kernel<true, FMT, 64, true><<<g, b, 0, stream>>>(A);
-  else if (D < 64) attn_direct_kernel<true, FMT, 64, false><<<g, b, 0, stream>>>(A);
-  else if (D == 128) attn_direct_kernel<true, FMT, 128, true><<<g, b, 0, stream>>>(A);
-  else if (D < 128) attn_direct_kernel<true, FMT, 128, false><<<g, b, 0, stream>>>(A);
-  else if (D == 256) attn_direct_kernel<true, FMT, 256, true><<<g, b, 0, stream>>>(A);
-  else attn_direct_kernel<true, FMT, 256, false><<<g, b, 0, stream>>>(A);
+  if (D == 64) return launch_direct<true, FMT, 64, true, R, 4>(A, slots, stream);
+  if (D < 64) return launch_direct<true, FMT, 64, false, R, 4>(A, slots, stream);
+  if (D == 128) return launch_direct<true, FMT, 128, true, R, 4>(A, slots, stream);
+  if (D < 128) return launch_direct<true, FMT, 128, false, R, 4>(A, slots, stream);
+  if constexpr (R == 1) return launch_direct<true, FMT, 256, false, 1, 4>(A, slots, stream);
+  return hipErrorInvalidValue;
+}
+
+template <int FMT>
+static hipError_t launch_fmt(const AttnArgs& A, unsigned slots, hipStream_t stream) {
+  return A.direct_tile == 16 ? launch_dim<FMT, 1>(A, slots, stream) : launch_dim<FMT, 2>(A, slots, stream);
 }
 
 hipError_t launch_attn_direct_f32(const AttnArgs& A, int fmt, unsigned slots, hipStream_t stream) {
-  const dim3 g(slots * (unsigned)A.n_split[0] * (unsigned)A.kv.H);
-  if (fmt == SGMV_KV_E4M3) launch_fmt<SGMV_KV_E4M3>(A, g, stream);
-  else if (fmt == SGMV_KV_I8) launch_fmt<SGMV_KV_I8>(A, g, stream);
-  else launch_fmt<SGMV_KV_F32>(A, g, stream);
-  return hipGetLastError();
+  if (fmt == SGMV_KV_E4M3) return launch_fmt<SGMV_KV_E4M3>(A, slots, stream);
+  if (fmt == SGMV_KV_I8) return launch_fmt<SGMV_KV_I8>(A, slots, stream);
+  return launch_fmt<SGMV_KV_F32>(A, slots, stream);
 }
 
 }  // namespace sgmv

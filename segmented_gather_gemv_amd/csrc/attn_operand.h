@@ -1,0 +1,63 @@
+// Operands of V as stored: which tokens to keep, and values that are not finite.
+#pragma once
+
+#include "attn.h"
+
+namespace sgmv {
+
+// The bits of a word of two bf16 whose flag is set.
+__device__ __forceinline__ uint32_t keep_pair(uint32_t w, uint32_t two) {
+  return w & ((two & 1 ? 0x0000ffffu : 0u) | (two & 2 ? 0xffff0000u : 0u));
+}
+
+// Keep the elements of a 16-byte piece whose bit of `keep` is set (bit i: element i), zero the others.
+template <int BYTES>
+__device__ __forceinline__ u32x4_t keep_elements(u32x4_t w, uint32_t keep) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BYTES == 1) {
+      const uint32_t m = keep >> (4 * i);
+      w[i] &= (m & 1 ? 0xffu : 0u) | (m & 2 ? 0xff00u : 0u) | (m & 4 ? 0xff0000u : 0u) | (m & 8 ? 0xff000000u : 0u);
+    } else if constexpr (BYTES == 2) {
+      w[i] = keep_pair(w[i], keep >> (2 * i));
+    } else {
+      w[i] = keep >> i & 1 ? w[i] : 0u;
+    }
+  }
+  return w;
+}
+
+// The places (16 bits, in V's order) of a group's first n tokens.
+__device__ __forceinline__ uint32_t places_below(int n) {
+  const uint32_t t = (1u << n) - 1u;  // tokens 4-7 and 8-11 change places
+  return (t & 0xf00fu) | (t & 0x00f0u) << 4 | (t & 0x0f00u) >> 4;
+}
+
+// bf16 or fp32 elements only: 8-bit codes are finite.
+template <int BYTES>
+__device__ __forceinline__ bool has_nonfinite(u32x4_t w) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    any |= (w[i] & 0x7f800000u) == 0x7f800000u;
+    if constexpr (BYTES == 2) any |= (w[i] & 0x7f80u) == 0x7f80u;
+  }
+  return any;
+}
+
+template <int BYTES>
+__device__ __forceinline__ u32x4_t drop_nonfinite(u32x4_t w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t high = (w[i] & 0x7f800000u) == 0x7f800000u;
+    if constexpr (BYTES == 2) {
+      if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
+      if (high) w[i] &= 0x0000ffffu;
+    } else {
+      if (high) w[i] = 0u;
+    }
+  }
+  return w;
+}
+
+}  // namespace sgmv

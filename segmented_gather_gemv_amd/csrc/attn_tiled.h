@@ -10,7 +10,7 @@
 // halves of 8 tokens exchanged in every second 8 values of d, so that 16 lanes read 16 different bank groups.
 #pragma once
 
-#include "attn_direct.h"
+#include "attn_operand.h"
 
 namespace sgmv {
 
@@ -138,21 +138,13 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
         const int piece = at % PIECES + lane;
         const int there = groups >> g & 1 ? min(max(s.kv_len - t0 - 16 * g, 0), 16) : 0;  // tokens
         if constexpr (!SCALED) {
-          VRegs<2> v;
-          v.w = rv[n];
-          if (!whole) keep_tokens(v, places_below(there) >> (8 * ((piece ^ (piece >> 4)) & 1)) & 0xffu);
-          if (has_nonfinite(v)) s_odd[buf] = i;
+          u32x4_t v = rv[n];
+          if (!whole) v = keep_elements<2>(v, places_below(there) >> (8 * ((piece ^ (piece >> 4)) & 1)));
+          if (has_nonfinite<2>(v)) s_odd[buf] = i;
           *reinterpret_cast<u32x4_t*>(&s_k[buf][g * GROUP + piece * 8]) = rk[n];
-          *reinterpret_cast<u32x4_t*>(&s_v[buf][g * GROUP + piece * 8]) = v.w;
+          *reinterpret_cast<u32x4_t*>(&s_v[buf][g * GROUP + piece * 8]) = v;
         } else {
-          if (!whole) {
-            VRegs<1> a, c;
-            a.w = u32x2_t{rv[n].x, rv[n].y};
-            c.w = u32x2_t{rv[n].z, rv[n].w};
-            keep_tokens(a, places_below(there) & 0xffu);
-            keep_tokens(c, places_below(there) >> 8);
-            rv[n] = u32x4_t{a.w.x, a.w.y, c.w.x, c.w.y};
-          }
+          if (!whole) rv[n] = keep_elements<1>(rv[n], places_below(there));
           // K piece: token piece % 16, values 16 (piece / 16) .. + 15: two octets of d
           uint16_t* k = &s_k[buf][g * GROUP + (piece >> 4) * 256 + (piece & 15) * 8];
           *reinterpret_cast<u32x4_t*>(k) = codes8_bf16<FMT>(u32x2_t{rk[n].x, rk[n].y});
@@ -272,10 +264,8 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
         for (int n = 0; n < NB; ++n)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            VRegs<2> v;
-            v.w = load_u32x4(vb + g * GROUP + n * 512);
-            drop_nonfinite(v);
-            o[n] = mfma_32x32_bf16(v.w, pb[g], o[n]);
+            const u32x4_t v = drop_nonfinite<2>(load_u32x4(vb + g * GROUP + n * 512));
+            o[n] = mfma_32x32_bf16(v, pb[g], o[n]);
             __builtin_amdgcn_sched_barrier(0);
           }
 #pragma unroll 1

@@ -11,12 +11,14 @@
 namespace sgmv {
 hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
-hipError_t launch_attn_direct_bf16(const AttnArgs& A, int fmt, unsigned slots, hipStream_t stream);
+hipError_t launch_attn_direct_bf16(const AttnArgs& A, unsigned slots, hipStream_t stream);
+hipError_t launch_attn_direct_e4m3(const AttnArgs& A, unsigned slots, hipStream_t stream);
+hipError_t launch_attn_direct_i8(const AttnArgs& A, unsigned slots, hipStream_t stream);
 hipError_t launch_attn_direct_f32(const AttnArgs& A, int fmt, unsigned slots, hipStream_t stream);
 hipError_t launch_attn_tiled_bf16(const AttnArgs& A, unsigned slots, hipStream_t stream);
 hipError_t launch_attn_tiled_e4m3(const AttnArgs& A, unsigned slots, hipStream_t stream);
 hipError_t launch_attn_tiled_i8(const AttnArgs& A, unsigned slots, hipStream_t stream);
-hipError_t launch_attn_combine(const AttnArgs& A, hipStream_t stream);
+hipError_t launch_attn_combine(const AttnArgs& A, int kernel, unsigned slots, hipStream_t stream);
 
 namespace {
 
@@ -118,8 +120,10 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   // sequences of up to 32 rows go to the direct kernel; so do all where the tiled one has no instance
   const bool tiled = !A.f32 && tiled_dim(c->head_dim) && (int64_t)s->max_q * A.G > AT_ROWS;
   A.direct_rows = tiled ? AT_ROWS : INT32_MAX;
-  A.one_tile = tiled || (int64_t)s->max_q * A.G <= AT_ROWS;
-  L.direct_slots = A.one_tile ? s->B : (int64_t)s->T * A.G / AT_ROWS + s->B;
+  const int64_t most = tiled ? AT_ROWS : (int64_t)s->max_q * A.G;  // rows of a direct sequence
+  A.direct_tile = most <= 16 || (A.f32 && c->head_dim > 128) ? 16 : 32;
+  A.one_tile = most <= A.direct_tile;
+  L.direct_slots = A.one_tile ? s->B : (int64_t)s->T * A.G / A.direct_tile + s->B;
   if (tiled && s->T == (int64_t)s->B * s->max_q) L.direct_slots = 0;  // no sequence is short
   if (tiled) L.tiled_slots = (int64_t)s->T * A.G / tiled_rows(c->head_dim) + s->B;
   int64_t tokens = s->max_kv;
@@ -128,7 +132,9 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   split_tokens(L.tiled_slots * c->heads, tokens, 256, 512, 64, a->n_split, A.n_split[1], A.chunk[1]);
   if (!L.direct_slots) A.n_split[0] = 1;
   if (!L.tiled_slots) A.n_split[1] = 1;
-  if (std::max(L.direct_slots * A.n_split[0], L.tiled_slots * A.n_split[1]) * c->heads > MOST_GRID)
+  // workgroups of the attention launches, and of those that join parts (4 rows each)
+  if (L.direct_slots * std::max(A.n_split[0], A.direct_tile / 4) * c->heads > MOST_GRID ||
+      L.tiled_slots * std::max(A.n_split[1], tiled_rows(c->head_dim) / 4) * c->heads > MOST_GRID)
     return SGMV_EUNSUPPORTED;
   return SGMV_OK;
 }
@@ -239,9 +245,12 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
            : cache->format == SGMV_KV_E4M3 ? launch_attn_tiled_e4m3
                                            : launch_attn_tiled_i8)(A, (unsigned)L.tiled_slots, st);
   if (err == hipSuccess && L.direct_slots)
-    err = (A.f32 ? launch_attn_direct_f32 : launch_attn_direct_bf16)(A, cache->format,
-                                                                     (unsigned)L.direct_slots, st);
-  if (err == hipSuccess && need) err = launch_attn_combine(A, st);
+    err = A.f32 ? launch_attn_direct_f32(A, cache->format, (unsigned)L.direct_slots, st)
+                : (cache->format == SGMV_KV_BF16   ? launch_attn_direct_bf16
+                   : cache->format == SGMV_KV_E4M3 ? launch_attn_direct_e4m3
+                                                   : launch_attn_direct_i8)(A, (unsigned)L.direct_slots, st);
+  if (err == hipSuccess && A.n_split[0] > 1) err = launch_attn_combine(A, 0, (unsigned)L.direct_slots, st);
+  if (err == hipSuccess && A.n_split[1] > 1) err = launch_attn_combine(A, 1, (unsigned)L.tiled_slots, st);
   return launched(err);
 }
 

@@ -113,15 +113,22 @@ __device__ __forceinline__ void codes4(uint32_t w, float (&f)[4]) {
 // Eight codes as bf16 (exact: e4m3 has 4 significant bits, int8 at most 8).
 template <int FMT>
 __device__ __forceinline__ u32x4_t codes8_bf16(u32x2_t w) {
-  float a[4], b[4];
-  codes4<FMT>(w.x, a);
-  codes4<FMT>(w.y, b);
   u32x4_t r;
-  // exact values: the upper halves of the floats
-  r.x = __builtin_amdgcn_perm(__float_as_uint(a[1]), __float_as_uint(a[0]), 0x07060302u);
-  r.y = __builtin_amdgcn_perm(__float_as_uint(a[3]), __float_as_uint(a[2]), 0x07060302u);
-  r.z = __builtin_amdgcn_perm(__float_as_uint(b[1]), __float_as_uint(b[0]), 0x07060302u);
-  r.w = __builtin_amdgcn_perm(__float_as_uint(b[3]), __float_as_uint(b[2]), 0x07060302u);
+  if constexpr (FMT == SGMV_KV_E4M3) {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, 1.f, false));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.x, 1.f, true));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, 1.f, false));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w.y, 1.f, true));
+  } else {
+    float a[4], b[4];
+    codes4<FMT>(w.x, a);
+    codes4<FMT>(w.y, b);
+    // exact values: the upper halves of the floats
+    r.x = __builtin_amdgcn_perm(__float_as_uint(a[1]), __float_as_uint(a[0]), 0x07060302u);
+    r.y = __builtin_amdgcn_perm(__float_as_uint(a[3]), __float_as_uint(a[2]), 0x07060302u);
+    r.z = __builtin_amdgcn_perm(__float_as_uint(b[1]), __float_as_uint(b[0]), 0x07060302u);
+    r.w = __builtin_amdgcn_perm(__float_as_uint(b[3]), __float_as_uint(b[2]), 0x07060302u);
+  }
   return r;
 }
 
