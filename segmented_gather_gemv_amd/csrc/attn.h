@@ -26,6 +26,7 @@ struct AttnArgs {
   // others); INT32_MAX: the direct kernel takes all
   int32_t direct_rows;
   int32_t direct_tile; // rows of the direct kernel's workgroups: 16 or 32
+  int32_t direct_waves;  // and their waves: 4 or 8
   int32_t one_tile;    // direct kernel: every sequence it takes has at most that many rows
   // split of a sequence's tokens over workgroups: `n_split` ranges of `chunk` tokens (a multiple
   // of the tile), the last one to the end
@@ -33,6 +34,12 @@ struct AttnArgs {
   float* part_o;       // [max n_split][T][Hq][D]
   float* part_ml;      // [max n_split][T][Hq][2]: maximum (of scores times log2(e)), sum
 };
+
+// Whether the direct kernel has instances of two 16-row tiles per workgroup.
+constexpr bool direct_two_tiles(int D, bool f32) { return D <= 128 || (D == 192 && !f32); }
+
+// Whether it has instances of 8 waves per workgroup next to those of 4 (bf16 rows).
+constexpr bool direct_eight_waves(int D, bool f32) { return D <= 128 && !f32; }
 
 // The tiled kernel: head dimensions it has instances of, waves and rows of its workgroups.
 constexpr bool tiled_dim(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
@@ -91,28 +98,6 @@ __device__ __forceinline__ void store_out(const AttnArgs& A, int64_t at, float a
 
 __device__ __forceinline__ f32x4_t mfma_16x16x4_f32(float a, float b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0);
-}
-
-// Maximum of a value over the two halves of the wave, in both.
-__device__ __forceinline__ float half_max(float v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-
-__device__ __forceinline__ float half_sum(float v) {
-  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-
-// Maximum and sum of a value over the lanes of equal lane % 16, in all of them.
-__device__ __forceinline__ float quad_max(float v) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
-}
-
-__device__ __forceinline__ float quad_sum(float v) {
-  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
 }  // namespace sgmv

@@ -44,20 +44,34 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A, int kerne
   float sum = l * f;
 #pragma unroll
   for (int o = 32; o; o >>= 1) sum += __shfl_xor(sum, o);
-  const int d = 4 * lane;
+  // lanes of a part: those that its D values take four each; several parts side by side
+  const int width = K.D <= 64 ? 16 : K.D <= 128 ? 32 : 64;
+  const int d = 4 * (lane & (width - 1)), side = lane / width, sides = WAVE / width;
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < used; ++i) {
-    const float w = __shfl(f, i);
-    if (d < K.D) {
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(A.part_o + (i * stride + at) * K.D + d);
+  constexpr int UNROLL = 8;  // loads in flight
+  for (int i0 = 0; i0 < used; i0 += UNROLL * sides) {
+    f32x4_t v[UNROLL];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] += w * v[j];
+    for (int u = 0; u < UNROLL; ++u) {
+      const int i = i0 + u * sides + side;
+      v[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      if (i < used && d < K.D) v[u] = *reinterpret_cast<const f32x4_t*>(A.part_o + (i * stride + at) * K.D + d);
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      const float w = __shfl(f, min(i0 + u * sides + side, WAVE - 1));
+      const bool in = i0 + u * sides + side < used;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] += in ? w * v[u][j] : 0.f;
     }
   }
+  for (int o = width; o < WAVE; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], o);
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   if (A.lse && lane == 0)
     A.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;
-  if (d < K.D)
+  if (side == 0 && d < K.D)
     store_out<F32>(A, (int64_t)token * A.ldo_t + (int64_t)head * A.ldo_h + d, acc.x * inv, acc.y * inv,
                    acc.z * inv, acc.w * inv);
 }

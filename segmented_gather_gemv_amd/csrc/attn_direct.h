@@ -16,6 +16,8 @@
 // of 128, which is what hides the memory's latency.
 #pragma once
 
+#include <utility>
+
 #include "attn_operand.h"
 
 namespace sgmv {
@@ -69,17 +71,32 @@ template <bool F32, int FMT> struct Direct {
   }
 };
 
+// The value of lane I of each 16 lanes, in all of them.
+template <int I>
+__device__ __forceinline__ float row_lane(float v) {
+  return __uint_as_float(__builtin_amdgcn_mov_dpp(__float_as_uint(v), 0x150 + I, 0xf, 0xf, true));
+}
+
+// f(0), .., f(15) with constants.
+template <class F, int... I>
+__device__ __forceinline__ void each_place(F f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <class F>
+__device__ __forceinline__ void for_places(F f) {
+  each_place(f, std::make_integer_sequence<int, 16>{});
+}
+
 // Waves per SIMD to allocate registers for.
-constexpr int direct_waves(bool f32, int fmt, int DP, int R) {
+constexpr int direct_occupancy(bool f32, int DP, int R) {
   if (f32) return DP <= 64 && R == 1 ? 2 : 1;
-  if (DP <= 64) return R == 1 ? 3 : 2;
-  if (DP <= 128) return 2;
-  return 1;
+  if (DP <= 64 && R == 1) return 3;
+  return DP <= 128 ? 2 : 1;
 }
 
 // DP: head dimension, or (not EXACT) an upper bound of it
 template <bool F32, int FMT, int DP, bool EXACT, int R, int WAVES>
-__global__ __launch_bounds__(WAVES* WAVE, direct_waves(F32, FMT, DP, R)) void attn_direct_kernel(AttnArgs A) {
+__global__ __launch_bounds__(WAVES* WAVE, direct_occupancy(F32, DP, R)) void attn_direct_kernel(AttnArgs A) {
   using X = Direct<F32, FMT>;
   constexpr int C = X::C, NT = X::NT, TOK = X::tokens, NG = TOK / 16, BYTES = X::bytes;
   constexpr bool SCALED = KvFormat<FMT>::scaled;
@@ -94,10 +111,12 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_waves(F32, FMT, DP, R)) void at
   const int r = lane & 15, quad = lane >> 4;
   const int D = EXACT ? DP : K.D;
 
-  // this workgroup's piece
+  // this workgroup's piece: first ranges first, so that the ranges that shorter sequences lack come
+  // last instead of leaving the same shader engines idle throughout
   const int kvh = blockIdx.x % K.H;
   const int rest = blockIdx.x / K.H;
-  const int split = rest % A.n_split[0], slot = rest / A.n_split[0];
+  const int slots = gridDim.x / (K.H * A.n_split[0]);
+  const int split = rest / slots, slot = rest - split * slots;
   int b, row0;
   if (A.one_tile) {
     b = slot;
@@ -197,8 +216,10 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_waves(F32, FMT, DP, R)) void at
   };
 
   u32x4_t kr[NT][NCH], vr[NB][VL];
-  f32x4_t ks[SCALED ? NT : 1], vs[SCALED ? NT : 1];
+  // scales of the 16 tokens of this quad's group, lane r that of place r
+  float ks = 0.f, vs = 0.f;
   (void)ks; (void)vs;
+  const int place_tok = tile_tok(r >> 2) + (r & 3);
   bool missing;  // of the step whose K is loaded: some group is not there
   int vpage;     // and the page of this lane's group of V
   auto load_k = [&](int i) {
@@ -206,6 +227,7 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_waves(F32, FMT, DP, R)) void at
     const int p = __shfl(pages, idx + kg);
     vpage = __shfl(pages, idx + vg);
     missing = __any(p < 0);
+    if constexpr (SCALED) ks = K.k_scale[group_at(vpage, i, vg) + place_tok];
     const char* base = static_cast<const char*>(K.k) + group_at(p, i, kg) * D * BYTES + k_tok * 16;
 #pragma unroll
     for (int x = 0; x < NT; ++x)
@@ -217,24 +239,16 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_waves(F32, FMT, DP, R)) void at
         kr[x][c] = load_u32x4(base + piece * 256 + tile_tok(x) * 16);
         if (!whole && 4 * c + quad >= D / C) kr[x][c] = u32x4_t{0u, 0u, 0u, 0u};
       }
-    if constexpr (SCALED) {
-      const float* at = K.k_scale + group_at(vpage, i, vg);
-#pragma unroll
-      for (int x = 0; x < NT; ++x) ks[x] = *reinterpret_cast<const f32x4_t*>(at + tile_tok(x));
-    }
   };
   auto load_v = [&](int i) {
     const int64_t g = group_at(vpage, i, vg);
+    if constexpr (SCALED) vs = K.v_scale[g + place_tok];
     const char* base = static_cast<const char*>(K.v) + (g * D + r * 16 + 8 * v_half) * BYTES;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int e = 0; e < VL; ++e)
         if (EXACT || 16 * n < D) vr[n][e] = load_u32x4(base + n * 256 * BYTES + 16 * e);
-    if constexpr (SCALED) {
-#pragma unroll
-      for (int x = 0; x < NT; ++x) vs[x] = *reinterpret_cast<const f32x4_t*>(K.v_scale + g + tile_tok(x));
-    }
   };
 
   if (mine > 0) {
@@ -259,14 +273,12 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_waves(F32, FMT, DP, R)) void at
           for (int t = 0; t < R; ++t) sc[t][x] = X::qk(k, q[t][c], sc[t][x]);
         }
     }
-    if constexpr (SCALED) {
+    if constexpr (SCALED)
+      for_places([&](auto at) {
+        const float f = row_lane<at.value>(ks);
 #pragma unroll
-      for (int t = 0; t < R; ++t)
-#pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) sc[t][x][j] *= ks[x][j];
-    }
+        for (int t = 0; t < R; ++t) sc[t][at.value / 4][at.value % 4] *= f;
+      });
     if (i + 1 < mine) {
       if (((i + 1) & (STEPS - 1)) == 0) {
         pages = pages_next;
@@ -291,8 +303,8 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_waves(F32, FMT, DP, R)) void at
         }
     }
 
-    u32x4_t pb[R][NT / 2];  // probabilities in bf16
-    float pf[F32 ? R : 1][NT][4];
+    u32x4_t pb[R][NT / 2];  // probabilities in bf16, or in fp32
+    float pf[R][NT][4];
 #pragma unroll
     for (int t = 0; t < R; ++t) {
       float top = sc[t][0][0];
@@ -314,25 +326,29 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_waves(F32, FMT, DP, R)) void at
       }
       const float base = m[t] == -INFINITY ? 0.f : m[t];
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        float p[4];
+      for (int x = 0; x < NT; ++x)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          p[j] = __builtin_amdgcn_exp2f(fmaf(sc[t][x][j], A.scale_log2, -base));
-          l[t] += p[j];
+          pf[t][x][j] = __builtin_amdgcn_exp2f(fmaf(sc[t][x][j], A.scale_log2, -base));
+          l[t] += pf[t][x][j];
         }
-        if constexpr (SCALED) {
+    }
+    if constexpr (SCALED)
+      for_places([&](auto at) {
+        const float f = row_lane<at.value>(vs);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] = edge && p[j] == 0.f ? 0.f : p[j] * vs[x][j];
+        for (int t = 0; t < R; ++t) {
+          float& p = pf[t][at.value / 4][at.value % 4];
+          p = edge && p == 0.f ? 0.f : p * f;
         }
-        if constexpr (F32) {
+      });
+    if constexpr (!F32) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) pf[t][x][j] = p[j];
-        } else {
-          pb[t][x / 2][2 * (x & 1)] = pack_bf16x2(p[0], p[1]);
-          pb[t][x / 2][2 * (x & 1) + 1] = pack_bf16x2(p[2], p[3]);
-        }
-      }
+      for (int t = 0; t < R; ++t)
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) pb[t][x / 2][2 * (x & 1) + j] = pack_bf16x2(pf[t][x][2 * j], pf[t][x][2 * j + 1]);
     }
 
     if (edge) {
@@ -479,17 +495,29 @@ hipError_t launch_direct(const AttnArgs& A, unsigned slots, hipStream_t stream) 
   return hipGetLastError();
 }
 
+template <bool F32, int FMT, int DP, bool EXACT, int R>
+hipError_t launch_direct_waves(const AttnArgs& A, unsigned slots, hipStream_t stream) {
+  if constexpr (direct_eight_waves(DP, F32)) {
+    if (A.direct_waves == 8) return launch_direct<F32, FMT, DP, EXACT, R, 8>(A, slots, stream);
+  }
+  return launch_direct<F32, FMT, DP, EXACT, R, 4>(A, slots, stream);
+}
+
+// Two tiles of rows per workgroup where their registers fit (direct_two_tiles).
 template <int FMT, int R>
 hipError_t launch_direct_dim(const AttnArgs& A, unsigned slots, hipStream_t stream) {
   const int D = A.kv.D;
-  if (D == 64) return launch_direct<false, FMT, 64, true, R, 4>(A, slots, stream);
-  if (D == 96) return launch_direct<false, FMT, 96, true, R, 4>(A, slots, stream);
-  if (D == 128) return launch_direct<false, FMT, 128, true, R, 4>(A, slots, stream);
-  if (D == 192) return launch_direct<false, FMT, 192, true, R, 4>(A, slots, stream);
-  if (D == 256) return launch_direct<false, FMT, 256, true, R, 4>(A, slots, stream);
-  if (D < 64) return launch_direct<false, FMT, 64, false, R, 4>(A, slots, stream);
-  if (D < 128) return launch_direct<false, FMT, 128, false, R, 4>(A, slots, stream);
-  return launch_direct<false, FMT, 256, false, R, 4>(A, slots, stream);
+  if (D == 64) return launch_direct_waves<false, FMT, 64, true, R>(A, slots, stream);
+  if (D == 96) return launch_direct_waves<false, FMT, 96, true, R>(A, slots, stream);
+  if (D == 128) return launch_direct_waves<false, FMT, 128, true, R>(A, slots, stream);
+  if (D == 192) return launch_direct_waves<false, FMT, 192, true, R>(A, slots, stream);
+  if (D < 64) return launch_direct_waves<false, FMT, 64, false, R>(A, slots, stream);
+  if (D < 128) return launch_direct_waves<false, FMT, 128, false, R>(A, slots, stream);
+  if constexpr (R == 1) {
+    if (D == 256) return launch_direct_waves<false, FMT, 256, true, 1>(A, slots, stream);
+    return launch_direct_waves<false, FMT, 256, false, 1>(A, slots, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 template <int FMT>

@@ -9,7 +9,7 @@
 #include "verify.h"
 
 namespace sgmv {
-hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
+hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, int max_q, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
 hipError_t launch_attn_direct_bf16(const AttnArgs& A, unsigned slots, hipStream_t stream);
 hipError_t launch_attn_direct_e4m3(const AttnArgs& A, unsigned slots, hipStream_t stream);
@@ -73,6 +73,12 @@ bool rows_ok(const void* p, int64_t n, int64_t ld_t, int64_t ld_h, int heads, in
   return p && ld_h >= D && (n <= 1 || ld_t >= (int64_t)(heads - 1) * ld_h + D);
 }
 
+// Whether rows of k and v may be accessed 16 bytes at a time.
+int rows_vec(const void* k, const void* v, int64_t kt, int64_t kh, int64_t vt, int64_t vh, int32_t dtype) {
+  const int64_t n = dtype == SGMV_F32 ? 4 : 8;
+  return aligned_to(k, 16) && aligned_to(v, 16) && kt % n == 0 && kh % n == 0 && vt % n == 0 && vh % n == 0;
+}
+
 sgmv_status launched(hipError_t e) { return e == hipSuccess ? SGMV_OK : SGMV_EHIP; }
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -82,13 +88,31 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 void split_tokens(int64_t base, int64_t tokens, int64_t want, int64_t least, int unit, int forced,
                   int32_t& n_split, int32_t& chunk) {
   int64_t n = forced > 0 ? forced : ceil_div(want, base > 0 ? base : 1);
-  const int64_t most = forced > 0 ? n : ceil_div(tokens, least);
+  const int64_t most = forced > 0 ? n : ceil_div(tokens, least > 0 ? least : 1);
   if (n > most) n = most;
   if (n > SGMV_KV_MAX_SPLITS) n = SGMV_KV_MAX_SPLITS;
   if (n < 1) n = 1;
   int64_t c = ceil_div(ceil_div(tokens > 0 ? tokens : 1, n), unit) * unit;
   chunk = (int32_t)(c < 0x40000000 ? c : 0x40000000);
   n_split = (int32_t)n;
+}
+
+// Ranges for the direct kernel. A split costs its parts and a launch that joins them, about as long as
+// five steps of the waves. From 1024 workgroups on (four per compute unit) a call is not split. With
+// fewer, sequences of different lengths are evened out by up to 1536 workgroups of long ranges, and
+// below 256 (of 8 waves: below 512 bf16 head_dim 128 workgroups of 4 waves leave registers unused) tokens
+// are spread over the compute units down to one step of each wave. fp32 steps take four times as long.
+//   64 sequences of 500..8000, e4m3, 32 / 8 heads: 119 us in 3, 121 in 1; 256 of 128..4096, bf16: 397 us
+//   in 1, 418 in 3; one of 4000, bf16: 10.4 us in 16, 19.6 in 1; one of 1000: 9.1 us in 1, 10.3 in 4
+void split_direct(AttnArgs& A, int64_t base, int64_t tokens, int forced) {
+  const int step = A.direct_waves * (A.kv.k_scale ? 64 : 32);
+  int64_t n = forced;
+  if (!n && base > 0) {
+    const int64_t fill = std::min<int64_t>((A.direct_waves == 8 ? 256 : 512) / base, ceil_div(tokens, step));
+    const int64_t even = std::min<int64_t>((A.direct_waves == 8 ? 1024 : 1536) / base, ceil_div(tokens, 2 * A.direct_waves * step));
+    n = !A.f32 && tokens <= 6 * step ? 1 : std::max(fill, even);
+  }
+  split_tokens(base, tokens, 0, 1, step, (int)std::max<int64_t>(n, 1), A.n_split[0], A.chunk[0]);
 }
 
 // Geometry of an attention call; everything but the pointers of its rows and workspace. Slots: tiles
@@ -121,14 +145,15 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   const bool tiled = !A.f32 && tiled_dim(c->head_dim) && (int64_t)s->max_q * A.G > AT_ROWS;
   A.direct_rows = tiled ? AT_ROWS : INT32_MAX;
   const int64_t most = tiled ? AT_ROWS : (int64_t)s->max_q * A.G;  // rows of a direct sequence
-  A.direct_tile = most <= 16 || (A.f32 && c->head_dim > 128) ? 16 : 32;
+  A.direct_tile = most > 16 && direct_two_tiles(c->head_dim, A.f32) ? 32 : 16;
   A.one_tile = most <= A.direct_tile;
   L.direct_slots = A.one_tile ? s->B : (int64_t)s->T * A.G / A.direct_tile + s->B;
   if (tiled && s->T == (int64_t)s->B * s->max_q) L.direct_slots = 0;  // no sequence is short
   if (tiled) L.tiled_slots = (int64_t)s->T * A.G / tiled_rows(c->head_dim) + s->B;
   int64_t tokens = s->max_kv;
   if (a->window) tokens = std::min(tokens, (int64_t)a->window + s->max_q + AT_TOKENS);
-  split_tokens(L.direct_slots * c->heads, tokens, 1024, 256, 128, a->n_split, A.n_split[0], A.chunk[0]);
+  A.direct_waves = direct_eight_waves(c->head_dim, A.f32) && L.direct_slots * c->heads < 512 ? 8 : 4;
+  split_direct(A, L.direct_slots * c->heads, tokens, a->n_split);
   split_tokens(L.tiled_slots * c->heads, tokens, 256, 512, 64, a->n_split, A.n_split[1], A.chunk[1]);
   if (!L.direct_slots) A.n_split[0] = 1;
   if (!L.tiled_slots) A.n_split[1] = 1;
@@ -176,8 +201,9 @@ sgmv_status sgmv_kv_write(const void* k, int64_t ldk_token, int64_t ldk_head, co
   if (!rows_ok(k, K.T, ldk_token, ldk_head, K.H, K.D) || !rows_ok(v, K.T, ldv_token, ldv_head, K.H, K.D))
     return SGMV_EINVAL;
   const KvRows R{const_cast<void*>(k), const_cast<void*>(v), ldk_token, ldk_head, ldv_token, ldv_head,
-                 nullptr, 0, dtype == SGMV_F32};
-  return launched(launch_kv_write(K, R, cache->format, static_cast<hipStream_t>(stream)));
+                 nullptr, 0, dtype == SGMV_F32,
+                 rows_vec(k, v, ldk_token, ldk_head, ldv_token, ldv_head, dtype)};
+  return launched(launch_kv_write(K, R, cache->format, batch->max_q, static_cast<hipStream_t>(stream)));
 }
 
 sgmv_status sgmv_kv_read(const sgmv_kv_batch* batch, const sgmv_kv_cache* cache,
@@ -193,7 +219,8 @@ sgmv_status sgmv_kv_read(const sgmv_kv_batch* batch, const sgmv_kv_cache* cache,
   if (!out_start || !rows_ok(k, rows, ldk_token, ldk_head, K.H, K.D) ||
       !rows_ok(v, rows, ldv_token, ldv_head, K.H, K.D))
     return SGMV_EINVAL;
-  const KvRows R{k, v, ldk_token, ldk_head, ldv_token, ldv_head, out_start, rows, dtype == SGMV_F32};
+  const KvRows R{k, v, ldk_token, ldk_head, ldv_token, ldv_head, out_start, rows, dtype == SGMV_F32,
+                 rows_vec(k, v, ldk_token, ldk_head, ldv_token, ldv_head, dtype)};
   return launched(launch_kv_read(K, R, cache->format, static_cast<hipStream_t>(stream)));
 }
 
@@ -256,7 +283,7 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
 
 size_t sgmv_verify_drafts_workspace(int32_t B, int32_t vocab) {
   if (B < 1 || vocab < 1) return 0;
-  return (size_t)B * (size_t)ceil_div(vocab, VF_CHUNK) * 2 * sizeof(double);
+  return (size_t)B * (size_t)ceil_div(vocab, VF_PART) * 2 * sizeof(double);
 }
 
 sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draft, int64_t ldd,
@@ -279,7 +306,7 @@ sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draf
                    (!draft || (aligned_to(draft, 4 * e) && ldd % 4 == 0));
   const VerifyArgs A{target, draft, ldt, ldd, draft_ids, draft_start, accept_u, sample_u, tokens, ldo,
                      accepted, static_cast<double*>(workspace), B, vocab, N, max_drafts,
-                     dtype == SGMV_BF16, (int32_t)ceil_div(vocab, VF_CHUNK), vec};
+                     dtype == SGMV_BF16, (int32_t)ceil_div(vocab, VF_PART), vec};
   return launched(launch_verify(A, static_cast<hipStream_t>(stream)));
 }
 

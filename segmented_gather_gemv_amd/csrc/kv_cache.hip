@@ -4,15 +4,20 @@
 //   amax = max |x|,  scale = amax / F,  code = round(x * F / amax) to the format, ties to even;
 //   a row of zeros has scale 0 and codes 0; a row with a non-finite value has scale NaN and codes
 //   0, so that it reads back as NaN whatever the format can hold.
-// bf16 rows: x * F is exact in fp32 and one correctly rounded division follows; a quotient of so
-// few bits lies on a border of the format or far from it, so the code is the definition's. fp32
-// rows: the quotient is formed in fp64 and rounded to odd before the last rounding, for the same
-// result. Either way the arithmetic hides behind the rows' bytes.
+// The code is that of the exact quotient. x * (F / amax) in fp32 is within 2^-23 of it: where a little
+// more and a little less round to the same code, that is it, and only where they do not (about one
+// value in ten thousand) the quotient is formed exactly: of bf16 rows x * F is exact in fp32 and a
+// quotient of so few bits lies on a border of the format or far from it, so that one correctly
+// rounded division decides; of fp32 rows in fp64, rounded to odd before the last rounding.
 //
-// One wave per group of 16 tokens (of one sequence) and head: lane l takes the values d = 2 l + ...
-// of one token after another, so loads of a row are contiguous; the codes go through LDS into
-// the group's layout, and the stores are contiguous pieces of it. A group whose 16 places are not all written keeps the
-// bytes of the others: every store is of one element run that belongs to a written token.
+// A wave takes 16 rows, lane r of each quarter (quad) row r, and of every row the pieces of K that are
+// 16 bytes in the cache, quad by quad. K is stored as it is held. V has tokens innermost: 4 lanes
+// exchange a 4x4 block, after which each holds one d of their four tokens, one word of the cache. The
+// 16 rows are the tokens of one group and head (a quad of tokens that is not written whole is stored
+// element by element, so that the others keep theirs), or, where sequences bring few tokens, whichever
+// rows follow each other (then a wave of V takes one row). K and V are separate waves.
+//
+// Bound: the rows' bytes; one token per sequence: the chain of loads from the sequence to its page.
 #include "kv_common.h"
 
 namespace sgmv {
@@ -21,199 +26,545 @@ namespace {
 
 constexpr int RW_WAVES = 4;
 
-__device__ __forceinline__ float load_elem(const float* p) { return *p; }
-__device__ __forceinline__ float load_elem(const uint16_t* p) { return bf16_bits_to_f32(*p); }
-__device__ __forceinline__ void store_elem(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_elem(uint16_t* p, float v) {
-  *p = (uint16_t)(pack_bf16x2(v, 0.f) & 0xffffu);
-}
-
 // fp32 nearest to d, rounded to odd: a later rounding to fewer bits then equals a single one.
 __device__ __forceinline__ float to_odd(double d) {
   const float f = __double2float_rz(d);
   return (double)f == d ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
+// Four values rounded to codes.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode(float q) {
+__device__ __forceinline__ uint32_t encode4(const float (&q)[4]) {
   if constexpr (FMT == SGMV_KV_E4M3) {
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q, q, 0, false) & 0xffu;
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
   } else {
-    return (uint32_t)(int)rintf(q) & 0xffu;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)rintf(q[i]) & 0xffu) << (8 * i);
+    return w;
   }
 }
 
+// Codes of four values of a row. s: a power of two that keeps the quotient's parts in range.
 template <int FMT, class T>
-__device__ __forceinline__ uint32_t quantise(float x, float amax) {
+__device__ __forceinline__ uint32_t quantise4(const float (&x)[4], float amax, float s, float inv) {
   constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
-  if constexpr (sizeof(T) == 4) {
-    return encode<FMT>(to_odd((double)x * (double)F / (double)amax));
-  } else {
-    // amax near fp32's largest would overflow x * F: both scaled by a power of two
-    const float s = amax > 1e30f ? 0x1p-32f : 1.f;
-    return encode<FMT>(x * s * F / (amax * s));
+  float lo[4], hi[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float y = x[i] * s * inv;
+    lo[i] = y * (1.f - 0x1p-22f);
+    hi[i] = y * (1.f + 0x1p-22f);
+  }
+  uint32_t w = encode4<FMT>(lo);
+  if (__any(w != encode4<FMT>(hi))) {
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      q[i] = sizeof(T) == 4 ? to_odd((double)x[i] * (double)F / (double)amax) : x[i] * s * F / (amax * s);
+    w = encode4<FMT>(q);
+  }
+  return w;
+}
+
+// Transposes a 4x4 block of bytes held by 4 neighbouring lanes, one row each.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
+  uint32_t t = __builtin_amdgcn_mov_dpp(w, 0xb1, 0xf, 0xf, true);  // lane ^ 1
+  w = __builtin_amdgcn_perm(t, w, lane & 1 ? 0x03070105u : 0x06020400u);
+  t = __builtin_amdgcn_mov_dpp(w, 0x4e, 0xf, 0xf, true);  // lane ^ 2
+  return __builtin_amdgcn_perm(t, w, lane & 2 ? 0x03020706u : 0x05040100u);
+}
+
+// The same of 16-bit elements, a row in two words.
+__device__ __forceinline__ void transpose_halves(uint32_t& a, uint32_t& b, int lane) {
+  const bool up = lane & 2, odd = lane & 1;
+  const uint32_t other = __builtin_amdgcn_mov_dpp(up ? a : b, 0x4e, 0xf, 0xf, true);
+  const uint32_t keep = up ? b : a;
+  const uint32_t x = up ? other : keep, y = up ? keep : other;  // of lanes 0 and 2, or 1 and 3
+  const uint32_t tx = __builtin_amdgcn_mov_dpp(x, 0xb1, 0xf, 0xf, true);
+  const uint32_t ty = __builtin_amdgcn_mov_dpp(y, 0xb1, 0xf, 0xf, true);
+  const uint32_t sel = odd ? 0x03020706u : 0x05040100u;  // high halves, low halves
+  a = __builtin_amdgcn_perm(tx, x, sel);
+  b = __builtin_amdgcn_perm(ty, y, sel);
+}
+
+// 4 C bytes (C values of T) of a row, as words; element by element where rows are not aligned.
+template <class T, int N>
+__device__ __forceinline__ void load_words(const T* p, bool vec, uint32_t (&w)[N]) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    u32x4_t v;
+    if (vec) {
+      v = load_u32x4(reinterpret_cast<const char*>(p) + 16 * i);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const T* e = p + (4 * i + j) * 4 / sizeof(T);
+        if constexpr (sizeof(T) == 4) v[j] = *reinterpret_cast<const uint32_t*>(e);
+        else v[j] = e[0] | (uint32_t)e[1] << 16;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[4 * i + j] = v[j];
   }
 }
 
-__device__ __forceinline__ float wave_max(float v) {
+template <class T, int N>
+__device__ __forceinline__ void store_words(T* p, bool vec, const uint32_t (&w)[N]) {
 #pragma unroll
-  for (int o = 32; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
-}
-
-// (sequence, first token of the group) of slot `w`: the groups of sequence b take the slots from
-// first(b) = (tokens before b) / 16 + 2 b on; a sequence of n tokens touches at most
-// (n + 14) / 16 + 1 groups of its own.
-template <int FMT, class T>
-__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_kernel(KvArgs K, KvRows A) {
-  const int lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE;
-  const int slot = blockIdx.x * RW_WAVES + wv, head = blockIdx.y;
-  const int b = wave_find(K.B, slot, [&](int i) { return min(max(K.q_start[i], 0), K.T) / 16 + 2 * i; });
-  const KvSeq s = kv_seq(K, b);
-  const int first = s.kv_len - s.q_len;  // position of the first new token; may be negative
-  const int g0 = (first >> 4) + (slot - (s.q0 / 16 + 2 * b));
-  const int t_lo = max(max(16 * g0, first), 0), t_hi = min(16 * g0 + 16, s.kv_len);
-  if (t_lo >= t_hi) return;
-  const int page = kv_page(K, K.table + (int64_t)b * K.ldp, t_lo);
-  if (page < 0) return;
-  const int ps = 1 << K.lps, D = K.D;
-  const int64_t row = ((int64_t)page * K.H + head) * ps;  // first token of the (page, head) block
-  const int64_t group = (row + ((16 * g0) & (ps - 1))) * D;
-  constexpr int C = 16 / KvFormat<FMT>::bytes;
-  for (int t = t_lo; t < t_hi; ++t) {
-    const int64_t src = s.q0 + (t - first);
-    const int r = t & 15, place = 8 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3);
-    const T* kr = static_cast<const T*>(A.k) + src * A.ldk_t + head * A.ldk_h;
-    const T* vr = static_cast<const T*>(A.v) + src * A.ldv_t + head * A.ldv_h;
-    if constexpr (!KvFormat<FMT>::scaled) {
-      T* kc = static_cast<T*>(const_cast<void*>(K.k)) + group;
-      T* vc = static_cast<T*>(const_cast<void*>(K.v)) + group;
-      for (int d = lane; d < D; d += WAVE) {
-        kc[(d / C) * (16 * C) + r * C + d % C] = kr[d];
-        vc[d * 16 + place] = vr[d];
-      }
+  for (int i = 0; i < N / 4; ++i) {
+    if (vec) {
+      *reinterpret_cast<u32x4_t*>(reinterpret_cast<char*>(p) + 16 * i) = u32x4_t{w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]};
     } else {
-      uint8_t* kc = static_cast<uint8_t*>(const_cast<void*>(K.k)) + group;
-      uint8_t* vc = static_cast<uint8_t*>(const_cast<void*>(K.v)) + group;
-      constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
-      float xk[4], xv[4], ak = 0.f, av = 0.f, bad_k = 0.f, bad_v = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = lane + WAVE * i;
-        xk[i] = d < D ? load_elem(kr + d) : 0.f;
-        xv[i] = d < D ? load_elem(vr + d) : 0.f;
-        ak = fmaxf(ak, fabsf(xk[i]));
-        av = fmaxf(av, fabsf(xv[i]));
-        bad_k += xk[i] * 0.f;  // NaN where x is not finite
-        bad_v += xv[i] * 0.f;
-      }
-      ak = wave_max(ak);
-      av = wave_max(av);
-      const bool ok_k = !__any(bad_k != 0.f), ok_v = !__any(bad_v != 0.f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int d = lane + WAVE * i;
-        if (d < D) {
-          kc[(d / C) * (16 * C) + r * C + d % C] =
-              ok_k && ak > 0.f ? (uint8_t)quantise<FMT, T>(xk[i], ak) : 0;
-          vc[d * 16 + place] = ok_v && av > 0.f ? (uint8_t)quantise<FMT, T>(xv[i], av) : 0;
+      for (int j = 0; j < 4; ++j) {
+        T* e = p + (4 * i + j) * 4 / sizeof(T);
+        if constexpr (sizeof(T) == 4) {
+          *reinterpret_cast<uint32_t*>(e) = w[4 * i + j];
+        } else {
+          e[0] = (uint16_t)w[4 * i + j];
+          e[1] = (uint16_t)(w[4 * i + j] >> 16);
         }
-      }
-      if (lane == 0) {
-        const float nan = __uint_as_float(0x7fc00000u);
-        const_cast<float*>(K.k_scale)[row + (t & (ps - 1))] = ok_k ? ak / F : nan;
-        const_cast<float*>(K.v_scale)[row + (t & (ps - 1))] = ok_v ? av / F : nan;
       }
     }
   }
 }
 
-template <int FMT>
-__device__ __forceinline__ float load_code(const void* p, int64_t i) {
-  if constexpr (FMT == SGMV_KV_F32) {
-    return static_cast<const float*>(p)[i];
-  } else if constexpr (FMT == SGMV_KV_BF16) {
-    return bf16_bits_to_f32(static_cast<const uint16_t*>(p)[i]);
-  } else {
-    float f[4];
-    codes4<FMT>((uint32_t)static_cast<const uint8_t*>(p)[i], f);
-    return f[0];
-  }
+// Value e of a unit held as words of T.
+template <class T, int N>
+__device__ __forceinline__ float word_value(const uint32_t (&w)[N], int e) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
+  return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
 }
 
-template <int FMT, class T>
-__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_read_kernel(KvArgs K, KvRows A) {
-  const int lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE;
-  const int slot = blockIdx.x * RW_WAVES + wv, head = blockIdx.y;
-  const int b = wave_find(K.B, slot, [&](int i) { return min(max(A.out_start[i], 0), A.rows) / 16 + 2 * i; });
-  const int r0 = min(max(A.out_start[b], 0), A.rows), r1 = min(max(A.out_start[b + 1], 0), A.rows);
+// Where the row of this lane goes to or comes from.
+struct Place {
+  bool ok;        // there is such a row
+  bool quad_ok;   // and its three neighbours' (the same quad of tokens) are there too
+  int64_t row;    // row beside the cache
+  int64_t token;  // [pages][H][page size] index, or -1: no page
+  int head;
+};
+
+// GROUPED: slot `w` of 16 tokens: the groups of sequence b take the slots from first(b) = (rows
+// before b) / 16 + 2 b on; n rows touch at most (n + 14) / 16 + 1 groups. start: rows of each sequence,
+// the last ones of it.
+__device__ __forceinline__ bool group_place(const KvArgs& K, const int32_t* start, int total, Place& P) {
+  const int lane = threadIdx.x & (WAVE - 1), r = lane & 15;
+  const int slot = blockIdx.x * RW_WAVES + threadIdx.x / WAVE;
+  const int b = wave_find(K.B, slot, [&](int i) { return min(max(start[i], 0), total) / 16 + 2 * i; });
+  const int r0 = min(max(start[b], 0), total), r1 = min(max(start[b + 1], 0), total);
   const int n = max(r1 - r0, 0), kv_len = kv_seq(K, b).kv_len;
-  const int first = kv_len - n;
+  const int first = kv_len - n;  // position of the first row; may be negative
   const int g0 = (first >> 4) + (slot - (r0 / 16 + 2 * b));
   const int t_lo = max(16 * g0, first), t_hi = min(16 * g0 + 16, kv_len);
-  if (t_lo >= t_hi) return;
-  const int page = kv_page(K, K.table + (int64_t)b * K.ldp, t_lo);
-  const int ps = 1 << K.lps, D = K.D;
-  const int64_t row = ((int64_t)max(page, 0) * K.H + head) * ps;
-  const int64_t group = (row + ((16 * g0) & (ps - 1))) * D;
-  constexpr int C = 16 / KvFormat<FMT>::bytes;
-  for (int t = t_lo; t < t_hi; ++t) {
-    const int64_t dst = r0 + (t - first);
-    const int r = t & 15, place = 8 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3);
-    T* kr = static_cast<T*>(A.k) + dst * A.ldk_t + head * A.ldk_h;
-    T* vr = static_cast<T*>(A.v) + dst * A.ldv_t + head * A.ldv_h;
-    float ks = 1.f, vs = 1.f;
-    if constexpr (KvFormat<FMT>::scaled) {
-      if (page >= 0) {
-        ks = K.k_scale[row + (t & (ps - 1))];
-        vs = K.v_scale[row + (t & (ps - 1))];
+  if (t_lo >= t_hi) return false;
+  const int page = kv_page(K, K.table + (int64_t)b * K.ldp, 16 * g0);
+  const int t = 16 * g0 + r, t4 = t & ~3;
+  P.head = blockIdx.y;
+  P.ok = t >= t_lo && t < t_hi;
+  P.quad_ok = t4 >= t_lo && t4 + 4 <= t_hi;
+  P.row = P.ok ? r0 + (t - first) : r0;
+  P.token = page < 0 ? -1 : ((int64_t)page * K.H + P.head) * (1 << K.lps) + (t & ((1 << K.lps) - 1));
+  return true;
+}
+
+// Not grouped: row `at` of the rows (token, head) in order, each lane its own; total: rows of tokens,
+// those of sequence b start[b] .. start[b + 1], the last ones of it.
+__device__ __forceinline__ void row_place(const KvArgs& K, const int32_t* starts, int total, int at, Place& P) {
+  const int token_at = at / K.H;
+  const bool in = token_at < total;
+  const int token = in ? token_at : 0;
+  P.head = at - token_at * K.H;
+  // the sequence: as if all had the same number of tokens, else by search
+  int b = min((int)(((float)token + 0.5f) * ((float)K.B / (float)total)), K.B - 1);
+  const auto start = [&](int i) { return min(max(starts[i], 0), total); };
+  int s0 = start(b), s1 = start(b + 1);
+  uint64_t left = __ballot(in && !(s0 <= token && token < s1));
+  while (left) {
+    const int t = __builtin_amdgcn_readlane(token, __ffsll((unsigned long long)left) - 1);
+    const int found = wave_find(K.B, t, start);
+    if (token == t) {
+      b = found;
+      s0 = start(b);
+      s1 = start(b + 1);
+    }
+    left &= ~__ballot(token == t);
+  }
+  const int pos = kv_seq(K, b).kv_len - s1 + token;
+  P.ok = in && s0 <= token && token < s1;
+  const int page = P.ok ? kv_page(K, K.table + (int64_t)b * K.ldp, pos) : -1;
+  P.quad_ok = false;
+  P.row = token;
+  P.token = page < 0 ? -1 : ((int64_t)page * K.H + P.head) * (1 << K.lps) + (pos & ((1 << K.lps) - 1));
+}
+
+template <int FMT, class T> struct Unit {
+  static constexpr int bytes = KvFormat<FMT>::bytes;
+  static constexpr int C = 16 / bytes;                          // values of d
+  static constexpr int words = C * sizeof(T) / 4;               // of a row beside the cache
+  static constexpr int most = SGMV_KV_MAX_HEAD_DIM / C / 4;     // of one lane
+};
+
+// Bytes of V that hold value e of unit u for a token of a group.
+template <int BYTES>
+__device__ __forceinline__ int64_t v_at(int d, int place) { return (int64_t)(d * 16 + place) * BYTES; }
+__device__ __forceinline__ int place_of(int r) { return 8 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
+
+// What quantising a row needs: its maximum, a power of two that keeps the quotient's parts in range, and
+// F over the maximum so scaled (0: codes 0); its scale.
+struct RowScale {
+  float amax, s, inv, scale;
+};
+
+// bad: NaN if a value of the row is not finite, else 0
+template <int FMT>
+__device__ __forceinline__ RowScale row_scale(float amax, float bad) {
+  constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
+  if (bad != 0.f) return {amax, 1.f, 0.f, __uint_as_float(0x7fc00000u)};
+  const float s = amax > 0x1p100f ? 0x1p-32f : amax < 0x1p-90f ? 0x1p64f : 1.f;
+  return {amax, s, amax > 0.f ? F / (amax * s) : 0.f, amax / F};
+}
+
+// 16 rows of K (or, grouped, of V) per wave.
+template <int FMT, class T, bool GROUPED>
+__device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, bool is_v, const Place& place16) {
+  using U = Unit<FMT, T>;
+  constexpr int BYTES = U::bytes, C = U::C;
+  constexpr bool SCALED = KvFormat<FMT>::scaled;
+  const int lane = threadIdx.x & (WAVE - 1), quad = lane >> 4;
+  Place P = place16;
+  P.ok = P.ok && P.token >= 0;
+  if (!__any(P.ok)) return;
+  const int D = K.D, units = D / C;
+  const T* src = static_cast<const T*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) +
+                 P.head * (is_v ? A.ldv_h : A.ldk_h);
+  const int64_t token = max(P.token, (int64_t)0), group = (token & ~(int64_t)15) * D * BYTES;
+  const int r = (int)(token & 15);
+  char* dst = static_cast<char*>(const_cast<void*>(is_v ? K.v : K.k)) + group;
+
+  uint32_t w[U::most][U::words];
+  float amax = 0.f, bad = 0.f;
+#pragma unroll
+  for (int n = 0; n < U::most; ++n) {
+    if (4 * n >= units) break;
+    const int u = quad + 4 * n;
+#pragma unroll
+    for (int i = 0; i < U::words; ++i) w[n][i] = 0u;
+    if (P.ok && u < units) load_words(src + u * C, A.vec, w[n]);
+  }
+  RowScale S = {0.f, 1.f, 0.f, 0.f};
+  if constexpr (SCALED) {
+#pragma unroll
+    for (int n = 0; n < U::most; ++n) {
+      if (4 * n >= units) break;
+#pragma unroll
+      for (int e = 0; e < C; ++e) {
+        const float x = word_value<T>(w[n], e);
+        amax = fmaxf(amax, fabsf(x));
+        bad = fmaf(x, 0.f, bad);
       }
     }
-    for (int d = lane; d < D; d += WAVE) {
-      float x = 0.f, y = 0.f;
-      if (page >= 0) {
-        x = load_code<FMT>(K.k, group + (d / C) * (16 * C) + r * C + d % C);
-        y = load_code<FMT>(K.v, group + d * 16 + place);
-        if constexpr (KvFormat<FMT>::scaled) {
-          x *= ks;
-          y *= vs;
+    S = row_scale<FMT>(quad_max(amax), quad_sum(bad));
+    if (P.ok && quad == 0) const_cast<float*>(is_v ? K.v_scale : K.k_scale)[token] = S.scale;
+  }
+#pragma unroll
+  for (int n = 0; n < U::most; ++n) {
+    if (4 * n >= units) break;
+    const int u = quad + 4 * n;
+    const bool in = u < units;
+    u32x4_t c;  // the unit as it is in the cache
+    if constexpr (SCALED) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = word_value<T>(w[n], 4 * k + j);
+        c[k] = S.inv == 0.f ? 0u : quantise4<FMT, T>(x, S.amax, S.s, S.inv);
+      }
+    } else {
+      c = u32x4_t{w[n][0], w[n][1], w[n][2], w[n][3]};
+    }
+    if (!GROUPED || !is_v) {
+      if (P.ok && in) *reinterpret_cast<u32x4_t*>(dst + (u * 16 + r) * 16) = c;
+      continue;
+    }
+    if constexpr (BYTES == 4) {  // 16 tokens are 64 bytes
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (P.ok && in) *reinterpret_cast<uint32_t*>(dst + v_at<4>(u * 4 + j, place_of(r))) = c[j];
+      continue;
+    }
+    if (__any(P.ok && !P.quad_ok)) {
+      if (P.ok && !P.quad_ok && in)
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+          if constexpr (BYTES == 1) dst[v_at<1>(u * C + e, place_of(r))] = (char)(c[e / 4] >> (8 * (e % 4)));
+          else *reinterpret_cast<uint16_t*>(dst + v_at<2>(u * C + e, place_of(r))) = (uint16_t)(c[e / 2] >> (16 * (e % 2)));
+        }
+    }
+    if constexpr (BYTES < 4) {
+      const bool put = P.ok && P.quad_ok && in;
+      const int j = lane & 3, place = place_of(r & ~3);
+      if constexpr (BYTES == 1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t x = transpose_bytes(c[k], lane);
+          if (put) *reinterpret_cast<uint32_t*>(dst + v_at<1>(u * 16 + 4 * k + j, place)) = x;
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t a = c[2 * k], b = c[2 * k + 1];
+          transpose_halves(a, b, lane);
+          if (put) *reinterpret_cast<u32x2_t*>(dst + v_at<2>(u * 8 + 4 * k + j, place)) = u32x2_t{a, b};
         }
       }
-      store_elem(kr + d, x);
-      store_elem(vr + d, y);
     }
   }
+}
+
+// One row of V per wave: its places in the cache are 16 elements apart, and lanes side by side in d
+// share cache lines (16 rows per wave, every lane in another line, took twice as long).
+template <int FMT, class T>
+__device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, const Place& P) {
+  constexpr int BYTES = KvFormat<FMT>::bytes, MOST = SGMV_KV_MAX_HEAD_DIM / WAVE;
+  const int lane = threadIdx.x & (WAVE - 1), D = K.D;
+  if (!P.ok || P.token < 0) return;
+  const T* src = static_cast<const T*>(A.v) + P.row * A.ldv_t + P.head * A.ldv_h;
+  char* dst = static_cast<char*>(const_cast<void*>(K.v)) + (P.token & ~(int64_t)15) * D * BYTES;
+  const int place = place_of((int)(P.token & 15));
+  T e[MOST];
+  float x[MOST], amax = 0.f, bad = 0.f;
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    e[i] = lane + WAVE * i < D ? src[lane + WAVE * i] : T(0);
+    if constexpr (sizeof(T) == 4) x[i] = e[i];
+    else x[i] = bf16_bits_to_f32(e[i]);
+    amax = fmaxf(amax, fabsf(x[i]));
+    bad = fmaf(x[i], 0.f, bad);
+  }
+  uint32_t c = 0;
+  if constexpr (KvFormat<FMT>::scaled) {
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      amax = fmaxf(amax, __shfl_xor(amax, o));
+      bad += __shfl_xor(bad, o);
+    }
+    const RowScale S = row_scale<FMT>(quad_max(amax), quad_sum(bad));
+    if (S.inv != 0.f) c = quantise4<FMT, T>(x, S.amax, S.s, S.inv);
+    if (lane == 0) const_cast<float*>(K.v_scale)[P.token] = S.scale;
+  }
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int d = lane + WAVE * i;
+    if (d >= D) break;
+    if constexpr (BYTES == 1) dst[v_at<1>(d, place)] = (char)(c >> (8 * i));
+    else *reinterpret_cast<T*>(dst + v_at<BYTES>(d, place)) = e[i];
+  }
+}
+
+template <int FMT, class T>
+__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_groups_kernel(KvArgs K, KvRows A) {
+  Place P;
+  if (group_place(K, K.q_start, K.T, P)) write_rows<FMT, T, true>(K, A, blockIdx.z, P);
+}
+
+// Workgroups [0, for_v) take V, the others K.
+template <int FMT, class T>
+__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_rows_kernel(KvArgs K, KvRows A, int for_v) {
+  const int wv = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1);
+  Place P;
+  if ((int)blockIdx.x < for_v) {
+    row_place(K, K.q_start, K.T, (int)blockIdx.x * RW_WAVES + wv, P);
+    write_v_row<FMT, T>(K, A, P);
+  } else {
+    row_place(K, K.q_start, K.T, (((int)blockIdx.x - for_v) * RW_WAVES + wv) * 16 + (lane & 15), P);
+    write_rows<FMT, T, false>(K, A, false, P);
+  }
+}
+
+// 16 rows of K (or, grouped, of V) per wave.
+template <int FMT, class T, bool GROUPED>
+__device__ __forceinline__ void read_rows(const KvArgs& K, const KvRows& A, bool is_v, const Place& P) {
+  using U = Unit<FMT, T>;
+  constexpr int BYTES = U::bytes, C = U::C;
+  const int lane = threadIdx.x & (WAVE - 1), quad = lane >> 4;
+  const int D = K.D, units = D / C;
+  const bool there = P.token >= 0;
+  const int64_t token = max(P.token, (int64_t)0);
+  const int r = GROUPED ? lane & 15 : (int)(token & 15);
+  const char* src = static_cast<const char*>(is_v ? K.v : K.k) + (token & ~(int64_t)15) * D * BYTES;
+  T* dst = static_cast<T*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) + P.head * (is_v ? A.ldv_h : A.ldk_h);
+  float scale = 1.f;
+  if constexpr (KvFormat<FMT>::scaled) {
+    if (there) scale = (is_v ? K.v_scale : K.k_scale)[token];
+  }
+#pragma unroll
+  for (int n = 0; n < U::most; ++n) {
+    if (4 * n >= units) break;
+    const int u = quad + 4 * n;
+    u32x4_t c = {0u, 0u, 0u, 0u};
+    if (there && u < units) {
+      if (!GROUPED || !is_v) {
+        c = load_u32x4(src + (u * 16 + r) * 16);
+      } else {
+        const int j = lane & 3, place = place_of(r & ~3);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (BYTES == 1) c[k] = *reinterpret_cast<const uint32_t*>(src + v_at<1>(u * 16 + 4 * k + j, place));
+          if constexpr (BYTES == 4) c[k] = *reinterpret_cast<const uint32_t*>(src + v_at<4>(u * 4 + k, place_of(r)));
+        }
+        if constexpr (BYTES == 2) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const u32x2_t x = *reinterpret_cast<const u32x2_t*>(src + v_at<2>(u * 8 + 4 * k + j, place));
+            c[2 * k] = x.x;
+            c[2 * k + 1] = x.y;
+          }
+        }
+      }
+    }
+    if (GROUPED && is_v) {
+      if constexpr (BYTES == 1) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) c[k] = transpose_bytes(c[k], lane);
+      }
+      if constexpr (BYTES == 2) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t a = c[2 * k], b = c[2 * k + 1];
+          transpose_halves(a, b, lane);
+          c[2 * k] = a;
+          c[2 * k + 1] = b;
+        }
+      }
+    }
+    uint32_t w[U::words];
+    if constexpr (KvFormat<FMT>::scaled) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float f[4];
+        codes4<FMT>(c[k], f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = there ? f[j] * scale : 0.f;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[4 * k + j] = __float_as_uint(f[j]);
+        } else {
+          w[2 * k] = pack_bf16x2(f[0], f[1]);
+          w[2 * k + 1] = pack_bf16x2(f[2], f[3]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] = c[k];
+    }
+    if (P.ok && u < units) store_words(dst + u * C, A.vec, w);
+  }
+}
+
+// One row of V per wave (see write_v_row).
+template <int FMT, class T>
+__device__ __forceinline__ void read_v_row(const KvArgs& K, const KvRows& A, const Place& P) {
+  constexpr int BYTES = KvFormat<FMT>::bytes, MOST = SGMV_KV_MAX_HEAD_DIM / WAVE;
+  const int lane = threadIdx.x & (WAVE - 1), D = K.D;
+  if (!P.ok) return;
+  T* dst = static_cast<T*>(A.v) + P.row * A.ldv_t + P.head * A.ldv_h;
+  const int64_t token = max(P.token, (int64_t)0);
+  const char* src = static_cast<const char*>(K.v) + (token & ~(int64_t)15) * D * BYTES;
+  const int place = place_of((int)(token & 15));
+  float scale = 1.f;
+  if constexpr (KvFormat<FMT>::scaled) scale = K.v_scale[token];
+  T e[MOST];
+#pragma unroll
+  for (int i = 0; i < MOST; ++i) {
+    const int d = min(lane + WAVE * i, D - 1);
+    if constexpr (BYTES == 1) {
+      float f[4];
+      codes4<FMT>(static_cast<const uint8_t*>(static_cast<const void*>(src))[d * 16 + place], f);
+      if constexpr (sizeof(T) == 4) e[i] = f[0] * scale;
+      else e[i] = (T)pack_bf16x2(f[0] * scale, 0.f);
+    } else {
+      e[i] = *reinterpret_cast<const T*>(src + v_at<BYTES>(d, place));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MOST; ++i)
+    if (lane + WAVE * i < D) dst[lane + WAVE * i] = P.token < 0 ? T(0) : e[i];
+}
+
+template <int FMT, class T>
+__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_read_groups_kernel(KvArgs K, KvRows A) {
+  Place P;
+  if (group_place(K, A.out_start, A.rows, P)) read_rows<FMT, T, true>(K, A, blockIdx.z, P);
+}
+
+template <int FMT, class T>
+__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_read_rows_kernel(KvArgs K, KvRows A, int for_v) {
+  const int wv = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1);
+  Place P;
+  if ((int)blockIdx.x < for_v) {
+    row_place(K, A.out_start, A.rows, (int)blockIdx.x * RW_WAVES + wv, P);
+    read_v_row<FMT, T>(K, A, P);
+  } else {
+    row_place(K, A.out_start, A.rows, (((int)blockIdx.x - for_v) * RW_WAVES + wv) * 16 + (lane & 15), P);
+    read_rows<FMT, T, false>(K, A, false, P);
+  }
+}
+
+// Slots of 16-token groups for `tokens` rows of B sequences (see group_place).
+dim3 group_grid(const KvArgs& K, int64_t tokens) {
+  const int64_t slots = tokens / 16 + 2 * (int64_t)K.B;
+  return dim3((unsigned)((slots + RW_WAVES - 1) / RW_WAVES), (unsigned)K.H, 2);
+}
+
+// Row by row while groups would be mostly empty: workgroups for V and in all (0: by groups).
+struct RowGrid {
+  int for_v;
+  unsigned all;
+};
+RowGrid row_grid(const KvArgs& K, int64_t tokens, bool few) {
+  const int64_t rows = tokens * K.H, for_v = (rows + RW_WAVES - 1) / RW_WAVES;
+  if (!few || rows > 0x40000000) return {0, 0};
+  return {(int)for_v, (unsigned)(for_v + (rows + 16 * RW_WAVES - 1) / (16 * RW_WAVES))};
+}
+
+template <int FMT, class T>
+void launch_write(const KvArgs& K, const KvRows& R, int max_q, hipStream_t stream) {
+  const RowGrid g = row_grid(K, K.T, max_q <= 8);
+  if (g.all) kv_write_rows_kernel<FMT, T><<<g.all, RW_WAVES * WAVE, 0, stream>>>(K, R, g.for_v);
+  else kv_write_groups_kernel<FMT, T><<<group_grid(K, K.T), RW_WAVES * WAVE, 0, stream>>>(K, R);
+}
+
+template <int FMT, class T>
+void launch_read(const KvArgs& K, const KvRows& R, hipStream_t stream) {
+  const RowGrid g = row_grid(K, R.rows, R.rows <= 4 * (int64_t)K.B);
+  if (g.all) kv_read_rows_kernel<FMT, T><<<g.all, RW_WAVES * WAVE, 0, stream>>>(K, R, g.for_v);
+  else kv_read_groups_kernel<FMT, T><<<group_grid(K, R.rows), RW_WAVES * WAVE, 0, stream>>>(K, R);
 }
 
 }  // namespace
 
-// Slots of 16-token groups for `tokens` rows of B sequences (see kv_write_kernel).
-static dim3 row_grid(const KvArgs& K, int64_t tokens) {
-  const int64_t slots = tokens / 16 + 2 * (int64_t)K.B;
-  return dim3((unsigned)((slots + RW_WAVES - 1) / RW_WAVES), (unsigned)K.H);
-}
-
-#define KV_ROWS(KERNEL_, N_)                                                                   \
-  do {                                                                                         \
-    const dim3 g = row_grid(K, N_), b(RW_WAVES * WAVE);                                        \
-    if (fmt == SGMV_KV_F32) KERNEL_<SGMV_KV_F32, float><<<g, b, 0, stream>>>(K, R);            \
-    else if (fmt == SGMV_KV_BF16) KERNEL_<SGMV_KV_BF16, uint16_t><<<g, b, 0, stream>>>(K, R);  \
-    else if (fmt == SGMV_KV_E4M3 && R.f32) KERNEL_<SGMV_KV_E4M3, float><<<g, b, 0, stream>>>(K, R); \
-    else if (fmt == SGMV_KV_E4M3) KERNEL_<SGMV_KV_E4M3, uint16_t><<<g, b, 0, stream>>>(K, R);  \
-    else if (R.f32) KERNEL_<SGMV_KV_I8, float><<<g, b, 0, stream>>>(K, R);                     \
-    else KERNEL_<SGMV_KV_I8, uint16_t><<<g, b, 0, stream>>>(K, R);                             \
-  } while (0)
-
-hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream) {
-  KV_ROWS(kv_write_kernel, K.T);
+hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, int max_q, hipStream_t stream) {
+  if (fmt == SGMV_KV_F32) launch_write<SGMV_KV_F32, float>(K, R, max_q, stream);
+  else if (fmt == SGMV_KV_BF16) launch_write<SGMV_KV_BF16, uint16_t>(K, R, max_q, stream);
+  else if (fmt == SGMV_KV_E4M3 && R.f32) launch_write<SGMV_KV_E4M3, float>(K, R, max_q, stream);
+  else if (fmt == SGMV_KV_E4M3) launch_write<SGMV_KV_E4M3, uint16_t>(K, R, max_q, stream);
+  else if (R.f32) launch_write<SGMV_KV_I8, float>(K, R, max_q, stream);
+  else launch_write<SGMV_KV_I8, uint16_t>(K, R, max_q, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream) {
-  KV_ROWS(kv_read_kernel, R.rows);
+  if (fmt == SGMV_KV_F32) launch_read<SGMV_KV_F32, float>(K, R, stream);
+  else if (fmt == SGMV_KV_BF16) launch_read<SGMV_KV_BF16, uint16_t>(K, R, stream);
+  else if (fmt == SGMV_KV_E4M3 && R.f32) launch_read<SGMV_KV_E4M3, float>(K, R, stream);
+  else if (fmt == SGMV_KV_E4M3) launch_read<SGMV_KV_E4M3, uint16_t>(K, R, stream);
+  else if (R.f32) launch_read<SGMV_KV_I8, float>(K, R, stream);
+  else launch_read<SGMV_KV_I8, uint16_t>(K, R, stream);
   return hipGetLastError();
 }
-
-#undef KV_ROWS
 
 }  // namespace sgmv

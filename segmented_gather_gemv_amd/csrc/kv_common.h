@@ -41,6 +41,7 @@ struct KvRows {
   const int32_t* out_start;  // read call: first row of each sequence
   int32_t rows;              // read call
   int32_t f32;               // rows are fp32, else bf16
+  int32_t vec;               // rows may be accessed 16 bytes at a time
 };
 
 // One sequence of the batch, whatever the arrays hold: its first new token, its new tokens and
@@ -84,6 +85,28 @@ __device__ __forceinline__ int wave_find(int B, int x, F start) {
     n = min(step, left);
   }
   return lo;
+}
+
+// Maximum of a value over the two halves of the wave, in both.
+__device__ __forceinline__ float half_max(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+__device__ __forceinline__ float half_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Maximum and sum of a value over the lanes of equal lane % 16, in all of them.
+__device__ __forceinline__ float quad_max(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return half_max(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+
+__device__ __forceinline__ float quad_sum(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return half_sum(__uint_as_float(r[0]) + __uint_as_float(r[1]));
 }
 
 // ---------------------------------------------------------------------------------------

@@ -5,7 +5,7 @@
 
 namespace sgmv {
 
-constexpr int VF_CHUNK = 4096;  // entries of a row that one workgroup sums
+constexpr int VF_PART = 1024;  // entries of a row that one wave sums
 
 struct VerifyArgs {
   const void* target;
@@ -18,8 +18,8 @@ struct VerifyArgs {
   int32_t* tokens;
   int64_t ldo;
   int32_t* accepted;
-  double* sums;  // [B][chunks][2]
-  int32_t B, V, N, max_drafts, bf16, chunks;
+  double* sums;  // [B][parts][2]: of what is left of the row, of the row itself
+  int32_t B, V, N, max_drafts, bf16, parts;
   int32_t vec;  // rows may be read four entries at a time
 };
 

@@ -7,19 +7,19 @@
 // p_{n+1}. A row is drawn from by its running sum: the lowest j whose sum passes r times the total.
 //
 // Sums are in fp64: with 2^17 entries a running sum in fp32 is off by more than an entry's own
-// weight. Bound by reading the one or two rows that are drawn from, so a row is cut into chunks of
-// VF_CHUNK entries, one workgroup each: the first launch sums them (every one of a sequence's
-// workgroups looks at the drafts itself, a few loads), the second finds the chunk that r falls into
-// and the entry in it. One launch in which the last workgroup of a sequence does the second part would need
-// a cleared counter, which is a launch too.
+// weight. Bound by reading the one or two rows that are drawn from, so a row is cut into parts of VF_PART
+// entries, one wave each: the first launch sums them (every wave looks at its sequence's drafts itself, a
+// few loads), the second, one wave per sequence without a barrier, finds the part that r falls into and
+// the entry in it. One launch in which the last wave of a sequence does the second part would need a
+// cleared counter, which is a launch too.
 #include "verify.h"
 
 namespace sgmv {
 
 namespace {
 
-constexpr int VF_THREADS = 256, VF_WAVES = VF_THREADS / WAVE;
-constexpr int VF_EACH = VF_CHUNK / VF_THREADS;  // entries of one thread
+constexpr int VF_WAVES = 4;               // of a workgroup of the first launch
+constexpr int VF_EACH = VF_PART / WAVE;   // entries of one lane
 
 __device__ __forceinline__ float prob(const float* p) { return *p; }
 __device__ __forceinline__ float prob(const uint16_t* p) { return bf16_bits_to_f32(*p); }
@@ -36,25 +36,6 @@ __device__ __forceinline__ double wave_scan(double v) {  // inclusive
     if (lane >= o) v += u;
   }
   return v;
-}
-
-// Inclusive running sum over the workgroup's threads, the sum before this thread (the very value that the
-// thread before has as its own, so that neighbours leave no gap) and the total.
-__device__ __forceinline__ double block_scan(double v, double* s_sum, double& before, double& total) {
-  const int lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE;
-  const double up = wave_scan(v);
-  __syncthreads();
-  if (lane == WAVE - 1) s_sum[wv] = up;
-  __syncthreads();
-  double base = 0.;
-  total = 0.;
-  for (int i = 0; i < VF_WAVES; ++i) {
-    if (i < wv) base += s_sum[i];
-    total += s_sum[i];
-  }
-  const double left = __shfl_up(up, 1);
-  before = lane ? base + left : base;
-  return base + up;
 }
 
 // The row that sequence b is drawn from: target row p, draft row q (or none), entry left out (or -1).
@@ -104,9 +85,10 @@ __device__ __forceinline__ void four(const T* row, int j, int V, float (&f)[4]) 
 }
 
 template <class T, bool VEC>
-__global__ __launch_bounds__(VF_THREADS) void verify_sum_kernel(VerifyArgs A) {
-  __shared__ double s_sum[2][VF_WAVES];
-  const int c = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & (WAVE - 1), wv = tid / WAVE;
+__global__ __launch_bounds__(VF_WAVES* WAVE) void verify_sum_kernel(VerifyArgs A) {
+  const int lane = threadIdx.x & (WAVE - 1), b = blockIdx.y;
+  const int part = blockIdx.x * VF_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  if (part >= A.parts) return;
   const Drafts d = drafts(A, b);
   const T* target = static_cast<const T*>(A.target) + (int64_t)(d.first + b) * A.ldt;
   const T* draft = static_cast<const T*>(A.draft) + (A.draft ? (int64_t)d.first * A.ldd : 0);
@@ -126,17 +108,17 @@ __global__ __launch_bounds__(VF_THREADS) void verify_sum_kernel(VerifyArgs A) {
     const uint64_t bad = __ballot(!ok);
     if (bad) taken = i0 + __ffsll((unsigned long long)bad) - 1;
   }
-  if (c == 0) {
+  if (part == 0) {
     int32_t* out = A.tokens + (int64_t)b * A.ldo;
-    for (int i = tid; i <= A.max_drafts; i += VF_THREADS)
+    for (int i = lane; i <= A.max_drafts; i += WAVE)
       if (i != taken) out[i] = i < taken ? A.ids[d.first + i] : -1;
-    if (tid == 0) A.accepted[b] = taken;
+    if (lane == 0) A.accepted[b] = taken;
   }
   const Row<T> row = drawn_row<T>(A, b, d, taken);
   double sum = 0., all = 0.;  // of what is left of p, and of p itself
 #pragma unroll
   for (int i = 0; i < VF_EACH / 4; ++i) {
-    const int j = c * VF_CHUNK + 4 * (i * VF_THREADS + tid);
+    const int j = part * VF_PART + 4 * (i * WAVE + lane);
     float p[4], q[4] = {0.f, 0.f, 0.f, 0.f};
     four<T, VEC>(row.p, j, A.V, p);
     if (row.q) four<T, VEC>(row.q, j, A.V, q);
@@ -151,59 +133,53 @@ __global__ __launch_bounds__(VF_THREADS) void verify_sum_kernel(VerifyArgs A) {
     sum += __shfl_xor(sum, o);
     all += __shfl_xor(all, o);
   }
-  if (lane == 0) {
-    s_sum[0][wv] = sum;
-    s_sum[1][wv] = all;
-  }
-  __syncthreads();
-  if (tid < 2) {
-    double t = 0.;
-    for (int i = 0; i < VF_WAVES; ++i) t += s_sum[tid][i];
-    A.sums[((int64_t)b * A.chunks + c) * 2 + tid] = t;
-  }
+  if (lane < 2) A.sums[((int64_t)b * A.parts + part) * 2 + lane] = lane ? all : sum;
 }
 
 template <class T, bool VEC>
-__global__ __launch_bounds__(VF_THREADS) void verify_draw_kernel(VerifyArgs A) {
-  __shared__ double s_sum[VF_WAVES], s_base;
-  __shared__ int s_chunk, s_token, s_last;
-  const int b = blockIdx.x, tid = threadIdx.x;
+__global__ __launch_bounds__(WAVE) void verify_draw_kernel(VerifyArgs A) {
+  const int b = blockIdx.x, lane = threadIdx.x;
   const int taken = A.accepted[b];
-  const Row<T> row = drawn_row<T>(A, b, drafts(A, b), taken);
-  if (tid == 0) s_chunk = s_token = s_last = -1;
-  // the chunk that r falls into; the second pass, over p itself, where nothing is left of it
-  const double* sums = A.sums + (int64_t)b * A.chunks * 2;
-  const int per = (A.chunks + VF_THREADS - 1) / VF_THREADS;
-  const int c0 = min(tid * per, A.chunks), c1 = min(c0 + per, A.chunks);
-  double at = 0.;
-  int pass = 0;
-  for (; pass < 2; ++pass) {
-    double mine = 0., before, total;
-    for (int c = c0; c < c1; ++c) mine += sums[2 * c + pass];
-    const double upto = block_scan(mine, s_sum, before, total);
-    if (!(total > 0.)) continue;
-    at = (double)A.sample_u[b] * total;
-    if (before <= at && at < upto) {  // one thread
-      double base = before, last = before;
-      int chunk = -1;
+  const double u = A.sample_u[b];
+  const Drafts d = drafts(A, b);
+  // the part that r falls into; over p itself where nothing is left of it
+  const double* sums = A.sums + (int64_t)b * A.parts * 2;
+  const int per = (A.parts + WAVE - 1) / WAVE;
+  const int c0 = min(lane * per, A.parts), c1 = min(c0 + per, A.parts);
+  double left = 0., all = 0.;
+  for (int c = c0; c < c1; ++c) {
+    left += sums[2 * c];
+    all += sums[2 * c + 1];
+  }
+  const int pass = __any(left > 0.) ? 0 : 1;
+  double upto = wave_scan(pass ? all : left);
+  double before = __shfl_up(upto, 1);
+  if (lane == 0) before = 0.;
+  const double at = u * __shfl(upto, WAVE - 1);
+  // `before` is the very value that the lane before has as its own: neighbours leave no gap
+  const uint64_t here = __ballot(before <= at && at < upto);
+  int token = -1;
+  if (here) {
+    const int owner = __ffsll((unsigned long long)here) - 1;
+    double base = before, last = before;
+    int part = c0;
+    if (lane == owner) {
+      double sum = before;
       for (int c = c0; c < c1; ++c) {
         const double x = sums[2 * c + pass];
         if (x > 0.) {
-          chunk = c;
-          last = base;
+          part = c;
+          last = sum;
         }
-        base += x;
-        if (base > at) break;
+        sum += x;
+        if (sum > at) break;
       }
-      s_chunk = chunk;
-      s_base = last;
     }
-    break;
-  }
-  __syncthreads();
-  int token = -1;
-  if (s_chunk >= 0) {
-    const int j0 = s_chunk * VF_CHUNK + tid * VF_EACH;
+    part = __shfl(part, owner);
+    base = __shfl(last, owner);
+
+    const Row<T> row = drawn_row<T>(A, b, d, taken);
+    const int j0 = part * VF_PART + lane * VF_EACH;
     double w[VF_EACH], mine = 0.;
 #pragma unroll
     for (int i = 0; i < VF_EACH / 4; ++i) {
@@ -216,32 +192,32 @@ __global__ __launch_bounds__(VF_THREADS) void verify_draw_kernel(VerifyArgs A) {
         mine += w[4 * i + e];
       }
     }
-    double before, total;
-    block_scan(mine, s_sum, before, total);
-    double sum = s_base + before;
-    // the lowest entry that passes; the last one with a weight if rounding leaves none (the chunk's sum was
+    upto = wave_scan(mine);
+    before = __shfl_up(upto, 1);
+    double sum = base + (lane ? before : 0.);
+    // the lowest entry that passes; the last one with a weight if rounding leaves none (the part's sum was
     // formed in another order)
-    int found = -1, last = -1;
+    int found = -1, weighted = -1;
 #pragma unroll
     for (int i = 0; i < VF_EACH; ++i) {
       sum += w[i];
       if (w[i] > 0.) {
-        last = j0 + i;
+        weighted = j0 + i;
         if (found < 0 && sum > at) found = j0 + i;
       }
     }
-    if (last >= 0) atomicMax(&s_last, last);
-    if (found >= 0) atomicMin((unsigned*)&s_token, (unsigned)found);  // -1 is the largest
-    __syncthreads();
-    token = s_token >= 0 ? s_token : s_last;
+    const uint64_t f = __ballot(found >= 0), l = __ballot(weighted >= 0);
+    if (f) token = __shfl(found, __ffsll((unsigned long long)f) - 1);
+    else if (l) token = __shfl(weighted, WAVE - 1 - __clzll((long long)l));
   }
-  if (tid == 0) A.tokens[(int64_t)b * A.ldo + taken] = token;
+  if (lane == 0) A.tokens[(int64_t)b * A.ldo + taken] = token;
 }
 
 template <class T, bool VEC>
 void launch(const VerifyArgs& A, hipStream_t stream) {
-  verify_sum_kernel<T, VEC><<<dim3(A.chunks, A.B), VF_THREADS, 0, stream>>>(A);
-  verify_draw_kernel<T, VEC><<<dim3(A.B), VF_THREADS, 0, stream>>>(A);
+  const dim3 g((unsigned)((A.parts + VF_WAVES - 1) / VF_WAVES), (unsigned)A.B);
+  verify_sum_kernel<T, VEC><<<g, VF_WAVES * WAVE, 0, stream>>>(A);
+  verify_draw_kernel<T, VEC><<<dim3((unsigned)A.B), WAVE, 0, stream>>>(A);
 }
 
 }  // namespace
