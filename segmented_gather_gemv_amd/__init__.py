@@ -176,7 +176,13 @@ def library():
 def _stream(device: torch.device):
     if device.type != "cuda":
         return None
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    return _raw_stream(device.index)
+
+
+def _raw_stream(index: Optional[int]) -> int:
+    """Handle of the current stream of a GPU (without a torch.cuda.Stream object around it, whose
+    construction takes longer than a launch's other arguments together)."""
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
 def _dtype_code(dt: torch.dtype) -> int:

@@ -17,7 +17,7 @@ from typing import Optional, Tuple, Union
 
 import torch
 
-from . import _check, _dtype_code, _lib, _ptr, _stream
+from . import SGMV_OK, _check, _dtype_code, _lib, _raw_stream
 
 KV_F32, KV_BF16, KV_E4M3, KV_I8 = range(4)
 KV_GROUP = 16
@@ -86,22 +86,14 @@ class KvCache:
     k_scale: Optional[torch.Tensor]  # fp32 [pages, heads, page_size], 8-bit formats
     v_scale: Optional[torch.Tensor]
     desc: _KvCache
-    ref: object = field(repr=False, default=None)
+    ref: object = field(init=False, repr=False)     # what the library takes
+    index: int = field(init=False, repr=False)      # of the GPU, -1: not on one
 
-    @property
-    def pages(self): return self.desc.pages
-
-    @property
-    def page_size(self): return self.desc.page_size
-
-    @property
-    def heads(self): return self.desc.heads
-
-    @property
-    def head_dim(self): return self.desc.head_dim
-
-    @property
-    def dtype(self): return self.k.dtype
+    def __post_init__(self):
+        d = self.desc
+        self.pages, self.page_size, self.heads, self.head_dim = (d.pages, d.page_size, d.heads,
+                                                                 d.head_dim)
+        self.dtype, self.ref, self.index = self.k.dtype, ctypes.byref(d), self.k.get_device()
 
 
 def _kv_shapes(desc: _KvCache, elem: int):
@@ -143,7 +135,7 @@ def sgmv_kv_wrap(k: torch.Tensor, v: torch.Tensor, k_scale: Optional[torch.Tenso
     desc.k, desc.v = k.data_ptr(), v.data_ptr()
     if scaled:
         desc.k_scale, desc.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-    return KvCache(k, v, k_scale, v_scale, desc, ctypes.byref(desc))
+    return KvCache(k, v, k_scale, v_scale, desc)
 
 
 def sgmv_kv_init(pages: int, page_size: int, heads: int, head_dim: int,
@@ -168,13 +160,12 @@ class KvBatch:
     kv_len: torch.Tensor      # int32 [B]
     page_table: torch.Tensor  # int32 [B, table_pages]
     desc: _KvBatch
-    ref: object = field(repr=False, default=None)
+    ref: object = field(init=False, repr=False)
+    index: int = field(init=False, repr=False)
 
-    @property
-    def B(self): return self.desc.B
-
-    @property
-    def T(self): return self.desc.T
+    def __post_init__(self):
+        self.B, self.T = self.desc.B, self.desc.T
+        self.ref, self.index = ctypes.byref(self.desc), self.kv_len.get_device()
 
 
 def sgmv_kv_batch(q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, T: int,
@@ -196,32 +187,35 @@ def sgmv_kv_batch(q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch
     desc = _KvBatch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
                     max(page_table.stride(0), cols) if B > 1 else cols, cols, B, int(T),
                     int(max_q), int(max_kv))
-    return KvBatch(q_start, kv_len, page_table, desc, ctypes.byref(desc))
+    return KvBatch(q_start, kv_len, page_table, desc)
 
 
 def _rows3(t: torch.Tensor, n: int, heads: Optional[int], cache: KvCache, what: str):
     """Checks rows [n, heads, head_dim]; returns their token and head strides."""
-    if t.dim() != 3 or t.shape[0] != n or t.shape[2] != cache.desc.head_dim or (
-            heads is not None and t.shape[1] != heads):
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != cache.head_dim or (
+            heads is not None and shape[1] != heads):
         raise ValueError(f"{what} must be [{n}, {'heads' if heads is None else heads}, "
-                         f"{cache.desc.head_dim}], got {tuple(t.shape)}")
+                         f"{cache.head_dim}], got {tuple(shape)}")
     st = t.stride()
     if st[2] != 1:
         raise ValueError(f"{what} must be contiguous over the head dimension")
-    if t.device != cache.k.device:
+    if t.get_device() != cache.index:
         raise ValueError(f"{what} must be on the cache's device")
     # a stride of a single token or head says nothing
-    return (st[0] if n > 1 else t.shape[1] * t.shape[2] + abs(st[1]) * t.shape[1],
-            st[1] if t.shape[1] > 1 else t.shape[2])
+    return (st[0] if n > 1 else shape[1] * shape[2] + abs(st[1]) * shape[1],
+            st[1] if shape[1] > 1 else shape[2])
 
 
-def _same_device(batch: KvBatch, cache: KvCache):
-    if batch.kv_len.device != cache.k.device:
+def _dense3(heads: int, cache: KvCache):
+    """The strides of rows that a call allocates itself."""
+    return heads * cache.head_dim, cache.head_dim
+
+
+def _on_gpu(batch: KvBatch, cache: KvCache):
+    if batch.index != cache.index:
         raise ValueError("the batch must be on the cache's device")
-
-
-def _on_gpu(t: torch.Tensor):
-    if t.device.type != "cuda":
+    if cache.index < 0:
         raise ValueError("the kernels run on GPU tensors")
 
 
@@ -231,16 +225,16 @@ def _on_gpu(t: torch.Tensor):
 def sgmv_kv_write(k: torch.Tensor, v: torch.Tensor, batch: KvBatch, cache: KvCache) -> None:
     """Write the step's keys and values [T, heads, head_dim] (strided views are fine) into the
     cache, quantised to its format."""
-    T, H = batch.desc.T, cache.desc.heads
-    kt, kh = _rows3(k, T, H, cache, "k")
-    vt, vh = _rows3(v, T, H, cache, "v")
+    kt, kh = _rows3(k, batch.T, cache.heads, cache, "k")
+    vt, vh = _rows3(v, batch.T, cache.heads, cache, "v")
     if v.dtype != k.dtype:
         raise TypeError("k and v must share a dtype")
     dtype = _dtype_code(k.dtype)
-    _same_device(batch, cache)
-    _on_gpu(k)
-    _check(_lib.sgmv_kv_write(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dtype,
-                              batch.ref, cache.ref, _stream(k.device)), "sgmv_kv_write")
+    _on_gpu(batch, cache)
+    st = _lib.sgmv_kv_write(k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, dtype, batch.ref,
+                            cache.ref, _raw_stream(cache.index))
+    if st != SGMV_OK:
+        _check(st, "sgmv_kv_write")
 
 
 def sgmv_kv_read(batch: KvBatch, cache: KvCache, out_start: torch.Tensor, rows: int,
@@ -249,24 +243,27 @@ def sgmv_kv_read(batch: KvBatch, cache: KvCache, out_start: torch.Tensor, rows: 
     """The last out_start[b + 1] - out_start[b] tokens of each sequence, as rows
     [rows, heads, head_dim]: out_start = q_start reads the step's new tokens back, running sums
     of kv_len whole sequences. Into k and v if given."""
-    rows = int(rows)
-    if out_start.dtype != torch.int32 or out_start.numel() != batch.desc.B + 1 or (
-            not out_start.is_contiguous() or out_start.device != cache.k.device):
+    rows, heads = int(rows), cache.heads
+    if out_start.dtype != torch.int32 or out_start.numel() != batch.B + 1 or (
+            not out_start.is_contiguous() or out_start.get_device() != cache.index):
         raise TypeError("out_start must be B + 1 contiguous int32 entries on the cache's device")
-    shape = (rows, cache.desc.heads, cache.desc.head_dim)
+    code = _dtype_code(dtype)
+    (kt, kh) = (vt, vh) = _dense3(heads, cache)
     if k is None:
-        k = torch.empty(shape, dtype=dtype, device=cache.k.device)
+        k = torch.empty((rows, heads, cache.head_dim), dtype=dtype, device=out_start.device)
+    else:
+        kt, kh = _rows3(k, rows, heads, cache, "k")
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=cache.k.device)
-    kt, kh = _rows3(k, rows, shape[1], cache, "k")
-    vt, vh = _rows3(v, rows, shape[1], cache, "v")
+        v = torch.empty((rows, heads, cache.head_dim), dtype=dtype, device=out_start.device)
+    else:
+        vt, vh = _rows3(v, rows, heads, cache, "v")
     if k.dtype != dtype or v.dtype != dtype:
         raise TypeError(f"k and v must be {dtype}")
-    _same_device(batch, cache)
-    _on_gpu(k)
-    _check(_lib.sgmv_kv_read(batch.ref, cache.ref, out_start.data_ptr(), rows, k.data_ptr(), kt,
-                             kh, v.data_ptr(), vt, vh, _dtype_code(dtype), _stream(k.device)),
-           "sgmv_kv_read")
+    _on_gpu(batch, cache)
+    st = _lib.sgmv_kv_read(batch.ref, cache.ref, out_start.data_ptr(), rows, k.data_ptr(), kt, kh,
+                           v.data_ptr(), vt, vh, code, _raw_stream(cache.index))
+    if st != SGMV_OK:
+        _check(st, "sgmv_kv_read")
     return k, v
 
 
@@ -280,36 +277,41 @@ def sgmv_kv_attention(q: torch.Tensor, batch: KvBatch, cache: KvCache,
     tokens only. Returns the output and the rows' log-sum-exp [T, query heads] fp32. ``scale``
     defaults to head_dim ** -0.5. A workspace (uint8) is allocated on the current stream
     unless one is given."""
-    T, D = batch.desc.T, cache.desc.head_dim
+    T, D = batch.T, cache.head_dim
     qt, qh = _rows3(q, T, None, cache, "q")
-    heads = q.shape[1]
+    heads, dtype = q.shape[1], q.dtype
+    code = _dtype_code(dtype)
     if out is None:
-        out = torch.empty((T, heads, D), dtype=q.dtype, device=q.device)
-    ot, oh = _rows3(out, T, heads, cache, "out")
-    if out.dtype != q.dtype:
-        raise TypeError("out must have q's dtype")
+        out = torch.empty((T, heads, D), dtype=dtype, device=q.device)
+        ot, oh = _dense3(heads, cache)
+    else:
+        ot, oh = _rows3(out, T, heads, cache, "out")
+        if out.dtype != dtype:
+            raise TypeError("out must have q's dtype")
     if lse is None:
         lse = torch.empty((T, heads), dtype=torch.float32, device=q.device)
     elif tuple(lse.shape) != (T, heads) or lse.dtype != torch.float32 or (
-            not lse.is_contiguous() or lse.device != q.device):
+            not lse.is_contiguous() or lse.get_device() != cache.index):
         raise TypeError("lse must be a contiguous float32 tensor of one entry per token and head")
-    _same_device(batch, cache)
-    a = _Attention(q.data_ptr(), out.data_ptr(), lse.data_ptr(), qt, qh, ot, oh, heads,
-                   _dtype_code(q.dtype), D ** -0.5 if scale is None else scale, window, n_split)
+    a = _Attention(q.data_ptr(), out.data_ptr(), lse.data_ptr(), qt, qh, ot, oh, heads, code,
+                   D ** -0.5 if scale is None else scale, window, n_split)
     ref, need = ctypes.byref(a), ctypes.c_size_t()
-    _check(_lib.sgmv_kv_attention_workspace(ref, batch.ref, cache.ref, ctypes.byref(need)),
-           "sgmv_kv_attention")
-    _on_gpu(q)
-    size = need.value
-    if workspace is None and size:
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    elif workspace is not None:
-        if workspace.device != q.device or not workspace.is_contiguous():
+    st = _lib.sgmv_kv_attention_workspace(ref, batch.ref, cache.ref, ctypes.byref(need))
+    if st != SGMV_OK:
+        _check(st, "sgmv_kv_attention")
+    _on_gpu(batch, cache)
+    size, ptr = need.value, None
+    if workspace is not None:
+        if workspace.get_device() != cache.index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on q's device")
         size = workspace.numel() * workspace.element_size()
-    _check(_lib.sgmv_kv_attention(ref, batch.ref, cache.ref,
-                                  None if workspace is None else workspace.data_ptr(), size,
-                                  _stream(q.device)), "sgmv_kv_attention")
+        ptr = workspace.data_ptr()
+    elif size:
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+        ptr = workspace.data_ptr()
+    st = _lib.sgmv_kv_attention(ref, batch.ref, cache.ref, ptr, size, _raw_stream(cache.index))
+    if st != SGMV_OK:
+        _check(st, "sgmv_kv_attention")
     return out, lse
 
 
@@ -327,6 +329,11 @@ def sgmv_kv_attention_workspace(q_heads: int, dtype: torch.dtype, batch: KvBatch
 # ---------------------------------------------------------------------------------------
 # drafts
 # ---------------------------------------------------------------------------------------
+def _entries(t: torch.Tensor, n: int, dtype: torch.dtype, index: int, what: str):
+    if t.dtype != dtype or t.numel() != n or t.get_device() != index or not t.is_contiguous():
+        raise TypeError(f"{what} must be {n} contiguous {dtype} entries on target's device")
+
+
 def sgmv_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
                        draft_ids: torch.Tensor, draft_start: torch.Tensor,
                        accept_u: torch.Tensor, sample_u: torch.Tensor, max_drafts: int,
@@ -338,45 +345,46 @@ def sgmv_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
     probabilities ``draft`` [N, vocab] or None for certain drafts, and the uniform numbers
     given. Returns tokens [B, max_drafts + 1] (those taken, the one drawn, then -1) and how
     many were taken [B], both int32."""
-    B, N = sample_u.numel(), draft_ids.numel()
-    dev = target.device
-    if target.dim() != 2 or target.shape[0] != N + B or target.shape[1] < 1 or (
-            target.shape[1] > 1 and target.stride(1) != 1):
-        raise ValueError(f"target must be row-major [{N + B}, vocab], got {tuple(target.shape)}")
-    V = target.shape[1]
+    B, N, shape = sample_u.numel(), draft_ids.numel(), target.shape
+    dev, dtype = target.get_device(), target.dtype
+    if len(shape) != 2 or shape[0] != N + B or shape[1] < 1 or (
+            shape[1] > 1 and target.stride(1) != 1):
+        raise ValueError(f"target must be row-major [{N + B}, vocab], got {tuple(shape)}")
+    V = shape[1]
     if draft is not None:
         if draft.dim() != 2 or tuple(draft.shape) != (N, V) or (V > 1 and draft.stride(1) != 1):
             raise ValueError(f"draft must be row-major [{N}, {V}], got {tuple(draft.shape)}")
-        if draft.dtype != target.dtype or draft.device != dev:
+        if draft.dtype != dtype or draft.get_device() != dev:
             raise TypeError("draft must have target's dtype and device")
-    for t, n, dt, what in ((draft_ids, N, torch.int32, "draft_ids"),
-                           (draft_start, B + 1, torch.int32, "draft_start"),
-                           (accept_u, N, torch.float32, "accept_u"),
-                           (sample_u, B, torch.float32, "sample_u")):
-        if t.dtype != dt or t.numel() != n or t.device != dev or not t.is_contiguous():
-            raise TypeError(f"{what} must be {n} contiguous {dt} entries on target's device")
+    _entries(draft_ids, N, torch.int32, dev, "draft_ids")
+    _entries(draft_start, B + 1, torch.int32, dev, "draft_start")
+    _entries(accept_u, N, torch.float32, dev, "accept_u")
+    _entries(sample_u, B, torch.float32, dev, "sample_u")
     if max_drafts < 0:
         raise ValueError("max_drafts must not be negative")
     if tokens is None:
-        tokens = torch.empty((B, max_drafts + 1), dtype=torch.int32, device=dev)
-    if accepted is None:
-        accepted = torch.empty(B, dtype=torch.int32, device=dev)
-    if tokens.dtype != torch.int32 or tuple(tokens.shape) != (B, max_drafts + 1) or (
-            tokens.device != dev or (max_drafts > 0 and tokens.stride(1) != 1)):
+        tokens = torch.empty((B, max_drafts + 1), dtype=torch.int32, device=target.device)
+    elif tokens.dtype != torch.int32 or tuple(tokens.shape) != (B, max_drafts + 1) or (
+            tokens.get_device() != dev or (max_drafts > 0 and tokens.stride(1) != 1)):
         raise ValueError("tokens must be row-major int32 [B, max_drafts + 1] on target's device")
-    if accepted.dtype != torch.int32 or accepted.numel() != B or accepted.device != dev or (
-            not accepted.is_contiguous()):
+    if accepted is None:
+        accepted = torch.empty(B, dtype=torch.int32, device=target.device)
+    elif accepted.dtype != torch.int32 or accepted.numel() != B or (
+            accepted.get_device() != dev or not accepted.is_contiguous()):
         raise ValueError("accepted must be B contiguous int32 entries on target's device")
-    _on_gpu(target)
+    code = _dtype_code(dtype)
+    if dev < 0:
+        raise ValueError("the kernels run on GPU tensors")
     size = _lib.sgmv_verify_drafts_workspace(B, V)
-    workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
-    _check(_lib.sgmv_verify_drafts(
+    workspace = torch.empty(max(size, 1), dtype=torch.uint8, device=target.device)
+    no_draft = draft is None or N == 0
+    st = _lib.sgmv_verify_drafts(
         target.data_ptr(), target.stride(0) if N + B > 1 else V,
-        None if draft is None or N == 0 else draft.data_ptr(),
-        V if draft is None or N <= 1 else draft.stride(0), V, _dtype_code(target.dtype),
+        None if no_draft else draft.data_ptr(), V if no_draft or N == 1 else draft.stride(0), V, code,
         draft_ids.data_ptr(), draft_start.data_ptr(), B, N, int(max_drafts), accept_u.data_ptr(),
         sample_u.data_ptr(), tokens.data_ptr(),
         tokens.stride(0) if B > 1 else max_drafts + 1, accepted.data_ptr(),
-        workspace.data_ptr(), size, _stream(dev)),
-        "sgmv_verify_drafts")
+        workspace.data_ptr(), size, _raw_stream(dev))
+    if st != SGMV_OK:
+        _check(st, "sgmv_verify_drafts")
     return tokens, accepted
