@@ -33,15 +33,19 @@ __device__ __forceinline__ uint32_t places_below(int n) {
   return (t & 0xf00fu) | (t & 0x00f0u) << 4 | (t & 0x0f00u) >> 4;
 }
 
+// Bit 15 of each bf16 of a word that is not finite: its exponent is all ones, so that one more carries.
+__device__ __forceinline__ uint32_t nonfinite_flags(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+// Both bytes of each half whose bit 15 is set.
+__device__ __forceinline__ uint32_t flag_mask(uint32_t f) { return (f - (f >> 15)) | f; }
+
 // bf16 or fp32 elements only: 8-bit codes are finite.
 template <int BYTES>
 __device__ __forceinline__ bool has_nonfinite(u32x4_t w) {
+  if constexpr (BYTES == 2)
+    return (nonfinite_flags(w.x) | nonfinite_flags(w.y) | nonfinite_flags(w.z) | nonfinite_flags(w.w)) != 0u;
   bool any = false;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    any |= (w[i] & 0x7f800000u) == 0x7f800000u;
-    if constexpr (BYTES == 2) any |= (w[i] & 0x7f80u) == 0x7f80u;
-  }
+  for (int i = 0; i < 4; ++i) any |= (w[i] & 0x7f800000u) == 0x7f800000u;
   return any;
 }
 
@@ -49,13 +53,8 @@ template <int BYTES>
 __device__ __forceinline__ u32x4_t drop_nonfinite(u32x4_t w) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t high = (w[i] & 0x7f800000u) == 0x7f800000u;
-    if constexpr (BYTES == 2) {
-      if ((w[i] & 0x7f80u) == 0x7f80u) w[i] &= 0xffff0000u;
-      if (high) w[i] &= 0x0000ffffu;
-    } else {
-      if (high) w[i] = 0u;
-    }
+    if constexpr (BYTES == 2) w[i] &= ~flag_mask(nonfinite_flags(w[i]));
+    else if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] = 0u;
   }
   return w;
 }

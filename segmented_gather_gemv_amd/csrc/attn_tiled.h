@@ -2,12 +2,18 @@
 // as bf16 and shared by the workgroup's waves.
 //
 // A workgroup takes WAVES * 32 rows (new token, query head of the group) of one (sequence, key/value
-// head); each wave keeps 32 rows' queries and outputs in registers. Per 64 tokens: the next 64 are
-// loaded into registers, S^T = K Q^T, the softmax step and O^T += V^T P^T run from LDS, then the
-// loaded ones are converted (8-bit formats: once here instead of once per wave) and written to the other
-// LDS buffer: one barrier per 64 tokens. Scores and probabilities stay in registers as in
-// attn_direct.h. LDS holds the operands in the order the products read them: K as stored, V with its 16-byte
-// halves of 8 tokens exchanged in every second 8 values of d, so that 16 lanes read 16 different bank groups.
+// head); each wave keeps 32 rows' queries and outputs in registers. Per tile of 64 tokens a wave has a
+// phase of matrix products (O^T += V^T P^T of the tile before, S^T = K Q^T of this one) and one of the
+// rest (softmax step; loaded pieces of the next tile converted and written to LDS; loads of the one
+// after issued). Scores and probabilities stay in registers as in attn_direct.h. Eight waves are two
+// per SIMD, in two groups half a tile apart: a barrier ends each phase, so that one wave of a SIMD has the
+// matrix cores while the other one computes exponentials. LDS holds the operands in the order the
+// products read them: K as stored, V with its 16-byte halves of 8 tokens exchanged in every second 8
+// values of d, so that 16 lanes read 16 different bank groups.
+//
+// Phase 2 i: group 0 multiplies by K(i) and V(i - 1), group 1 (in its tile i - 1) stages its share of K(i
+// + 1) and V(i); phase 2 i + 1: the other way round. K(i + 1) takes the buffer of K(i - 1), last read in
+// phase 2 i - 1, and V(i) that of V(i - 2), so two buffers of each are enough.
 #pragma once
 
 #include "attn_operand.h"
@@ -15,6 +21,22 @@
 namespace sgmv {
 
 constexpr int TL_TOKENS = 64;
+
+// All bits set where bit `at` of w is.
+__device__ __forceinline__ uint32_t bit_mask(uint32_t w, int at) { return (uint32_t)((int32_t)(w << (31 - at)) >> 31); }
+
+// Schedule of N products whose left operands come from LDS: four loads ahead.
+template <int N>
+__device__ __forceinline__ void read_ahead() {
+  constexpr int MFMA = 0x008, DS_READ = 0x100;
+  __builtin_amdgcn_sched_group_barrier(DS_READ, 4, 0);
+#pragma unroll
+  for (int i = 0; i < N / 2 - 2; ++i) {
+    __builtin_amdgcn_sched_group_barrier(MFMA, 2, 0);
+    __builtin_amdgcn_sched_group_barrier(DS_READ, 2, 0);
+  }
+  __builtin_amdgcn_sched_group_barrier(MFMA, 4, 0);
+}
 
 template <int FMT, int D>
 __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnArgs A) {
@@ -75,85 +97,85 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
   }
   const int first = s.kv_len - s.q_len;
   const int pos = first + tok;
-  const bool any = row0 < rows;
   const int lo_pos = first + min(row0, rows - 1) / A.G;
   const int hi_pos = first + (min(row0 + AT_ROWS, rows) - 1) / A.G;
+  const int tile_lo = first + tile0 / A.G;  // of the whole workgroup
+  const int tile_hi = first + (min(tile0 + ROWS, rows) - 1) / A.G;
   const int ps = 1 << K.lps;
   const int32_t* table = K.table + (int64_t)b * K.ldp;
+
+  const int n_tiles = max((t_end - t_begin + TL_TOKENS - 1) / TL_TOKENS, 0);
 
   f32x16_t o[NB];
 #pragma unroll
   for (int i = 0; i < NB; ++i) o[i] = f32x16_t{};
   float m = -INFINITY, l = 0.f;
 
-  // pages of the groups of the next 16 tiles, one per lane
-  int pages = -1;
-  uint64_t have = 0;
+  // pages of the groups of 16 tiles, one per lane, and of the next 16; which exist (also of the 16 before)
   auto load_pages = [&](int i0) {
     const int t = t_begin + TL_TOKENS * i0 + 16 * lane;
-    pages = t < t_end ? kv_page(K, table, t) : -1;
+    return t < t_end ? kv_page(K, table, t) : -1;
   };
+  int pages = load_pages(0), pages_next = load_pages(16), block = 0;
+  uint64_t have = __ballot(pages >= 0), have_before = 0;
+  auto groups_of = [&](int i) { return (uint32_t)((i >> 4 == block ? have : have_before) >> ((4 * i) & 63)) & 15u; };
 
-  // the pieces that this thread stages: pieces of one group belong to whole waves
+  // The pieces that this thread stages: pieces of one group belong to whole waves. They are in
+  // registers for K of a tile and V of the tile before.
   u32x4_t rk[NP], rv[NP];
+  int page_k[NP] = {}, page_v[NP];  // their pages
   float rs = 0.f;
-  auto load_tile = [&](int i) {
+  (void)rs;
+  auto load_tile = [&](int i) {  // K of tile i, V of tile i - 1
     const int t0 = t_begin + TL_TOKENS * i;
+    if ((i & 15) == 0 && i > 0) {
+      pages = pages_next;
+      pages_next = load_pages(i + 16);
+      have_before = have;
+      have = __ballot(pages >= 0);
+      block = i >> 4;
+    }
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
       const int at = n * THREADS + wv * WAVE;
       const int g = at / PIECES;
       if (4 * PIECES % THREADS == 0 || g < 4) {
-        const int p = max(__builtin_amdgcn_readlane(pages, (4 * i + g) & 63), 0);
-        const int64_t block = (((int64_t)p * K.H + kvh) * ps + ((t0 + 16 * g) & (ps - 1))) * D * BYTES;
         const int off = (at % PIECES + lane) * 16;
         int voff = off;
         if constexpr (!SCALED) {  // the exchange of halves
           const int slot16 = at % PIECES + lane, d = slot16 >> 1;
           voff = d * 32 + ((slot16 ^ (d >> 3)) & 1) * 16;
         }
-        rk[n] = load_u32x4(static_cast<const char*>(K.k) + block + off);
-        rv[n] = load_u32x4(static_cast<const char*>(K.v) + block + voff);
+        page_v[n] = page_k[n];
+        page_k[n] = max(__builtin_amdgcn_readlane(pages, (4 * i + g) & 63), 0);
+        const auto bytes_at = [&](int p, int t) { return (((int64_t)p * K.H + kvh) * ps + (t & (ps - 1))) * D * BYTES; };
+        if (i < n_tiles) rk[n] = load_u32x4(static_cast<const char*>(K.k) + bytes_at(page_k[n], t0 + 16 * g) + off);
+        if (i > 0)
+          rv[n] = load_u32x4(static_cast<const char*>(K.v) + bytes_at(page_v[n], t0 - TL_TOKENS + 16 * g) + voff);
       }
     }
     if constexpr (SCALED) {
-      if (wv < 2) {  // wave 0 the K scales, wave 1 the V scales
+      if (wv < 2) {  // wave 0 the K scales, wave 1 the V scales of the tile of K
         const int p = max(__shfl(pages, (4 * i + (lane >> 4)) & 63), 0);
         const int64_t at = ((int64_t)p * K.H + kvh) * ps + ((t0 + lane) & (ps - 1));
-        rs = (wv ? K.v_scale : K.k_scale)[at];
+        rs = (wv ? K.v_scale : K.k_scale)[at] * (wv ? 1.f : A.scale_log2);
       }
     }
   };
-  // `i`: the tile that load_tile has loaded. V of tokens that are not there becomes 0, so that their
-  // probability 0 counts as such; a V value that is not finite is noted.
-  auto store_tile = [&](int buf, int i) {
-    const int t0 = t_begin + TL_TOKENS * i;
-    const uint32_t groups = (uint32_t)(have >> ((4 * i) & 63)) & 15u;
-    const bool whole = groups == 15u && t0 + TL_TOKENS <= s.kv_len;
+  auto store_k = [&](int i) {
+    const int buf = i & 1;
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
       const int at = n * THREADS + wv * WAVE;
-      const int g = at / PIECES;
+      const int g = at / PIECES, piece = at % PIECES + lane;
       if (4 * PIECES % THREADS == 0 || g < 4) {
-        const int piece = at % PIECES + lane;
-        const int there = groups >> g & 1 ? min(max(s.kv_len - t0 - 16 * g, 0), 16) : 0;  // tokens
         if constexpr (!SCALED) {
-          u32x4_t v = rv[n];
-          if (!whole) v = keep_elements<2>(v, places_below(there) >> (8 * ((piece ^ (piece >> 4)) & 1)));
-          if (has_nonfinite<2>(v)) s_odd[buf] = i;
           *reinterpret_cast<u32x4_t*>(&s_k[buf][g * GROUP + piece * 8]) = rk[n];
-          *reinterpret_cast<u32x4_t*>(&s_v[buf][g * GROUP + piece * 8]) = v;
         } else {
-          if (!whole) rv[n] = keep_elements<1>(rv[n], places_below(there));
-          // K piece: token piece % 16, values 16 (piece / 16) .. + 15: two octets of d
+          // piece: token piece % 16, values 16 (piece / 16) .. + 15: two octets of d
           uint16_t* k = &s_k[buf][g * GROUP + (piece >> 4) * 256 + (piece & 15) * 8];
           *reinterpret_cast<u32x4_t*>(k) = codes8_bf16<FMT>(u32x2_t{rk[n].x, rk[n].y});
           *reinterpret_cast<u32x4_t*>(k + 128) = codes8_bf16<FMT>(u32x2_t{rk[n].z, rk[n].w});
-          // V piece: both halves of d = piece
-          uint16_t* v = &s_v[buf][g * GROUP + piece * 16];
-          const int x = (piece >> 3) & 1;
-          *reinterpret_cast<u32x4_t*>(v + 8 * x) = codes8_bf16<FMT>(u32x2_t{rv[n].x, rv[n].y});
-          *reinterpret_cast<u32x4_t*>(v + 8 * (1 - x)) = codes8_bf16<FMT>(u32x2_t{rv[n].z, rv[n].w});
         }
       }
     }
@@ -161,130 +183,212 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
       if (wv < 2) (wv ? s_vs : s_ks)[buf][lane] = rs;
     }
   };
-
-  const int n_tiles = max((t_end - t_begin + TL_TOKENS - 1) / TL_TOKENS, 0);
-  if (tid < 2) s_odd[tid] = -1;
-  __syncthreads();
-  if (n_tiles > 0) {
-    load_pages(0);
-    have = __ballot(pages >= 0);
-    load_tile(0);
-    store_tile(0, 0);
-  }
-  __syncthreads();
-  for (int i = 0; i < n_tiles; ++i) {
-    const int buf = i & 1, t0 = t_begin + TL_TOKENS * i;
-    const uint32_t groups = (uint32_t)(have >> ((4 * i) & 63)) & 15u;
-    if (i + 1 < n_tiles) {
-      if (((i + 1) & 15) == 0) {
-        load_pages(i + 1);
-        have = __ballot(pages >= 0);
+  // V of tokens that are not there becomes 0, so that their probability 0 counts as such. Where some rows
+  // of the workgroup see only part of the tile, so do values that are not finite, for 0 * inf would spoil
+  // the rows that do not see them, and the tile is marked for restore().
+  auto store_v = [&](int i) {
+    const int t0 = t_begin + TL_TOKENS * i, buf = i & 1;
+    const uint32_t groups = groups_of(i);
+    const bool whole = groups == 15u && t0 + TL_TOKENS <= s.kv_len;
+    const bool some = !whole || t0 + TL_TOKENS - 1 > tile_lo || (A.window && t0 <= tile_hi - A.window);
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+      const int at = n * THREADS + wv * WAVE;
+      const int g = at / PIECES, piece = at % PIECES + lane;
+      if (4 * PIECES % THREADS == 0 || g < 4) {
+        const int there = groups >> g & 1 ? min(max(s.kv_len - t0 - 16 * g, 0), 16) : 0;  // tokens
+        if constexpr (!SCALED) {
+          if (!whole) rv[n] = keep_elements<2>(rv[n], places_below(there) >> (8 * ((piece ^ (piece >> 4)) & 1)));
+          if (some && has_nonfinite<2>(rv[n])) {
+            s_odd[buf] = i;
+            rv[n] = drop_nonfinite<2>(rv[n]);
+          }
+          *reinterpret_cast<u32x4_t*>(&s_v[buf][g * GROUP + piece * 8]) = rv[n];
+        } else {
+          if (!whole) rv[n] = keep_elements<1>(rv[n], places_below(there));
+          // both halves of d = piece
+          uint16_t* v = &s_v[buf][g * GROUP + piece * 16];
+          const int x = (piece >> 3) & 1;
+          *reinterpret_cast<u32x4_t*>(v + 8 * x) = codes8_bf16<FMT>(u32x2_t{rv[n].x, rv[n].y});
+          *reinterpret_cast<u32x4_t*>(v + 8 * (1 - x)) = codes8_bf16<FMT>(u32x2_t{rv[n].z, rv[n].w});
+        }
       }
-      load_tile(i + 1);
     }
-    if (any && hi_pos >= t0 && !(A.window && t0 + TL_TOKENS - 1 <= lo_pos - A.window)) {
-      f32x16_t sc[2] = {};
-      const uint16_t* kb = &s_k[buf][(lane >> 4 & 1) * GROUP + half * 128 + (lane & 15) * 8];
+  };
+
+  // whether some of this wave's rows see only part of a tile
+  auto partly = [&](int i) {
+    const int t0 = t_begin + TL_TOKENS * i;
+    return t0 + TL_TOKENS - 1 > lo_pos || (A.window && t0 <= hi_pos - A.window) || groups_of(i) != 15u;
+  };
+
+  // tokens of tile i that this lane's row sees: bit reg_token(j, 0) of mask[u] for register j of product u
+  auto visible = [&](int i, uint32_t (&mask)[2]) {
+    const int t0 = t_begin + TL_TOKENS * i, n = pos - t0 + 1;
+    const uint32_t groups = groups_of(i);
+    uint64_t seen = n >= 64 ? ~0ull : n <= 0 ? 0ull : (1ull << n) - 1ull;
+    if (A.window) {
+      const int gone = n - A.window;
+      seen &= gone >= 64 ? 0ull : gone <= 0 ? ~0ull : ~((1ull << gone) - 1ull);
+    }
+    uint64_t there = 0;
 #pragma unroll
-      for (int c = 0; c < NK; ++c)
+    for (int g = 0; g < 4; ++g) there |= (groups >> g & 1 ? 0xffffull : 0ull) << (16 * g);
+    seen = (seen & there) >> (4 * half);
+    mask[0] = (uint32_t)seen;
+    mask[1] = (uint32_t)(seen >> 32);
+  };
+
+  f32x16_t sc[2];
+  u32x4_t pb[4];  // probabilities, per group
+  // O^T += V^T P^T of tile i
+  auto values = [&](int i) {
+    const int buf = i & 1;
+    // V operand of block n and group g: d = 32 n + col, this half's 8 tokens
+    const uint16_t* vb = &s_v[buf][col * 16 + ((half ^ (col >> 3)) & 1) * 8];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          sc[u] = mfma_32x32_bf16(load_u32x4(kb + u * 2 * GROUP + c * 256), q[c], sc[u]);
-      if constexpr (SCALED) {
+    for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+      for (int n = 0; n < NB; ++n)
+        o[n] = mfma_32x32_bf16(load_u32x4(vb + g * GROUP + n * 512), pb[g], o[n]);
+    read_ahead<4 * NB>();
+  };
+  // What store_v has left out of tile i, added to the rows that see it, token by token. (8-bit codes are
+  // finite; their scales meet only probabilities that are not 0.)
+  auto restore = [&](int i) {
+#pragma unroll 1
+    for (int t = t_begin + TL_TOKENS * i, end = min(t + TL_TOKENS, s.kv_len); t < end; ++t) {
+      const int p = kv_page(K, table, t);
+      if (p < 0) continue;
+      const bool seen = t <= pos && !(A.window && t <= pos - A.window);
+      const int place = 8 * ((t >> 2) & 1) + 4 * ((t >> 3) & 1) + (t & 3);
+      const uint16_t* v = static_cast<const uint16_t*>(K.v) +
+                          (((int64_t)p * K.H + kvh) * ps + (t & (ps - 1) & ~15)) * D + place + 64 * half;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4_t f = *reinterpret_cast<const f32x4_t*>(&s_ks[buf][32 * u + 8 * j + 4 * half]);
+      for (int n = 0; n < NB; ++n) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[u][4 * j + e] *= f[e];
-          }
+        for (int j = 0; j < 16; ++j) {
+          const float f = bf16_bits_to_f32(v[(32 * n + reg_token(j, 0)) * 16]);
+          o[n][j] += seen && !(fabsf(f) < INFINITY) ? f : 0.f;
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const bool edge = t0 + TL_TOKENS - 1 > lo_pos || (A.window && t0 <= hi_pos - A.window) || groups != 15u;
-      if (edge) {  // a row's own position is below kv_len
+    }
+  };
+  // S^T = K Q^T of tile i
+  auto scores = [&](int i) {
+    const uint16_t* kb = &s_k[i & 1][(lane >> 4 & 1) * GROUP + half * 128 + (lane & 15) * 8];
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u) sc[u] = f32x16_t{};
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int t = t0 + 32 * u + reg_token(j, half);
-            if (!(groups >> (2 * u + (j >> 3)) & 1) || t > pos || (A.window && t <= pos - A.window))
-              sc[u][j] = -INFINITY;
-          }
-      }
-      float top = sc[0][0];
+    for (int c = 0; c < NK; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        sc[u] = mfma_32x32_bf16(load_u32x4(kb + u * 2 * GROUP + c * 256), q[c], sc[u]);
+    read_ahead<2 * NK>();
+  };
+  auto softmax = [&](int i) {
+    const int t0 = t_begin + TL_TOKENS * i, buf = i & 1;
+    if constexpr (SCALED) {  // from here on in base 2
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) top = fmaxf(top, sc[u][j]);
-      top = half_max(top) * A.scale_log2;
-      if (__any(top > m + 8.f)) {
-        const float now = fmaxf(m, top);
-        const float f = m == now ? 1.f : exp2f(m - now);
-        m = now;
-        l *= f;
+        for (int j = 0; j < 4; ++j) {
+          const f32x4_t f = *reinterpret_cast<const f32x4_t*>(&s_ks[buf][32 * u + 8 * j + 4 * half]);
 #pragma unroll
-        for (int n = 0; n < NB; ++n)
+          for (int e = 0; e < 4; ++e) sc[u][4 * j + e] *= f[e];
+        }
+    }
+    const bool edge = partly(i);
+    if (edge) {  // a row's own position is below kv_len
+      uint32_t mask[2];
+      visible(i, mask);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[n][j] *= f;
-      }
-      const float base = m == -INFINITY ? 0.f : m;
-      u32x4_t pb[4];  // per group
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        float p[16];
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
-          p[j] = __builtin_amdgcn_exp2f(fmaf(sc[u][j], A.scale_log2, -base));
-          l += p[j];
+          const uint32_t on = bit_mask(mask[u], reg_token(j, 0));
+          sc[u][j] = __uint_as_float((__float_as_uint(sc[u][j]) & on) | (0xff800000u & ~on));
         }
-        if constexpr (SCALED) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const f32x4_t f = *reinterpret_cast<const f32x4_t*>(&s_vs[buf][32 * u + 8 * j + 4 * half]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              p[4 * j + e] = edge && p[4 * j + e] == 0.f ? 0.f : p[4 * j + e] * f[e];
-          }
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) pb[2 * u + g][j] = pack_bf16x2(p[8 * g + 2 * j], p[8 * g + 2 * j + 1]);
-      }
-      // V operand of block n and group g: d = 32 n + col, this half's 8 tokens
-      const uint16_t* vb = &s_v[buf][col * 16 + ((half ^ (col >> 3)) & 1) * 8];
-      if (SCALED || !edge || s_odd[buf] != i) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            o[n] = mfma_32x32_bf16(load_u32x4(vb + g * GROUP + n * 512), pb[g], o[n]);
-      } else {  // see attn_direct.h
-#pragma unroll
-        for (int n = 0; n < NB; ++n)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const u32x4_t v = drop_nonfinite<2>(load_u32x4(vb + g * GROUP + n * 512));
-            o[n] = mfma_32x32_bf16(v, pb[g], o[n]);
-            __builtin_amdgcn_sched_barrier(0);
-          }
-#pragma unroll 1
-        for (int x = 0; x < TL_TOKENS; ++x) {
-          const int t = t0 + x, place = 8 * ((x >> 2) & 1) + 4 * ((x >> 3) & 1) + (x & 3);
-          if (!(groups >> (x >> 4) & 1) || t > pos || (A.window && t <= pos - A.window)) continue;
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int d = 32 * n + reg_token(j, half);
-              const float f = bf16_bits_to_f32(s_v[buf][(x >> 4) * GROUP + d * 16 + (place ^ (d & 8))]);
-              if (!(fabsf(f) < INFINITY)) o[n][j] += f;
-            }
-        }
-      }
     }
-    if (i + 1 < n_tiles) store_tile(buf ^ 1, i + 1);
-    __syncthreads();
+    float top = sc[0][0];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, sc[u][j]);
+    if constexpr (!SCALED) top *= A.scale_log2;
+    // a stale maximum is as good as long as nothing grows past 2^8
+    if (__any(top > m + 8.f)) {
+      const float now = fmaxf(m, half_max(top));
+      const float f = m == now ? 1.f : exp2f(m - now);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[n][j] *= f;
+    }
+    const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float p[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        p[j] = __builtin_amdgcn_exp2f(SCALED ? sc[u][j] - base : fmaf(sc[u][j], A.scale_log2, -base));
+        l += p[j];
+      }
+      if constexpr (SCALED) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const f32x4_t f = *reinterpret_cast<const f32x4_t*>(&s_vs[buf][32 * u + 8 * j + 4 * half]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            p[4 * j + e] *= f[e];
+            if (edge && sc[u][4 * j + e] == -INFINITY) p[4 * j + e] = 0.f;
+          }
+        }
+      }
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pb[2 * u + g][j] = pack_bf16x2(p[8 * g + 2 * j], p[8 * g + 2 * j + 1]);
+    }
+  };
+
+  const int group = WAVES == 8 ? wv >> 2 : 0;
+  // after softmax step i: K of tile i + 1 + group, V of the tile before that
+  auto stage = [&](int i) {
+    const int j = i + 1 + group;
+    if (j < n_tiles) store_k(j);
+    if (j > 0 && j - 1 < n_tiles) store_v(j - 1);
+    if (j + 1 <= n_tiles) load_tile(j + 1);
+  };
+  if (tid < 2) s_odd[tid] = -1;
+  if (n_tiles > 0) {
+    load_tile(0);
+    store_k(0);
+    load_tile(1);
+  }
+  __syncthreads();
+  if (n_tiles > 0) {
+    if (group) {
+      stage(-1);
+      __syncthreads();
+    }
+    scores(0);
+    for (int i = 0; i < n_tiles; ++i) {
+      __builtin_amdgcn_s_setprio(0);
+      __syncthreads();
+      softmax(i);
+      stage(i);
+      __syncthreads();
+      __builtin_amdgcn_s_setprio(1);
+      values(i);
+      if (!SCALED && __builtin_amdgcn_readfirstlane(s_odd[i & 1]) == i) restore(i);
+      scores(i + 1);  // of the last tile again after it, unused
+    }
+    __builtin_amdgcn_s_setprio(0);
+    if (WAVES == 8 && !group) __syncthreads();  // as many barriers as the other group
   }
   if (!row_ok) return;
 
