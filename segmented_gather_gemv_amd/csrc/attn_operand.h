@@ -33,6 +33,16 @@ __device__ __forceinline__ uint32_t places_below(int n) {
   return (t & 0xf00fu) | (t & 0x00f0u) << 4 | (t & 0x0f00u) >> 4;
 }
 
+// Eight codes with those that are not finite (e4m3: 0x7f and 0xff) replaced by finite ones.
+template <int FMT>
+__device__ __forceinline__ u32x2_t finite_codes(u32x2_t w) {
+  if constexpr (FMT == SGMV_KV_E4M3) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) w[i] &= ~((((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7);
+  }
+  return w;
+}
+
 // Bit 15 of each bf16 of a word that is not finite: its exponent is all ones, so that one more carries.
 __device__ __forceinline__ uint32_t nonfinite_flags(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
 // Both bytes of each half whose bit 15 is set.

@@ -3,17 +3,18 @@
 //
 // A workgroup takes WAVES * 32 rows (new token, query head of the group) of one (sequence, key/value
 // head); each wave keeps 32 rows' queries and outputs in registers. Per tile of 64 tokens a wave has a
-// phase of matrix products (O^T += V^T P^T of the tile before, S^T = K Q^T of this one) and one of the
-// rest (softmax step; loaded pieces of the next tile converted and written to LDS; loads of the one
-// after issued). Scores and probabilities stay in registers as in attn_direct.h. Eight waves are two
-// per SIMD, in two groups half a tile apart: a barrier ends each phase, so that one wave of a SIMD has the
-// matrix cores while the other one computes exponentials. LDS holds the operands in the order the
-// products read them: K as stored, V with its 16-byte halves of 8 tokens exchanged in every second 8
-// values of d, so that 16 lanes read 16 different bank groups.
+// phase of matrix products (O^T += V^T P^T of this tile, S^T = K Q^T of the next; between them the pieces
+// that it loaded are converted and written to LDS, and the next ones' loads issued) and one of the softmax
+// step. Scores and probabilities stay in registers as in attn_direct.h. Eight waves are two per SIMD, in
+// two groups half a tile apart: a barrier ends each phase, so that one wave of a SIMD has the matrix cores
+// while the other one computes exponentials. LDS holds the operands in the order the products read them: K
+// as stored, V with its 16-byte halves of 8 tokens exchanged in every second 8 values of d, so that 16
+// lanes read 16 different bank groups.
 //
-// Phase 2 i: group 0 multiplies by K(i) and V(i - 1), group 1 (in its tile i - 1) stages its share of K(i
-// + 1) and V(i); phase 2 i + 1: the other way round. K(i + 1) takes the buffer of K(i - 1), last read in
-// phase 2 i - 1, and V(i) that of V(i - 2), so two buffers of each are enough.
+// Group 0 multiplies by V(i) and K(i + 1) in phase 2 i + 2, group 1 in phase 2 i + 3, and both then write
+// their shares of K(i + 2) and V(i + 1): over K(i) and V(i - 1), last read in phase 2 i + 1, and in time for
+// phase 2 i + 4, so two buffers of each are enough. The scales of tile i are read in phases 2 i + 1 and 2 i + 2
+// of it; group 1 writes them.
 #pragma once
 
 #include "attn_operand.h"
@@ -44,11 +45,12 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
   constexpr int BYTES = KvFormat<FMT>::bytes;
   constexpr bool SCALED = KvFormat<FMT>::scaled;
   constexpr int NK = D / 16, NB = D / 32;
+  constexpr int SCALE_WAVE = WAVES == 8 ? 4 : 0;  // the first of two waves that stage scales
   constexpr int GROUP = D * 16;                         // elements of a group
   constexpr int PIECES = GROUP * BYTES / 16;            // 16-byte pieces of a group as stored
   constexpr int NP = (4 * PIECES + THREADS - 1) / THREADS;
   __shared__ __align__(16) uint16_t s_k[2][4 * GROUP], s_v[2][4 * GROUP];
-  __shared__ int s_odd[2];  // the last tile in each buffer with a V value that is not finite
+  __shared__ int s_odd[4];  // [i % 4] = i: something that is not finite was left out of tile i
   __shared__ __align__(16) float s_ks[2][SCALED ? TL_TOKENS : 4], s_vs[2][SCALED ? TL_TOKENS : 4];
 
   const KvArgs& K = A.kv;
@@ -121,9 +123,10 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
   auto groups_of = [&](int i) { return (uint32_t)((i >> 4 == block ? have : have_before) >> ((4 * i) & 63)) & 15u; };
 
   // The pieces that this thread stages: pieces of one group belong to whole waves. They are in
-  // registers for K of a tile and V of the tile before.
+  // registers for K of a tile and V of the tile before. (Past the last tile, of page 0, unused.)
   u32x4_t rk[NP], rv[NP];
-  int page_k[NP] = {}, page_v[NP];  // their pages
+  int64_t at_k[NP] = {}, at_v[NP];  // bytes before the groups that they are from
+  const int64_t page_bytes = (int64_t)K.H * ps * D * BYTES, head_bytes = (int64_t)kvh * ps * D * BYTES;
   float rs = 0.f;
   (void)rs;
   auto load_tile = [&](int i) {  // K of tile i, V of tile i - 1
@@ -146,21 +149,25 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
           const int slot16 = at % PIECES + lane, d = slot16 >> 1;
           voff = d * 32 + ((slot16 ^ (d >> 3)) & 1) * 16;
         }
-        page_v[n] = page_k[n];
-        page_k[n] = max(__builtin_amdgcn_readlane(pages, (4 * i + g) & 63), 0);
-        const auto bytes_at = [&](int p, int t) { return (((int64_t)p * K.H + kvh) * ps + (t & (ps - 1))) * D * BYTES; };
-        if (i < n_tiles) rk[n] = load_u32x4(static_cast<const char*>(K.k) + bytes_at(page_k[n], t0 + 16 * g) + off);
-        if (i > 0)
-          rv[n] = load_u32x4(static_cast<const char*>(K.v) + bytes_at(page_v[n], t0 - TL_TOKENS + 16 * g) + voff);
+        at_v[n] = at_k[n];
+        at_k[n] = max(__builtin_amdgcn_readlane(pages, (4 * i + g) & 63), 0) * page_bytes + head_bytes +
+                  ((t0 + 16 * g) & (ps - 1)) * (D * BYTES);
+        rk[n] = load_u32x4(static_cast<const char*>(K.k) + at_k[n] + off);
+        rv[n] = load_u32x4(static_cast<const char*>(K.v) + at_v[n] + voff);
       }
     }
     if constexpr (SCALED) {
-      if (wv < 2) {  // wave 0 the K scales, wave 1 the V scales of the tile of K
+      if (wv >> 1 == SCALE_WAVE >> 1) {  // one wave the K scales, one the V scales of the tile of K
         const int p = max(__shfl(pages, (4 * i + (lane >> 4)) & 63), 0);
         const int64_t at = ((int64_t)p * K.H + kvh) * ps + ((t0 + lane) & (ps - 1));
-        rs = (wv ? K.v_scale : K.k_scale)[at] * (wv ? 1.f : A.scale_log2);
+        rs = (wv & 1 ? K.v_scale : K.k_scale)[at];
       }
     }
+  };
+  // whether some row of the workgroup sees only part of a tile
+  auto some_see_part = [&](int i) {
+    const int t0 = t_begin + TL_TOKENS * i;
+    return t0 + TL_TOKENS - 1 > tile_lo || (A.window && t0 <= tile_hi - A.window) || groups_of(i) != 15u;
   };
   auto store_k = [&](int i) {
     const int buf = i & 1;
@@ -179,38 +186,47 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
         }
       }
     }
+  };
+  // A V scale that is not finite is left out as such a V value is (store_v).
+  auto store_scales = [&](int i) {
     if constexpr (SCALED) {
-      if (wv < 2) (wv ? s_vs : s_ks)[buf][lane] = rs;
+      if (wv >> 1 == SCALE_WAVE >> 1) {
+        if (wv & 1) {
+          if (!(fabsf(rs) < INFINITY)) {
+            s_odd[i & 3] = i;
+            rs = 0.f;
+          }
+        } else {
+          rs *= A.scale_log2;
+        }
+        (wv & 1 ? s_vs : s_ks)[i & 1][lane] = rs;
+      }
     }
   };
-  // V of tokens that are not there becomes 0, so that their probability 0 counts as such. Where some rows
-  // of the workgroup see only part of the tile, so do values that are not finite, for 0 * inf would spoil
-  // the rows that do not see them, and the tile is marked for restore().
+  // V of tokens that are not there has to be finite, so that their probability 0 counts as such: bytes that
+  // no code uses become ones that are. Where some rows of the workgroup see only part of the tile, bf16
+  // values that are not finite are left out, for 0 * inf would spoil the rows that do not see them, and
+  // the tile is marked for restore().
   auto store_v = [&](int i) {
-    const int t0 = t_begin + TL_TOKENS * i, buf = i & 1;
-    const uint32_t groups = groups_of(i);
-    const bool whole = groups == 15u && t0 + TL_TOKENS <= s.kv_len;
-    const bool some = !whole || t0 + TL_TOKENS - 1 > tile_lo || (A.window && t0 <= tile_hi - A.window);
+    const int buf = i & 1;
+    const bool some = !SCALED && some_see_part(i);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
       const int at = n * THREADS + wv * WAVE;
       const int g = at / PIECES, piece = at % PIECES + lane;
       if (4 * PIECES % THREADS == 0 || g < 4) {
-        const int there = groups >> g & 1 ? min(max(s.kv_len - t0 - 16 * g, 0), 16) : 0;  // tokens
         if constexpr (!SCALED) {
-          if (!whole) rv[n] = keep_elements<2>(rv[n], places_below(there) >> (8 * ((piece ^ (piece >> 4)) & 1)));
           if (some && has_nonfinite<2>(rv[n])) {
-            s_odd[buf] = i;
+            s_odd[i & 3] = i;
             rv[n] = drop_nonfinite<2>(rv[n]);
           }
           *reinterpret_cast<u32x4_t*>(&s_v[buf][g * GROUP + piece * 8]) = rv[n];
         } else {
-          if (!whole) rv[n] = keep_elements<1>(rv[n], places_below(there));
           // both halves of d = piece
           uint16_t* v = &s_v[buf][g * GROUP + piece * 16];
           const int x = (piece >> 3) & 1;
-          *reinterpret_cast<u32x4_t*>(v + 8 * x) = codes8_bf16<FMT>(u32x2_t{rv[n].x, rv[n].y});
-          *reinterpret_cast<u32x4_t*>(v + 8 * (1 - x)) = codes8_bf16<FMT>(u32x2_t{rv[n].z, rv[n].w});
+          *reinterpret_cast<u32x4_t*>(v + 8 * x) = codes8_bf16<FMT>(finite_codes<FMT>(u32x2_t{rv[n].x, rv[n].y}));
+          *reinterpret_cast<u32x4_t*>(v + 8 * (1 - x)) = codes8_bf16<FMT>(finite_codes<FMT>(u32x2_t{rv[n].z, rv[n].w}));
         }
       }
     }
@@ -253,14 +269,22 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
         o[n] = mfma_32x32_bf16(load_u32x4(vb + g * GROUP + n * 512), pb[g], o[n]);
     read_ahead<4 * NB>();
   };
-  // What store_v has left out of tile i, added to the rows that see it, token by token. (8-bit codes are
-  // finite; their scales meet only probabilities that are not 0.)
+  // What store_v (8-bit codes are finite: store_k, of the scales) has left out of tile i, added to the rows
+  // that see it, token by token.
   auto restore = [&](int i) {
 #pragma unroll 1
     for (int t = t_begin + TL_TOKENS * i, end = min(t + TL_TOKENS, s.kv_len); t < end; ++t) {
       const int p = kv_page(K, table, t);
       if (p < 0) continue;
       const bool seen = t <= pos && !(A.window && t <= pos - A.window);
+      if constexpr (SCALED) {
+        const float f = K.v_scale[((int64_t)p * K.H + kvh) * ps + (t & (ps - 1))];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[n][j] += seen && !(fabsf(f) < INFINITY) ? NAN : 0.f;
+        continue;
+      }
       const int place = 8 * ((t >> 2) & 1) + 4 * ((t >> 3) & 1) + (t & 3);
       const uint16_t* v = static_cast<const uint16_t*>(K.v) +
                           (((int64_t)p * K.H + kvh) * ps + (t & (ps - 1) & ~15)) * D + place + 64 * half;
@@ -288,19 +312,19 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
     read_ahead<2 * NK>();
   };
   auto softmax = [&](int i) {
-    const int t0 = t_begin + TL_TOKENS * i, buf = i & 1;
-    if constexpr (SCALED) {  // from here on in base 2
+    const int buf = i & 1;
+    // exponents with the old maximum: wherever they stay below 8, it is as good as the new one
+    float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const f32x4_t f = *reinterpret_cast<const f32x4_t*>(&s_ks[buf][32 * u + 8 * j + 4 * half]);
+      for (int j = 0; j < 4; ++j) {
+        f32x4_t f = {A.scale_log2, A.scale_log2, A.scale_log2, A.scale_log2};
+        if constexpr (SCALED) f = *reinterpret_cast<const f32x4_t*>(&s_ks[buf][32 * u + 8 * j + 4 * half]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[u][4 * j + e] *= f[e];
-        }
-    }
-    const bool edge = partly(i);
-    if (edge) {  // a row's own position is below kv_len
+        for (int e = 0; e < 4; ++e) sc[u][4 * j + e] = fmaf(sc[u][4 * j + e], f[e], -base);
+      }
+    if (partly(i)) {  // a row's own position is below kv_len
       uint32_t mask[2];
       visible(i, mask);
 #pragma unroll
@@ -316,25 +340,27 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
     for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int j = 0; j < 16; ++j) top = fmaxf(top, sc[u][j]);
-    if constexpr (!SCALED) top *= A.scale_log2;
-    // a stale maximum is as good as long as nothing grows past 2^8
-    if (__any(top > m + 8.f)) {
-      const float now = fmaxf(m, half_max(top));
-      const float f = m == now ? 1.f : exp2f(m - now);
+    if (__any(top > (m == -INFINITY ? -INFINITY : 8.f))) {
+      const float up = half_max(top), now = fmaxf(m, base + up);
+      const float f = m == now ? 1.f : exp2f(m - now);  // 0 from -inf on
+      const float step = now == -INFINITY ? 0.f : now - base;
       m = now;
       l *= f;
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[n][j] *= f;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sc[u][j] -= step;
     }
-    const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       float p[16];
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        p[j] = __builtin_amdgcn_exp2f(SCALED ? sc[u][j] - base : fmaf(sc[u][j], A.scale_log2, -base));
+        p[j] = __builtin_amdgcn_exp2f(sc[u][j]);
         l += p[j];
       }
       if constexpr (SCALED) {
@@ -342,10 +368,7 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
         for (int j = 0; j < 4; ++j) {
           const f32x4_t f = *reinterpret_cast<const f32x4_t*>(&s_vs[buf][32 * u + 8 * j + 4 * half]);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            p[4 * j + e] *= f[e];
-            if (edge && sc[u][4 * j + e] == -INFINITY) p[4 * j + e] = 0.f;
-          }
+          for (int e = 0; e < 4; ++e) p[4 * j + e] *= f[e];
         }
       }
 #pragma unroll
@@ -356,36 +379,36 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
   };
 
   const int group = WAVES == 8 ? wv >> 2 : 0;
-  // after softmax step i: K of tile i + 1 + group, V of the tile before that
-  auto stage = [&](int i) {
-    const int j = i + 1 + group;
-    if (j < n_tiles) store_k(j);
-    if (j > 0 && j - 1 < n_tiles) store_v(j - 1);
-    if (j + 1 <= n_tiles) load_tile(j + 1);
-  };
-  if (tid < 2) s_odd[tid] = -1;
+  if (tid < 4) s_odd[tid] = -1;
   if (n_tiles > 0) {
     load_tile(0);
+    __syncthreads();  // s_odd
     store_k(0);
+    store_scales(0);
     load_tile(1);
-  }
-  __syncthreads();
-  if (n_tiles > 0) {
-    if (group) {
-      stage(-1);
-      __syncthreads();
-    }
+    store_k(1);
+    store_scales(1);
+    store_v(0);
+    load_tile(2);
+    __syncthreads();
+    if (group) __syncthreads();
     scores(0);
     for (int i = 0; i < n_tiles; ++i) {
       __builtin_amdgcn_s_setprio(0);
       __syncthreads();
       softmax(i);
-      stage(i);
+      asm volatile("" : "+v"(l));
+#pragma unroll
+      for (int g = 0; g < 4; ++g) asm volatile("" : "+v"(pb[g]));
       __syncthreads();
       __builtin_amdgcn_s_setprio(1);
       values(i);
-      if (!SCALED && __builtin_amdgcn_readfirstlane(s_odd[i & 1]) == i) restore(i);
-      scores(i + 1);  // of the last tile again after it, unused
+      store_k(i + 2);
+      store_v(i + 1);
+      if (__builtin_amdgcn_readfirstlane(s_odd[i & 3]) == i) restore(i);
+      scores(i + 1);  // of the last tile: of what was there, unused
+      store_scales(i + 2);
+      load_tile(i + 3);
     }
     __builtin_amdgcn_s_setprio(0);
     if (WAVES == 8 && !group) __syncthreads();  // as many barriers as the other group
