@@ -396,6 +396,7 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
     for (int i = 0; i < n_tiles; ++i) {
       __builtin_amdgcn_s_setprio(0);
       __syncthreads();
+      if (i > 0 && __builtin_amdgcn_readfirstlane(s_odd[(i - 1) & 3]) == i - 1) restore(i - 1);
       softmax(i);
       asm volatile("" : "+v"(l));
 #pragma unroll
@@ -405,11 +406,11 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
       values(i);
       store_k(i + 2);
       store_v(i + 1);
-      if (__builtin_amdgcn_readfirstlane(s_odd[i & 3]) == i) restore(i);
       scores(i + 1);  // of the last tile: of what was there, unused
       store_scales(i + 2);
       load_tile(i + 3);
     }
+    if (__builtin_amdgcn_readfirstlane(s_odd[(n_tiles - 1) & 3]) == n_tiles - 1) restore(n_tiles - 1);
     __builtin_amdgcn_s_setprio(0);
     if (WAVES == 8 && !group) __syncthreads();  // as many barriers as the other group
   }
