@@ -31,6 +31,7 @@ struct AttnArgs {
   // split of a sequence's tokens over workgroups: `n_split` ranges of `chunk` tokens (a multiple
   // of the tile), the last one to the end
   int32_t chunk[2], n_split[2];  // [0] direct kernel, [1] tiled kernel
+  int32_t slots[2];    // tiles of rows that the grid has room for (0: none)
   float* part_o;       // [max n_split][T][Hq][D]
   float* part_ml;      // [max n_split][T][Hq][2]: maximum (of scores times log2(e)), sum
 };
@@ -45,6 +46,9 @@ constexpr bool direct_eight_waves(int D, bool f32) { return D <= 128 && !f32; }
 constexpr bool tiled_dim(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
 constexpr int tiled_waves(int D) { return D <= 128 ? 8 : 4; }
 constexpr int tiled_rows(int D) { return tiled_waves(D) * AT_ROWS; }
+
+// Rows of a sequence up to which a call with tiles of many rows takes it directly.
+constexpr int tiled_direct_rows(int D) { return direct_two_tiles(D, false) ? 32 : 16; }
 
 // Tokens that rows [row0, row0 + n) of a sequence look at: [begin, end), begin a multiple of 32.
 struct Span {

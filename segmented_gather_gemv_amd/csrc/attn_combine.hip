@@ -78,9 +78,9 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A, int kerne
 
 }  // namespace
 
-hipError_t launch_attn_combine(const AttnArgs& A, int kernel, unsigned slots, hipStream_t stream) {
+hipError_t launch_attn_combine(const AttnArgs& A, int kernel, hipStream_t stream) {
   const int tile = kernel ? tiled_rows(A.kv.D) : A.direct_tile;
-  const dim3 g(slots * (unsigned)(tile / JOIN_ROWS) * (unsigned)A.kv.H), b(JOIN_ROWS * WAVE);
+  const dim3 g((unsigned)A.slots[kernel] * (unsigned)(tile / JOIN_ROWS) * (unsigned)A.kv.H), b(JOIN_ROWS * WAVE);
   if (A.f32) attn_combine_kernel<true><<<g, b, 0, stream>>>(A, kernel);
   else attn_combine_kernel<false><<<g, b, 0, stream>>>(A, kernel);
   return hipGetLastError();

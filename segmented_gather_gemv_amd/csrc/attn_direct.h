@@ -94,9 +94,16 @@ constexpr int direct_occupancy(bool f32, int DP, int R) {
   return DP <= 128 ? 2 : 1;
 }
 
-// DP: head dimension, or (not EXACT) an upper bound of it
+// The waves' sums.
+template <int DP, int R, int WAVES> struct DirectShared {
+  static constexpr int ROWS = 16 * R, LD = DP + 4;
+  float m[WAVES][ROWS], l[WAVES][ROWS];
+  alignas(16) float o[WAVES][ROWS * LD];
+};
+
+// One workgroup's piece. DP: head dimension, or (not EXACT) an upper bound of it
 template <bool F32, int FMT, int DP, bool EXACT, int R, int WAVES>
-__global__ __launch_bounds__(WAVES* WAVE, direct_occupancy(F32, DP, R)) void attn_direct_kernel(AttnArgs A) {
+__device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, DirectShared<DP, R, WAVES>& sh) {
   using X = Direct<F32, FMT>;
   constexpr int C = X::C, NT = X::NT, TOK = X::tokens, NG = TOK / 16, BYTES = X::bytes;
   constexpr bool SCALED = KvFormat<FMT>::scaled;
@@ -104,8 +111,9 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_occupancy(F32, DP, R)) void att
   constexpr int NB = DP / 16;            // blocks of 16 values of d
   constexpr int VL = X::v_loads;
   constexpr int ROWS = 16 * R, LD = DP + 4;
-  __shared__ float s_m[WAVES][ROWS], s_l[WAVES][ROWS];
-  __shared__ __align__(16) float s_o[WAVES][ROWS * LD];
+  auto& s_m = sh.m;
+  auto& s_l = sh.l;
+  auto& s_o = sh.o;
   const KvArgs& K = A.kv;
   const int lane = threadIdx.x & (WAVE - 1), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
   const int r = lane & 15, quad = lane >> 4;
@@ -113,10 +121,9 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_occupancy(F32, DP, R)) void att
 
   // this workgroup's piece: first ranges first, so that the ranges that shorter sequences lack come
   // last instead of leaving the same shader engines idle throughout
-  const int kvh = blockIdx.x % K.H;
-  const int rest = blockIdx.x / K.H;
-  const int slots = gridDim.x / (K.H * A.n_split[0]);
-  const int split = rest / slots, slot = rest - split * slots;
+  const int kvh = piece % K.H;
+  const int rest = piece / K.H;
+  const int split = rest / A.slots[0], slot = rest - split * A.slots[0];
   int b, row0;
   if (A.one_tile) {
     b = slot;
@@ -489,41 +496,47 @@ __global__ __launch_bounds__(WAVES* WAVE, direct_occupancy(F32, DP, R)) void att
 }
 
 template <bool F32, int FMT, int DP, bool EXACT, int R, int WAVES>
-hipError_t launch_direct(const AttnArgs& A, unsigned slots, hipStream_t stream) {
-  const dim3 g(slots * (unsigned)A.n_split[0] * (unsigned)A.kv.H);
+__global__ __launch_bounds__(WAVES* WAVE, direct_occupancy(F32, DP, R)) void attn_direct_kernel(AttnArgs A) {
+  __shared__ DirectShared<DP, R, WAVES> sh;
+  attn_direct<F32, FMT, DP, EXACT, R, WAVES>(A, blockIdx.x, sh);
+}
+
+template <bool F32, int FMT, int DP, bool EXACT, int R, int WAVES>
+hipError_t launch_direct(const AttnArgs& A, hipStream_t stream) {
+  const dim3 g((unsigned)A.slots[0] * (unsigned)A.n_split[0] * (unsigned)A.kv.H);
   attn_direct_kernel<F32, FMT, DP, EXACT, R, WAVES><<<g, WAVES * WAVE, 0, stream>>>(A);
   return hipGetLastError();
 }
 
 template <bool F32, int FMT, int DP, bool EXACT, int R>
-hipError_t launch_direct_waves(const AttnArgs& A, unsigned slots, hipStream_t stream) {
+hipError_t launch_direct_waves(const AttnArgs& A, hipStream_t stream) {
   if constexpr (direct_eight_waves(DP, F32)) {
-    if (A.direct_waves == 8) return launch_direct<F32, FMT, DP, EXACT, R, 8>(A, slots, stream);
+    if (A.direct_waves == 8) return launch_direct<F32, FMT, DP, EXACT, R, 8>(A, stream);
   }
-  return launch_direct<F32, FMT, DP, EXACT, R, 4>(A, slots, stream);
+  return launch_direct<F32, FMT, DP, EXACT, R, 4>(A, stream);
 }
 
 // Two tiles of rows per workgroup where their registers fit (direct_two_tiles).
 template <int FMT, int R>
-hipError_t launch_direct_dim(const AttnArgs& A, unsigned slots, hipStream_t stream) {
+hipError_t launch_direct_dim(const AttnArgs& A, hipStream_t stream) {
   const int D = A.kv.D;
-  if (D == 64) return launch_direct_waves<false, FMT, 64, true, R>(A, slots, stream);
-  if (D == 96) return launch_direct_waves<false, FMT, 96, true, R>(A, slots, stream);
-  if (D == 128) return launch_direct_waves<false, FMT, 128, true, R>(A, slots, stream);
-  if (D == 192) return launch_direct_waves<false, FMT, 192, true, R>(A, slots, stream);
-  if (D < 64) return launch_direct_waves<false, FMT, 64, false, R>(A, slots, stream);
-  if (D < 128) return launch_direct_waves<false, FMT, 128, false, R>(A, slots, stream);
+  if (D == 64) return launch_direct_waves<false, FMT, 64, true, R>(A, stream);
+  if (D == 96) return launch_direct_waves<false, FMT, 96, true, R>(A, stream);
+  if (D == 128) return launch_direct_waves<false, FMT, 128, true, R>(A, stream);
+  if (D == 192) return launch_direct_waves<false, FMT, 192, true, R>(A, stream);
+  if (D < 64) return launch_direct_waves<false, FMT, 64, false, R>(A, stream);
+  if (D < 128) return launch_direct_waves<false, FMT, 128, false, R>(A, stream);
   if constexpr (R == 1) {
-    if (D == 256) return launch_direct_waves<false, FMT, 256, true, 1>(A, slots, stream);
-    return launch_direct_waves<false, FMT, 256, false, 1>(A, slots, stream);
+    if (D == 256) return launch_direct_waves<false, FMT, 256, true, 1>(A, stream);
+    return launch_direct_waves<false, FMT, 256, false, 1>(A, stream);
   }
   return hipErrorInvalidValue;
 }
 
 template <int FMT>
-hipError_t launch_direct_bf16(const AttnArgs& A, unsigned slots, hipStream_t stream) {
-  return A.direct_tile == 16 ? launch_direct_dim<FMT, 1>(A, slots, stream)
-                             : launch_direct_dim<FMT, 2>(A, slots, stream);
+hipError_t launch_direct_bf16(const AttnArgs& A, hipStream_t stream) {
+  return A.direct_tile == 16 ? launch_direct_dim<FMT, 1>(A, stream)
+                             : launch_direct_dim<FMT, 2>(A, stream);
 }
 
 }  // namespace sgmv

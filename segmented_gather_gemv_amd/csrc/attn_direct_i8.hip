@@ -3,8 +3,6 @@
 
 namespace sgmv {
 
-hipError_t launch_attn_direct_i8(const AttnArgs& A, unsigned slots, hipStream_t stream) {
-  return launch_direct_bf16<SGMV_KV_I8>(A, slots, stream);
-}
+hipError_t launch_attn_direct_i8(const AttnArgs& A, hipStream_t stream) { return launch_direct_bf16<SGMV_KV_I8>(A, stream); }
 
 }  // namespace sgmv

@@ -17,7 +17,7 @@
 // of it; group 1 writes them.
 #pragma once
 
-#include "attn_operand.h"
+#include "attn_direct.h"
 
 namespace sgmv {
 
@@ -39,19 +39,29 @@ __device__ __forceinline__ void read_ahead() {
   __builtin_amdgcn_sched_group_barrier(MFMA, 4, 0);
 }
 
+template <int FMT, int D> struct TiledShared {
+  static constexpr int GROUP = D * 16;  // elements of a group
+  alignas(16) uint16_t k[2][4 * GROUP], v[2][4 * GROUP];
+  alignas(16) float ks[2][KvFormat<FMT>::scaled ? TL_TOKENS : 4], vs[2][KvFormat<FMT>::scaled ? TL_TOKENS : 4];
+  int odd[4];  // [i % 4] = i: something that is not finite was left out of tile i
+};
+
+// One workgroup's piece.
 template <int FMT, int D>
-__global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnArgs A) {
+__device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledShared<FMT, D>& sh) {
   constexpr int WAVES = tiled_waves(D), THREADS = WAVES * WAVE, ROWS = WAVES * AT_ROWS;
   constexpr int BYTES = KvFormat<FMT>::bytes;
   constexpr bool SCALED = KvFormat<FMT>::scaled;
   constexpr int NK = D / 16, NB = D / 32;
   constexpr int SCALE_WAVE = WAVES == 8 ? 4 : 0;  // the first of two waves that stage scales
-  constexpr int GROUP = D * 16;                         // elements of a group
-  constexpr int PIECES = GROUP * BYTES / 16;            // 16-byte pieces of a group as stored
+  constexpr int GROUP = D * 16;                   // elements of a group
+  constexpr int PIECES = GROUP * BYTES / 16;      // 16-byte pieces of a group as stored
   constexpr int NP = (4 * PIECES + THREADS - 1) / THREADS;
-  __shared__ __align__(16) uint16_t s_k[2][4 * GROUP], s_v[2][4 * GROUP];
-  __shared__ int s_odd[4];  // [i % 4] = i: something that is not finite was left out of tile i
-  __shared__ __align__(16) float s_ks[2][SCALED ? TL_TOKENS : 4], s_vs[2][SCALED ? TL_TOKENS : 4];
+  auto& s_k = sh.k;
+  auto& s_v = sh.v;
+  auto& s_ks = sh.ks;
+  auto& s_vs = sh.vs;
+  auto& s_odd = sh.odd;
 
   const KvArgs& K = A.kv;
   const int tid = threadIdx.x, lane = tid & (WAVE - 1);
@@ -59,8 +69,8 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
   const int col = lane & 31, half = lane >> 5;
 
   // this workgroup's piece; the last tiles of a sequence look at the most tokens and start first
-  const int kvh = blockIdx.x % K.H;
-  const int rest = (gridDim.x - 1 - blockIdx.x) / K.H;
+  const int kvh = piece % K.H;
+  const int rest = A.slots[1] * A.n_split[1] - 1 - piece / K.H;
   const int split = rest % A.n_split[1], slot = rest / A.n_split[1];
   const auto first_slot = [&](int i) {
     return (int)((int64_t)min(max(K.q_start[i], 0), K.T) * A.G / ROWS) + i;
@@ -443,6 +453,40 @@ __global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnA
     for (int j = 0; j < 4; ++j)
       store_out<false>(A, oat + 32 * n + 8 * j + 4 * half, o[n][4 * j] * inv, o[n][4 * j + 1] * inv,
                        o[n][4 * j + 2] * inv, o[n][4 * j + 3] * inv);
+}
+
+// Workgroups [0, tiled) take tiles of many rows, the others the sequences of few rows (as attn_direct.h
+// does by itself): in one launch, these fill the compute units that finish their tiles early.
+template <int FMT, int D>
+__global__ __launch_bounds__(tiled_waves(D) * WAVE) void attn_tiled_kernel(AttnArgs A) {
+  constexpr int WAVES = tiled_waves(D), R = tiled_direct_rows(D) / 16;
+  __shared__ union Shared {
+    TiledShared<FMT, D> tiled;
+    DirectShared<D, R, WAVES> direct;
+    __device__ Shared() {}
+  } sh;
+  const int tiled = A.slots[1] * A.n_split[1] * A.kv.H;
+  if ((int)blockIdx.x < tiled) attn_tiled<FMT, D>(A, blockIdx.x, sh.tiled);
+  else attn_direct<false, FMT, D, true, R, WAVES>(A, blockIdx.x - tiled, sh.direct);
+}
+
+template <int FMT, int D>
+hipError_t launch_tiled(const AttnArgs& A, hipStream_t stream) {
+  const dim3 g((unsigned)(A.slots[1] * A.n_split[1] + A.slots[0] * A.n_split[0]) * (unsigned)A.kv.H);
+  attn_tiled_kernel<FMT, D><<<g, tiled_waves(D) * WAVE, 0, stream>>>(A);
+  return hipGetLastError();
+}
+
+template <int FMT>
+hipError_t launch_tiled_dim(const AttnArgs& A, hipStream_t stream) {
+  switch (A.kv.D) {
+    case 64: return launch_tiled<FMT, 64>(A, stream);
+    case 96: return launch_tiled<FMT, 96>(A, stream);
+    case 128: return launch_tiled<FMT, 128>(A, stream);
+    case 192: return launch_tiled<FMT, 192>(A, stream);
+    case 256: return launch_tiled<FMT, 256>(A, stream);
+    default: return hipErrorInvalidValue;
+  }
 }
 
 }  // namespace sgmv

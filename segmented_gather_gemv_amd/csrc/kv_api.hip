@@ -11,14 +11,14 @@
 namespace sgmv {
 hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, int max_q, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
-hipError_t launch_attn_direct_bf16(const AttnArgs& A, unsigned slots, hipStream_t stream);
-hipError_t launch_attn_direct_e4m3(const AttnArgs& A, unsigned slots, hipStream_t stream);
-hipError_t launch_attn_direct_i8(const AttnArgs& A, unsigned slots, hipStream_t stream);
-hipError_t launch_attn_direct_f32(const AttnArgs& A, int fmt, unsigned slots, hipStream_t stream);
-hipError_t launch_attn_tiled_bf16(const AttnArgs& A, unsigned slots, hipStream_t stream);
-hipError_t launch_attn_tiled_e4m3(const AttnArgs& A, unsigned slots, hipStream_t stream);
-hipError_t launch_attn_tiled_i8(const AttnArgs& A, unsigned slots, hipStream_t stream);
-hipError_t launch_attn_combine(const AttnArgs& A, int kernel, unsigned slots, hipStream_t stream);
+hipError_t launch_attn_direct_bf16(const AttnArgs& A, hipStream_t stream);
+hipError_t launch_attn_direct_e4m3(const AttnArgs& A, hipStream_t stream);
+hipError_t launch_attn_direct_i8(const AttnArgs& A, hipStream_t stream);
+hipError_t launch_attn_direct_f32(const AttnArgs& A, int fmt, hipStream_t stream);
+hipError_t launch_attn_tiled_bf16(const AttnArgs& A, hipStream_t stream);
+hipError_t launch_attn_tiled_e4m3(const AttnArgs& A, hipStream_t stream);
+hipError_t launch_attn_tiled_i8(const AttnArgs& A, hipStream_t stream);
+hipError_t launch_attn_combine(const AttnArgs& A, int kernel, hipStream_t stream);
 
 namespace {
 
@@ -115,18 +115,12 @@ void split_direct(AttnArgs& A, int64_t base, int64_t tokens, int forced) {
   split_tokens(base, tokens, 0, 1, step, (int)std::max<int64_t>(n, 1), A.n_split[0], A.chunk[0]);
 }
 
-// Geometry of an attention call; everything but the pointers of its rows and workspace. Slots: tiles
-// of rows that each kernel's grid has room for (0: not launched).
-struct Launch {
-  int64_t direct_slots = 0, tiled_slots = 0;
-  bool empty = true;
-};
-
+// Geometry of an attention call; everything but the pointers of its rows and workspace.
 sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_cache* c, AttnArgs& A,
-                 Launch& L) {
+                 bool& empty) {
   std::memset(&A, 0, sizeof(A));
   if (!a) return SGMV_EINVAL;
-  const sgmv_status st = fill(s, c, A.kv, L.empty);
+  const sgmv_status st = fill(s, c, A.kv, empty);
   if (st != SGMV_OK) return st;
   if (!row_type_ok(a->dtype) || !types_fit(a->dtype, c->format) || a->heads < 1 ||
       a->heads % c->heads || !std::isfinite(a->scale) || a->scale <= 0.f || a->window < 0 ||
@@ -139,28 +133,31 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   A.scale_log2 = a->scale * 1.44269504088896341f;
   if (!std::isfinite(A.scale_log2)) return SGMV_EINVAL;
   A.window = a->window;
-  L.empty = L.empty || s->T == 0;
+  empty = empty || s->T == 0;
   if ((int64_t)s->T * A.Hq > MOST_GRID) return SGMV_EUNSUPPORTED;
-  // sequences of up to 32 rows go to the direct kernel; so do all where the tiled one has no instance
-  const bool tiled = !A.f32 && tiled_dim(c->head_dim) && (int64_t)s->max_q * A.G > AT_ROWS;
-  A.direct_rows = tiled ? AT_ROWS : INT32_MAX;
-  const int64_t most = tiled ? AT_ROWS : (int64_t)s->max_q * A.G;  // rows of a direct sequence
-  A.direct_tile = most > 16 && direct_two_tiles(c->head_dim, A.f32) ? 32 : 16;
+  // sequences of few rows are taken directly; so are all where the tiled kernel has no instance
+  const int D = c->head_dim, few = tiled_direct_rows(D);
+  const bool tiled = !A.f32 && tiled_dim(D) && (int64_t)s->max_q * A.G > few;
+  A.direct_rows = tiled ? few : INT32_MAX;
+  const int64_t most = tiled ? few : (int64_t)s->max_q * A.G;  // rows of such a sequence
+  A.direct_tile = most > 16 && direct_two_tiles(D, A.f32) ? 32 : 16;
   A.one_tile = most <= A.direct_tile;
-  L.direct_slots = A.one_tile ? s->B : (int64_t)s->T * A.G / A.direct_tile + s->B;
-  if (tiled && s->T == (int64_t)s->B * s->max_q) L.direct_slots = 0;  // no sequence is short
-  if (tiled) L.tiled_slots = (int64_t)s->T * A.G / tiled_rows(c->head_dim) + s->B;
+  int64_t direct = A.one_tile ? s->B : (int64_t)s->T * A.G / A.direct_tile + s->B;
+  if (tiled && s->T == (int64_t)s->B * s->max_q) direct = 0;  // no sequence is short
+  const int64_t tiles = tiled ? (int64_t)s->T * A.G / tiled_rows(D) + s->B : 0;
   int64_t tokens = s->max_kv;
   if (a->window) tokens = std::min(tokens, (int64_t)a->window + s->max_q + AT_TOKENS);
-  A.direct_waves = direct_eight_waves(c->head_dim, A.f32) && L.direct_slots * c->heads < 512 ? 8 : 4;
-  split_direct(A, L.direct_slots * c->heads, tokens, a->n_split);
-  split_tokens(L.tiled_slots * c->heads, tokens, 256, 512, 64, a->n_split, A.n_split[1], A.chunk[1]);
-  if (!L.direct_slots) A.n_split[0] = 1;
-  if (!L.tiled_slots) A.n_split[1] = 1;
-  // workgroups of the attention launches, and of those that join parts (4 rows each)
-  if (L.direct_slots * std::max(A.n_split[0], A.direct_tile / 4) * c->heads > MOST_GRID ||
-      L.tiled_slots * std::max(A.n_split[1], tiled_rows(c->head_dim) / 4) * c->heads > MOST_GRID)
+  A.direct_waves = tiled ? tiled_waves(D) : direct_eight_waves(D, A.f32) && direct * c->heads < 512 ? 8 : 4;
+  split_direct(A, direct * c->heads, tokens, a->n_split);
+  split_tokens(tiles * c->heads, tokens, 256, 512, 64, a->n_split, A.n_split[1], A.chunk[1]);
+  if (!direct) A.n_split[0] = 1;
+  if (!tiles) A.n_split[1] = 1;
+  // workgroups of the attention launch, and of those that join parts (4 rows each)
+  if ((direct * A.n_split[0] + tiles * A.n_split[1]) * c->heads > MOST_GRID ||
+      std::max(direct * A.direct_tile, tiles * tiled_rows(D)) / 4 * c->heads > MOST_GRID)
     return SGMV_EUNSUPPORTED;
+  A.slots[0] = (int32_t)direct;
+  A.slots[1] = (int32_t)tiles;
   return SGMV_OK;
 }
 
@@ -228,10 +225,10 @@ sgmv_status sgmv_kv_attention_workspace(const sgmv_attention* attn, const sgmv_k
                                         const sgmv_kv_cache* cache, size_t* bytes) {
   if (!bytes) return SGMV_EINVAL;
   AttnArgs A;
-  Launch L;
-  const sgmv_status s = plan(attn, batch, cache, A, L);
+  bool empty = true;
+  const sgmv_status s = plan(attn, batch, cache, A, empty);
   if (s != SGMV_OK) return s;
-  *bytes = L.empty ? 0 : part_bytes(A);
+  *bytes = empty ? 0 : part_bytes(A);
   return SGMV_OK;
 }
 
@@ -239,10 +236,10 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
                               const sgmv_kv_cache* cache, void* workspace, size_t workspace_bytes,
                               void* stream) {
   AttnArgs A;
-  Launch L;
-  const sgmv_status s = plan(attn, batch, cache, A, L);
+  bool empty = true;
+  const sgmv_status s = plan(attn, batch, cache, A, empty);
   if (s != SGMV_OK) return s;
-  if (L.empty) return SGMV_OK;
+  if (empty) return SGMV_OK;
   const int D = A.kv.D;
   if (!rows_ok(attn->q, A.kv.T, attn->ldq_token, attn->ldq_head, A.Hq, D) ||
       !rows_ok(attn->out, A.kv.T, attn->ldo_token, attn->ldo_head, A.Hq, D))
@@ -267,17 +264,18 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
   }
   hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t err = hipSuccess;
-  if (L.tiled_slots)
+  if (A.slots[1])
     err = (cache->format == SGMV_KV_BF16   ? launch_attn_tiled_bf16
            : cache->format == SGMV_KV_E4M3 ? launch_attn_tiled_e4m3
-                                           : launch_attn_tiled_i8)(A, (unsigned)L.tiled_slots, st);
-  if (err == hipSuccess && L.direct_slots)
-    err = A.f32 ? launch_attn_direct_f32(A, cache->format, (unsigned)L.direct_slots, st)
-                : (cache->format == SGMV_KV_BF16   ? launch_attn_direct_bf16
-                   : cache->format == SGMV_KV_E4M3 ? launch_attn_direct_e4m3
-                                                   : launch_attn_direct_i8)(A, (unsigned)L.direct_slots, st);
-  if (err == hipSuccess && A.n_split[0] > 1) err = launch_attn_combine(A, 0, (unsigned)L.direct_slots, st);
-  if (err == hipSuccess && A.n_split[1] > 1) err = launch_attn_combine(A, 1, (unsigned)L.tiled_slots, st);
+                                           : launch_attn_tiled_i8)(A, st);
+  else if (A.f32)
+    err = launch_attn_direct_f32(A, cache->format, st);
+  else
+    err = (cache->format == SGMV_KV_BF16   ? launch_attn_direct_bf16
+           : cache->format == SGMV_KV_E4M3 ? launch_attn_direct_e4m3
+                                           : launch_attn_direct_i8)(A, st);
+  for (int kernel = 0; kernel < 2 && err == hipSuccess; ++kernel)
+    if (A.n_split[kernel] > 1) err = launch_attn_combine(A, kernel, st);
   return launched(err);
 }
 
