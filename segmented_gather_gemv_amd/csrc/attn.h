@@ -43,7 +43,7 @@ constexpr bool direct_two_tiles(int D, bool f32) { return D <= 128 || (D == 192 
 constexpr bool direct_eight_waves(int D, bool f32) { return D <= 128 && !f32; }
 
 // The tiled kernel: head dimensions it has instances of, waves and rows of its workgroups.
-constexpr bool tiled_dim(int D) { return D == 64 || D == 96 || D == 128 || D == 192 || D == 256; }
+constexpr bool tiled_dim(int D) { return D == 64 || D == 80 || D == 96 || D == 128 || D == 192 || D == 256; }
 constexpr int tiled_waves(int D) { return D <= 128 ? 8 : 4; }
 constexpr int tiled_rows(int D) { return tiled_waves(D) * AT_ROWS; }
 

@@ -111,6 +111,8 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
   constexpr int NB = DP / 16;            // blocks of 16 values of d
   constexpr int VL = X::v_loads;
   constexpr int ROWS = 16 * R, LD = DP + 4;
+  // wide fp32 rows: V in the registers that K had, not next to it (its products take longer than a load)
+  constexpr bool LATE_V = BYTES == 4 && DP > 128;
   auto& s_m = sh.m;
   auto& s_l = sh.l;
   auto& s_o = sh.o;
@@ -260,7 +262,7 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
 
   if (mine > 0) {
     load_k(0);
-    load_v(0);
+    if (!LATE_V) load_v(0);
   }
   for (int i = 0; i < mine; ++i) {
     const int t0 = t_begin + TOK * (wv + WAVES * i);
@@ -286,13 +288,15 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
 #pragma unroll
         for (int t = 0; t < R; ++t) sc[t][at.value / 4][at.value % 4] *= f;
       });
-    if (i + 1 < mine) {
+    if (LATE_V) load_v(i);
+    auto load_next = [&] {
       if (((i + 1) & (STEPS - 1)) == 0) {
         pages = pages_next;
         pages_next = load_pages(i + 1 + STEPS);
       }
       load_k(i + 1);
-    }
+    };
+    if (!LATE_V && i + 1 < mine) load_next();
 
     // a step that some row sees only part of, or with tokens that are not there
     const bool edge = t0 + TOK - 1 > lo_pos || (A.window && t0 <= hi_pos - A.window) || gap;
@@ -432,7 +436,10 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
         }
       }
     }
-    if (i + 1 < mine) load_v(i + 1);
+    if (i + 1 < mine) {
+      if (LATE_V) load_next();
+      else load_v(i + 1);
+    }
   }
 
   // The waves' sums. A wave that saw nothing has m = -inf, l = 0, o = 0 (or NaN where all it saw
@@ -521,6 +528,7 @@ template <int FMT, int R>
 hipError_t launch_direct_dim(const AttnArgs& A, hipStream_t stream) {
   const int D = A.kv.D;
   if (D == 64) return launch_direct_waves<false, FMT, 64, true, R>(A, stream);
+  if (D == 80) return launch_direct_waves<false, FMT, 80, true, R>(A, stream);
   if (D == 96) return launch_direct_waves<false, FMT, 96, true, R>(A, stream);
   if (D == 128) return launch_direct_waves<false, FMT, 128, true, R>(A, stream);
   if (D == 192) return launch_direct_waves<false, FMT, 192, true, R>(A, stream);

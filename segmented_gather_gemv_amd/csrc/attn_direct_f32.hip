@@ -9,9 +9,14 @@ static hipError_t launch_dim(const AttnArgs& A, hipStream_t stream) {
   const int D = A.kv.D;
   if (D == 64) return launch_direct<true, FMT, 64, true, R, 4>(A, stream);
   if (D < 64) return launch_direct<true, FMT, 64, false, R, 4>(A, stream);
+  if (D == 80) return launch_direct<true, FMT, 80, true, R, 4>(A, stream);
   if (D == 128) return launch_direct<true, FMT, 128, true, R, 4>(A, stream);
   if (D < 128) return launch_direct<true, FMT, 128, false, R, 4>(A, stream);
-  if constexpr (R == 1) return launch_direct<true, FMT, 256, false, 1, 4>(A, stream);
+  if constexpr (R == 1) {
+    if (D == 192) return launch_direct<true, FMT, 192, true, 1, 4>(A, stream);
+    if (D == 256) return launch_direct<true, FMT, 256, true, 1, 4>(A, stream);
+    return launch_direct<true, FMT, 256, false, 1, 4>(A, stream);
+  }
   return hipErrorInvalidValue;
 }
 

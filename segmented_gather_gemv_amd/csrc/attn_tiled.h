@@ -52,11 +52,12 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
   constexpr int WAVES = tiled_waves(D), THREADS = WAVES * WAVE, ROWS = WAVES * AT_ROWS;
   constexpr int BYTES = KvFormat<FMT>::bytes;
   constexpr bool SCALED = KvFormat<FMT>::scaled;
-  constexpr int NK = D / 16, NB = D / 32;
+  constexpr int NK = D / 16, NB = (D + 31) / 32;
   constexpr int SCALE_WAVE = WAVES == 8 ? 4 : 0;  // the first of two waves that stage scales
   constexpr int GROUP = D * 16;                   // elements of a group
   constexpr int PIECES = GROUP * BYTES / 16;      // 16-byte pieces of a group as stored
   constexpr int NP = (4 * PIECES + THREADS - 1) / THREADS;
+  constexpr bool BY_WAVE = PIECES % WAVE == 0;    // pieces of one group belong to whole waves
   auto& s_k = sh.k;
   auto& s_v = sh.v;
   auto& s_ks = sh.ks;
@@ -132,13 +133,15 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
   uint64_t have = __ballot(pages >= 0), have_before = 0;
   auto groups_of = [&](int i) { return (uint32_t)((i >> 4 == block ? have : have_before) >> ((4 * i) & 63)) & 15u; };
 
-  // The pieces that this thread stages: pieces of one group belong to whole waves. They are in
-  // registers for K of a tile and V of the tile before. (Past the last tile, of page 0, unused.)
+  // The pieces that this thread stages, in registers for K of a tile and V of the tile before. (Past the
+  // last tile, of page 0, unused.)
   u32x4_t rk[NP], rv[NP];
   int64_t at_k[NP] = {}, at_v[NP];  // bytes before the groups that they are from
   const int64_t page_bytes = (int64_t)K.H * ps * D * BYTES, head_bytes = (int64_t)kvh * ps * D * BYTES;
   float rs = 0.f;
   (void)rs;
+  auto group_of = [&](int n) { return (n * THREADS + (BY_WAVE ? wv * WAVE : tid)) / PIECES; };
+  auto piece_of = [&](int n) { return BY_WAVE ? (n * THREADS + wv * WAVE) % PIECES + lane : (n * THREADS + tid) % PIECES; };
   auto load_tile = [&](int i) {  // K of tile i, V of tile i - 1
     const int t0 = t_begin + TL_TOKENS * i;
     if ((i & 15) == 0 && i > 0) {
@@ -150,17 +153,18 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
     }
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-      const int at = n * THREADS + wv * WAVE;
-      const int g = at / PIECES;
+      const int g = group_of(n), piece = piece_of(n);
+      const int from = (4 * i + g) & 63;
+      const int page = BY_WAVE ? __builtin_amdgcn_readlane(pages, from) : __shfl(pages, from);
       if (4 * PIECES % THREADS == 0 || g < 4) {
-        const int off = (at % PIECES + lane) * 16;
+        const int off = piece * 16;
         int voff = off;
         if constexpr (!SCALED) {  // the exchange of halves
-          const int slot16 = at % PIECES + lane, d = slot16 >> 1;
-          voff = d * 32 + ((slot16 ^ (d >> 3)) & 1) * 16;
+          const int d = piece >> 1;
+          voff = d * 32 + ((piece ^ (d >> 3)) & 1) * 16;
         }
         at_v[n] = at_k[n];
-        at_k[n] = max(__builtin_amdgcn_readlane(pages, (4 * i + g) & 63), 0) * page_bytes + head_bytes +
+        at_k[n] = max(page, 0) * page_bytes + head_bytes +
                   ((t0 + 16 * g) & (ps - 1)) * (D * BYTES);
         rk[n] = load_u32x4(static_cast<const char*>(K.k) + at_k[n] + off);
         rv[n] = load_u32x4(static_cast<const char*>(K.v) + at_v[n] + voff);
@@ -183,8 +187,7 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
     const int buf = i & 1;
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-      const int at = n * THREADS + wv * WAVE;
-      const int g = at / PIECES, piece = at % PIECES + lane;
+      const int g = group_of(n), piece = piece_of(n);
       if (4 * PIECES % THREADS == 0 || g < 4) {
         if constexpr (!SCALED) {
           *reinterpret_cast<u32x4_t*>(&s_k[buf][g * GROUP + piece * 8]) = rk[n];
@@ -222,8 +225,7 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
     const bool some = !SCALED && some_see_part(i);
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
-      const int at = n * THREADS + wv * WAVE;
-      const int g = at / PIECES, piece = at % PIECES + lane;
+      const int g = group_of(n), piece = piece_of(n);
       if (4 * PIECES % THREADS == 0 || g < 4) {
         if constexpr (!SCALED) {
           if (some && has_nonfinite<2>(rv[n])) {
@@ -270,13 +272,16 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
   // O^T += V^T P^T of tile i
   auto values = [&](int i) {
     const int buf = i & 1;
-    // V operand of block n and group g: d = 32 n + col, this half's 8 tokens
+    // V operand of block n and group g: d = 32 n + col (D - 1 where there is no such d: its results are
+    // not used), this half's 8 tokens
     const uint16_t* vb = &s_v[buf][col * 16 + ((half ^ (col >> 3)) & 1) * 8];
+    const int last = min(32 * (NB - 1) + col, D - 1);
+    const uint16_t* vl = &s_v[buf][last * 16 + ((half ^ (last >> 3)) & 1) * 8];
 #pragma unroll
     for (int g = 0; g < 4; ++g)
 #pragma unroll
       for (int n = 0; n < NB; ++n)
-        o[n] = mfma_32x32_bf16(load_u32x4(vb + g * GROUP + n * 512), pb[g], o[n]);
+        o[n] = mfma_32x32_bf16(load_u32x4(D % 32 && n == NB - 1 ? vl + g * GROUP : vb + g * GROUP + n * 512), pb[g], o[n]);
     read_ahead<4 * NB>();
   };
   // What store_v (8-bit codes are finite: store_k, of the scales) has left out of tile i, added to the rows
@@ -302,6 +307,7 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
       for (int n = 0; n < NB; ++n) {
 #pragma unroll
         for (int j = 0; j < 16; ++j) {
+          if (32 * n + reg_token(j, 0) >= D) continue;
           const float f = bf16_bits_to_f32(v[(32 * n + reg_token(j, 0)) * 16]);
           o[n][j] += seen && !(fabsf(f) < INFINITY) ? f : 0.f;
         }
@@ -439,8 +445,9 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
     for (int n = 0; n < NB; ++n)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f32x4_t*>(dst + 32 * n + 8 * j + 4 * half) =
-            f32x4_t{o[n][4 * j], o[n][4 * j + 1], o[n][4 * j + 2], o[n][4 * j + 3]};
+        if (32 * n + 8 * j < D)
+          *reinterpret_cast<f32x4_t*>(dst + 32 * n + 8 * j + 4 * half) =
+              f32x4_t{o[n][4 * j], o[n][4 * j + 1], o[n][4 * j + 2], o[n][4 * j + 3]};
     return;
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -451,7 +458,8 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
   for (int n = 0; n < NB; ++n)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      store_out<false>(A, oat + 32 * n + 8 * j + 4 * half, o[n][4 * j] * inv, o[n][4 * j + 1] * inv,
+      if (32 * n + 8 * j < D)
+        store_out<false>(A, oat + 32 * n + 8 * j + 4 * half, o[n][4 * j] * inv, o[n][4 * j + 1] * inv,
                        o[n][4 * j + 2] * inv, o[n][4 * j + 3] * inv);
 }
 
@@ -481,6 +489,7 @@ template <int FMT>
 hipError_t launch_tiled_dim(const AttnArgs& A, hipStream_t stream) {
   switch (A.kv.D) {
     case 64: return launch_tiled<FMT, 64>(A, stream);
+    case 80: return launch_tiled<FMT, 80>(A, stream);
     case 96: return launch_tiled<FMT, 96>(A, stream);
     case 128: return launch_tiled<FMT, 128>(A, stream);
     case 192: return launch_tiled<FMT, 192>(A, stream);
