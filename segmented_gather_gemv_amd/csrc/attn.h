@@ -32,8 +32,13 @@ struct AttnArgs {
   // of the tile), the last one to the end
   int32_t chunk[2], n_split[2];  // [0] direct kernel, [1] tiled kernel
   int32_t slots[2];    // tiles of rows that the grid has room for (0: none)
-  float* part_o;       // [max n_split][T][Hq][D]
-  float* part_ml;      // [max n_split][T][Hq][2]: maximum (of scores times log2(e)), sum
+  // parts of the ranges, for each kernel [n_split][part_rows][D] and [n_split][part_rows][2]: maximum (of
+  // scores times log2(e)), sum. The row of a part: token and query head, or, where there are fewer of
+  // those, row of the kernel's tiles (part_row).
+  float* part_o[2];
+  float* part_ml[2];
+  int64_t part_rows[2];
+  int32_t part_tile[2];  // rows of a tile, 0: by token and query head
 };
 
 // Whether the direct kernel has instances of two 16-row tiles per workgroup.
@@ -69,6 +74,11 @@ __device__ __forceinline__ Span row_span(const AttnArgs& A, const KvSeq& s, int 
 __device__ __forceinline__ int span_splits(const AttnArgs& A, const Span& p, int kernel) {
   const int chunk = A.chunk[kernel];
   return min(max((p.end - p.begin + chunk - 1) / chunk, 1), A.n_split[kernel]);
+}
+
+// Row of the parts that belong to row `local` of a tile, of token and query head `at`.
+__device__ __forceinline__ int64_t part_row(const AttnArgs& A, int kernel, int slot, int kvh, int local, int64_t at) {
+  return A.part_tile[kernel] ? ((int64_t)slot * A.kv.H + kvh) * A.part_tile[kernel] + local : at;
 }
 
 __device__ __forceinline__ f32x16_t mfma_32x32_bf16(u32x4_t a, u32x4_t b, f32x16_t c) {

@@ -30,10 +30,11 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A, int kerne
   const int token = s.q0 + row / A.G, head = kvh * A.G + row % A.G;
   const int64_t at = (int64_t)token * A.Hq + head;
 
-  const int64_t stride = (int64_t)K.T * A.Hq;
+  const int64_t stride = A.part_rows[kernel], part = part_row(A, kernel, slot, kvh, row - tile0, at);
+  const float *part_o = A.part_o[kernel], *part_ml = A.part_ml[kernel];
   float m = -INFINITY, l = 0.f;
   if (lane < used) {
-    const f32x2_t v = *reinterpret_cast<const f32x2_t*>(A.part_ml + 2 * (lane * stride + at));
+    const f32x2_t v = *reinterpret_cast<const f32x2_t*>(part_ml + 2 * (lane * stride + part));
     m = v.x;
     l = v.y;
   }
@@ -55,7 +56,7 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs A, int kerne
     for (int u = 0; u < UNROLL; ++u) {
       const int i = i0 + u * sides + side;
       v[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-      if (i < used && d < K.D) v[u] = *reinterpret_cast<const f32x4_t*>(A.part_o + (i * stride + at) * K.D + d);
+      if (i < used && d < K.D) v[u] = *reinterpret_cast<const f32x4_t*>(part_o + (i * stride + part) * K.D + d);
     }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {

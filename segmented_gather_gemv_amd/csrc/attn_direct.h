@@ -487,12 +487,12 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
     const int tok = (row0 + lr) / A.G, head = kvh * A.G + (row0 + lr) % A.G;
     const int64_t at = (int64_t)(s.q0 + tok) * A.Hq + head;
     if (used > 1) {
-      const int64_t place = (int64_t)split * K.T * A.Hq + at;
+      const int64_t place = split * A.part_rows[0] + part_row(A, 0, slot, kvh, lr, at);
       if (d == 0) {
-        A.part_ml[2 * place] = top;
-        A.part_ml[2 * place + 1] = sum;
+        A.part_ml[0][2 * place] = top;
+        A.part_ml[0][2 * place + 1] = sum;
       }
-      *reinterpret_cast<f32x4_t*>(A.part_o + place * D + d) = sum_o;
+      *reinterpret_cast<f32x4_t*>(A.part_o[0] + place * D + d) = sum_o;
     } else {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;
       if (A.lse && d == 0) A.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.69314718055994531f;

@@ -435,12 +435,12 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
   const float sum = half_sum(l);
   const int64_t at = (int64_t)(s.q0 + tok) * A.Hq + head;
   if (used > 1) {
-    const int64_t place = (int64_t)split * K.T * A.Hq + at;
+    const int64_t place = split * A.part_rows[1] + part_row(A, 1, slot, kvh, row - tile0, at);
     if (half == 0) {
-      A.part_ml[2 * place] = m;
-      A.part_ml[2 * place + 1] = sum;
+      A.part_ml[1][2 * place] = m;
+      A.part_ml[1][2 * place + 1] = sum;
     }
-    float* dst = A.part_o + place * D;
+    float* dst = A.part_o[1] + place * D;
 #pragma unroll
     for (int n = 0; n < NB; ++n)
 #pragma unroll

@@ -161,9 +161,23 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   return SGMV_OK;
 }
 
-size_t part_bytes(const AttnArgs& A) {
-  const int n = A.n_split[0] > A.n_split[1] ? A.n_split[0] : A.n_split[1];
-  return n <= 1 ? 0 : (size_t)n * A.kv.T * A.Hq * (A.kv.D + 2) * sizeof(float);
+// Places the parts of both kernels in the workspace; returns its bytes.
+size_t place_parts(AttnArgs& A, void* workspace) {
+  float* at = static_cast<float*>(workspace);
+  size_t floats = 0;
+  for (int kernel = 0; kernel < 2; ++kernel) {
+    if (A.n_split[kernel] <= 1) continue;
+    const int tile = kernel ? tiled_rows(A.kv.D) : A.direct_tile;
+    const int64_t rows = (int64_t)A.kv.T * A.Hq, slots = (int64_t)A.slots[kernel] * tile * A.kv.H;
+    A.part_rows[kernel] = std::min(rows, slots);
+    A.part_tile[kernel] = slots < rows ? tile : 0;
+    const size_t n = (size_t)A.n_split[kernel] * A.part_rows[kernel];
+    A.part_o[kernel] = at ? at + floats : nullptr;  // 16-byte aligned: D is a multiple of 16, and so is the rest
+    A.part_ml[kernel] = at ? A.part_o[kernel] + n * A.kv.D : nullptr;
+    floats += n * (A.kv.D + 2);
+    if (kernel == 0) floats = (floats + 3) & ~(size_t)3;
+  }
+  return floats * sizeof(float);
 }
 
 }  // namespace
@@ -228,7 +242,7 @@ sgmv_status sgmv_kv_attention_workspace(const sgmv_attention* attn, const sgmv_k
   bool empty = true;
   const sgmv_status s = plan(attn, batch, cache, A, empty);
   if (s != SGMV_OK) return s;
-  *bytes = empty ? 0 : part_bytes(A);
+  *bytes = empty ? 0 : place_parts(A, nullptr);
   return SGMV_OK;
 }
 
@@ -254,13 +268,9 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
   const int e = A.f32 ? 4 : 2;
   A.q_vec = aligned_to(A.q, 16) && A.ldq_t * e % 16 == 0 && A.ldq_h * e % 16 == 0;
   A.o_vec = aligned_to(A.out, 4 * e) && A.ldo_t % 4 == 0 && A.ldo_h % 4 == 0;
-  const size_t need = part_bytes(A);
-  if (need) {
+  if (const size_t need = place_parts(A, workspace)) {
     if (!workspace || !aligned_to(workspace, 16)) return SGMV_EINVAL;
     if (workspace_bytes < need) return SGMV_ECAPACITY;
-    const int n = A.n_split[0] > A.n_split[1] ? A.n_split[0] : A.n_split[1];
-    A.part_o = static_cast<float*>(workspace);
-    A.part_ml = A.part_o + (size_t)n * A.kv.T * A.Hq * D;
   }
   hipStream_t st = static_cast<hipStream_t>(stream);
   hipError_t err = hipSuccess;
