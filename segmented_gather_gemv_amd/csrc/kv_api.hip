@@ -140,7 +140,10 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   const bool tiled = !A.f32 && tiled_dim(D) && (int64_t)s->max_q * A.G > few;
   A.direct_rows = tiled ? few : INT32_MAX;
   const int64_t most = tiled ? few : (int64_t)s->max_q * A.G;  // rows of such a sequence
-  A.direct_tile = most > 16 && direct_two_tiles(D, A.f32) ? 32 : 16;
+  // two tiles of 16 rows share K and V; of fp32 rows, whose products take their time, only where that
+  // leaves workgroups for every compute unit
+  const bool pair = direct_two_tiles(D, A.f32) && (!A.f32 || ((int64_t)s->T * A.G / 32 + s->B) * c->heads >= 512);
+  A.direct_tile = most > 16 && pair ? 32 : 16;
   A.one_tile = most <= A.direct_tile;
   int64_t direct = A.one_tile ? s->B : (int64_t)s->T * A.G / A.direct_tile + s->B;
   if (tiled && s->T == (int64_t)s->B * s->max_q) direct = 0;  // no sequence is short

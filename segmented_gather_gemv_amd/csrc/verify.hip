@@ -19,6 +19,7 @@ namespace sgmv {
 namespace {
 
 constexpr int VF_WAVES = 4;               // of a workgroup of the first launch
+constexpr int VF_ONE_PARTS = 16;          // of a row that one workgroup does, a wave each
 constexpr int VF_EACH = VF_PART / WAVE;   // entries of one lane
 
 __device__ __forceinline__ float prob(const float* p) { return *p; }
@@ -84,16 +85,13 @@ __device__ __forceinline__ void four(const T* row, int j, int V, float (&f)[4]) 
   }
 }
 
-template <class T, bool VEC>
-__global__ __launch_bounds__(VF_WAVES* WAVE) void verify_sum_kernel(VerifyArgs A) {
-  const int lane = threadIdx.x & (WAVE - 1), b = blockIdx.y;
-  const int part = blockIdx.x * VF_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
-  if (part >= A.parts) return;
-  const Drafts d = drafts(A, b);
+// How many of sequence b's drafts are taken, in every lane.
+template <class T>
+__device__ __forceinline__ int count_taken(const VerifyArgs& A, int b, Drafts d) {
+  const int lane = threadIdx.x & (WAVE - 1);
   const T* target = static_cast<const T*>(A.target) + (int64_t)(d.first + b) * A.ldt;
   const T* draft = static_cast<const T*>(A.draft) + (A.draft ? (int64_t)d.first * A.ldd : 0);
-  int taken = d.n;
-  for (int i0 = 0; i0 < d.n && taken == d.n; i0 += WAVE) {
+  for (int i0 = 0; i0 < d.n; i0 += WAVE) {
     const int i = i0 + lane;
     bool ok = true;
     if (i < d.n) {
@@ -106,16 +104,26 @@ __global__ __launch_bounds__(VF_WAVES* WAVE) void verify_sum_kernel(VerifyArgs A
       }
     }
     const uint64_t bad = __ballot(!ok);
-    if (bad) taken = i0 + __ffsll((unsigned long long)bad) - 1;
+    if (bad) return i0 + __ffsll((unsigned long long)bad) - 1;
   }
-  if (part == 0) {
-    int32_t* out = A.tokens + (int64_t)b * A.ldo;
-    for (int i = lane; i <= A.max_drafts; i += WAVE)
-      if (i != taken) out[i] = i < taken ? A.ids[d.first + i] : -1;
-    if (lane == 0) A.accepted[b] = taken;
-  }
-  const Row<T> row = drawn_row<T>(A, b, d, taken);
-  double sum = 0., all = 0.;  // of what is left of p, and of p itself
+  return d.n;
+}
+
+// Everything of sequence b's outputs but the drawn token: one wave.
+__device__ __forceinline__ void store_taken(const VerifyArgs& A, int b, Drafts d, int taken) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  int32_t* out = A.tokens + (int64_t)b * A.ldo;
+  for (int i = lane; i <= A.max_drafts; i += WAVE)
+    if (i != taken) out[i] = i < taken ? A.ids[d.first + i] : -1;
+  if (lane == 0) A.accepted[b] = taken;
+}
+
+// Sums of one part of the row (what lies past its end counts as 0): of what is left of p, and of p itself;
+// in every lane.
+template <class T, bool VEC>
+__device__ __forceinline__ void sum_part(const VerifyArgs& A, const Row<T>& row, int part, double& sum, double& all) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  sum = all = 0.;
 #pragma unroll
   for (int i = 0; i < VF_EACH / 4; ++i) {
     const int j = part * VF_PART + 4 * (i * WAVE + lane);
@@ -133,17 +141,13 @@ __global__ __launch_bounds__(VF_WAVES* WAVE) void verify_sum_kernel(VerifyArgs A
     sum += __shfl_xor(sum, o);
     all += __shfl_xor(all, o);
   }
-  if (lane < 2) A.sums[((int64_t)b * A.parts + part) * 2 + lane] = lane ? all : sum;
 }
 
+// The token that u falls on in a row whose parts have these sums (pairs as sum_part has them): one wave.
 template <class T, bool VEC>
-__global__ __launch_bounds__(WAVE) void verify_draw_kernel(VerifyArgs A) {
-  const int b = blockIdx.x, lane = threadIdx.x;
-  const int taken = A.accepted[b];
-  const double u = A.sample_u[b];
-  const Drafts d = drafts(A, b);
-  // the part that r falls into; over p itself where nothing is left of it
-  const double* sums = A.sums + (int64_t)b * A.parts * 2;
+__device__ __forceinline__ int draw(const VerifyArgs& A, const Row<T>& row, const double* sums, double u) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  // the part that u falls into; over p itself where nothing is left of it
   const int per = (A.parts + WAVE - 1) / WAVE;
   const int c0 = min(lane * per, A.parts), c1 = min(c0 + per, A.parts);
   double left = 0., all = 0.;
@@ -178,7 +182,6 @@ __global__ __launch_bounds__(WAVE) void verify_draw_kernel(VerifyArgs A) {
     part = __shfl(part, owner);
     base = __shfl(last, owner);
 
-    const Row<T> row = drawn_row<T>(A, b, d, taken);
     const int j0 = part * VF_PART + lane * VF_EACH;
     double w[VF_EACH], mine = 0.;
 #pragma unroll
@@ -210,11 +213,60 @@ __global__ __launch_bounds__(WAVE) void verify_draw_kernel(VerifyArgs A) {
     if (f) token = __shfl(found, __ffsll((unsigned long long)f) - 1);
     else if (l) token = __shfl(weighted, WAVE - 1 - __clzll((long long)l));
   }
-  if (lane == 0) A.tokens[(int64_t)b * A.ldo + taken] = token;
+  return token;
+}
+
+template <class T, bool VEC>
+__global__ __launch_bounds__(VF_WAVES* WAVE) void verify_sum_kernel(VerifyArgs A) {
+  const int lane = threadIdx.x & (WAVE - 1), b = blockIdx.y;
+  const int part = blockIdx.x * VF_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  if (part >= A.parts) return;
+  const Drafts d = drafts(A, b);
+  const int taken = count_taken<T>(A, b, d);
+  if (part == 0) store_taken(A, b, d, taken);
+  double sum, all;
+  sum_part<T, VEC>(A, drawn_row<T>(A, b, d, taken), part, sum, all);
+  if (lane < 2) A.sums[((int64_t)b * A.parts + part) * 2 + lane] = lane ? all : sum;
+}
+
+template <class T, bool VEC>
+__global__ __launch_bounds__(WAVE) void verify_draw_kernel(VerifyArgs A) {
+  const int b = blockIdx.x, taken = A.accepted[b];
+  const int token = draw<T, VEC>(A, drawn_row<T>(A, b, drafts(A, b), taken), A.sums + (int64_t)b * A.parts * 2,
+                                 (double)A.sample_u[b]);
+  if (threadIdx.x == 0) A.tokens[(int64_t)b * A.ldo + taken] = token;
+}
+
+// Both in one launch, one workgroup per sequence, for rows of few parts (64 sequences of 8000 entries: 8.6 us, 10.0
+// us in two launches; with two parts per wave, 32000 entries, 11.2 us and 10.0 us: the fp64 sums take a
+// compute unit as long as a launch).
+template <class T, bool VEC>
+__global__ __launch_bounds__(VF_ONE_PARTS* WAVE) void verify_one_kernel(VerifyArgs A) {
+  __shared__ double s_sums[2 * VF_ONE_PARTS];
+  const int b = blockIdx.x, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const Drafts d = drafts(A, b);
+  const double u = A.sample_u[b];
+  const int taken = count_taken<T>(A, b, d);
+  if (wv == 0) store_taken(A, b, d, taken);
+  const Row<T> row = drawn_row<T>(A, b, d, taken);
+  double sum, all;
+  sum_part<T, VEC>(A, row, wv, sum, all);
+  if ((threadIdx.x & (WAVE - 1)) == 0) {
+    s_sums[2 * wv] = sum;
+    s_sums[2 * wv + 1] = all;
+  }
+  __syncthreads();
+  if (wv) return;
+  const int token = draw<T, VEC>(A, row, s_sums, u);
+  if (threadIdx.x == 0) A.tokens[(int64_t)b * A.ldo + taken] = token;
 }
 
 template <class T, bool VEC>
 void launch(const VerifyArgs& A, hipStream_t stream) {
+  if (A.parts <= VF_ONE_PARTS) {
+    verify_one_kernel<T, VEC><<<dim3((unsigned)A.B), VF_ONE_PARTS * WAVE, 0, stream>>>(A);
+    return;
+  }
   const dim3 g((unsigned)((A.parts + VF_WAVES - 1) / VF_WAVES), (unsigned)A.B);
   verify_sum_kernel<T, VEC><<<g, VF_WAVES * WAVE, 0, stream>>>(A);
   verify_draw_kernel<T, VEC><<<dim3((unsigned)A.B), WAVE, 0, stream>>>(A);
