@@ -15,6 +15,14 @@
 // their shares of K(i + 2) and V(i + 1): over K(i) and V(i - 1), last read in phase 2 i + 1, and in time for
 // phase 2 i + 4, so two buffers of each are enough. The scales of tile i are read in phases 2 i + 1 and 2 i + 2
 // of it; group 1 writes them.
+//
+// Bound: the matrix cores, at the clock that they leave themselves: the products alone, without loads,
+// softmax and LDS reads, ran at 1420..1520 TFLOP/s on the largest shape here (a large matrix product of the
+// library: 1250). 2048 tokens over 14001, e4m3, 32 / 8 heads of 128: 485..515 us (980..1040 TFLOP/s), matrix
+// cores busy 46% of the cycles, a phase of products 1.5 thousand cycles where they need 1.0; eight prompts'
+// chunks, bf16, 64 / 8 heads: 335..350 us (870..910). What did not pay: 64 rows per wave with the softmax
+// between the products of one wave (registers: 954 us), e4m3 codes of V or of both in LDS, converted at
+// each use (531 and 589 us beside 512), longer read-ahead, no or other wave priorities (533, 566).
 #pragma once
 
 #include "attn_direct.h"

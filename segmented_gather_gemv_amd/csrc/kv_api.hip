@@ -98,12 +98,14 @@ int64_t tiled_splits(int64_t base, int64_t tokens) {
 }
 
 // Ranges for the direct kernel. A split costs its parts and a launch that joins them, about as long as
-// five steps of the waves. From 1024 workgroups on (four per compute unit) a call is not split. With
-// fewer, sequences of different lengths are evened out by up to 1536 workgroups of long ranges, and
-// below 256 (of 8 waves: below 512 bf16 head_dim 128 workgroups of 4 waves leave registers unused) tokens
-// are spread over the compute units down to one step of each wave. fp32 steps take four times as long.
-//   64 sequences of 500..8000, e4m3, 32 / 8 heads: 119 us in 3, 121 in 1; 256 of 128..4096, bf16: 397 us
-//   in 1, 418 in 3; one of 4000, bf16: 10.4 us in 16, 19.6 in 1; one of 1000: 9.1 us in 1, 10.3 in 4
+// five steps of the waves: rows of no more than six steps are not split (one sequence of 1000 tokens,
+// bf16: 9.1 us in 1 range, 10.3 in 4; of 4000: 19.6 in 1, 10.4 in 16). Short of that, two rules:
+//   fill  up to a workgroup of 8 waves (two of 4) per compute unit, down to one step of each wave;
+//   even  sequences of different lengths leave compute units idle at the end: up to four workgroups of 8
+//         waves (six of 4) per compute unit, of long ranges (16 sequences of 8001..64003, e4m3: 361 us in 1
+//         range, 238 in 2, 231 in 8). From 1024 workgroups of 4 waves on a call is not split (256 of
+//         128..4096, bf16: 397 us in 1, 418 in 3).
+// fp32 steps take four times as long and are split whatever their number.
 void split_direct(AttnArgs& A, int64_t base, int64_t tokens, int forced) {
   const int step = A.direct_waves * (A.kv.k_scale ? 64 : 32);
   int64_t n = forced;

@@ -18,6 +18,8 @@
 // rows follow each other (then a wave of V takes one row). K and V are separate waves.
 //
 // Bound: the rows' bytes; one token per sequence: the chain of loads from the sequence to its page.
+// Measured, 8 heads of 128: 256 sequences' new tokens written as e4m3 6.5 us and read back 4.0 us; 16 prompts' chunks written as int8 19 us (54 MB), 42 thousand tokens read back as bf16 61 us (264
+// MB, 4.3 TB/s; a large copy: 5.1).
 #include "kv_common.h"
 
 namespace sgmv {
