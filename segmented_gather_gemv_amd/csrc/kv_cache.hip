@@ -11,11 +11,13 @@
 // rounded division decides; of fp32 rows in fp64, rounded to odd before the last rounding.
 //
 // A wave takes 16 rows, lane r of each quarter (quad) row r, and of every row the pieces of K that are
-// 16 bytes in the cache, quad by quad. K is stored as it is held. V has tokens innermost: 4 lanes
-// exchange a 4x4 block, after which each holds one d of their four tokens, one word of the cache. The
-// 16 rows are the tokens of one group and head (a quad of tokens that is not written whole is stored
-// element by element, so that the others keep theirs), or, where sequences bring few tokens, whichever
-// rows follow each other (then a wave of V takes one row). K and V are separate waves.
+// 16 bytes in the cache, quad by quad, all of them loaded before the first is stored. K is stored as it is
+// held. V has tokens innermost: of 8-bit codes 16 lanes exchange a 16x16 block, after which each holds one d
+// of their tokens, 16 bytes of the cache (4x4 blocks and words of 4 bytes took 4% longer); of bf16 four
+// exchange a 4x4 block. The 16 rows are the tokens of one group and head (a group, or of bf16 a quad of
+// tokens, that is not written whole is stored element by element, so that the others keep theirs), or, where
+// sequences bring few tokens, whichever rows follow each other (then a wave of V takes one row). K and V are
+// separate waves.
 //
 // Bound: the rows' bytes; one token per sequence: the chain of loads from the sequence to its page.
 // Measured, 8 heads of 128: 256 sequences' new tokens written as e4m3 6.5 us and read back 4.0 us; 16 prompts' chunks written as int8 19 us (54 MB), 42 thousand tokens read back as bf16 61 us (264
@@ -78,7 +80,29 @@ __device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
   return __builtin_amdgcn_perm(t, w, lane & 2 ? 0x03020706u : 0x05040100u);
 }
 
-// The same of 16-bit elements, a row in two words.
+// Transposes a 16x16 block of bytes held by 16 neighbouring lanes, one row each: words between lanes 8 and 4
+// apart, then bytes between neighbours.
+__device__ __forceinline__ void transpose_16x16(u32x4_t& c, int lane) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {  // lane ^ 8: a rotation by half of the 16
+    const bool up = lane & 8;
+    const uint32_t x = c[k], y = c[k + 2], got = __builtin_amdgcn_mov_dpp(up ? x : y, 0x128, 0xf, 0xf, true);
+    c[k] = up ? got : x;
+    c[k + 2] = up ? y : got;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; k += 2) {  // lane ^ 4: mirrored in 8 (^ 7), then in 4 (^ 3)
+    const bool up = lane & 4;
+    const uint32_t x = c[k], y = c[k + 1];
+    const uint32_t got = __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(up ? x : y, 0x141, 0xf, 0xf, true), 0x1b, 0xf, 0xf, true);
+    c[k] = up ? got : x;
+    c[k + 1] = up ? y : got;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c[k] = transpose_bytes(c[k], lane);
+}
+
+// The same of 4x4 16-bit elements, a row in two words.
 __device__ __forceinline__ void transpose_halves(uint32_t& a, uint32_t& b, int lane) {
   const bool up = lane & 2, odd = lane & 1;
   const uint32_t other = __builtin_amdgcn_mov_dpp(up ? a : b, 0x4e, 0xf, 0xf, true);
@@ -144,16 +168,27 @@ __device__ __forceinline__ float word_value(const uint32_t (&w)[N], int e) {
 struct Place {
   bool ok;        // there is such a row
   bool quad_ok;   // and its three neighbours' (the same quad of tokens) are there too
+  bool whole;     // and all 16 of the group
   int64_t row;    // row beside the cache
-  int64_t token;  // [pages][H][page size] index, or -1: no page
+  int b, pos;     // sequence, position in it
   int head;
 };
+
+// [pages][H][page size] index of a place, or -1: no page.
+__device__ __forceinline__ int64_t token_of(const KvArgs& K, const Place& P) {
+  const int page = kv_page(K, K.table + (int64_t)P.b * K.ldp, P.pos);
+  return page < 0 ? -1 : ((int64_t)page * K.H + P.head) * (1 << K.lps) + (P.pos & ((1 << K.lps) - 1));
+}
+
+// Place of token r of a group, and token at place r.
+__device__ __forceinline__ int place_of(int r) { return 8 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
 
 // GROUPED: slot `w` of 16 tokens: the groups of sequence b take the slots from first(b) = (rows
 // before b) / 16 + 2 b on; n rows touch at most (n + 14) / 16 + 1 groups. start: rows of each sequence,
 // the last ones of it.
-__device__ __forceinline__ bool group_place(const KvArgs& K, const int32_t* start, int total, Place& P) {
-  const int lane = threadIdx.x & (WAVE - 1), r = lane & 15;
+// by_place: lane r of 16 has the token at place r, not token r.
+__device__ __forceinline__ bool group_place(const KvArgs& K, const int32_t* start, int total, bool by_place, Place& P) {
+  const int lane = threadIdx.x & (WAVE - 1), r = by_place ? place_of(lane & 15) : lane & 15;
   const int slot = blockIdx.x * RW_WAVES + threadIdx.x / WAVE;
   const int b = wave_find(K.B, slot, [&](int i) { return min(max(start[i], 0), total) / 16 + 2 * i; });
   const int r0 = min(max(start[b], 0), total), r1 = min(max(start[b + 1], 0), total);
@@ -162,13 +197,14 @@ __device__ __forceinline__ bool group_place(const KvArgs& K, const int32_t* star
   const int g0 = (first >> 4) + (slot - (r0 / 16 + 2 * b));
   const int t_lo = max(16 * g0, first), t_hi = min(16 * g0 + 16, kv_len);
   if (t_lo >= t_hi) return false;
-  const int page = kv_page(K, K.table + (int64_t)b * K.ldp, 16 * g0);
   const int t = 16 * g0 + r, t4 = t & ~3;
   P.head = blockIdx.y;
   P.ok = t >= t_lo && t < t_hi;
   P.quad_ok = t4 >= t_lo && t4 + 4 <= t_hi;
+  P.whole = t_lo == 16 * g0 && t_hi == 16 * g0 + 16;
   P.row = P.ok ? r0 + (t - first) : r0;
-  P.token = page < 0 ? -1 : ((int64_t)page * K.H + P.head) * (1 << K.lps) + (t & ((1 << K.lps) - 1));
+  P.b = b;
+  P.pos = t;
   return true;
 }
 
@@ -194,12 +230,11 @@ __device__ __forceinline__ void row_place(const KvArgs& K, const int32_t* starts
     }
     left &= ~__ballot(token == t);
   }
-  const int pos = kv_seq(K, b).kv_len - s1 + token;
   P.ok = in && s0 <= token && token < s1;
-  const int page = P.ok ? kv_page(K, K.table + (int64_t)b * K.ldp, pos) : -1;
-  P.quad_ok = false;
+  P.quad_ok = P.whole = false;
   P.row = token;
-  P.token = page < 0 ? -1 : ((int64_t)page * K.H + P.head) * (1 << K.lps) + (pos & ((1 << K.lps) - 1));
+  P.b = b;
+  P.pos = P.ok ? kv_seq(K, b).kv_len - s1 + token : -1;
 }
 
 template <int FMT, class T> struct Unit {
@@ -212,7 +247,6 @@ template <int FMT, class T> struct Unit {
 // Bytes of V that hold value e of unit u for a token of a group.
 template <int BYTES>
 __device__ __forceinline__ int64_t v_at(int d, int place) { return (int64_t)(d * 16 + place) * BYTES; }
-__device__ __forceinline__ int place_of(int r) { return 8 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
 
 // What quantising a row needs: its maximum, a power of two that keeps the quotient's parts in range, and
 // F over the maximum so scaled (0: codes 0); its scale.
@@ -237,15 +271,10 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, boo
   constexpr bool SCALED = KvFormat<FMT>::scaled;
   const int lane = threadIdx.x & (WAVE - 1), quad = lane >> 4;
   Place P = place16;
-  P.ok = P.ok && P.token >= 0;
   if (!__any(P.ok)) return;
   const int D = K.D, units = D / C;
   const T* src = static_cast<const T*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) +
                  P.head * (is_v ? A.ldv_h : A.ldk_h);
-  const int64_t token = max(P.token, (int64_t)0), group = (token & ~(int64_t)15) * D * BYTES;
-  const int r = (int)(token & 15);
-  char* dst = static_cast<char*>(const_cast<void*>(is_v ? K.v : K.k)) + group;
-
   uint32_t w[U::most][U::words];
   float amax = 0.f, bad = 0.f;
 #pragma unroll
@@ -256,6 +285,10 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, boo
     for (int i = 0; i < U::words; ++i) w[n][i] = 0u;
     if (P.ok && u < units) load_words(src + u * C, A.vec, w[n]);
   }
+  const int64_t at = token_of(K, P), token = max(at, (int64_t)0);  // the page's load beside the row's
+  P.ok = P.ok && at >= 0;
+  const int r = (int)(token & 15);
+  char* dst = static_cast<char*>(const_cast<void*>(is_v ? K.v : K.k)) + (token & ~(int64_t)15) * D * BYTES;
   RowScale S = {0.f, 1.f, 0.f, 0.f};
   if constexpr (SCALED) {
 #pragma unroll
@@ -298,30 +331,27 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, boo
         if (P.ok && in) *reinterpret_cast<uint32_t*>(dst + v_at<4>(u * 4 + j, place_of(r))) = c[j];
       continue;
     }
-    if (__any(P.ok && !P.quad_ok)) {
-      if (P.ok && !P.quad_ok && in)
+    const bool apart = BYTES == 1 ? !P.whole : !P.quad_ok;  // stored element by element
+    if (__any(P.ok && apart)) {
+      if (P.ok && apart && in)
 #pragma unroll
         for (int e = 0; e < C; ++e) {
           if constexpr (BYTES == 1) dst[v_at<1>(u * C + e, place_of(r))] = (char)(c[e / 4] >> (8 * (e % 4)));
           else *reinterpret_cast<uint16_t*>(dst + v_at<2>(u * C + e, place_of(r))) = (uint16_t)(c[e / 2] >> (16 * (e % 2)));
         }
     }
-    if constexpr (BYTES < 4) {
+    if constexpr (BYTES == 1) {
+      transpose_16x16(c, lane);
+      if (P.whole && P.ok && in) *reinterpret_cast<u32x4_t*>(dst + v_at<1>(u * 16 + (lane & 15), 0)) = c;
+    }
+    if constexpr (BYTES == 2) {
       const bool put = P.ok && P.quad_ok && in;
       const int j = lane & 3, place = place_of(r & ~3);
-      if constexpr (BYTES == 1) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t x = transpose_bytes(c[k], lane);
-          if (put) *reinterpret_cast<uint32_t*>(dst + v_at<1>(u * 16 + 4 * k + j, place)) = x;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t a = c[2 * k], b = c[2 * k + 1];
-          transpose_halves(a, b, lane);
-          if (put) *reinterpret_cast<u32x2_t*>(dst + v_at<2>(u * 8 + 4 * k + j, place)) = u32x2_t{a, b};
-        }
+      for (int k = 0; k < 2; ++k) {
+        uint32_t a = c[2 * k], b = c[2 * k + 1];
+        transpose_halves(a, b, lane);
+        if (put) *reinterpret_cast<u32x2_t*>(dst + v_at<2>(u * 8 + 4 * k + j, place)) = u32x2_t{a, b};
       }
     }
   }
@@ -333,10 +363,8 @@ template <int FMT, class T>
 __device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, const Place& P) {
   constexpr int BYTES = KvFormat<FMT>::bytes, MOST = SGMV_KV_MAX_HEAD_DIM / WAVE;
   const int lane = threadIdx.x & (WAVE - 1), D = K.D;
-  if (!P.ok || P.token < 0) return;
+  if (!P.ok) return;
   const T* src = static_cast<const T*>(A.v) + P.row * A.ldv_t + P.head * A.ldv_h;
-  char* dst = static_cast<char*>(const_cast<void*>(K.v)) + (P.token & ~(int64_t)15) * D * BYTES;
-  const int place = place_of((int)(P.token & 15));
   T e[MOST];
   float x[MOST], amax = 0.f, bad = 0.f;
 #pragma unroll
@@ -347,6 +375,10 @@ __device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, co
     amax = fmaxf(amax, fabsf(x[i]));
     bad = fmaf(x[i], 0.f, bad);
   }
+  const int64_t token = token_of(K, P);
+  if (token < 0) return;
+  char* dst = static_cast<char*>(const_cast<void*>(K.v)) + (token & ~(int64_t)15) * D * BYTES;
+  const int place = place_of((int)(token & 15));
   uint32_t c = 0;
   if constexpr (KvFormat<FMT>::scaled) {
 #pragma unroll
@@ -356,7 +388,7 @@ __device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, co
     }
     const RowScale S = row_scale<FMT>(quad_max(amax), quad_sum(bad));
     if (S.inv != 0.f) c = quantise4<FMT, T>(x, S.amax, S.s, S.inv);
-    if (lane == 0) const_cast<float*>(K.v_scale)[P.token] = S.scale;
+    if (lane == 0) const_cast<float*>(K.v_scale)[token] = S.scale;
   }
 #pragma unroll
   for (int i = 0; i < MOST; ++i) {
@@ -370,7 +402,7 @@ __device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, co
 template <int FMT, class T>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_groups_kernel(KvArgs K, KvRows A) {
   Place P;
-  if (group_place(K, K.q_start, K.T, P)) write_rows<FMT, T, true>(K, A, blockIdx.z, P);
+  if (group_place(K, K.q_start, K.T, blockIdx.z && KvFormat<FMT>::bytes == 1, P)) write_rows<FMT, T, true>(K, A, blockIdx.z, P);
 }
 
 // Workgroups [0, for_v) take V, the others K.
@@ -394,15 +426,16 @@ __device__ __forceinline__ void read_rows(const KvArgs& K, const KvRows& A, bool
   constexpr int BYTES = U::bytes, C = U::C;
   const int lane = threadIdx.x & (WAVE - 1), quad = lane >> 4;
   const int D = K.D, units = D / C;
-  const bool there = P.token >= 0;
-  const int64_t token = max(P.token, (int64_t)0);
-  const int r = GROUPED ? lane & 15 : (int)(token & 15);
+  const int64_t at = token_of(K, P), token = max(at, (int64_t)0);
+  const bool there = at >= 0;
+  const int r = (int)(token & 15);
   const char* src = static_cast<const char*>(is_v ? K.v : K.k) + (token & ~(int64_t)15) * D * BYTES;
   T* dst = static_cast<T*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) + P.head * (is_v ? A.ldv_h : A.ldk_h);
   float scale = 1.f;
   if constexpr (KvFormat<FMT>::scaled) {
     if (there) scale = (is_v ? K.v_scale : K.k_scale)[token];
   }
+  u32x4_t all[U::most];  // of every unit before the first store
 #pragma unroll
   for (int n = 0; n < U::most; ++n) {
     if (4 * n >= units) break;
@@ -413,10 +446,10 @@ __device__ __forceinline__ void read_rows(const KvArgs& K, const KvRows& A, bool
         c = load_u32x4(src + (u * 16 + r) * 16);
       } else {
         const int j = lane & 3, place = place_of(r & ~3);
+        if constexpr (BYTES == 1) c = load_u32x4(src + v_at<1>(u * 16 + (lane & 15), 0));
+        if constexpr (BYTES == 4) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (BYTES == 1) c[k] = *reinterpret_cast<const uint32_t*>(src + v_at<1>(u * 16 + 4 * k + j, place));
-          if constexpr (BYTES == 4) c[k] = *reinterpret_cast<const uint32_t*>(src + v_at<4>(u * 4 + k, place_of(r)));
+          for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const uint32_t*>(src + v_at<4>(u * 4 + k, place_of(r)));
         }
         if constexpr (BYTES == 2) {
 #pragma unroll
@@ -428,11 +461,15 @@ __device__ __forceinline__ void read_rows(const KvArgs& K, const KvRows& A, bool
         }
       }
     }
-    if (GROUPED && is_v) {
-      if constexpr (BYTES == 1) {
+    all[n] = c;
+  }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = transpose_bytes(c[k], lane);
-      }
+  for (int n = 0; n < U::most; ++n) {
+    if (4 * n >= units) break;
+    const int u = quad + 4 * n;
+    u32x4_t c = all[n];
+    if (GROUPED && is_v) {
+      if constexpr (BYTES == 1) transpose_16x16(c, lane);
       if constexpr (BYTES == 2) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -474,7 +511,7 @@ __device__ __forceinline__ void read_v_row(const KvArgs& K, const KvRows& A, con
   const int lane = threadIdx.x & (WAVE - 1), D = K.D;
   if (!P.ok) return;
   T* dst = static_cast<T*>(A.v) + P.row * A.ldv_t + P.head * A.ldv_h;
-  const int64_t token = max(P.token, (int64_t)0);
+  const int64_t at = token_of(K, P), token = max(at, (int64_t)0);
   const char* src = static_cast<const char*>(K.v) + (token & ~(int64_t)15) * D * BYTES;
   const int place = place_of((int)(token & 15));
   float scale = 1.f;
@@ -494,13 +531,13 @@ __device__ __forceinline__ void read_v_row(const KvArgs& K, const KvRows& A, con
   }
 #pragma unroll
   for (int i = 0; i < MOST; ++i)
-    if (lane + WAVE * i < D) dst[lane + WAVE * i] = P.token < 0 ? T(0) : e[i];
+    if (lane + WAVE * i < D) dst[lane + WAVE * i] = at < 0 ? T(0) : e[i];
 }
 
 template <int FMT, class T>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_read_groups_kernel(KvArgs K, KvRows A) {
   Place P;
-  if (group_place(K, A.out_start, A.rows, P)) read_rows<FMT, T, true>(K, A, blockIdx.z, P);
+  if (group_place(K, A.out_start, A.rows, blockIdx.z && KvFormat<FMT>::bytes == 1, P)) read_rows<FMT, T, true>(K, A, blockIdx.z, P);
 }
 
 template <int FMT, class T>
