@@ -8,7 +8,9 @@
 // more and a little less round to the same code, that is it, and only where they do not (about one
 // value in ten thousand) the quotient is formed exactly: of bf16 rows x * F is exact in fp32 and a
 // quotient of so few bits lies on a border of the format or far from it, so that one correctly
-// rounded division decides; of fp32 rows in fp64, rounded to odd before the last rounding.
+// rounded division decides; of fp32 rows in fp64, rounded to odd before the last rounding. In a long write
+// quantising is a third of the time: the maximum is taken of the bits, two bf16 at once,
+// and an int8 code costs one addition for each of the two (19.6 us with float maxima, products and rint; 16.8 so).
 //
 // A wave takes 16 rows, lane r of each quarter (quad) row r, and of every row the pieces of K that are
 // 16 bytes in the cache, quad by quad, all of them loaded before the first is stored. K is stored as it is
@@ -20,8 +22,9 @@
 // separate waves.
 //
 // Bound: the rows' bytes; one token per sequence: the chain of loads from the sequence to its page.
-// Measured, 8 heads of 128: 256 sequences' new tokens written as e4m3 6.5 us and read back 4.0 us; 16 prompts' chunks written as int8 19 us (54 MB), 42 thousand tokens read back as bf16 61 us (264
-// MB, 4.3 TB/s; a large copy: 5.1).
+// Measured, 8 heads of 128: 256 sequences' new tokens written as e4m3 6.2 us and read back 4.2 us; 16 prompts'
+// chunks written as int8 16.8 us (54 MB, all waves at once: load, quantise, store), 42 thousand tokens read
+// back as bf16 57 us (264 MB, 4.6 TB/s; a large copy: 5.1).
 #include "kv_common.h"
 
 namespace sgmv {
@@ -36,40 +39,52 @@ __device__ __forceinline__ float to_odd(double d) {
   return (double)f == d ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// Four values rounded to codes.
+// What quantising a row needs: its maximum; a power of two that keeps the parts of a quotient in range; F over
+// the maximum, a little less and a little more; its scale.
+struct RowScale {
+  float amax, s, lo, hi, scale;
+};
+
+// top: bits of the row's maximum of |x| (as integers they order as the values do, infinity and NaN last)
 template <int FMT>
-__device__ __forceinline__ uint32_t encode4(const float (&q)[4]) {
+__device__ __forceinline__ RowScale row_scale(uint32_t top) {
+  constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
+  if (top == 0u || top >= 0x7f800000u) return {0.f, 1.f, 0.f, 0.f, top ? __uint_as_float(0x7fc00000u) : 0.f};
+  const float amax = __uint_as_float(top), s = amax > 0x1p100f ? 0x1p-32f : amax < 0x1p-90f ? 0x1p64f : 1.f;
+  const float inv = F / (amax * s) * (s < 1.f ? s : 1.f);
+  return {amax, s, inv * (1.f - 0x1p-22f), inv * (1.f + 0x1p-22f), amax / F};
+}
+
+// Four values times f, rounded to codes. int8: in 1.5 * 2^23 + q the low bits are those of q rounded, of
+// the exact product.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(const float (&q)[4], float f) {
   if constexpr (FMT == SGMV_KV_E4M3) {
-    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0] * f, q[1] * f, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2] * f, q[3] * f, w, true);
   } else {
-    uint32_t w = 0;
+    uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w |= ((uint32_t)(int)rintf(q[i]) & 0xffu) << (8 * i);
-    return w;
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(fmaf(q[i], f, 0x1.8p23f));
+    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
+                                 __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
   }
 }
 
-// Codes of four values of a row. s: a power of two that keeps the quotient's parts in range.
+// Codes of four values of a row. Rows so small that F over their maximum is no fp32 number: all by the
+// exact quotient.
 template <int FMT, class T>
-__device__ __forceinline__ uint32_t quantise4(const float (&x)[4], float amax, float s, float inv) {
+__device__ __forceinline__ uint32_t quantise4(const float (&x)[4], const RowScale& S) {
   constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
-  float lo[4], hi[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float y = x[i] * s * inv;
-    lo[i] = y * (1.f - 0x1p-22f);
-    hi[i] = y * (1.f + 0x1p-22f);
-  }
-  uint32_t w = encode4<FMT>(lo);
-  if (__any(w != encode4<FMT>(hi))) {
+  uint32_t w = encode4<FMT>(x, S.lo);
+  if (__any(w != encode4<FMT>(x, S.hi) || S.s > 1.f)) {
     float q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      q[i] = sizeof(T) == 4 ? to_odd((double)x[i] * (double)F / (double)amax) : x[i] * s * F / (amax * s);
-    w = encode4<FMT>(q);
+      q[i] = sizeof(T) == 4 ? to_odd((double)x[i] * (double)F / (double)S.amax) : x[i] * S.s * F / (S.amax * S.s);
+    w = encode4<FMT>(q, 1.f);
   }
-  return w;
+  return S.lo == 0.f ? 0u : w;
 }
 
 // Transposes a 4x4 block of bytes held by 4 neighbouring lanes, one row each.
@@ -164,6 +179,25 @@ __device__ __forceinline__ float word_value(const uint32_t (&w)[N], int e) {
   return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
 }
 
+// The larger |value| of a word of T and of `top`, as bits; 16-bit values in both halves.
+template <class T>
+__device__ __forceinline__ uint32_t word_top(uint32_t top, uint32_t w) {
+  if constexpr (sizeof(T) == 4) return max(top, w & 0x7fffffffu);
+  typedef uint16_t u16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2_t, top),
+                                                                __builtin_bit_cast(u16x2_t, w & 0x7fff7fffu)));
+}
+
+// That of the lanes of equal lane % 16, as fp32 bits.
+template <class T>
+__device__ __forceinline__ uint32_t quad_top(uint32_t top) {
+  if constexpr (sizeof(T) == 2) top = max(top & 0xffff0000u, top << 16);
+  auto r = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+  top = max(r[0], r[1]);
+  r = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+  return max(r[0], r[1]);
+}
+
 // Where the row of this lane goes to or comes from.
 struct Place {
   bool ok;        // there is such a row
@@ -248,21 +282,6 @@ template <int FMT, class T> struct Unit {
 template <int BYTES>
 __device__ __forceinline__ int64_t v_at(int d, int place) { return (int64_t)(d * 16 + place) * BYTES; }
 
-// What quantising a row needs: its maximum, a power of two that keeps the quotient's parts in range, and
-// F over the maximum so scaled (0: codes 0); its scale.
-struct RowScale {
-  float amax, s, inv, scale;
-};
-
-// bad: NaN if a value of the row is not finite, else 0
-template <int FMT>
-__device__ __forceinline__ RowScale row_scale(float amax, float bad) {
-  constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
-  if (bad != 0.f) return {amax, 1.f, 0.f, __uint_as_float(0x7fc00000u)};
-  const float s = amax > 0x1p100f ? 0x1p-32f : amax < 0x1p-90f ? 0x1p64f : 1.f;
-  return {amax, s, amax > 0.f ? F / (amax * s) : 0.f, amax / F};
-}
-
 // 16 rows of K (or, grouped, of V) per wave.
 template <int FMT, class T, bool GROUPED>
 __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, bool is_v, const Place& place16) {
@@ -276,7 +295,6 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, boo
   const T* src = static_cast<const T*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) +
                  P.head * (is_v ? A.ldv_h : A.ldk_h);
   uint32_t w[U::most][U::words];
-  float amax = 0.f, bad = 0.f;
 #pragma unroll
   for (int n = 0; n < U::most; ++n) {
     if (4 * n >= units) break;
@@ -289,19 +307,16 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, boo
   P.ok = P.ok && at >= 0;
   const int r = (int)(token & 15);
   char* dst = static_cast<char*>(const_cast<void*>(is_v ? K.v : K.k)) + (token & ~(int64_t)15) * D * BYTES;
-  RowScale S = {0.f, 1.f, 0.f, 0.f};
+  RowScale S = {};
   if constexpr (SCALED) {
+    uint32_t top = 0;
 #pragma unroll
     for (int n = 0; n < U::most; ++n) {
       if (4 * n >= units) break;
 #pragma unroll
-      for (int e = 0; e < C; ++e) {
-        const float x = word_value<T>(w[n], e);
-        amax = fmaxf(amax, fabsf(x));
-        bad = fmaf(x, 0.f, bad);
-      }
+      for (int i = 0; i < U::words; ++i) top = word_top<T>(top, w[n][i]);
     }
-    S = row_scale<FMT>(quad_max(amax), quad_sum(bad));
+    S = row_scale<FMT>(quad_top<T>(top));
     if (P.ok && quad == 0) const_cast<float*>(is_v ? K.v_scale : K.k_scale)[token] = S.scale;
   }
 #pragma unroll
@@ -316,7 +331,7 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, boo
         float x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[j] = word_value<T>(w[n], 4 * k + j);
-        c[k] = S.inv == 0.f ? 0u : quantise4<FMT, T>(x, S.amax, S.s, S.inv);
+        c[k] = quantise4<FMT, T>(x, S);
       }
     } else {
       c = u32x4_t{w[n][0], w[n][1], w[n][2], w[n][3]};
@@ -366,14 +381,14 @@ __device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, co
   if (!P.ok) return;
   const T* src = static_cast<const T*>(A.v) + P.row * A.ldv_t + P.head * A.ldv_h;
   T e[MOST];
-  float x[MOST], amax = 0.f, bad = 0.f;
+  float x[MOST];
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < MOST; ++i) {
     e[i] = lane + WAVE * i < D ? src[lane + WAVE * i] : T(0);
     if constexpr (sizeof(T) == 4) x[i] = e[i];
     else x[i] = bf16_bits_to_f32(e[i]);
-    amax = fmaxf(amax, fabsf(x[i]));
-    bad = fmaf(x[i], 0.f, bad);
+    top = word_top<float>(top, __float_as_uint(x[i]));
   }
   const int64_t token = token_of(K, P);
   if (token < 0) return;
@@ -382,12 +397,9 @@ __device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, co
   uint32_t c = 0;
   if constexpr (KvFormat<FMT>::scaled) {
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-      amax = fmaxf(amax, __shfl_xor(amax, o));
-      bad += __shfl_xor(bad, o);
-    }
-    const RowScale S = row_scale<FMT>(quad_max(amax), quad_sum(bad));
-    if (S.inv != 0.f) c = quantise4<FMT, T>(x, S.amax, S.s, S.inv);
+    for (int o = 1; o < 16; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    const RowScale S = row_scale<FMT>(quad_top<float>(top));
+    c = quantise4<FMT, T>(x, S);
     if (lane == 0) const_cast<float*>(K.v_scale)[token] = S.scale;
   }
 #pragma unroll
