@@ -214,6 +214,28 @@ def test_quotients_on_a_border_go_to_the_even_code(sg, fmt):
         assert got == [50, 50, 54]
 
 
+@pytest.mark.parametrize("by_rows", [True, False])
+@pytest.mark.parametrize("fmt,rows", [(E4M3, BF16), (I8, BF16), (E4M3, F32), (I8, F32)])
+def test_rows_of_every_magnitude(sg, fmt, rows, by_rows):
+    """Maxima of every exponent of the type, subnormal ones too, beside rows of zeros and of NaN: one sequence's
+    tokens (by groups), or each its own (by rows)."""
+    exps = list(range(-149 if rows is F32 else -133, 128))
+    T = len(exps)
+    st = Step(sg, [1] * T if by_rows else [T], [5] * T if by_rows else [T + 3], 16, 2, 48, fmt, seed=14, rows=rows)
+    k = st.randn(T, 2, 48)
+    k = (k / k.abs().amax(-1, keepdim=True)).double() * 1.99
+    k = k * torch.tensor([2.0 ** e for e in exps], dtype=torch.float64)[:, None, None]
+    k = k.to(torch.float32).to(rows)
+    assert torch.isfinite(k).all()
+    k[::17, 0] = 0
+    k[5::31, 1, 40] = float("nan")
+    bufs, scales = _expected_cache(st, k, k)
+    sg.sgmv_kv_write(k.to(DEV), k.to(DEV), st.batch, st.cache)
+    assert _same(_raw(st.cache.k), bufs[0]) and _same(_raw(st.cache.v), bufs[1])
+    _check_scales(st.cache.k_scale, scales[0])
+    _check_scales(st.cache.v_scale, scales[1])
+
+
 def test_rows_of_sequences_with_different_counts(sg):
     """Writes and reads by rows where a sequence's number is not its share of the tokens."""
     news = [0] * 30 + [8, 1] + [0] * 5 + [2] * 3 + [0, 7]
