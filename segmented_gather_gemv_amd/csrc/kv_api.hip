@@ -92,7 +92,9 @@ void split_tokens(int64_t n, int64_t tokens, int unit, int32_t& n_split, int32_t
 }
 
 // Ranges for the tiled kernel, whose workgroups fill a compute unit each: as many as fit beside each other,
-// of at least two tiles (100 tokens over 4096, 8 heads: 17 us in 16 ranges, 91 us in 1).
+// of at least two tiles (100 tokens over 4096, 8 heads: 17 us in 16 ranges, 91 us in 1). Not beyond, where
+// tiles of different lengths leave units idle at the end: their parts cost more than that (4 chunks of
+// 300..700 beside 28 single tokens, 200 tiles: 73 us in 1 range, 134 in 2).
 int64_t tiled_splits(int64_t base, int64_t tokens) {
   return base > 0 ? std::min(256 / base, ceil_div(tokens, 128)) : 1;
 }

@@ -20,7 +20,8 @@ namespace sgmv {
 namespace {
 
 constexpr int VF_WAVES = 4;               // of a workgroup of the first launch
-constexpr int VF_ONE_PARTS = 16;          // of a row that one workgroup does, a wave each
+constexpr int VF_ONE_WAVES = 16;          // of a workgroup that does a row alone
+constexpr int VF_ONE_PARTS = 32;          // of such a row
 constexpr int VF_EACH = VF_PART / WAVE;   // entries of one lane
 
 __device__ __forceinline__ float prob(const float* p) { return *p; }
@@ -119,9 +120,9 @@ __device__ __forceinline__ void store_taken(const VerifyArgs& A, int b, Drafts d
   if (lane == 0) A.accepted[b] = taken;
 }
 
-// Sums of one part of the row (what lies past its end counts as 0): of what is left of p, and of p itself;
-// in every lane.
-template <class T, bool VEC>
+// Sums of one part of the row (what lies past its end counts as 0): of what is left of p, and, BOTH, of p
+// itself; in every lane.
+template <class T, bool VEC, bool BOTH>
 __device__ __forceinline__ void sum_part(const VerifyArgs& A, const Row<T>& row, int part, double& sum, double& all) {
   const int lane = threadIdx.x & (WAVE - 1);
   sum = all = 0.;
@@ -133,14 +134,14 @@ __device__ __forceinline__ void sum_part(const VerifyArgs& A, const Row<T>& row,
     if (row.q) four<T, VEC>(row.q, j, A.V, q);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      all += p[e];
+      if constexpr (BOTH) all += p[e];
       sum += j + e == row.hole ? 0. : rest(p[e], q[e]);
     }
   }
 #pragma unroll
   for (int o = 32; o; o >>= 1) {
     sum += __shfl_xor(sum, o);
-    all += __shfl_xor(all, o);
+    if constexpr (BOTH) all += __shfl_xor(all, o);
   }
 }
 
@@ -226,7 +227,7 @@ __global__ __launch_bounds__(VF_WAVES* WAVE) void verify_sum_kernel(VerifyArgs A
   const int taken = count_taken<T>(A, b, d);
   if (part == 0) store_taken(A, b, d, taken);
   double sum, all;
-  sum_part<T, VEC>(A, drawn_row<T>(A, b, d, taken), part, sum, all);
+  sum_part<T, VEC, true>(A, drawn_row<T>(A, b, d, taken), part, sum, all);
   if (lane < 2) A.sums[((int64_t)b * A.parts + part) * 2 + lane] = lane ? all : sum;
 }
 
@@ -238,25 +239,32 @@ __global__ __launch_bounds__(WAVE) void verify_draw_kernel(VerifyArgs A) {
   if (threadIdx.x == 0) A.tokens[(int64_t)b * A.ldo + taken] = token;
 }
 
-// Both in one launch, one workgroup per sequence, for rows of few parts (64 sequences of 8000 entries: 8.6 us, 10.0
-// us in two launches; with two parts per wave, 32000 entries, 11.2 us and 10.0 us: the fp64 sums take a
-// compute unit as long as a launch).
+// Both in one launch, one workgroup per sequence, for rows of few parts: the fp64 sums of two parts per wave
+// take a compute unit about as long as the second launch (fp32 rows, 4 drafts; replayed: 64 sequences of
+// 32000 entries 10.9 us, 10.5 in two launches; 256 of them 17.2 and 19.3, one 8.5 and 8.6), and the host launches
+// once (12 us a call, 14.5). The sums of p itself are formed only where nothing is left of it.
 template <class T, bool VEC>
-__global__ __launch_bounds__(VF_ONE_PARTS* WAVE) void verify_one_kernel(VerifyArgs A) {
+__global__ __launch_bounds__(VF_ONE_WAVES* WAVE) void verify_one_kernel(VerifyArgs A) {
   __shared__ double s_sums[2 * VF_ONE_PARTS];
-  const int b = blockIdx.x, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
+  const int b = blockIdx.x, wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE), lane = threadIdx.x & (WAVE - 1);
   const Drafts d = drafts(A, b);
   const double u = A.sample_u[b];
   const int taken = count_taken<T>(A, b, d);
   if (wv == 0) store_taken(A, b, d, taken);
   const Row<T> row = drawn_row<T>(A, b, d, taken);
-  double sum, all;
-  sum_part<T, VEC>(A, row, wv, sum, all);
-  if ((threadIdx.x & (WAVE - 1)) == 0) {
-    s_sums[2 * wv] = sum;
-    s_sums[2 * wv + 1] = all;
+  double sum, none;
+  for (int part = wv; part < A.parts; part += VF_ONE_WAVES) {
+    sum_part<T, VEC, false>(A, row, part, sum, none);
+    if (lane < 2) s_sums[2 * part + lane] = lane ? 0. : sum;
   }
   __syncthreads();
+  if (!__any(lane < A.parts && s_sums[2 * min(lane, VF_ONE_PARTS - 1)] > 0.)) {  // the same in every wave
+    for (int part = wv; part < A.parts; part += VF_ONE_WAVES) {
+      sum_part<T, VEC, false>(A, Row<T>{row.p, nullptr, -1}, part, sum, none);
+      if (lane == 0) s_sums[2 * part + 1] = sum;
+    }
+    __syncthreads();
+  }
   if (wv) return;
   const int token = draw<T, VEC>(A, row, s_sums, u);
   if (threadIdx.x == 0) A.tokens[(int64_t)b * A.ldo + taken] = token;
@@ -265,7 +273,7 @@ __global__ __launch_bounds__(VF_ONE_PARTS* WAVE) void verify_one_kernel(VerifyAr
 template <class T, bool VEC>
 void launch(const VerifyArgs& A, hipStream_t stream) {
   if (A.parts <= VF_ONE_PARTS) {
-    verify_one_kernel<T, VEC><<<dim3((unsigned)A.B), VF_ONE_PARTS * WAVE, 0, stream>>>(A);
+    verify_one_kernel<T, VEC><<<dim3((unsigned)A.B), VF_ONE_WAVES * WAVE, 0, stream>>>(A);
     return;
   }
   const dim3 g((unsigned)((A.parts + VF_WAVES - 1) / VF_WAVES), (unsigned)A.B);

@@ -271,3 +271,39 @@ def test_draws_at_the_borders_of_parts(sg, V, dtype):
     for b in range(B):
         ref, _ = ko.verify(t[b:b + 1].float().numpy(), None, [], [], float(su[b]))
         assert tokens[b].cpu().tolist() == ref, (b, places[b // len(us)], us[b % len(us)])
+
+
+@pytest.mark.parametrize("V", [16384, 16385, 20001, 32767, 32768, 32769])
+def test_draws_of_rows_in_one_launch_and_in_two(sg, V):
+    """Rows of as many parts as one workgroup does, one more and fewer: weights at their ends, and rejected
+    drafts that leave nothing (the draft at least as likely everywhere; all weight on a certain draft), where
+    the token comes from the target's own row."""
+    places = sorted({0, 1023, 1024, 16383, min(16384, V - 1), V // 2 + 1, V - 2, V - 1})
+    us = [0.0, 0.3, 0.5, 0.7, 1 - 2.0 ** -24]
+    cases = [(p, u) for p in places for u in us]
+    B = len(cases)
+    t = torch.zeros(2 * B, V)
+    d = torch.zeros(B, V)
+    for b, (p, _) in enumerate(cases):
+        t[2 * b, p], t[2 * b, (p + V // 3) % V] = 0.25, 0.125
+        d[b, p], d[b, (p + V // 3) % V] = 0.5, 0.25
+        if b % 3 == 0:  # something left, in one place
+            t[2 * b, (p + V // 2) % V] = 0.0625
+        t[2 * b + 1, p] = 1.0
+    ids = [p for p, _ in cases]
+    au = [0.25 if b % 7 == 6 else 0.75 for b in range(B)]
+    su = [u for _, u in cases]
+    for draft in (d, None):
+        if draft is None:
+            for b, (p, _) in enumerate(cases):
+                if b % 3 == 1:
+                    t[2 * b] = 0
+                    t[2 * b, p] = 0.25
+        tokens, accepted = sg.sgmv_verify_drafts(
+            t.to(DEV), None if draft is None else draft.to(DEV), _i32(ids), _i32(list(range(B + 1))),
+            torch.tensor(au, device=DEV), torch.tensor(su, device=DEV), 1)
+        for b in range(B):
+            ref, taken = ko.verify(t[2 * b:2 * b + 2].numpy(), None if draft is None else draft[b:b + 1].numpy(),
+                                   ids[b:b + 1], au[b:b + 1], su[b])
+            assert accepted[b].item() == taken, b
+            assert tokens[b].cpu().tolist() == ref + [-1] * (1 - taken), (b, cases[b])
