@@ -107,14 +107,17 @@ int64_t tiled_splits(int64_t base, int64_t tokens) {
 //         waves (six of 4) per compute unit, of long ranges (16 sequences of 8001..64003, e4m3: 361 us in 1
 //         range, 238 in 2, 231 in 8). From 1024 workgroups of 4 waves on a call is not split (256 of
 //         128..4096, bf16: 397 us in 1, 418 in 3).
-// fp32 steps take four times as long and are split whatever their number.
+// fp32 steps, of 4 waves, take four times as long: up to 512 tokens are not split (4 x 20 rows over 400, 32 /
+// 8 heads of 128: 18.4 us in 1 range, 27.5 in 2; over 300 in a window of 256, 14 / 2 heads of 80: 12.1 and
+// 14.5; 4 single tokens over 500: 12.2 and, in 4, 11.1 and a second launch for the host), and fill stops
+// at one workgroup per compute unit (4 x 8 over 1000, heads of 128: 24.2 us in 2 ranges, 29.0 in 4).
 void split_direct(AttnArgs& A, int64_t base, int64_t tokens, int forced) {
   const int step = A.direct_waves * (A.kv.k_scale ? 64 : 32);
   int64_t n = forced;
   if (!n && base > 0) {
-    const int64_t fill = std::min<int64_t>((A.direct_waves == 8 ? 256 : 512) / base, ceil_div(tokens, step));
+    const int64_t fill = std::min<int64_t>((A.direct_waves == 8 || A.f32 ? 256 : 512) / base, ceil_div(tokens, step));
     const int64_t even = std::min<int64_t>((A.direct_waves == 8 ? 1024 : 1536) / base, ceil_div(tokens, 2 * A.direct_waves * step));
-    n = !A.f32 && tokens <= 6 * step ? 1 : std::max(fill, even);
+    n = tokens <= (A.f32 ? 512 : 6 * step) ? 1 : std::max(fill, even);
   }
   split_tokens(n, tokens, step, A.n_split[0], A.chunk[0]);
 }
