@@ -4,13 +4,15 @@
 //   amax = max |x|,  scale = amax / F,  code = round(x * F / amax) to the format, ties to even;
 //   a row of zeros has scale 0 and codes 0; a row with a non-finite value has scale NaN and codes
 //   0, so that it reads back as NaN whatever the format can hold.
-// The code is that of the exact quotient. x * (F / amax) in fp32 is within 2^-23 of it: where a little
-// more and a little less round to the same code, that is it, and only where they do not (about one
-// value in ten thousand) the quotient is formed exactly: of bf16 rows x * F is exact in fp32 and a
-// quotient of so few bits lies on a border of the format or far from it, so that one correctly
-// rounded division decides; of fp32 rows in fp64, rounded to odd before the last rounding. In a long write
-// quantising is a third of the time: the maximum is taken of the bits, two bf16 at once,
-// and an int8 code costs one addition for each of the two (19.6 us with float maxima, products and rint; 16.8 so).
+// The code is that of the exact quotient; y = x * (F / amax) in fp32 is within 2^-23 of it.
+//   bf16 rows: the quotient of 8-bit significands and F is a border between two codes or at least 2^-16 of
+//   it away (their difference, times both denominators, is a whole number). y rounded to 19 bits is that border
+//   or on the quotient's side of it, so its code is the quotient's, ties to even with it.
+//   fp32 rows: where a little more and a little less than y round to the same code, that is it, and only where
+//   they do not (two values in a hundred thousand) the quotient is formed in fp64, rounded to odd first.
+// The maximum is taken of the bits, two bf16 at once. So done, a write as e4m3 takes no longer than one of
+// bf16 (64 sequences' 100 tokens: 12.4 us both; with an exact division of bf16 values on a border as well, which
+// half of all waves have at any step, 18.1).
 //
 // A wave takes 16 rows, lane r of each quarter (quad) row r, and of every row the pieces of K that are
 // 16 bytes in the cache, quad by quad, all of them loaded before the first is stored. K is stored as it is
@@ -22,8 +24,8 @@
 // separate waves.
 //
 // Bound: the rows' bytes; one token per sequence: the chain of loads from the sequence to its page.
-// Measured, 8 heads of 128: 256 sequences' new tokens written as e4m3 6.2 us and read back 4.2 us; 16 prompts'
-// chunks written as int8 16.8 us (54 MB, all waves at once: load, quantise, store), 42 thousand tokens read
+// Measured, 8 heads of 128: 256 sequences' new tokens written as e4m3 5.6 us and read back 4.2 us; 16 prompts'
+// chunks written as int8 16.0 us (54 MB, all waves at once: load, quantise, store), 42 thousand tokens read
 // back as bf16 57 us (264 MB, 4.6 TB/s; a large copy: 5.1).
 #include "kv_common.h"
 
@@ -39,52 +41,62 @@ __device__ __forceinline__ float to_odd(double d) {
   return (double)f == d ? f : __uint_as_float(__float_as_uint(f) | 1u);
 }
 
-// What quantising a row needs: its maximum; a power of two that keeps the parts of a quotient in range; F over
-// the maximum, a little less and a little more; its scale.
+// What quantising a row needs: its maximum; a power of two that keeps the parts of a quotient in range, and F
+// over the maximum so scaled (0: codes 0); its scale.
 struct RowScale {
-  float amax, s, lo, hi, scale;
+  float amax, s, inv, scale;
 };
 
 // top: bits of the row's maximum of |x| (as integers they order as the values do, infinity and NaN last)
 template <int FMT>
 __device__ __forceinline__ RowScale row_scale(uint32_t top) {
   constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
-  if (top == 0u || top >= 0x7f800000u) return {0.f, 1.f, 0.f, 0.f, top ? __uint_as_float(0x7fc00000u) : 0.f};
+  if (top == 0u || top >= 0x7f800000u) return {0.f, 1.f, 0.f, top ? __uint_as_float(0x7fc00000u) : 0.f};
   const float amax = __uint_as_float(top), s = amax > 0x1p100f ? 0x1p-32f : amax < 0x1p-90f ? 0x1p64f : 1.f;
-  const float inv = F / (amax * s) * (s < 1.f ? s : 1.f);
-  return {amax, s, inv * (1.f - 0x1p-22f), inv * (1.f + 0x1p-22f), amax / F};
+  return {amax, s, F / (amax * s), amax / F};
 }
 
-// Four values times f, rounded to codes. int8: in 1.5 * 2^23 + q the low bits are those of q rounded, of
-// the exact product.
+// Four values rounded to codes. int8: the low bits of 1.5 * 2^23 + q are those of q rounded.
 template <int FMT>
-__device__ __forceinline__ uint32_t encode4(const float (&q)[4], float f) {
+__device__ __forceinline__ uint32_t encode4(const float (&q)[4]) {
   if constexpr (FMT == SGMV_KV_E4M3) {
-    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0] * f, q[1] * f, 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2] * f, q[3] * f, w, true);
+    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
   } else {
     uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(fmaf(q[i], f, 0x1.8p23f));
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(q[i] + 0x1.8p23f);
     return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
                                  __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
   }
 }
 
-// Codes of four values of a row. Rows so small that F over their maximum is no fp32 number: all by the
-// exact quotient.
+// Codes of four values of a row.
 template <int FMT, class T>
 __device__ __forceinline__ uint32_t quantise4(const float (&x)[4], const RowScale& S) {
   constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
-  uint32_t w = encode4<FMT>(x, S.lo);
-  if (__any(w != encode4<FMT>(x, S.hi) || S.s > 1.f)) {
-    float q[4];
+  uint32_t w;
+  float q[4];
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      q[i] = sizeof(T) == 4 ? to_odd((double)x[i] * (double)F / (double)S.amax) : x[i] * S.s * F / (S.amax * S.s);
-    w = encode4<FMT>(q, 1.f);
+    for (int i = 0; i < 4; ++i) q[i] = __uint_as_float((__float_as_uint(x[i] * S.s * S.inv) + 16u) & ~31u);
+    w = encode4<FMT>(q);
+  } else {
+    float hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float y = x[i] * S.s * S.inv;
+      q[i] = y * (1.f - 0x1p-22f);
+      hi[i] = y * (1.f + 0x1p-22f);
+    }
+    w = encode4<FMT>(q);
+    if (__any(w != encode4<FMT>(hi))) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = to_odd((double)x[i] * (double)F / (double)S.amax);
+      w = encode4<FMT>(q);
+    }
   }
-  return S.lo == 0.f ? 0u : w;
+  return S.inv == 0.f ? 0u : w;
 }
 
 // Transposes a 4x4 block of bytes held by 4 neighbouring lanes, one row each.

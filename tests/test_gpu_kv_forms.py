@@ -236,6 +236,32 @@ def test_rows_of_every_magnitude(sg, fmt, rows, by_rows):
     _check_scales(st.cache.v_scale, scales[1])
 
 
+@pytest.mark.parametrize("fmt", [E4M3, I8])
+def test_every_quotient_of_two_bf16_significands(sg, fmt):
+    """Rows with each significand as their maximum, and each other one below it in nine binades and a few far
+    down: every border that a quotient can lie on or next to."""
+    small = torch.tensor([(128 + m) * 2.0 ** -e for e in (8, 9, 10, 11, 12, 13, 14, 15, 16, 17, 18, 24)
+                          for m in range(128)])
+    per = 240
+    rows = []
+    for top in range(128, 256):
+        x = small[small < top / 128.0] * torch.tensor([1.0, -1.0]).repeat(len(small))[:int((small < top / 128.0).sum())]
+        for i in range(0, len(x), per - 1):
+            row = torch.full((per,), top / 128.0)
+            row[1:1 + len(x[i:i + per - 1])] = x[i:i + per - 1]
+            rows.append(row)
+    if len(rows) % 2:
+        rows.append(rows[0])
+    k = torch.stack(rows).reshape(-1, 2, per)
+    assert torch.equal(k.to(BF16).float(), k)
+    k = k.to(BF16)
+    T = k.shape[0]
+    st = Step(sg, [T], [T + 3], 64, 2, per, fmt, seed=2)
+    bufs, _ = _expected_cache(st, k, k)
+    sg.sgmv_kv_write(k.to(DEV), k.to(DEV), st.batch, st.cache)
+    assert _same(_raw(st.cache.k), bufs[0]) and _same(_raw(st.cache.v), bufs[1])
+
+
 def test_rows_of_sequences_with_different_counts(sg):
     """Writes and reads by rows where a sequence's number is not its share of the tokens."""
     news = [0] * 30 + [8, 1] + [0] * 5 + [2] * 3 + [0, 7]
