@@ -473,7 +473,9 @@ sgmv_status sgmv_kv_init(int32_t pages, int32_t page_size, int32_t heads, int32_
  * nothing). A page id outside [0, pages) (use -1) means that those tokens are not there: not
  * written, not attended to, read back as zeros. Pages may be shared by sequences as long as
  * no two tokens of one write call go to the same place. kv_len is cut to table_pages *
- * page_size, q_start to [0, T]: no contents of these arrays lead outside the arrays.
+ * page_size, q_start to [0, T]: no contents of these arrays lead outside the arrays. Rows
+ * before q_start[0] and from q_start[B] on (a step padded to T rows) belong to no sequence:
+ * they are not read, and nothing is written for them.
  * Host numbers: T rows, max_q >= every n_b, max_kv >= every kv_len (they choose the launch;
  * rows of a sequence with more than max_q new tokens may stay unwritten). */
 typedef struct {

@@ -172,7 +172,8 @@ def sgmv_kv_batch(q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch
                   max_q: int, max_kv: int) -> KvBatch:
     """The sequences of a step (device tensors that later calls read again: refill them in
     place for another step of the same sizes). T rows of new tokens, at most max_q of one
-    sequence, at most max_kv tokens in one sequence, the new ones included."""
+    sequence, at most max_kv tokens in one sequence, the new ones included. Rows that q_start
+    leaves over (a step padded to T rows) are neither read nor written."""
     for t, d in ((q_start, 1), (kv_len, 1), (page_table, 2)):
         if t.dtype != torch.int32 or t.dim() != d or t.device != kv_len.device:
             raise TypeError("q_start [B + 1], kv_len [B] and page_table [B, pages] must be int32 "

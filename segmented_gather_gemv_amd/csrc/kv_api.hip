@@ -154,7 +154,14 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   A.direct_tile = most > 16 && pair ? 32 : 16;
   A.one_tile = most <= A.direct_tile;
   int64_t direct = A.one_tile ? s->B : (int64_t)s->T * A.G / A.direct_tile + s->B;
-  if (tiled && s->T == (int64_t)s->B * s->max_q) direct = 0;  // no sequence is short
+  // B max_q rows: as a rule every sequence has max_q, and nothing is left for the direct kernel. What q_start
+  // holds is not known here, so shorter sequences are the tiled kernel's then, instead of workgroups that
+  // mostly find nothing (1 x 2048 over 14001, e4m3: 424 us, 427 with them; 1 x 256 over 4096: 43 and 44; 32
+  // single tokens in a step of 32 x 64, over 4096: 124 and 106).
+  if (tiled && s->T == (int64_t)s->B * s->max_q) {
+    direct = 0;
+    A.direct_rows = 0;
+  }
   const int64_t tiles = tiled ? (int64_t)s->T * A.G / tiled_rows(D) + s->B : 0;
   int64_t tokens = s->max_kv;
   if (a->window) tokens = std::min(tokens, (int64_t)a->window + s->max_q + AT_TOKENS);

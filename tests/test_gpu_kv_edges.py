@@ -1,0 +1,113 @@
+"""GPU tests of the edges of the cache's, the attention's and the draft check's contracts: steps padded to a
+fixed number of rows.
+
+The bars are those of test_gpu_kv (derived there).
+"""
+import pytest
+import torch
+
+from test_gpu_kv import BF16, DEV, E4M3, F32, I8, Step, _check_attention, _expected_cache, _i32, _raw, _same
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sg():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import segmented_gather_gemv_amd as m
+    return m
+
+
+# ---- steps of more rows than their sequences have ------------------------------------------
+PADDED = {
+    # name: new tokens, length, rows of the step's largest sequence, query heads, key/value heads, D
+    "one_short": ([8], [300], 256, 8, 2, 128),
+    "one_token": ([1], [90], 64, 4, 1, 64),
+    "long_short_empty": ([64, 1, 0, 33], [200, 150, 40, 33], 64, 8, 2, 128),
+    "all_empty_but_the_last": ([0, 0, 3], [5, 0, 70], 40, 4, 1, 96),
+    "wide": ([2, 50], [60, 170], 50, 8, 2, 256),
+    "no_tiles_of_this_dimension": ([2, 50], [60, 170], 50, 8, 2, 112),
+}
+
+
+def _padded(sg, st, max_q):
+    """The step's batch with room for max_q rows of every sequence; q_start ends before them."""
+    return sg.sgmv_kv_batch(st.batch.q_start, st.batch.kv_len, st.batch.page_table, len(st.new) * max_q, max_q,
+                            max(st.kv_len))
+
+
+def _pad(x, T):
+    """Rows x on the GPU, followed by rows of NaN."""
+    y = torch.full((T, *x.shape[1:]), float("nan"), dtype=x.dtype)
+    y[:x.shape[0]] = x
+    return y.to(DEV)
+
+
+@pytest.mark.parametrize("fmt,rows", [(BF16, BF16), (E4M3, BF16), (I8, BF16), (F32, F32)])
+@pytest.mark.parametrize("name", sorted(PADDED))
+def test_padded_steps(sg, name, fmt, rows):
+    """Sequences of any number of rows up to max_q, in a step of B max_q rows: each row of a sequence is
+    there, and rows of none are not touched."""
+    new, kv_len, max_q, Hq, H, D = PADDED[name]
+    st = Step(sg, new, kv_len, 16, H, D, fmt, seed=17, rows=rows)
+    kv = st.fill(sg)
+    batch = _padded(sg, st, max_q)
+    q = st.randn(st.T, Hq, D).to(rows)
+    for n_split in (0, 3):
+        out = torch.full((batch.T, Hq, D), float("nan"), dtype=rows, device=DEV)
+        lse = torch.full((batch.T, Hq), float("nan"), device=DEV)
+        out[st.T:], lse[st.T:] = 7, 7
+        sg.sgmv_kv_attention(_pad(q, batch.T), batch, st.cache, out=out, lse=lse, n_split=n_split)
+        _check_attention(st, q, kv, out, lse, D ** -0.5)
+        assert (out[st.T:] == 7).all() and (lse[st.T:] == 7).all()
+    k, v = st.randn(st.T, H, D).to(rows), st.randn(st.T, H, D).to(rows)
+    bufs, _ = _expected_cache(st, k, v)
+    sg.sgmv_kv_write(_pad(k, batch.T), _pad(v, batch.T), batch, st.cache)
+    assert _same(_raw(st.cache.k), bufs[0]) and _same(_raw(st.cache.v), bufs[1])
+    back = [torch.full((batch.T, H, D), 7.0, dtype=rows, device=DEV) for _ in range(2)]
+    sg.sgmv_kv_read(batch, st.cache, batch.q_start, batch.T, rows, k=back[0], v=back[1])
+    for x in back:
+        assert (x[st.T:] == 7).all() and (st.T == 0 or not (x[:st.T] == 7).all())
+
+
+@pytest.mark.parametrize("fmt", [BF16, E4M3])
+def test_padded_step_in_a_graph(sg, fmt):
+    """A step captured at its full size and replayed with fewer rows, against the oracle and eager calls."""
+    max_q, Hq, H, D = 96, 8, 2, 128
+    st = Step(sg, [max_q, max_q], [250, 180], 32, H, D, fmt, seed=5)
+    kv = st.fill(sg)
+    q = st.randn(st.T, Hq, D).to(BF16).to(DEV)
+    out, lse = torch.empty(st.T, Hq, D, dtype=BF16, device=DEV), torch.empty(st.T, Hq, device=DEV)
+    size = sg.sgmv_kv_attention_workspace(Hq, BF16, st.batch, st.cache, n_split=3)
+    ws = torch.empty(max(size, 16), dtype=torch.uint8, device=DEV)
+
+    def step():
+        sg.sgmv_kv_attention(q, st.batch, st.cache, out=out, lse=lse, n_split=3, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        with torch.cuda.graph(graph, stream=s):
+            step()
+    torch.cuda.synchronize()
+    for new in ([max_q, max_q], [1, max_q], [0, 3], [5, 0], [max_q - 1, 8], [max_q, 1]):
+        st.new, st.start = new, [0, new[0], sum(new)]
+        st.T = sum(new)
+        st.batch.q_start.copy_(_i32(st.start))
+        q.copy_(st.randn(2 * max_q, Hq, D).to(BF16).to(DEV))
+        got = []
+        for run in (graph.replay, step):
+            out.fill_(float("nan"))
+            lse.fill_(float("nan"))
+            torch.cuda.synchronize()
+            run()
+            torch.cuda.synchronize()
+            got.append((out[:st.T].clone(), lse[:st.T].clone()))
+            assert torch.isnan(out[st.T:]).all() and torch.isnan(lse[st.T:]).all()
+        same = torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+        assert same, new
+        some = {(b, i) for b, n in enumerate(new) for i in range(0, n, 9)} | {(b, n - 1) for b, n in enumerate(new) if n}
+        _check_attention(st, q[:st.T].cpu(), kv, *got[0], D ** -0.5, rows=some)
