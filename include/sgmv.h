@@ -556,7 +556,8 @@ sgmv_status sgmv_kv_attention(const sgmv_attention* attn, const sgmv_kv_batch* b
  *   draft_ids [N] int32, accept_u [N] fp32, sample_u [B] fp32 in [0, 1), draft_start [B + 1]
  *            int32 not decreasing, all device. A draft outside [0, vocab) is not taken.
  *   tokens   device [B][ldo >= max_drafts + 1] int32: the drafts taken, the drawn token, then
- *            -1. The drawn token is -1 where its row has no positive entry.
+ *            -1. The drawn token is -1 where its row has no positive entry, or sample_u is not
+ *            in [0, 1).
  *   accepted device [B] int32: drafts taken
  * max_drafts >= every n_b (further drafts are not looked at).
  *   workspace  device, 16-byte aligned, of sgmv_verify_drafts_workspace(B, vocab) bytes

@@ -158,31 +158,33 @@ __device__ __forceinline__ int draw(const VerifyArgs& A, const Row<T>& row, cons
     all += sums[2 * c + 1];
   }
   const int pass = __any(left > 0.) ? 0 : 1;
-  double upto = wave_scan(pass ? all : left);
+  const double weight = pass ? all : left;
+  double upto = wave_scan(weight);
   double before = __shfl_up(upto, 1);
   if (lane == 0) before = 0.;
   const double at = u * __shfl(upto, WAVE - 1);
-  // `before` is the very value that the lane before has as its own: neighbours leave no gap
-  const uint64_t here = __ballot(before <= at && at < upto);
+  // The lowest lane with a weight whose sum passes; the last one with a weight if rounding leaves none. (The
+  // lanes' sums are formed in different orders: that of a lane without a weight can pass where the sum of the
+  // lane before it, or any lane's, does not.)
+  const uint64_t some = __ballot(weight > 0.), here = __ballot(weight > 0. && at < upto);
   int token = -1;
-  if (here) {
-    const int owner = __ffsll((unsigned long long)here) - 1;
-    double base = before, last = before;
+  if (some && u >= 0. && u < 1.) {
+    const int owner = here ? __ffsll((unsigned long long)here) - 1 : WAVE - 1 - __clzll((long long)some);
+    double base = before;
     int part = c0;
     if (lane == owner) {
       double sum = before;
       for (int c = c0; c < c1; ++c) {
         const double x = sums[2 * c + pass];
-        if (x > 0.) {
-          part = c;
-          last = sum;
-        }
+        if (!(x > 0.)) continue;
+        part = c;
+        base = sum;
         sum += x;
         if (sum > at) break;
       }
     }
     part = __shfl(part, owner);
-    base = __shfl(last, owner);
+    base = __shfl(base, owner);
 
     const int j0 = part * VF_PART + lane * VF_EACH;
     double w[VF_EACH], mine = 0.;

@@ -1,8 +1,9 @@
 """GPU tests of the edges of the cache's, the attention's and the draft check's contracts: steps padded to a
-fixed number of rows.
+fixed number of rows, draws that fall on the border of a part without a weight.
 
 The bars are those of test_gpu_kv (derived there).
 """
+import numpy as np
 import pytest
 import torch
 
@@ -111,3 +112,44 @@ def test_padded_step_in_a_graph(sg, fmt):
         assert same, new
         some = {(b, i) for b, n in enumerate(new) for i in range(0, n, 9)} | {(b, n - 1) for b, n in enumerate(new) if n}
         _check_attention(st, q[:st.T].cpu(), kv, *got[0], D ** -0.5, rows=some)
+
+
+# ---- drafts -------------------------------------------------------------------------------
+@pytest.mark.parametrize("V", [16 * 1024, 30 * 1024 + 5, 128 * 1024])
+def test_draws_between_parts_without_weight(sg, V):
+    """Parts of a row without a weight, where sums of the parts before them in different orders differ in their
+    last bit and the number falls in between: 2^-53 + 2^-53 + 1 is 1 or 1 + 2^-52. The token has a weight, and the
+    number falls on it to the rounding of such sums (V additions of at most 2^-53 of the total, on either side)."""
+    per = 2048 if V > 64 * 1024 else 1024  # entries of a lane's parts
+    rows = []
+    for a in range(3, 12):
+        for ones in ((2, a), (2,), (0, 5, a)):
+            w = torch.zeros(V)
+            w[0], w[per] = 2.0 ** -53, 2.0 ** -53
+            for i in ones:
+                w[i * per + a] = 1.0
+            rows.append(w)
+    us = [0.0, 2.0 ** -24, 0.25, 0.5, 0.75, 1 - 2.0 ** -24]
+    t = torch.stack([w for w in rows for _ in us])
+    su = torch.tensor(us * len(rows))
+    none, B = torch.empty(0, dtype=torch.int32, device=DEV), t.shape[0]
+    tokens, _ = sg.sgmv_verify_drafts(t.to(DEV), None, none, _i32([0] * (B + 1)), torch.empty(0, device=DEV),
+                                      su.to(DEV), 0)
+    tokens = tokens[:, 0].cpu().tolist()
+    for b in range(B):
+        w = t[b].double().numpy()
+        at = np.flatnonzero(w)
+        c = np.cumsum(w[at])
+        tol = V * 2.0 ** -53 * c[-1]
+        assert tokens[b] in at, (b, tokens[b])
+        i = int(np.searchsorted(at, tokens[b]))
+        x = float(su[b]) * c[-1]
+        assert (c[i - 1] if i else 0.0) - tol <= x < c[i] + tol, (b, tokens[b])
+
+
+def test_numbers_outside_the_unit_interval_draw_nothing(sg):
+    t = torch.full((5, 3000), 1.0 / 3000, device=DEV)
+    su = torch.tensor([-0.25, 1.0, float("nan"), float("inf"), 0.5], device=DEV)
+    none = torch.empty(0, dtype=torch.int32, device=DEV)
+    tokens, accepted = sg.sgmv_verify_drafts(t, None, none, _i32([0] * 6), torch.empty(0, device=DEV), su, 0)
+    assert tokens[:4, 0].tolist() == [-1] * 4 and tokens[4, 0].item() == 1500 and accepted.tolist() == [0] * 5
