@@ -185,9 +185,11 @@ def sgmv_kv_batch(q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch
             page_table.shape[1] > 1 and page_table.stride(1) != 1):
         raise ValueError("q_start, kv_len and the rows of page_table must be contiguous")
     cols = page_table.shape[1]
-    desc = _KvBatch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
-                    max(page_table.stride(0), cols) if B > 1 else cols, cols, B, int(T),
-                    int(max_q), int(max_kv))
+    ldp = page_table.stride(0) if B > 1 else cols
+    if ldp < cols:
+        raise ValueError("the rows of page_table must not share memory (an expanded table: copy it)")
+    desc = _KvBatch(q_start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), ldp, cols, B,
+                    int(T), int(max_q), int(max_kv))
     return KvBatch(q_start, kv_len, page_table, desc)
 
 

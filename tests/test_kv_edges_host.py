@@ -1,0 +1,28 @@
+"""CPU tests of the binding's refusals of arguments that the calls could not follow. Nothing is launched."""
+import pytest
+import torch
+
+import segmented_gather_gemv_amd as sg
+
+
+def _i32(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def test_page_tables_whose_rows_share_memory_are_refused():
+    """A row is read at its number times the row stride: of a table expanded over the batch, or of overlapping
+    windows, that led past its memory."""
+    start, lens = _i32(0, 1, 3), _i32(5, 6)
+    table = torch.arange(8, dtype=torch.int32)
+    for bad in (table[:4].expand(2, 4), table.as_strided((2, 4), (2, 1)), table[:1].expand(2, 1)):
+        with pytest.raises(ValueError, match="page_table"):
+            sg.sgmv_kv_batch(start, lens, bad, 3, 2, 6)
+    wide = torch.zeros(3, 9, dtype=torch.int32)
+    for good, ldp in ((table.view(2, 4), 4), (table.view(2, 4)[:, :3], 4), (wide[:2, 8:], 9), (wide[:2, :0], 9),
+                      (table.as_strided((2, 1), (3, 1)), 3)):
+        b = sg.sgmv_kv_batch(start, lens, good, 3, 2, 6)
+        assert b.desc.ldp == ldp and b.desc.table_pages == good.shape[1]
+        last = b.desc.ldp + good.shape[1] + good.storage_offset()  # of the entries up to row 1's end
+        assert last <= good.untyped_storage().nbytes() // 4
+    one = sg.sgmv_kv_batch(_i32(0, 3), _i32(5), table[:4].expand(1, 4), 3, 3, 6)  # the stride of one row says nothing
+    assert one.desc.ldp == 4
