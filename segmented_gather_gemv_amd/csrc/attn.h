@@ -66,7 +66,8 @@ __device__ __forceinline__ Span row_span(const AttnArgs& A, const KvSeq& s, int 
   const int first = s.kv_len - s.q_len;
   Span p;
   p.end = max(first + hi + 1, 0);
-  p.begin = A.window ? max(first + lo - A.window + 1, 0) & ~(AT_TOKENS - 1) : 0;
+  // (a row before the first token sees nothing: no difference that passes 32 bits for the widest windows)
+  p.begin = A.window ? max(max(first + lo + 1, 0) - A.window, 0) & ~(AT_TOKENS - 1) : 0;
   return p;
 }
 

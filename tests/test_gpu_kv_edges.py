@@ -1,5 +1,5 @@
 """GPU tests of the edges of the cache's, the attention's and the draft check's contracts: steps padded to a
-fixed number of rows, draws that fall on the border of a part without a weight.
+fixed number of rows, windows of any width, draws that fall on the border of a part without a weight.
 
 The bars are those of test_gpu_kv (derived there).
 """
@@ -112,6 +112,21 @@ def test_padded_step_in_a_graph(sg, fmt):
         assert same, new
         some = {(b, i) for b, n in enumerate(new) for i in range(0, n, 9)} | {(b, n - 1) for b, n in enumerate(new) if n}
         _check_attention(st, q[:st.T].cpu(), kv, *got[0], D ** -0.5, rows=some)
+
+
+# ---- windows ------------------------------------------------------------------------------
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30])
+@pytest.mark.parametrize("new,kv_len", [([5, 3, 2], [2, 0, 30]), ([100, 9], [60, 4])])
+@pytest.mark.parametrize("fmt,rows", [(BF16, BF16), (E4M3, BF16), (F32, F32)])
+def test_wide_windows_with_rows_before_the_first_token(sg, new, kv_len, window, fmt, rows):
+    """A window wider than any sequence is none, also where a tile's first rows stand at negative positions: their
+    position less the window is below -2^31."""
+    st = Step(sg, new, kv_len, 16, 2, 128, fmt, seed=7, rows=rows)
+    kv = st.fill(sg)
+    q = st.randn(st.T, 8, 128).to(rows)
+    for n_split in (0, 2):
+        out, lse = sg.sgmv_kv_attention(q.to(DEV), st.batch, st.cache, window=window, n_split=n_split)
+        _check_attention(st, q, kv, out, lse, 128 ** -0.5, window)
 
 
 # ---- drafts -------------------------------------------------------------------------------
