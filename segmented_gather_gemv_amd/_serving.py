@@ -54,6 +54,16 @@ class _Attention(ctypes.Structure):
                 ("window", ctypes.c_int32), ("n_split", ctypes.c_int32)]
 
 
+_MOST = 2 ** 31 - 1
+
+
+def _int32(what: str, *values):
+    """ctypes would cut them to 32 bits."""
+    for v in values:
+        if not -_MOST <= v <= _MOST:
+            raise ValueError(f"{what} must fit in 32 bits, got {v}")
+
+
 def _bind():
     i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
     P = ctypes.POINTER
@@ -106,6 +116,7 @@ def _kv_shapes(desc: _KvCache, elem: int):
 def _kv_desc(pages, page_size, heads, head_dim, dtype) -> _KvCache:
     if dtype not in _FORMATS:
         raise TypeError(f"a cache holds float32, bfloat16, float8_e4m3fn or int8, got {dtype}")
+    _int32("a cache's sizes", pages, page_size, heads, head_dim)
     desc, data, scale = _KvCache(), ctypes.c_size_t(), ctypes.c_size_t()
     _check(_lib.sgmv_kv_init(int(pages), int(page_size), int(heads), int(head_dim),
                              _FORMATS[dtype], ctypes.byref(desc), ctypes.byref(data),
@@ -178,6 +189,7 @@ def sgmv_kv_batch(q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch
         if t.dtype != torch.int32 or t.dim() != d or t.device != kv_len.device:
             raise TypeError("q_start [B + 1], kv_len [B] and page_table [B, pages] must be int32 "
                             "tensors on one device")
+    _int32("T, max_q and max_kv", T, max_q, max_kv)
     B = kv_len.numel()
     if q_start.numel() != B + 1 or page_table.shape[0] != B:
         raise ValueError("q_start needs B + 1 entries and page_table B rows")
@@ -247,6 +259,7 @@ def sgmv_kv_read(batch: KvBatch, cache: KvCache, out_start: torch.Tensor, rows: 
     [rows, heads, head_dim]: out_start = q_start reads the step's new tokens back, running sums
     of kv_len whole sequences. Into k and v if given."""
     rows, heads = int(rows), cache.heads
+    _int32("rows", rows)
     if out_start.dtype != torch.int32 or out_start.numel() != batch.B + 1 or (
             not out_start.is_contiguous() or out_start.get_device() != cache.index):
         raise TypeError("out_start must be B + 1 contiguous int32 entries on the cache's device")
@@ -281,6 +294,8 @@ def sgmv_kv_attention(q: torch.Tensor, batch: KvBatch, cache: KvCache,
     defaults to head_dim ** -0.5. A workspace (uint8) is allocated on the current stream
     unless one is given."""
     T, D = batch.T, cache.head_dim
+    if abs(window) > _MOST or abs(n_split) > _MOST:
+        _int32("window and n_split", window, n_split)
     qt, qh = _rows3(q, T, None, cache, "q")
     heads, dtype = q.shape[1], q.dtype
     code = _dtype_code(dtype)
@@ -321,6 +336,7 @@ def sgmv_kv_attention(q: torch.Tensor, batch: KvBatch, cache: KvCache,
 def sgmv_kv_attention_workspace(q_heads: int, dtype: torch.dtype, batch: KvBatch, cache: KvCache,
                                 window: int = 0, n_split: int = 0) -> int:
     """Bytes of workspace that sgmv_kv_attention takes for such a call."""
+    _int32("q_heads, window and n_split", q_heads, window, n_split)
     a = _Attention(None, None, None, 0, 0, 0, 0, int(q_heads), _dtype_code(dtype), 1.0, int(window),
                    int(n_split))
     need = ctypes.c_size_t()
@@ -363,6 +379,7 @@ def sgmv_verify_drafts(target: torch.Tensor, draft: Optional[torch.Tensor],
     _entries(draft_start, B + 1, torch.int32, dev, "draft_start")
     _entries(accept_u, N, torch.float32, dev, "accept_u")
     _entries(sample_u, B, torch.float32, dev, "sample_u")
+    _int32("vocab and max_drafts", V, max_drafts)
     if max_drafts < 0:
         raise ValueError("max_drafts must not be negative")
     if tokens is None:

@@ -26,3 +26,29 @@ def test_page_tables_whose_rows_share_memory_are_refused():
         assert last <= good.untyped_storage().nbytes() // 4
     one = sg.sgmv_kv_batch(_i32(0, 3), _i32(5), table[:4].expand(1, 4), 3, 3, 6)  # the stride of one row says nothing
     assert one.desc.ldp == 4
+
+
+def test_whole_numbers_past_32_bits_are_refused():
+    """ctypes cuts them to 32 bits: 2^32 + 4 pages were 4, a window of 2^32 + 5 tokens was 5."""
+    start, lens, table, big = _i32(0, 1, 3), _i32(5, 6), torch.zeros(2, 4, dtype=torch.int32), 2 ** 32
+    for sizes in ((4 + big, 16, 2, 64), (4, 16 + big, 2, 64), (4, 16, 2 + big, 64), (4, 16, 2, 64 + big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            sg.sgmv_kv_init(*sizes, torch.int8, "cpu")
+    for sizes in ((3 + big, 2, 6), (3, 2 + big, 6), (3, 2, 6 + big), (3, 2, -big), (3, 2, 2 ** 31)):
+        with pytest.raises(ValueError, match="32 bits"):
+            sg.sgmv_kv_batch(start, lens, table, *sizes)
+    c = sg.sgmv_kv_init(4, 16, 2, 64, torch.int8, "cpu")
+    b = sg.sgmv_kv_batch(start, lens, table, 3, 2, 6)
+    q = torch.zeros(3, 4, 64)
+    for kw in (dict(window=big + 5), dict(n_split=big + 2), dict(window=-big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            sg.sgmv_kv_attention(q, b, c, **kw)
+        with pytest.raises(ValueError, match="32 bits"):
+            sg.sgmv_kv_attention_workspace(4, torch.float32, b, c, **kw)
+    with pytest.raises(ValueError, match="32 bits"):
+        sg.sgmv_kv_attention_workspace(4 + big, torch.float32, b, c)
+    with pytest.raises(ValueError, match="32 bits"):
+        sg.sgmv_kv_read(b, c, start, big + 3)
+    f, t = torch.zeros(3), torch.zeros(5, 10)
+    with pytest.raises(ValueError, match="32 bits"):
+        sg.sgmv_verify_drafts(t, None, _i32(0, 0, 0), start, f, f[:2], big + 2)
