@@ -264,6 +264,12 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
         if (EXACT || 16 * n < D) vr[n][e] = load_u32x4(base + n * 256 * BYTES + 16 * e);
   };
 
+  int nan_first = mine, nan_last = -1;  // steps from which codes of NaN were left out
+  (void)nan_first; (void)nan_last;
+  if constexpr (FMT == SGMV_KV_E4M3 && !EXACT) {  // past D
+#pragma unroll
+    for (int n = 0; n < NB; ++n) vr[n][0] = u32x4_t{0u, 0u, 0u, 0u};
+  }
   if (mine > 0) {
     load_k(0);
     if (!LATE_V) load_v(0);
@@ -368,17 +374,30 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
 
     if (edge) {
       uint32_t there = 0;  // this lane's places whose token exists
+      bool nan_codes = false;
+      (void)nan_codes;
       const int n_there = page >= 0 ? min(max(s.kv_len - (t0 + 16 * vg), 0), 16) : 0;
       there = places_below(n_there) >> (8 * v_half);
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int e = 0; e < VL; ++e) vr[n][e] = keep_elements<BYTES>(vr[n][e], there >> (4 * e));
+        for (int e = 0; e < VL; ++e) {
+          vr[n][e] = keep_elements<BYTES>(vr[n][e], there >> (4 * e));
+          // An e4m3 code of NaN is left out as the V values below are, but its NaN waits until the end: next to
+          // codes and operands, that loop took 66 registers more.
+          if constexpr (FMT == SGMV_KV_E4M3) {
+            nan_codes |= __any(nan_code_any(vr[n][e]) != 0u);
+            vr[n][e] = drop_nonfinite<1>(vr[n][e]);
+          }
+        }
+      if constexpr (FMT == SGMV_KV_E4M3) {
+        nan_first = nan_codes ? min(nan_first, i) : nan_first;
+        nan_last = nan_codes ? i : nan_last;
+      }
       if constexpr (!SCALED) {
         // A V value that is not finite, in a step that some rows see only part of: in the product,
         // 0 * inf would spoil the rows that do not see it. It is left out of the product and added
-        // to the rows that see it, token by token. (8-bit codes are finite; their scales meet only
-        // probabilities that are not 0.)
+        // to the rows that see it, token by token. (8-bit scales meet only probabilities that are not 0.)
         bool odd = false;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -468,6 +487,22 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
       if (EXACT || 16 * n < D)
         *reinterpret_cast<f32x4_t*>(&s_o[wv][(16 * t + r) * LD + 16 * n + 4 * quad]) =
             f32x4_t{o[t][n][0] * f, o[t][n][1] * f, o[t][n][2] * f, o[t][n][3] * f};
+  }
+  if constexpr (FMT == SGMV_KV_E4M3) {  // the NaN of the codes left out, to the rows that see them
+#pragma unroll 1
+    for (int i = nan_first * NG; i < (nan_last + 1) * NG; ++i) {
+      const int g0 = t_begin + TOK * (wv + WAVES * (i / NG)) + 16 * (i % NG), p = kv_page(K, table, g0);
+      if (p < 0) continue;
+      const char* v = static_cast<const char*>(K.v) + (((int64_t)p * K.H + kvh) * ps + (g0 & (ps - 1))) * D;
+#pragma unroll 1
+      for (int e = 0; e < D / 4; ++e) {
+        const int d = 16 * (e >> 2) + 4 * quad + (e & 3);  // one that this lane has stored
+        const u32x4_t w = load_u32x4(v + 16 * d);
+#pragma unroll
+        for (int t = 0; t < R; ++t)
+          if (nan_among(w, place_flags(places_seen(A, pos[t], g0)))) s_o[wv][(16 * t + r) * LD + d] = NAN;
+      }
+    }
   }
   __syncthreads();
   const int tile_rows = min(ROWS, rows - row0);

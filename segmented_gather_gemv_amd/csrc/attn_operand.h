@@ -33,14 +33,38 @@ __device__ __forceinline__ uint32_t places_below(int n) {
   return (t & 0xf00fu) | (t & 0x00f0u) << 4 | (t & 0x0f00u) >> 4;
 }
 
-// Eight codes with those that are not finite (e4m3: 0x7f and 0xff) replaced by finite ones.
-template <int FMT>
-__device__ __forceinline__ u32x2_t finite_codes(u32x2_t w) {
-  if constexpr (FMT == SGMV_KV_E4M3) {
+// The places of the group of tokens [g0, g0 + 16) that a row at position pos sees.
+__device__ __forceinline__ uint32_t places_seen(const AttnArgs& A, int pos, int g0) {
+  const int n = max(pos - g0 + 1, 0);
+  return places_below(min(n, 16)) & ~(A.window ? places_below(min(max(n - A.window, 0), 16)) : 0u);
+}
+
+// Bit 7 of each byte of a word that is an e4m3 code of NaN (0x7f, 0xff).
+__device__ __forceinline__ uint32_t nan_code_flags(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// Not 0 if a code of a 16-byte piece is NaN.
+__device__ __forceinline__ uint32_t nan_code_any(u32x4_t w) {
+  uint32_t any = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) w[i] &= ~((((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7);
-  }
-  return w;
+  for (int i = 0; i < 4; ++i) any |= (w[i] & 0x7f7f7f7fu) + 0x01010101u;
+  return any & 0x80808080u;
+}
+
+// Bit 7 of each byte (token) of a 16-byte piece of codes whose bit of `places` is set.
+__device__ __forceinline__ u32x4_t place_flags(uint32_t places) {
+  u32x4_t f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)  // bit k of four to bit 8 k
+    f[i] = ((places >> (4 * i) & 15u) * 0x204081u & 0x01010101u) << 7;
+  return f;
+}
+
+// Whether one of a piece's codes is NaN, among those with a flag.
+__device__ __forceinline__ bool nan_among(u32x4_t w, u32x4_t flags) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) any |= nan_code_flags(w[i]) & flags[i];
+  return any != 0u;
 }
 
 // Bit 15 of each bf16 of a word that is not finite: its exponent is all ones, so that one more carries.
@@ -48,9 +72,10 @@ __device__ __forceinline__ uint32_t nonfinite_flags(uint32_t w) { return ((w & 0
 // Both bytes of each half whose bit 15 is set.
 __device__ __forceinline__ uint32_t flag_mask(uint32_t f) { return (f - (f >> 15)) | f; }
 
-// bf16 or fp32 elements only: 8-bit codes are finite.
+// One byte: e4m3 codes (int8 has none of NaN).
 template <int BYTES>
 __device__ __forceinline__ bool has_nonfinite(u32x4_t w) {
+  if constexpr (BYTES == 1) return nan_code_any(w) != 0u;
   if constexpr (BYTES == 2)
     return (nonfinite_flags(w.x) | nonfinite_flags(w.y) | nonfinite_flags(w.z) | nonfinite_flags(w.w)) != 0u;
   bool any = false;
@@ -63,7 +88,8 @@ template <int BYTES>
 __device__ __forceinline__ u32x4_t drop_nonfinite(u32x4_t w) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (BYTES == 2) w[i] &= ~flag_mask(nonfinite_flags(w[i]));
+    if constexpr (BYTES == 1) w[i] &= ~(nan_code_flags(w[i]) >> 7);
+    else if constexpr (BYTES == 2) w[i] &= ~flag_mask(nonfinite_flags(w[i]));
     else if ((w[i] & 0x7f800000u) == 0x7f800000u) w[i] = 0u;
   }
   return w;

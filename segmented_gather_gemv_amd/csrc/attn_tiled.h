@@ -52,6 +52,7 @@ template <int FMT, int D> struct TiledShared {
   alignas(16) uint16_t k[2][4 * GROUP], v[2][4 * GROUP];
   alignas(16) float ks[2][KvFormat<FMT>::scaled ? TL_TOKENS : 4], vs[2][KvFormat<FMT>::scaled ? TL_TOKENS : 4];
   int odd[4];  // [i % 4] = i: something that is not finite was left out of tile i
+  int nan_first, nan_last;  // tiles from which e4m3 codes of NaN were left out
 };
 
 // One workgroup's piece.
@@ -224,13 +225,28 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
       }
     }
   };
-  // V of tokens that are not there has to be finite, so that their probability 0 counts as such: bytes that
-  // no code uses become ones that are. Where some rows of the workgroup see only part of the tile, bf16
-  // values that are not finite are left out, for 0 * inf would spoil the rows that do not see them, and
-  // the tile is marked for restore().
+  // V of tokens that are not there has to be finite, so that their probability 0 counts as such: e4m3 codes of
+  // NaN become finite ones, and their tiles are noted for spoil(). (With a test of the codes alone in the way
+  // of those that have none, 501 us for the largest shape above; with the change made to every code, 507.) Where
+  // some rows of the workgroup see only part of the tile, bf16 values that are not finite are left out, for
+  // 0 * inf would spoil the rows that do not see them, and the tile is marked for restore().
+  int nan_first = n_tiles, nan_last = -1;  // (of this wave's pieces)
+  (void)nan_first; (void)nan_last;
   auto store_v = [&](int i) {
     const int buf = i & 1;
     const bool some = !SCALED && some_see_part(i);
+    if constexpr (FMT == SGMV_KV_E4M3) {
+      uint32_t nan_codes = 0;
+#pragma unroll
+      for (int n = 0; n < NP; ++n)
+        if (4 * PIECES % THREADS == 0 || group_of(n) < 4) nan_codes |= nan_code_any(rv[n]);
+      if (__any(nan_codes != 0u)) {
+        nan_first = min(nan_first, i);
+        nan_last = i;
+#pragma unroll
+        for (int n = 0; n < NP; ++n) rv[n] = drop_nonfinite<1>(rv[n]);
+      }
+    }
 #pragma unroll
     for (int n = 0; n < NP; ++n) {
       const int g = group_of(n), piece = piece_of(n);
@@ -245,8 +261,8 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
           // both halves of d = piece
           uint16_t* v = &s_v[buf][g * GROUP + piece * 16];
           const int x = (piece >> 3) & 1;
-          *reinterpret_cast<u32x4_t*>(v + 8 * x) = codes8_bf16<FMT>(finite_codes<FMT>(u32x2_t{rv[n].x, rv[n].y}));
-          *reinterpret_cast<u32x4_t*>(v + 8 * (1 - x)) = codes8_bf16<FMT>(finite_codes<FMT>(u32x2_t{rv[n].z, rv[n].w}));
+          *reinterpret_cast<u32x4_t*>(v + 8 * x) = codes8_bf16<FMT>(u32x2_t{rv[n].x, rv[n].y});
+          *reinterpret_cast<u32x4_t*>(v + 8 * (1 - x)) = codes8_bf16<FMT>(u32x2_t{rv[n].z, rv[n].w});
         }
       }
     }
@@ -292,8 +308,8 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
         o[n] = mfma_32x32_bf16(load_u32x4(D % 32 && n == NB - 1 ? vl + g * GROUP : vb + g * GROUP + n * 512), pb[g], o[n]);
     read_ahead<4 * NB>();
   };
-  // What store_v (8-bit codes are finite: store_k, of the scales) has left out of tile i, added to the rows
-  // that see it, token by token.
+  // What store_v (of 8-bit formats store_scales) has left out of tile i, added to the rows that see it, token by
+  // token.
   auto restore = [&](int i) {
 #pragma unroll 1
     for (int t = t_begin + TL_TOKENS * i, end = min(t + TL_TOKENS, s.kv_len); t < end; ++t) {
@@ -404,6 +420,10 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
 
   const int group = WAVES == 8 ? wv >> 2 : 0;
   if (tid < 4) s_odd[tid] = -1;
+  if (tid == 0) {
+    sh.nan_first = n_tiles;
+    sh.nan_last = -1;
+  }
   if (n_tiles > 0) {
     load_tile(0);
     __syncthreads();  // s_odd
@@ -437,8 +457,35 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
     if (__builtin_amdgcn_readfirstlane(s_odd[(n_tiles - 1) & 3]) == n_tiles - 1) restore(n_tiles - 1);
     __builtin_amdgcn_s_setprio(0);
     if (WAVES == 8 && !group) __syncthreads();  // as many barriers as the other group
+    if constexpr (FMT == SGMV_KV_E4M3) {
+      if (nan_last >= 0 && lane == 0) {
+        atomicMin(&sh.nan_first, nan_first);
+        atomicMax(&sh.nan_last, nan_last);
+      }
+      __syncthreads();
+    }
   }
   if (!row_ok) return;
+
+  // The NaN of the codes that store_v has changed, over what this lane has stored of a row that sees them.
+  auto spoil = [&](auto store_nan) {
+    if constexpr (FMT == SGMV_KV_E4M3) {
+      if (n_tiles == 0) return;
+      const int g_end = 4 * min(__builtin_amdgcn_readfirstlane(sh.nan_last) + 1, n_tiles);
+#pragma unroll 1
+      for (int g = 4 * __builtin_amdgcn_readfirstlane(sh.nan_first); g < g_end; ++g) {
+        const int g0 = t_begin + 16 * g, p = kv_page(K, table, g0);
+        if (p < 0) continue;
+        const char* v = static_cast<const char*>(K.v) + p * page_bytes + head_bytes + (g0 & (ps - 1)) * D;
+        const u32x4_t seen = place_flags(places_seen(A, pos, g0));
+#pragma unroll 1
+        for (int e = 0; e < D / 2; ++e) {
+          const int d = 8 * (e >> 2) + 4 * half + (e & 3);
+          if (nan_among(load_u32x4(v + 16 * d), seen)) store_nan(d);
+        }
+      }
+    }
+  };
 
   const float sum = half_sum(l);
   const int64_t at = (int64_t)(s.q0 + tok) * A.Hq + head;
@@ -456,6 +503,7 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
         if (32 * n + 8 * j < D)
           *reinterpret_cast<f32x4_t*>(dst + 32 * n + 8 * j + 4 * half) =
               f32x4_t{o[n][4 * j], o[n][4 * j + 1], o[n][4 * j + 2], o[n][4 * j + 3]};
+    spoil([&](int d) { dst[d] = NAN; });
     return;
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -469,6 +517,7 @@ __device__ __forceinline__ void attn_tiled(const AttnArgs& A, int piece, TiledSh
       if (32 * n + 8 * j < D)
         store_out<false>(A, oat + 32 * n + 8 * j + 4 * half, o[n][4 * j] * inv, o[n][4 * j + 1] * inv,
                        o[n][4 * j + 2] * inv, o[n][4 * j + 3] * inv);
+  spoil([&](int d) { static_cast<uint16_t*>(A.out)[oat + d] = 0x7fc0; });
 }
 
 // Workgroups [0, tiled) take tiles of many rows, the others the sequences of few rows (as attn_direct.h

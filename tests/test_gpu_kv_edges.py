@@ -1,5 +1,5 @@
 """GPU tests of the edges of the cache's, the attention's and the draft check's contracts: steps padded to a
-fixed number of rows, windows of any width, draws that fall on the border of a part without a weight.
+fixed number of rows, windows of any width, codes of NaN, draws that fall on the border of a part without a weight.
 
 The bars are those of test_gpu_kv (derived there).
 """
@@ -7,6 +7,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import kv_oracle as ko
 from test_gpu_kv import BF16, DEV, E4M3, F32, I8, Step, _check_attention, _expected_cache, _i32, _raw, _same
 
 pytestmark = pytest.mark.gpu
@@ -127,6 +128,76 @@ def test_wide_windows_with_rows_before_the_first_token(sg, new, kv_len, window, 
     for n_split in (0, 2):
         out, lse = sg.sgmv_kv_attention(q.to(DEV), st.batch, st.cache, window=window, n_split=n_split)
         _check_attention(st, q, kv, out, lse, 128 ** -0.5, window)
+
+
+# ---- codes of NaN ---------------------------------------------------------------------------
+NAN_CODES = {
+    # name: new tokens, length, query heads, key/value heads, D, rows, window
+    "decode": ([1, 1], [100, 70], 8, 2, 128, BF16, 0),
+    "decode_window": ([1, 2], [400, 170], 4, 2, 80, BF16, 60),
+    "drafts": ([3, 5], [150, 70], 8, 2, 128, BF16, 0),
+    "drafts_odd_dim": ([6, 2], [90, 64], 4, 2, 48, BF16, 0),
+    "drafts_256": ([6, 2], [90, 64], 4, 2, 256, BF16, 0),
+    "chunk": ([90, 1], [150, 80], 8, 2, 128, BF16, 0),
+    "chunk_window": ([90, 40], [300, 70], 8, 2, 80, BF16, 50),
+    "chunk_64": ([200], [500], 4, 2, 64, BF16, 0),
+    "chunk_256": ([70, 70], [150, 130], 4, 2, 256, BF16, 0),
+    "chunk_112": ([70], [150], 4, 2, 112, BF16, 0),
+    "fp32": ([40, 3], [100, 70], 4, 2, 128, F32, 0),
+    "fp32_48": ([40, 3], [100, 70], 4, 2, 48, F32, 30),
+}
+
+
+@pytest.mark.parametrize("n_split", [0, 2])
+@pytest.mark.parametrize("name", sorted(NAN_CODES))
+def test_nan_codes_reach_the_rows_that_see_them(sg, name, n_split):
+    """Codes of NaN (0x7f, 0xff) in a wrapped e4m3 cache: in V, their value of d is NaN in the rows that see the
+    token; in K, the rows that see the token are NaN. All else is as without them."""
+    new, kv_len, Hq, H, D, rows, window = NAN_CODES[name]
+    st = Step(sg, new, kv_len, 16, H, D, E4M3, seed=9, rows=rows)
+    st.fill(sg)
+    c = st.cache
+    cache = sg.sgmv_kv_wrap(c.k, c.v, c.k_scale, c.v_scale)
+    q = st.randn(st.T, Hq, D).to(rows).to(DEV)
+    lay, G = ko.Cache(16, D, 1), Hq // H
+    run = lambda: sg.sgmv_kv_attention(q, st.batch, cache, window=window, n_split=n_split)
+    clean, clean_lse = run()
+    assert torch.isfinite(clean).all()
+
+    def at(b, pos, h, d, which):
+        """Where the code of (sequence, position, head, d) is held, in a flat view of K or V."""
+        index = (lay.k_index if which == "k" else lay.v_index)(pos % 16)[d]
+        return (int(st.table[b, pos // 16]) * H + h) * 16 * D + int(index)
+
+    def spoil(which, places):
+        flat = _raw(getattr(c, which)).view(-1)
+        where = torch.tensor([at(*p, which) for p in places], device=DEV)
+        kept = flat[where].clone()
+        flat[where] = torch.tensor([0x7f, 0xff], dtype=torch.uint8, device=DEV)[torch.arange(len(places), device=DEV) % 2]
+        got = run()
+        flat[where] = kept
+        return got
+
+    for b in range(len(new)):
+        first = kv_len[b] - new[b]
+        lo = max(first - window + 1, 0) if window else 0
+        for pos in sorted({lo, (lo + first) // 2, first, first + new[b] // 2, kv_len[b] - 1}):
+            places = [(b, pos, 0, D - 1), (b, pos, H - 1, 3)]
+            out, lse = spoil("v", places)
+            bad = torch.zeros_like(clean, dtype=torch.bool)
+            seen = torch.zeros(st.T, dtype=torch.bool, device=DEV)
+            for i in range(new[b]):
+                here = first + i
+                seen[int(st.start[b]) + i] = pos <= here and not (window and pos <= here - window)
+            for _, _, h, d in places:
+                bad[seen, h * G:(h + 1) * G, d] = True
+            assert torch.isnan(out[bad]).all(), (b, pos)
+            assert bool((out[~bad] == clean[~bad]).all()) and torch.equal(lse, clean_lse), (b, pos)
+            out, lse = spoil("k", places[:1])
+            bad[:] = False
+            bad[seen, :G] = True
+            assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad[:, :, 0]]).all(), (b, pos)
+            assert bool((out[~bad] == clean[~bad]).all()) and bool((lse[~bad[:, :, 0]] == clean_lse[~bad[:, :, 0]]).all())
 
 
 # ---- drafts -------------------------------------------------------------------------------
