@@ -1,8 +1,10 @@
 """GPU tests of the edges of the cache's, the attention's and the draft check's contracts: steps padded to a
-fixed number of rows, windows of any width, codes of NaN, draws that fall on the border of a part without a weight.
+fixed number of rows, lengths and starts that are cut, sequences of different counts, windows of any width, codes of NaN, draws that fall on the border of a part without a weight.
 
 The bars are those of test_gpu_kv (derived there).
 """
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -113,6 +115,85 @@ def test_padded_step_in_a_graph(sg, fmt):
         assert same, new
         some = {(b, i) for b, n in enumerate(new) for i in range(0, n, 9)} | {(b, n - 1) for b, n in enumerate(new) if n}
         _check_attention(st, q[:st.T].cpu(), kv, *got[0], D ** -0.5, rows=some)
+
+
+# ---- what the calls touch -------------------------------------------------------------------
+def _within(x, lo, hi, value):
+    """Nothing but x[lo:hi] has changed from `value`."""
+    assert bool((x[:lo] == value).all()) and bool((x[hi:] == value).all())
+
+
+@pytest.mark.parametrize("fmt", [BF16, I8])
+@pytest.mark.parametrize("start,kv_len", [([0, 2, 4], [1 << 30, -5]), ([0, 900, 3], [30, 30]), ([-4, 2, 1 << 30], [30, 0]),
+                                          ([3, 1, 0], [30, 30]), ([0, 1, 4], [2 ** 31 - 1, 2]), ([1, 1, 3], [-2 ** 31, 31])])
+def test_cut_lengths_and_starts_change_nothing_else(sg, start, kv_len, fmt):
+    """q_start cut to [0, T], kv_len to what the table holds: the cache is as after a write of the rows and lengths
+    so cut, and nothing around the outputs, the rows read and the workspace is written."""
+    T, D = 4, 64
+    st = Step(sg, [2, 2], [30, 30], 16, 1, D, fmt)
+    st.fill(sg)
+    k, v = st.randn(T, 1, D).to(BF16), st.randn(T, 1, D).to(BF16)
+    q = st.randn(T, 2, D).to(BF16).to(DEV)
+    cut = np.clip(np.array(start, np.int64), 0, T)
+    as_cut = copy.copy(st)
+    as_cut.start, as_cut.new = cut[:2], [max(int(cut[b + 1] - cut[b]), 0) for b in range(2)]
+    as_cut.kv_len = [int(min(max(n, 0), st.table.shape[1] * 16)) for n in kv_len]
+    bufs, _ = _expected_cache(as_cut, k, v)
+    mine = sorted({int(cut[b]) + i for b in range(2) for i in range(as_cut.new[b])})
+    others = [i for i in range(T) if i not in mine]
+    for max_q in (4, 100):  # row by row, and by groups; few rows, and tiles
+        b = sg.sgmv_kv_batch(_i32(start), _i32(kv_len), st.batch.page_table, T, max_q, 48)
+        sg.sgmv_kv_write(k.to(DEV), v.to(DEV), b, st.cache)
+        assert _same(_raw(st.cache.k), bufs[0]) and _same(_raw(st.cache.v), bufs[1])
+        for n_split in (1, 3):
+            out = torch.full((T + 8, 2, D), 7.0, dtype=BF16, device=DEV)
+            lse = torch.full((T + 8, 2), 7.0, device=DEV)
+            size = sg.sgmv_kv_attention_workspace(2, BF16, b, st.cache, n_split=n_split)
+            ws = torch.full((size + 512,), 0xab, dtype=torch.uint8, device=DEV)
+            sg.sgmv_kv_attention(q, b, st.cache, out=out[4:4 + T], lse=lse[4:4 + T], n_split=n_split,
+                                 workspace=ws[256:256 + size])
+            _within(out, 4, 4 + T, 7)
+            _within(lse, 4, 4 + T, 7)
+            _within(ws, 256, 256 + size, 0xab)
+            assert bool((out[4:4 + T][others] == 7).all()) and bool((lse[4:4 + T][others] == 7).all())
+            assert not (out[4:4 + T][mine] == 7).any()
+        for rows in (T, T + 40):  # both ways of reading, the second with room to spare
+            back = [torch.full((rows + 8, 1, D), 7.0, dtype=BF16, device=DEV) for _ in range(2)]
+            sg.sgmv_kv_read(b, st.cache, _i32([min(x, T) for x in start]), rows, k=back[0][4:4 + rows], v=back[1][4:4 + rows])
+            for x in back:
+                _within(x, 4, 4 + T, 7)
+                assert bool((x[4:4 + T][others] == 7).all()) and not (x[4:4 + T][mine] == 7).any()
+
+
+@pytest.mark.parametrize("fmt,rows", [(I8, BF16), (E4M3, F32), (BF16, BF16), (F32, F32)])
+def test_every_row_of_sequences_with_different_counts(sg, fmt, rows):
+    """Rows written and read where a sequence's number is not its share of the tokens, row by row and by groups of
+    tokens: each is the code times the scale of its own token and head."""
+    news = [0] * 30 + [8, 1] + [0] * 5 + [2] * 3 + [0, 7]
+    lens = [max(n, (11 * i) % 50) for i, n in enumerate(news)]
+    st = Step(sg, news, lens, 16, 2, 64, fmt, seed=6, rows=rows)
+    k, v = st.randn(st.T, 2, 64).to(rows), st.randn(st.T, 2, 64).to(rows)
+    bufs, scales = _expected_cache(st, k, v)
+    sg.sgmv_kv_write(k.to(DEV), v.to(DEV), st.batch, st.cache)
+    assert _same(_raw(st.cache.k), bufs[0]) and _same(_raw(st.cache.v), bufs[1])
+    lay = ko.Cache(16, 64, st.cache.k.element_size())
+    ref = [torch.empty(st.T, 2, 64, dtype=rows) for _ in range(2)]
+    for which, index in ((0, lay.k_index), (1, lay.v_index)):
+        for b, n in enumerate(news):
+            for i in range(n):
+                pos = lens[b] - n + i
+                page, off = st.table[b, pos // 16], pos % 16
+                x = bufs[which][page][:, torch.from_numpy(index(off))].contiguous()
+                if fmt in (I8, E4M3):
+                    x = x.view(fmt).float() * scales[which][page, :, off][:, None]
+                ref[which][int(st.start[b]) + i] = x.to(rows)
+    got = sg.sgmv_kv_read(st.batch, st.cache, st.batch.q_start, st.T, rows)
+    pad = np.concatenate([[0], np.cumsum([n + 20 if n else 0 for n in news])])
+    more = sg.sgmv_kv_read(st.batch, st.cache, _i32(pad.tolist()), int(pad[-1]), rows)
+    for which in range(2):
+        assert _same(got[which], ref[which])
+        for b, n in enumerate(news):
+            assert _same(more[which][int(pad[b + 1]) - n:int(pad[b + 1])].contiguous(), ref[which][int(st.start[b]):int(st.start[b + 1])].contiguous())
 
 
 # ---- windows ------------------------------------------------------------------------------
