@@ -30,7 +30,8 @@ inline bool row_type_ok(int dtype) { return dtype == SGMV_F32 || dtype == SGMV_B
 inline bool types_fit(int dtype, int fmt) {
   return scaled(fmt) || (fmt == SGMV_KV_F32) == (dtype == SGMV_F32);
 }
-constexpr int64_t MOST_GRID = 0x7fffffff;
+constexpr int64_t MOST_ROWS = 0x7fffffff;
+constexpr int64_t MOST_WAVES = 0xffffffffll / 64;  // of a launch: it takes fewer than 2^32 work items
 
 sgmv_status shape_ok(int32_t pages, int32_t page_size, int32_t heads, int32_t head_dim, int32_t fmt) {
   if (pages < 1 || page_size < 1 || heads < 1 || head_dim < 1 || fmt < SGMV_KV_F32 || fmt > SGMV_KV_I8)
@@ -142,7 +143,7 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   if (!std::isfinite(A.scale_log2)) return SGMV_EINVAL;
   A.window = a->window;
   empty = empty || s->T == 0;
-  if ((int64_t)s->T * A.Hq > MOST_GRID) return SGMV_EUNSUPPORTED;
+  if ((int64_t)s->T * A.Hq > MOST_ROWS) return SGMV_EUNSUPPORTED;
   // sequences of few rows are taken directly; so are all where the tiled kernel has no instance
   const int D = c->head_dim, few = tiled_direct_rows(D);
   const bool tiled = !A.f32 && tiled_dim(D) && (int64_t)s->max_q * A.G > few;
@@ -170,9 +171,10 @@ sgmv_status plan(const sgmv_attention* a, const sgmv_kv_batch* s, const sgmv_kv_
   split_tokens(a->n_split ? a->n_split : tiled_splits(tiles * c->heads, tokens), tokens, 64, A.n_split[1], A.chunk[1]);
   if (!direct) A.n_split[0] = 1;
   if (!tiles) A.n_split[1] = 1;
-  // workgroups of the attention launch, and of those that join parts (4 rows each)
-  if ((direct * A.n_split[0] + tiles * A.n_split[1]) * c->heads > MOST_GRID ||
-      std::max(direct * A.direct_tile, tiles * tiled_rows(D)) / 4 * c->heads > MOST_GRID)
+  // workgroups of the attention launch, and of those that join parts (a wave for a row)
+  const int64_t joined = std::max(A.n_split[0] > 1 ? direct * A.direct_tile : 0, A.n_split[1] > 1 ? tiles * tiled_rows(D) : 0);
+  if ((direct * A.n_split[0] + tiles * A.n_split[1]) * c->heads * (tiled ? tiled_waves(D) : A.direct_waves) > MOST_WAVES ||
+      joined * c->heads > MOST_WAVES)
     return SGMV_EUNSUPPORTED;
   A.slots[0] = (int32_t)direct;
   A.slots[1] = (int32_t)tiles;

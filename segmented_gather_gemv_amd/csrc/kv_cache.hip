@@ -590,7 +590,7 @@ struct RowGrid {
 };
 RowGrid row_grid(const KvArgs& K, int64_t tokens, bool few) {
   const int64_t rows = tokens * K.H, for_v = (rows + RW_WAVES - 1) / RW_WAVES;
-  if (!few || rows > 0x40000000) return {0, 0};
+  if (!few || rows > 0x3000000) return {0, 0};  // (a launch takes fewer than 2^32 work items, 68 of each row)
   return {(int)for_v, (unsigned)(for_v + (rows + 16 * RW_WAVES - 1) / (16 * RW_WAVES))};
 }
 

@@ -196,6 +196,22 @@ def test_every_row_of_sequences_with_different_counts(sg, fmt, rows):
             assert _same(more[which][int(pad[b + 1]) - n:int(pad[b + 1])].contiguous(), ref[which][int(st.start[b]):int(st.start[b + 1])].contiguous())
 
 
+def test_more_rows_than_one_launch_by_rows_takes(sg):
+    """65536 sequences' 8 tokens, 128 heads: 2^26 rows, of which a launch row by row would take 2^32 work items and
+    more. (17 GB of device memory.)"""
+    B, n, H, D = 65535, 8, 128, 16
+    cache = sg.sgmv_kv_init(B, 16, H, D, BF16, DEV)
+    g = torch.Generator(device=DEV).manual_seed(3)
+    k = torch.randn(B * n, H, D, generator=g, device=DEV, dtype=BF16)
+    v = torch.randn(B * n, H, D, generator=g, device=DEV, dtype=BF16)
+    start = torch.arange(B + 1, dtype=torch.int32, device=DEV) * n
+    table = torch.randperm(B, generator=g, device=DEV).to(torch.int32).view(B, 1)
+    batch = sg.sgmv_kv_batch(start, torch.full((B,), n + 3, dtype=torch.int32, device=DEV), table, B * n, n, n + 3)
+    sg.sgmv_kv_write(k, v, batch, cache)
+    back = sg.sgmv_kv_read(batch, cache, start, B * n)
+    assert torch.equal(back[0], k) and torch.equal(back[1], v)
+
+
 # ---- windows ------------------------------------------------------------------------------
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 3, 2 ** 30])
 @pytest.mark.parametrize("new,kv_len", [([5, 3, 2], [2, 0, 30]), ([100, 9], [60, 4])])

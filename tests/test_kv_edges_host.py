@@ -52,3 +52,28 @@ def test_whole_numbers_past_32_bits_are_refused():
     f, t = torch.zeros(3), torch.zeros(5, 10)
     with pytest.raises(ValueError, match="32 bits"):
         sg.sgmv_verify_drafts(t, None, _i32(0, 0, 0), start, f, f[:2], big + 2)
+
+
+def test_launches_past_the_limit_of_work_items_are_refused():
+    """A launch takes fewer than 2^32 work items. Nothing is launched here: pointers are not followed."""
+    import ctypes
+
+    from segmented_gather_gemv_amd import _serving as sv
+    lib = sg.library()
+
+    def need(T, heads, head_dim, n_split, max_q=4096, fmt=sg.KV_I8):
+        c = sv._KvCache(0x10000, 0x20000, 0x30000, 0x40000, 4, 16, 2, head_dim, fmt)
+        b = sv._KvBatch(0x50000, 0x60000, 0x70000, 4, 4, 2, T, max_q, 64)
+        a = sv._Attention(0x80000, 0x90000, None, heads * head_dim, head_dim, heads * head_dim, head_dim, heads,
+                          sg.SGMV_BF16, 0.125, 0, n_split)
+        size = ctypes.c_size_t()
+        return lib.sgmv_kv_attention_workspace(ctypes.byref(a), ctypes.byref(b), ctypes.byref(c), ctypes.byref(size))
+
+    # of the direct kernel, 8 of a row and head (256 of 32 of them); of the join, 64
+    assert need(2 ** 24, 30, 112, 1) == sg.SGMV_OK
+    assert need(2 ** 24, 32, 112, 1) == sg.SGMV_EUNSUPPORTED
+    # of the tiled kernel, 2 of a row and head
+    assert need(2 ** 24, 120, 128, 1) == sg.SGMV_OK
+    assert need(2 ** 24, 120, 128, 2) == sg.SGMV_EUNSUPPORTED
+    assert need(2 ** 21, 30, 128, 2) == sg.SGMV_OK
+    assert need(2 ** 21, 32, 128, 2) == sg.SGMV_EUNSUPPORTED
