@@ -517,7 +517,9 @@ sgmv_status sgmv_kv_read(const sgmv_kv_batch* batch, const sgmv_kv_cache* cache,
  * A row that sees nothing gets out = 0 and lse = -inf. A value that is not finite reaches only
  * the rows that see its token. Products are of bf16 or fp32 operands (the 8-bit formats'
  * codes are exact in bf16), summed in fp32; with bf16 rows the probabilities (times the V
- * scale) are rounded to bf16 for their product with V.
+ * scale) are rounded to bf16 for their product with V. Scores are meant to stay below 2^30 in
+ * magnitude: past that their fp32 steps exceed what e^x covers, and a row may come out as NaN
+ * or as if it saw nothing.
  *   q, out  device rows [T][heads][head_dim] of `dtype` with token and head strides, as in
  *           sgmv_kv_write; out must not overlap q
  *   lse     device [T][heads] fp32, or NULL

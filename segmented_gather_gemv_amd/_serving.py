@@ -1,5 +1,6 @@
 """Binding of the paged key/value cache, its attention and the draft check (include/sgmv.h);
-imported by the package, whose names these are. Argument marshalling only.
+imported by the package, whose names these are. Argument marshalling only; calls for serving, which
+autograd does not see: what they return carries no gradient, whatever their inputs require.
 
     sgmv_kv_init(pages, page_size, heads, head_dim, format)  -> KvCache
     sgmv_kv_batch(q_start, kv_len, page_table, T, max_q, max_kv) -> KvBatch
@@ -292,7 +293,7 @@ def sgmv_kv_attention(q: torch.Tensor, batch: KvBatch, cache: KvCache,
     holds the step's keys and values: causal, with ``window`` > 0 over the last ``window``
     tokens only. Returns the output and the rows' log-sum-exp [T, query heads] fp32. ``scale``
     defaults to head_dim ** -0.5. A workspace (uint8) is allocated on the current stream
-    unless one is given."""
+    unless one is given. No gradient flows through the call."""
     T, D = batch.T, cache.head_dim
     if abs(window) > _MOST or abs(n_split) > _MOST:
         _int32("window and n_split", window, n_split)

@@ -23,7 +23,7 @@ struct AttnArgs {
   float scale_log2;    // scale * log2(e)
   int32_t window;      // 0: none
   // rows of one sequence up to which the direct kernel takes it (the tiled kernel takes the
-  // others); INT32_MAX: the direct kernel takes all
+  // others; 0: all); INT32_MAX: the direct kernel takes all
   int32_t direct_rows;
   int32_t direct_tile; // rows of the direct kernel's workgroups: 16 or 32
   int32_t direct_waves;  // and their waves: 4 or 8

@@ -8,13 +8,15 @@
 // + 3 of column r. Which token is a product's row is free: tile x gives row 4 q + i the token at place
 // 4 x + i (V's order) of the piece that quad q loads of V, 16 bytes of one d. So a lane's probabilities
 // are the right operand of the next product as they stand, every load of K and V is 16 bytes wide, and
-// nothing goes through LDS but the waves' sums at the end. TOK is what makes those pieces whole:
+// nothing goes through LDS but the waves' sums at the end. Scores, maxima, sums and outputs are fp32. With bf16
+// rows the probabilities, times V's scales, are rounded to bf16 for that product: at most 2^-8 of sum p |v| / sum p,
+// as the output's own rounding is 2^-8 of it, where fp32 products have a sixteenth of the rate. TOK is what makes those pieces whole:
 // 64 tokens of 8-bit codes (quad q: group q), 32 of wider ones (quad q: half q % 2 of group q / 2).
 //
 // Bound: the bytes of K and V, read once per tile of rows. K and V of the next step are in flight while
 // this one is computed, with two waves per SIMD at a head dimension of 128. Scales of 8-bit tokens are one
 // load per lane, spread by row broadcasts: as 16-byte loads they took the registers that make the
-// difference (64 sequences' drafts, int8: 238 us, 150 us without spills). Measured (64 / 8 heads of 128):
+// difference (64 sequences' drafts, int8: 238 us, 150 without their spills; 138 now). Measured (64 / 8 heads of 128):
 // 256 sequences of 128..4096, bf16: 397 us, 5.6 TB/s of K and V (a large copy: 5.1); 16 of
 // 8001..64003, e4m3: 233 us, 5.2 TB/s. One token over 1001, bf16: 8.9 us, the chain of loads from the
 // sequence to its page to K, then 4 steps of 8 waves.

@@ -102,8 +102,8 @@ int64_t tiled_splits(int64_t base, int64_t tokens) {
 
 // Ranges for the direct kernel. A split costs its parts and a launch that joins them, about as long as
 // five steps of the waves: rows of no more than six steps are not split (one sequence of 1000 tokens,
-// bf16: 9.1 us in 1 range, 10.3 in 4; of 4000: 19.6 in 1, 10.4 in 16), beside tiles of many rows neither (8
-// prompts of 512 and one token over 6000: 91 us split, 102 not). Short of that, two rules:
+// bf16: 9.1 us in 1 range, 10.3 in 4; of 4000: 19.6 in 1, 10.4 in 16). Longer ones are by two rules, also
+// beside tiles of many rows (8 prompts of 512 and one token over 6000: 91 us split, 102 not):
 //   fill  up to a workgroup of 8 waves (two of 4) per compute unit, down to one step of each wave;
 //   even  sequences of different lengths leave compute units idle at the end: up to four workgroups of 8
 //         waves (six of 4) per compute unit, of long ranges (16 sequences of 8001..64003, e4m3: 361 us in 1
