@@ -18,8 +18,8 @@
 //
 // Bound: the matrix cores, at the clock that they leave themselves: the products alone, without loads,
 // softmax and LDS reads, ran at 1420..1520 TFLOP/s on the largest shape here (a large matrix product of the
-// library: 1250). 2048 tokens over 14001, e4m3, 32 / 8 heads of 128: 485..515 us (980..1040 TFLOP/s), matrix
-// cores busy 46% of the cycles, a phase of products 1.5 thousand cycles where they need 1.0; eight prompts'
+// library: 1250). 2048 tokens over 14001, e4m3, 32 / 8 heads of 128: 477..507 us (990..1050 TFLOP/s), matrix
+// cores busy 48% of the cycles, a phase of products 1.5 thousand cycles where they need 1.0; eight prompts'
 // chunks, bf16, 64 / 8 heads: 335..350 us (870..910): there the order of the tiles counts too, 2 us each, the last
 // of the last sequence first. Handed to 256 compute units so, the 1192 of that shape end after 176 tiles, the
 // longest first would after 153 (no order before 150). What did not pay: 64 rows per wave with the softmax
