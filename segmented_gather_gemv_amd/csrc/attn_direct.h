@@ -266,8 +266,9 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
         if (EXACT || 16 * n < D) vr[n][e] = load_u32x4(base + n * 256 * BYTES + 16 * e);
   };
 
-  int nan_first = mine, nan_last = -1;  // steps from which codes of NaN were left out
-  (void)nan_first; (void)nan_last;
+  int nan_first = mine, nan_last = -1;  // steps whose NaN, of codes or of scales, is written at the end
+  bool nan_codes = false;  // codes among them
+  (void)nan_first; (void)nan_last; (void)nan_codes;
   if constexpr (FMT == SGMV_KV_E4M3 && !EXACT) {  // past D
 #pragma unroll
     for (int n = 0; n < NB; ++n) vr[n][0] = u32x4_t{0u, 0u, 0u, 0u};
@@ -313,7 +314,13 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
     // a step that some row sees only part of, or with tokens that are not there
     const bool edge = t0 + TOK - 1 > lo_pos || (A.window && t0 <= hi_pos - A.window) || gap;
     const int t_lane = t0 + 16 * vg + 4 * v_half;  // this lane's first token
+    bool nan = false;
+    (void)nan;
     if (edge) {
+      // A V scale that is not finite meets only probabilities that are not 0, of rows that see its token. Rows that
+      // see it with a probability too small for fp32 get its NaN at the end. (Whether the token is there is asked
+      // then: here, that took three registers, and 5 us of 138 for 64 sequences' drafts, int8.)
+      if constexpr (SCALED) nan = __any(!(fabsf(vs) < INFINITY));
 #pragma unroll
       for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -376,8 +383,6 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
 
     if (edge) {
       uint32_t there = 0;  // this lane's places whose token exists
-      bool nan_codes = false;
-      (void)nan_codes;
       const int n_there = page >= 0 ? min(max(s.kv_len - (t0 + 16 * vg), 0), 16) : 0;
       there = places_below(n_there) >> (8 * v_half);
 #pragma unroll
@@ -392,14 +397,15 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
             vr[n][e] = drop_nonfinite<1>(vr[n][e]);
           }
         }
-      if constexpr (FMT == SGMV_KV_E4M3) {
-        nan_first = nan_codes ? min(nan_first, i) : nan_first;
-        nan_last = nan_codes ? i : nan_last;
+      if constexpr (SCALED) {
+        nan |= nan_codes;
+        nan_first = nan ? min(nan_first, i) : nan_first;
+        nan_last = nan ? i : nan_last;
       }
       if constexpr (!SCALED) {
         // A V value that is not finite, in a step that some rows see only part of: in the product,
         // 0 * inf would spoil the rows that do not see it. It is left out of the product and added
-        // to the rows that see it, token by token. (8-bit scales meet only probabilities that are not 0.)
+        // to the rows that see it, token by token.
         bool odd = false;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -490,19 +496,30 @@ __device__ __forceinline__ void attn_direct(const AttnArgs& A, int piece, Direct
         *reinterpret_cast<f32x4_t*>(&s_o[wv][(16 * t + r) * LD + 16 * n + 4 * quad]) =
             f32x4_t{o[t][n][0] * f, o[t][n][1] * f, o[t][n][2] * f, o[t][n][3] * f};
   }
-  if constexpr (FMT == SGMV_KV_E4M3) {  // the NaN of the codes left out, to the rows that see them
+  if constexpr (SCALED) {  // the NaN of codes and scales, to the rows that see them
+    int thread = threadIdx.x;
+    asm volatile("" : "+v"(thread));  // (lane numbers of its own: shared ones cost the steps a register)
+    const int r2 = thread & 15, quad2 = thread >> 4 & 3;
 #pragma unroll 1
     for (int i = nan_first * NG; i < (nan_last + 1) * NG; ++i) {
       const int g0 = t_begin + TOK * (wv + WAVES * (i / NG)) + 16 * (i % NG), p = kv_page(K, table, g0);
       if (p < 0) continue;
-      const char* v = static_cast<const char*>(K.v) + (((int64_t)p * K.H + kvh) * ps + (g0 & (ps - 1))) * D;
+      const int64_t group = ((int64_t)p * K.H + kvh) * ps + (g0 & (ps - 1));
+      const uint32_t odd = places_of_nan(K.v_scale + group);
+      uint32_t seen[R], some = 0;
+#pragma unroll
+      for (int t = 0; t < R; ++t) some |= odd & (seen[t] = places_seen(A, pos[t], g0));
+      if (!nan_codes && !__any(some != 0u)) continue;
+      const char* v = static_cast<const char*>(K.v) + group * D;
 #pragma unroll 1
       for (int e = 0; e < D / 4; ++e) {
-        const int d = 16 * (e >> 2) + 4 * quad + (e & 3);  // one that this lane has stored
-        const u32x4_t w = load_u32x4(v + 16 * d);
+        const int d = 16 * (e >> 2) + 4 * quad2 + (e & 3);  // one that this lane has stored
 #pragma unroll
-        for (int t = 0; t < R; ++t)
-          if (nan_among(w, place_flags(places_seen(A, pos[t], g0)))) s_o[wv][(16 * t + r) * LD + d] = NAN;
+        for (int t = 0; t < R; ++t) {
+          bool nan = (seen[t] & odd) != 0u;
+          if constexpr (FMT == SGMV_KV_E4M3) nan |= nan_among(load_u32x4(v + 16 * d), place_flags(seen[t]));
+          if (nan) s_o[wv][(16 * t + r2) * LD + d] = NAN;
+        }
       }
     }
   }

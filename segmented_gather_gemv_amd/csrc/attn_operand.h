@@ -39,6 +39,15 @@ __device__ __forceinline__ uint32_t places_seen(const AttnArgs& A, int pos, int 
   return places_below(min(n, 16)) & ~(A.window ? places_below(min(max(n - A.window, 0), 16)) : 0u);
 }
 
+// The places of a group whose scale (of 16 tokens in order) is not finite.
+__device__ __forceinline__ uint32_t places_of_nan(const float* scale) {
+  uint32_t odd = 0;
+#pragma unroll
+  for (int t = 0; t < KV_GROUP; ++t)
+    if (!(fabsf(scale[t]) < INFINITY)) odd |= places_below(t + 1) & ~places_below(t);
+  return odd;
+}
+
 // Bit 7 of each byte of a word that is an e4m3 code of NaN (0x7f, 0xff).
 __device__ __forceinline__ uint32_t nan_code_flags(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 

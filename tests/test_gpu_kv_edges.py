@@ -297,6 +297,32 @@ def test_nan_codes_reach_the_rows_that_see_them(sg, name, n_split):
             assert bool((out[~bad] == clean[~bad]).all()) and bool((lse[~bad[:, :, 0]] == clean_lse[~bad[:, :, 0]]).all())
 
 
+@pytest.mark.parametrize("n_split", [0, 2])
+@pytest.mark.parametrize("fmt", [E4M3, I8])
+@pytest.mark.parametrize("new,rows,D", [(1, BF16, 128), (4, BF16, 64), (5, F32, 80), (5, BF16, 48), (90, BF16, 128)])
+def test_nan_rows_of_no_weight_reach_the_rows_that_see_them(sg, new, rows, D, fmt, n_split):
+    """A V row of NaN whose token's probability is below the smallest fp32 number: the rows that see it are NaN
+    all the same, wherever in the sequence the token stands."""
+    n = 150
+    st = Step(sg, [new], [n], 16, 1, D, fmt, seed=12, rows=rows)
+    k, v = st.randn(n, 1, D) * 0.1, st.randn(n, 1, D)
+    whole = sg.sgmv_kv_batch(_i32([0, n]), _i32([n]), st.batch.page_table, n, n, n)
+    q = (st.randn(new, 2, D).abs() + 0.5).to(rows)
+    for pos in sorted({0, 63, 64, 70, 127, 128, n - new, n - new // 2 - 1, n - 1}):
+        low = k.clone()
+        low[pos] = -400.0  # scores below -200 sqrt(D), next to at most 0.1 * 128
+        got = []
+        for x in (0.0, float("nan")):
+            spoilt = v.clone()
+            spoilt[pos, 0, 5] = x
+            sg.sgmv_kv_write(low.to(rows).to(DEV), spoilt.to(rows).to(DEV), whole, st.cache)
+            got.append(sg.sgmv_kv_attention(q.to(DEV), st.batch, st.cache, n_split=n_split))
+        (ref, ref_lse), (out, lse) = got
+        seen = max(pos - (n - new), 0)  # the first row that sees it
+        assert torch.isfinite(ref).all() and torch.equal(lse, ref_lse), pos
+        assert torch.equal(out[:seen], ref[:seen]) and torch.isnan(out[seen:]).all(), pos
+
+
 # ---- drafts -------------------------------------------------------------------------------
 @pytest.mark.parametrize("V", [16 * 1024, 30 * 1024 + 5, 128 * 1024])
 def test_draws_between_parts_without_weight(sg, V):
