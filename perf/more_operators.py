@@ -14,7 +14,8 @@ c = 16 bytes of elements):
 and one fp32 scale per (page, head, token) for the 8-bit formats. A value is code * scale.
 
 A 4-bit weight is [N][ceil(K / 2)] bytes, the even k in the low bits, with a scale (and a zero point) for every
-`group` values of k of a row; its values are scale * (code - zero) or, of e2m1 codes, scale * e2m1(code).
+`group` values of k of a row; its values are scale * (code - zero) or, of e2m1 codes (32 values of k to a scale
+that is a power of two, one byte), 2^(scale - 127) * e2m1(code).
 """
 import math
 
@@ -137,7 +138,8 @@ def work(case):
         return {"bytes": rows * (W * each + (4.0 if case["quantise"] else 0.0)) + W * e, "flops": 5.0 * rows * W}
     if case["kind"] == "product":
         T, N, K, g = case["T"], case["N"], case["K"], _groups(case)
-        return {"bytes": N * ((K + 1) // 2) + float(N) * g * (e + (1 if case["zero"] else 0)) + float(e) * T * (K + N),
+        scale = 1 if case["form"] == "e2m1" else e + (1 if case["zero"] else 0)
+        return {"bytes": N * ((K + 1) // 2) + float(N) * g * scale + float(e) * T * (K + N),
                 "flops": 2.0 * T * N * K}
     q, _ = _lengths(case)
     T, H, D, c = sum(q), case["kv_heads"], case["dim"], BYTES[case["cache"]]
@@ -215,9 +217,8 @@ def _prepare_product(case, g, dtype):
     T, N, K, G = case["T"], case["N"], case["K"], _groups(case)
     codes = torch.randint(0, 256, (N, (K + 1) // 2), generator=g, device=DEVICE, dtype=torch.uint8)
     scale = (0.5 + torch.rand((N, G), generator=g, device=DEVICE)) * (0.2 * K ** -0.5)
-    if case["form"] == "e2m1":  # powers of two
-        scale = torch.exp2(torch.log2(scale).round())
-    st = {"case": case, "codes": codes, "scale": scale.to(dtype), "zero": None,
+    scale = (127 + torch.log2(scale).round()).to(torch.uint8) if case["form"] == "e2m1" else scale.to(dtype)
+    st = {"case": case, "codes": codes, "scale": scale, "zero": None,
           "x": torch.randn((T, K), generator=g, device=DEVICE).to(dtype)}
     if case["zero"]:
         st["zero"] = torch.randint(6, 11, (N, G), generator=g, device=DEVICE, dtype=torch.uint8)
@@ -243,9 +244,9 @@ def _own(st, kind):
         return {"out": got.out, "residual": got.residual, "codes": got.codes, "scale": got.scale}
     if kind == "product":
         if "plan" not in st:  # the weight as a serving program keeps it
-            st["plan"] = sg.sgmv_w4_pack(st["codes"], st["scale"], st["zero"], K=case["K"], group=case["group"],
-                                         format=sg.W4_I4 if case["form"] == "i4" else sg.W4_E2M1)
-        return {"y": sg.sgmv_w4_product(st["x"], st["plan"])}
+            st["plan"] = sg.sgmv_base_pack(st["codes"], st["scale"], st["zero"], K=case["K"], group=case["group"],
+                                           format=sg.BASE_I4 if case["form"] == "i4" else sg.BASE_E2M1)
+        return {"y": sg.sgmv_base_product(st["x"], st["plan"])}
     if "plan" not in st:  # the handles a serving loop keeps beside its cache and its batch
         st["plan"] = (sg.sgmv_kv_wrap(st["k"], st["v"], st.get("k_scale"), st.get("v_scale")),
                       sg.sgmv_kv_batch(st["q_start"], st["kv_len"], st["table"], st["tokens"],
@@ -289,10 +290,8 @@ def _weight(st, dtype):
     code = torch.stack([st["codes"] & 15, st["codes"] >> 4], 2).flatten(1)[:, :case["K"]]
     at = torch.arange(case["K"], device=DEVICE) // case["group"]
     if case["form"] == "e2m1":
-        value = torch.tensor(E2M1, dtype=dtype, device=DEVICE)[code.long()]
-    else:
-        value = code.to(dtype) - (8 if st["zero"] is None else st["zero"].to(dtype)[:, at])
-    return value * st["scale"].to(dtype)[:, at]
+        return torch.tensor(E2M1, dtype=dtype, device=DEVICE)[code.long()] * torch.exp2(st["scale"].to(dtype) - 127)[:, at]
+    return (code.to(dtype) - (8 if st["zero"] is None else st["zero"].to(dtype)[:, at])) * st["scale"].to(dtype)[:, at]
 
 
 def _plain_product(st):
@@ -383,7 +382,8 @@ def exact(case, seed):
                 w = code[:, at]
                 if case["form"] == "i4":
                     w = w - (8.0 if st["zero"] is None else st["zero"][n:n + 4096, i, None].double())
-                total = total + (x[:, at] @ w.T) * st["scale"][n:n + 4096, i].double()
+                scale = st["scale"][n:n + 4096, i].double()
+                total = total + (x[:, at] @ w.T) * (torch.exp2(scale - 127) if case["form"] == "e2m1" else scale)
             y[:, n:n + 4096] = total
         return {"y": y}
     # turned as complex numbers, one angle for each pair
