@@ -497,6 +497,37 @@ sgmv_status sgmv_kv_write(const void* k, int64_t ldk_token, int64_t ldk_head, co
                           int64_t ldv_token, int64_t ldv_head, int32_t dtype,
                           const sgmv_kv_batch* batch, const sgmv_kv_cache* cache, void* stream);
 
+/* Write the step's new keys and values into the cache as sgmv_kv_write does, the keys turned by
+ * their positions on the way, and turn the step's queries, in one launch. A row of position pos
+ * has its first `rotary` values turned in pairs (a, b) by angle i of the position:
+ *   (a, b) -> (a c - b s, b c + a s),   c = cos_sin[pos][i],  s = cos_sin[pos][rotary / 2 + i],
+ *   (a, b) = values (i, i + rotary / 2), or with `interleaved` (2 i, 2 i + 1),  i < rotary / 2,
+ * each product and each sum rounded to fp32; the others stay as they are. Queries are then
+ * rounded once to `dtype`, keys once to the cache's format (the 8-bit formats: quantised from the
+ * fp32 values). Rows of no sequence and those at negative positions are neither read nor written;
+ * queries and keys at positions past the table come out as NaN, and a missing page leaves out its
+ * keys and values but not the queries.
+ *   cos_sin  device [positions][ld >= rotary] fp32
+ *   rotary   a multiple of 16 up to head_dim
+ *   q, q_out device rows [T][heads][head_dim] of `dtype`; q_out may be q itself (with the same
+ *            strides), must not overlap it otherwise. heads = 0: no queries
+ * Errors: EINVAL; EUNSUPPORTED; EHIP. */
+typedef struct {
+  const float* cos_sin;
+  int64_t ld;
+  int32_t positions, rotary;
+  int32_t interleaved; /* 0 or 1 */
+  int32_t heads;
+  const void* q;
+  void* q_out;
+  int64_t ldq_token, ldq_head, ldo_token, ldo_head;
+} sgmv_kv_rotation;
+
+sgmv_status sgmv_kv_append(const sgmv_kv_rotation* turn, const void* k, int64_t ldk_token,
+                           int64_t ldk_head, const void* v, int64_t ldv_token, int64_t ldv_head,
+                           int32_t dtype, const sgmv_kv_batch* batch, const sgmv_kv_cache* cache,
+                           void* stream);
+
 /* Read tokens back (to move a sequence, or to check): with m_b = out_start[b + 1] -
  * out_start[b], output rows out_start[b] .. are the last m_b tokens of sequence b, so
  * out_start = q_start gives the step's new tokens and running sums of kv_len whole sequences.
@@ -571,6 +602,98 @@ sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draf
                                int32_t max_drafts, const float* accept_u, const float* sample_u,
                                int32_t* tokens, int64_t ldo, int32_t* accepted, void* workspace,
                                size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------ *
+ * The rows and the base product around the delta of a layer: not part of the source pages.
+ * ------------------------------------------------------------------------------------ */
+
+/* Root-mean-square norm of rows [T][heads][width] (heads = 1: of a layer's input; heads > 1: of
+ * each head's queries or keys), with the residual's addition before it and codes of 8 bits beside
+ * its output (for a base product of such rows, where the delta takes `out`):
+ *   h = x + residual, residual_out = h,  g = h * weight,  root = sqrt(sum h^2 / width + eps),
+ *   out = g / root,   scale = max |g| / root / F,   code = g * F / max |g|, F = 448 (E4M3) or 127 (I8)
+ * h and g are fp32, each rounded once; h and out are then rounded once to `dtype`, codes as in the
+ * cache above: zeros give scale 0 and codes 0, a row with a g that is not finite scale NaN and codes 0.
+ *   x, residual, residual_out, out  device, row of token t and head j at t * ld_token + j * ld_head,
+ *            `width` contiguous elements of `dtype`; residual may be NULL (h = x), and then
+ *            residual_out is NULL; residual_out may be NULL, and so may out where codes are asked for.
+ *            residual_out and out may be x or residual themselves (with the same strides, each another
+ *            one), none of the outputs may overlap anything otherwise
+ *   weight   device [width] of `dtype`
+ *   codes    device bytes, rows as above, with strides ldc, or NULL;  scale  device [T][heads] fp32
+ *   eps      finite and > 0;  width up to SGMV_MAX_NORM_WIDTH
+ * Errors: EINVAL; EUNSUPPORTED; EHIP. */
+#define SGMV_MAX_NORM_WIDTH 32768
+
+typedef struct {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* residual_out;
+  void* out;
+  void* codes;
+  float* scale;
+  int64_t ldx_token, ldx_head, ldr_token, ldr_head, lds_token, lds_head; /* lds: residual_out */
+  int64_t ldo_token, ldo_head, ldc_token, ldc_head;
+  int32_t T, heads, width;
+  int32_t dtype;  /* sgmv_dtype */
+  int32_t format; /* of codes: SGMV_KV_E4M3 or SGMV_KV_I8 */
+  float eps;
+} sgmv_norm;
+
+sgmv_status sgmv_rms_norm(const sgmv_norm* norm, void* stream);
+
+/* Base weight [N][K] held in 4 bits, of the product y = x W^T that the delta is added to. Every
+ * `group` values of k of a row share a scale:
+ *   I4    w[n][k] = scale[n][k / group] * (code - zero[n][k / group]), codes and zeros 0..15, zero 8
+ *         where there are none; scales of the product's `dtype`
+ *   E2M1  w[n][k] = 2^(scale[n][k / 32] - 127) * value(code): codes of sign, 2 exponent bits and 1 of
+ *         mantissa (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), scales one byte (255: NaN), group 32
+ * Packed once, when weights are loaded, into the library's layout:
+ *   codes        [N / 16][K / 128][64][4] words: word j of lane l holds, of row 16 (n / 16) + l % 16, the 8
+ *                values from k = 128 (k / 128) + 32 j + 8 (l / 16) on, value i in the four bits from
+ *                4 i (E2M1) or 8 (i % 4) + 4 (i / 4) (I4) on
+ *   scale, zero  [N / 16][blocks][16][s], s = 128 / group scales of a block of 128 k, or 1 for longer groups
+ * K is padded to whole blocks and N to 16, with zeros. */
+typedef enum { SGMV_BASE_I4 = 0, SGMV_BASE_E2M1 = 1 } sgmv_base_format;
+
+typedef struct {
+  void* codes;
+  void* scale;
+  uint8_t* zero; /* I4 with zero points, else NULL */
+  int32_t N, K, group;
+  int32_t format;   /* sgmv_base_format */
+  int32_t dtype;    /* sgmv_dtype of x, y and I4's scales */
+  int32_t has_zero;
+} sgmv_base;
+
+/* Fill the dimensions of `base` and report the byte sizes the caller must allocate (zero_bytes is
+ * 0 without zero points). group: 32, 64 or a multiple of 128 (one scale per row: K rounded up to
+ * that). Pointers in `base` are cleared.
+ * Errors: EINVAL (null pointer, a size < 1, unknown format or dtype, zero points or a group other
+ * than 32 with E2M1); EUNSUPPORTED (other groups; N or K past SGMV_BASE_MAX_SIZE). */
+#define SGMV_BASE_MAX_SIZE 4194304
+sgmv_status sgmv_base_init(int32_t N, int32_t K, int32_t group, int32_t format, int32_t dtype,
+                           int32_t has_zero, sgmv_base* base, size_t* code_bytes,
+                           size_t* scale_bytes, size_t* zero_bytes);
+
+/* Pack a weight: codes device [N][ldc >= (K + 1) / 2] bytes, k even in the low four bits; scale device
+ * [N][groups] (groups = K / group rounded up) of base->dtype (E2M1: bytes); zero [N][groups] bytes, or NULL
+ * without zero points. base's pointers are 16-byte aligned.
+ * Errors: EINVAL; EHIP. */
+sgmv_status sgmv_base_pack(const uint8_t* codes, int64_t ldc, const void* scale, const uint8_t* zero,
+                           const sgmv_base* base, void* stream);
+
+/* y[t][n] = sum_k w[n][k] x[t][k] for T rows (0 is allowed), products and sums in fp32 (of fp32 rows all
+ * their bits enter), scales applied to the fp32 sums of their groups, rounded once to dtype. A row of x that
+ * is not finite spoils its own row of y only. I4 sums codes as they are and takes the zero points' share off
+ * after: products of 16 |x| have to stay in fp32.
+ *   x  device [T][ldx >= K], y device [T][ldy >= N], of base->dtype; y must not overlap x
+ *   workspace  device, 16-byte aligned, of sgmv_base_product_workspace bytes (0: may be NULL)
+ * Errors: EINVAL; EUNSUPPORTED; ECAPACITY (workspace); EHIP. */
+sgmv_status sgmv_base_product_workspace(int32_t T, const sgmv_base* base, size_t* bytes);
+sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, const sgmv_base* base, void* y,
+                              int64_t ldy, void* workspace, size_t workspace_bytes, void* stream);
 
 /* Human-readable name of a status code (static string). */
 const char* sgmv_status_string(sgmv_status s);

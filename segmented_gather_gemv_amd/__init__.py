@@ -11,7 +11,8 @@ those of the C-ABI in ``include/sgmv.h``:
     sgmv_lora_delta(x, pool, seg, y | [slices])       -> None (y updated in place)
 
 and, for the attention of the same step, sgmv_kv_write, sgmv_kv_read, sgmv_kv_attention and
-sgmv_verify_drafts (_serving.py).
+sgmv_verify_drafts (_serving.py), for the rest of its layer sgmv_rms_norm, sgmv_base_product and
+sgmv_kv_append (_layer.py).
 
 The shared library is loaded from this package directory; importing raises if it is
 missing (build it with ``python -m segmented_gather_gemv_amd.build``).
@@ -51,6 +52,8 @@ EXPORTED = [
     "sgmv_version", "sgmv_chunk_size_for_batch", "sgmv_lora_delta_ids_noalloc",
     "sgmv_exchange_placement", "sgmv_kv_init", "sgmv_kv_write", "sgmv_kv_read",
     "sgmv_kv_attention_workspace", "sgmv_kv_attention", "sgmv_verify_drafts", "sgmv_verify_drafts_workspace",
+    "sgmv_kv_append", "sgmv_rms_norm", "sgmv_base_init", "sgmv_base_pack", "sgmv_base_product_workspace",
+    "sgmv_base_product",
 ]
 
 
@@ -550,6 +553,10 @@ from ._serving import (  # noqa: E402
     KV_F32, KV_BF16, KV_E4M3, KV_I8, KV_GROUP, KV_MAX_PAGE, KV_MAX_HEAD_DIM, KV_MAX_HEADS, KV_MAX_B,
     KV_MAX_SPLITS, KvCache, KvBatch, sgmv_kv_init, sgmv_kv_wrap, sgmv_kv_batch, sgmv_kv_write,
     sgmv_kv_read, sgmv_kv_attention, sgmv_kv_attention_workspace, sgmv_verify_drafts)
+# the norm, the 4-bit base product and the rotated append
+from ._layer import (  # noqa: E402
+    MAX_NORM_WIDTH, BASE_MAX_SIZE, BASE_I4, BASE_E2M1, Normed, BaseWeight, sgmv_rms_norm, sgmv_base_pack,
+    sgmv_base_product, sgmv_base_product_workspace, sgmv_kv_append)
 
 __all__ = [
     "LIB_PATH", "EXPORTED", "SgmvError", "Pool", "Segments", "LaunchOpts", "library",
@@ -559,4 +566,6 @@ __all__ = [
     "sgmv_chunk_size_for_batch", "sgmv_exchange_placement",
     "KvCache", "KvBatch", "sgmv_kv_init", "sgmv_kv_wrap", "sgmv_kv_batch", "sgmv_kv_write",
     "sgmv_kv_read", "sgmv_kv_attention", "sgmv_kv_attention_workspace", "sgmv_verify_drafts",
+    "Normed", "BaseWeight", "sgmv_rms_norm", "sgmv_base_pack", "sgmv_base_product",
+    "sgmv_base_product_workspace", "sgmv_kv_append",
 ]

@@ -1,0 +1,148 @@
+// Product with a base weight held in 4 bits: arguments and the operands that both kernels share.
+//
+// A block of 16 n and 128 k is 1 KB, 16 bytes of each lane; its word j is the right operand of the 16x16x32
+// product over k = 32 j .. 32 j + 31 once converted: lane (n = lane % 16, quad = lane / 16) holds k = 8 quad .. + 7 of
+// column n. The left operand is 16 rows of x; lane (n, quad) gets rows 4 quad .. 4 quad + 3 of column n, so that a
+// group's scale and zero point are one value of the lane.
+//   I4    c is an e4m3 code as it stands (a number below 16 in the low bits of a byte is c 2^-9), so that two codes
+//         become two exact bf16 by one instruction: y += s (sum c x - z sum x), with sum x from a product by ones.
+//   E2M1  the scale is a power of two, which the conversion applies: the operand is the weight itself, exact.
+// fp32 rows are split into three bf16 (24 bits), of I4 with c - z as the operand.
+#pragma once
+
+#include "common.h"
+
+namespace sgmv {
+
+constexpr int BASE_K = 128;  // k of a block
+constexpr int BASE_N = 16;   // n
+
+struct BaseArgs {
+  const void* codes;
+  const void* scale;
+  const uint8_t* zero;
+  const void* x;
+  void* y;
+  int64_t ldx, ldy;
+  int32_t T, N, K;
+  int32_t blocks;      // of 128 k
+  int32_t scale_rows;  // [16][s] rows of scales of 16 n
+  int32_t per_group;   // blocks of a group (1 for short ones)
+  int32_t x_vec;       // rows of x may be read 16 bytes at a time
+};
+
+struct BasePackArgs {
+  const uint8_t* codes;
+  int64_t ldc;
+  const void* scale;
+  const uint8_t* zero;
+  void *codes_out, *scale_out;
+  uint8_t* zero_out;
+  int32_t N, K, groups, blocks, scale_rows, s, e2m1, scale_bytes;
+};
+
+hipError_t launch_base_pack(const BasePackArgs& A, hipStream_t stream);
+hipError_t launch_base_direct_bf16(const BaseArgs& A, int format, int s, hipStream_t stream);
+hipError_t launch_base_direct_f32(const BaseArgs& A, int format, int s, hipStream_t stream);
+
+// Eight I4 codes as bf16.
+__device__ __forceinline__ u32x4_t base_codes(uint32_t w) {
+  const uint32_t lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
+  return u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 512.f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)lo, 512.f, true)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 512.f, false)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((int)hi, 512.f, true))};
+}
+
+// Eight E2M1 codes times a power of two, as bf16.
+__device__ __forceinline__ u32x4_t base_floats(uint32_t w, float scale) {
+  return u32x4_t{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3))};
+}
+
+// Eight codes less their zero point, as bf16 (exact: whole numbers below 16).
+__device__ __forceinline__ u32x4_t base_less(u32x4_t c, float zero) {
+  u32x4_t r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = __uint_as_float(c[i] << 16) - zero, b = __uint_as_float(c[i] & 0xffff0000u) - zero;
+    r[i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+  }
+  return r;
+}
+
+// The scales of one row of 16 n, or E2M1's as what the conversion takes.
+template <bool E2M1, bool F32, int S>
+struct BaseScale {
+  float f[S];
+  static __device__ __forceinline__ BaseScale load(const void* p, int64_t row, int n) {
+    BaseScale r;
+    const int64_t at = (row * BASE_N + n) * S;
+    if constexpr (E2M1) {
+      static_assert(S == 4, "groups of 32");
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + at);
+#pragma unroll
+      for (int i = 0; i < S; ++i) r.f[i] = __uint_as_float((w >> (8 * i) & 255u) << 23);
+    } else if constexpr (F32) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) r.f[i] = static_cast<const float*>(p)[at + i];
+    } else {
+      const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+      if constexpr (S == 1) {
+        r.f[0] = bf16_bits_to_f32(*q);
+      } else {
+#pragma unroll
+        for (int i = 0; i < S / 2; ++i) {
+          const uint32_t w = reinterpret_cast<const uint32_t*>(q)[i];
+          r.f[2 * i] = __uint_as_float(w << 16);
+          r.f[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
+        }
+      }
+    }
+    return r;
+  }
+};
+
+// Zero points of one row of 16 n (8 where there are none).
+template <bool ZERO, int S>
+struct BaseZero {
+  float f[S];
+  static __device__ __forceinline__ BaseZero load(const uint8_t* p, int64_t row, int n) {
+    BaseZero r;
+    if constexpr (!ZERO) {
+#pragma unroll
+      for (int i = 0; i < S; ++i) r.f[i] = 8.f;
+    } else {
+      const uint8_t* q = p + (row * BASE_N + n) * S;
+      uint32_t w;
+      if constexpr (S == 4) w = *reinterpret_cast<const uint32_t*>(q);
+      else if constexpr (S == 2) w = *reinterpret_cast<const uint16_t*>(q);
+      else w = *q;
+#pragma unroll
+      for (int i = 0; i < S; ++i) r.f[i] = (float)(w >> (8 * i) & 255u);
+    }
+    return r;
+  }
+};
+
+// fp32 values as three bf16 each that add up to them: their leading 8 bits, the next 8, the last (numbers below
+// 2^-110 lose bits that bf16 does not hold).
+__device__ __forceinline__ void split3(const u32x4_t (&x)[2], bf16x8_t (&p)[3]) {
+  u32x4_t w[3];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a = x[i / 2][2 * (i % 2)], b = x[i / 2][2 * (i % 2) + 1];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      w[k][i] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+      a = __float_as_uint(__uint_as_float(a) - __uint_as_float(a & 0xffff0000u));
+      b = __float_as_uint(__uint_as_float(b) - __uint_as_float(b & 0xffff0000u));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) p[k] = as_bf16x8(w[k]);
+}
+
+}  // namespace sgmv

@@ -11,6 +11,8 @@
 namespace sgmv {
 hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, int max_q, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
+hipError_t launch_kv_append(const KvArgs& K, const KvRows& R, const KvTurn& turn, int fmt, int max_q, hipStream_t stream);
+int64_t kv_append_waves(const KvArgs& K, const KvTurn& turn);
 hipError_t launch_attn_direct_bf16(const AttnArgs& A, hipStream_t stream);
 hipError_t launch_attn_direct_e4m3(const AttnArgs& A, hipStream_t stream);
 hipError_t launch_attn_direct_i8(const AttnArgs& A, hipStream_t stream);
@@ -235,6 +237,35 @@ sgmv_status sgmv_kv_write(const void* k, int64_t ldk_token, int64_t ldk_head, co
                  nullptr, 0, dtype == SGMV_F32,
                  rows_vec(k, v, ldk_token, ldk_head, ldv_token, ldv_head, dtype)};
   return launched(launch_kv_write(K, R, cache->format, batch->max_q, static_cast<hipStream_t>(stream)));
+}
+
+sgmv_status sgmv_kv_append(const sgmv_kv_rotation* turn, const void* k, int64_t ldk_token, int64_t ldk_head,
+                           const void* v, int64_t ldv_token, int64_t ldv_head, int32_t dtype,
+                           const sgmv_kv_batch* batch, const sgmv_kv_cache* cache, void* stream) {
+  KvArgs K;
+  bool empty;
+  const sgmv_status s = fill(batch, cache, K, empty);
+  if (s != SGMV_OK) return s;
+  if (!turn || !row_type_ok(dtype) || !types_fit(dtype, cache->format) || turn->rotary < 1 || turn->rotary > K.D ||
+      turn->positions < 1 || turn->ld < turn->rotary || turn->heads < 0 || (turn->interleaved != 0 && turn->interleaved != 1))
+    return SGMV_EINVAL;
+  if (turn->rotary % 16 || turn->heads > SGMV_KV_MAX_HEADS) return SGMV_EUNSUPPORTED;
+  if (empty || batch->T == 0) return SGMV_OK;
+  if (!turn->cos_sin || !aligned_to(turn->cos_sin, 4) || !rows_ok(k, K.T, ldk_token, ldk_head, K.H, K.D) ||
+      !rows_ok(v, K.T, ldv_token, ldv_head, K.H, K.D))
+    return SGMV_EINVAL;
+  if (turn->heads > 0 && (!rows_ok(turn->q, K.T, turn->ldq_token, turn->ldq_head, turn->heads, K.D) ||
+                          !rows_ok(turn->q_out, K.T, turn->ldo_token, turn->ldo_head, turn->heads, K.D)))
+    return SGMV_EINVAL;
+  const KvRows R{const_cast<void*>(k), const_cast<void*>(v), ldk_token, ldk_head, ldv_token, ldv_head,
+                 nullptr, 0, dtype == SGMV_F32,
+                 rows_vec(k, v, ldk_token, ldk_head, ldv_token, ldv_head, dtype)};
+  const KvTurn t{turn->cos_sin, turn->ld, turn->positions, turn->rotary, turn->interleaved,
+                 aligned_to(turn->cos_sin, 16) && turn->ld % 4 == 0, turn->q, turn->q_out, turn->ldq_token,
+                 turn->ldq_head, turn->ldo_token, turn->ldo_head, turn->heads,
+                 rows_vec(turn->q, turn->q_out, turn->ldq_token, turn->ldq_head, turn->ldo_token, turn->ldo_head, dtype)};
+  if (kv_append_waves(K, t) > MOST_WAVES) return SGMV_EUNSUPPORTED;
+  return launched(launch_kv_append(K, R, t, cache->format, batch->max_q, static_cast<hipStream_t>(stream)));
 }
 
 sgmv_status sgmv_kv_read(const sgmv_kv_batch* batch, const sgmv_kv_cache* cache,

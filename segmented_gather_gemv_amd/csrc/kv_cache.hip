@@ -29,77 +29,16 @@
 // so that loads, quantising and stores follow each other), 41 thousand tokens read back as bf16 57 us (258 MB,
 // 4.5 TB/s; a large copy: 5.1). Fp32 rows written as e4m3 or int8 19.4 us (floor 17.9), read back 143 (84); rows that
 // are held as they are: bf16 written in 13.9 us (14.2), read in 75 (67), fp32 25 (28) and 181 (133).
-#include "kv_common.h"
+#include <algorithm>
+#include <type_traits>
+
+#include "quantise.h"
 
 namespace sgmv {
 
 namespace {
 
 constexpr int RW_WAVES = 4;
-
-// fp32 nearest to d, rounded to odd: a later rounding to fewer bits then equals a single one.
-__device__ __forceinline__ float to_odd(double d) {
-  const float f = __double2float_rz(d);
-  return (double)f == d ? f : __uint_as_float(__float_as_uint(f) | 1u);
-}
-
-// What quantising a row needs: its maximum; a power of two that keeps the parts of a quotient in range, and F
-// over the maximum so scaled (0: codes 0); its scale.
-struct RowScale {
-  float amax, s, inv, scale;
-};
-
-// top: bits of the row's maximum of |x| (as integers they order as the values do, infinity and NaN last)
-template <int FMT>
-__device__ __forceinline__ RowScale row_scale(uint32_t top) {
-  constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
-  if (top == 0u || top >= 0x7f800000u) return {0.f, 1.f, 0.f, top ? __uint_as_float(0x7fc00000u) : 0.f};
-  const float amax = __uint_as_float(top), s = amax > 0x1p100f ? 0x1p-32f : amax < 0x1p-90f ? 0x1p64f : 1.f;
-  return {amax, s, F / (amax * s), amax / F};
-}
-
-// Four values rounded to codes. int8: the low bits of 1.5 * 2^23 + q are those of q rounded.
-template <int FMT>
-__device__ __forceinline__ uint32_t encode4(const float (&q)[4]) {
-  if constexpr (FMT == SGMV_KV_E4M3) {
-    const int w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
-  } else {
-    uint32_t b[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(q[i] + 0x1.8p23f);
-    return __builtin_amdgcn_perm(__builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u),
-                                 __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u), 0x05040100u);
-  }
-}
-
-// Codes of four values of a row.
-template <int FMT, class T>
-__device__ __forceinline__ uint32_t quantise4(const float (&x)[4], const RowScale& S) {
-  constexpr float F = FMT == SGMV_KV_E4M3 ? 448.f : 127.f;
-  uint32_t w;
-  float q[4];
-  if constexpr (sizeof(T) == 2) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = __uint_as_float((__float_as_uint(x[i] * S.s * S.inv) + 16u) & ~31u);
-    w = encode4<FMT>(q);
-  } else {
-    float hi[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float y = x[i] * S.s * S.inv;
-      q[i] = y * (1.f - 0x1p-22f);
-      hi[i] = y * (1.f + 0x1p-22f);
-    }
-    w = encode4<FMT>(q);
-    if (__any(w != encode4<FMT>(hi))) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = to_odd((double)x[i] * (double)F / (double)S.amax);
-      w = encode4<FMT>(q);
-    }
-  }
-  return S.inv == 0.f ? 0u : w;
-}
 
 // Transposes a 4x4 block of bytes held by 4 neighbouring lanes, one row each.
 __device__ __forceinline__ uint32_t transpose_bytes(uint32_t w, int lane) {
@@ -235,9 +174,10 @@ __device__ __forceinline__ int place_of(int r) { return 8 * ((r >> 2) & 1) + 4 *
 // before b) / 16 + 2 b on; n rows touch at most (n + 14) / 16 + 1 groups. start: rows of each sequence,
 // the last ones of it.
 // by_place: lane r of 16 has the token at place r, not token r.
-__device__ __forceinline__ bool group_place(const KvArgs& K, const int32_t* start, int total, bool by_place, Place& P) {
+__device__ __forceinline__ bool group_place(const KvArgs& K, const int32_t* start, int total, int slots, int head,
+                                            bool by_place, Place& P) {
   const int lane = threadIdx.x & (WAVE - 1), r = by_place ? place_of(lane & 15) : lane & 15;
-  const int slot = blockIdx.x * RW_WAVES + threadIdx.x / WAVE;
+  const int slot = slots * RW_WAVES + threadIdx.x / WAVE;
   const int b = wave_find(K.B, slot, [&](int i) { return min(max(start[i], 0), total) / 16 + 2 * i; });
   const int r0 = min(max(start[b], 0), total), r1 = min(max(start[b + 1], 0), total);
   const int n = max(r1 - r0, 0), kv_len = kv_seq(K, b).kv_len;
@@ -246,7 +186,7 @@ __device__ __forceinline__ bool group_place(const KvArgs& K, const int32_t* star
   const int t_lo = max(16 * g0, first), t_hi = min(16 * g0 + 16, kv_len);
   if (t_lo >= t_hi) return false;
   const int t = 16 * g0 + r, t4 = t & ~3;
-  P.head = blockIdx.y;
+  P.head = head;
   P.ok = t >= t_lo && t < t_hi;
   P.quad_ok = t4 >= t_lo && t4 + 4 <= t_hi;
   P.whole = t_lo == 16 * g0 && t_hi == 16 * g0 + 16;
@@ -296,9 +236,92 @@ template <int FMT, class T> struct Unit {
 template <int BYTES>
 __device__ __forceinline__ int64_t v_at(int d, int place) { return (int64_t)(d * 16 + place) * BYTES; }
 
-// 16 rows of K (or, grouped, of V) per wave.
-template <int FMT, class T, bool GROUPED>
-__device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, bool is_v, const Place& place16) {
+// N floats of the table of cosines and sines.
+template <int N>
+__device__ __forceinline__ void load_angles(const float* p, bool vec, float (&f)[N]) {
+  if (!vec) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) f[i] = p[i];
+  } else if constexpr (N == 2) {
+    const f32x2_t v = *reinterpret_cast<const f32x2_t*>(p);
+    f[0] = v.x;
+    f[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + i);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f[i + j] = v[j];
+    }
+  }
+}
+
+// Cosines and sines i .. i + N - 1 of a position; past the table they are NaN, so that what they turn is.
+template <int N>
+__device__ __forceinline__ void angles(const KvTurn& R, int pos, int i, float (&c)[N], float (&s)[N]) {
+  const bool in = (uint32_t)pos < (uint32_t)R.positions;  // (a row before the first token is not written anyway)
+  const float* row = R.cos_sin + (in ? pos : 0) * R.ld + i;
+  load_angles(row, R.vec, c);
+  load_angles(row + R.rotary / 2, R.vec, s);
+  if (!in)
+#pragma unroll
+    for (int j = 0; j < N; ++j) c[j] = s[j] = __uint_as_float(0x7fc00000u);
+}
+
+// A pair turned by its angle: two products and their sum, each rounded to fp32.
+__device__ __forceinline__ float turn_low(float a, float b, float c, float s) {
+#pragma clang fp contract(off)
+  return a * c - b * s;
+}
+__device__ __forceinline__ float turn_high(float a, float b, float c, float s) {
+#pragma clang fp contract(off)
+  return b * c + a * s;
+}
+
+// Values d .. d + N - 1 (d a multiple of N, N of 4 and a divisor of 8) of a row at a position, turned.
+template <class T, int N>
+__device__ __forceinline__ void turned(const KvTurn& R, const T* row, bool vec, int pos, int d, float* y) {
+  constexpr int W = N * sizeof(T) / 4;
+  uint32_t own[W];
+  if constexpr (W >= 4) {
+    load_words(row + d, vec, own);
+  } else {  // 4 values of 16 bits
+#pragma unroll
+    for (int i = 0; i < W; ++i) own[i] = row[d + 2 * i] | (uint32_t)row[d + 2 * i + 1] << 16;
+  }
+  float x[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) x[e] = word_value<T>(own, e);
+  const int half = R.rotary / 2;
+  if (d >= R.rotary) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] = x[e];
+  } else if (R.interleaved) {
+    float c[N / 2], s[N / 2];
+    angles(R, pos, d / 2, c, s);
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      y[2 * e] = turn_low(x[2 * e], x[2 * e + 1], c[e], s[e]);
+      y[2 * e + 1] = turn_high(x[2 * e], x[2 * e + 1], c[e], s[e]);
+    }
+  } else {  // the other half's values (the same lines of the row)
+    const bool low = d < half;
+    uint32_t other[W];
+    load_words(row + (low ? d + half : d - half), vec, other);
+    float c[N], s[N];
+    angles(R, pos, low ? d : d - half, c, s);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      const float o = word_value<T>(other, e);
+      y[e] = low ? turn_low(x[e], o, c[e], s[e]) : turn_high(o, x[e], c[e], s[e]);
+    }
+  }
+}
+
+// 16 rows of K (or, grouped, of V) per wave. TURN: of K, turned by their positions on the way.
+template <int FMT, class ROW, bool GROUPED, bool TURN>
+__device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, const KvTurn& R, bool is_v, const Place& place16) {
+  using T = std::conditional_t<TURN, float, ROW>;  // of the values in registers
   using U = Unit<FMT, T>;
   constexpr int BYTES = U::bytes, C = U::C;
   constexpr bool SCALED = KvFormat<FMT>::scaled;
@@ -306,8 +329,8 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, boo
   Place P = place16;
   if (!__any(P.ok)) return;
   const int D = K.D, units = D / C;
-  const T* src = static_cast<const T*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) +
-                 P.head * (is_v ? A.ldv_h : A.ldk_h);
+  const ROW* src = static_cast<const ROW*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) +
+                   P.head * (is_v ? A.ldv_h : A.ldk_h);
   uint32_t w[U::most][U::words];
 #pragma unroll
   for (int n = 0; n < U::most; ++n) {
@@ -315,7 +338,17 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, boo
     const int u = quad + 4 * n;
 #pragma unroll
     for (int i = 0; i < U::words; ++i) w[n][i] = 0u;
-    if (P.ok && u < units) load_words(src + u * C, A.vec, w[n]);
+    if (!P.ok || u >= units) continue;
+    if constexpr (TURN) {
+      constexpr int N = C < 8 ? C : 8;
+      float x[C];
+#pragma unroll
+      for (int e = 0; e < C; e += N) turned<ROW, N>(R, src, A.vec, P.pos, u * C + e, x + e);
+#pragma unroll
+      for (int e = 0; e < C; ++e) w[n][e] = __float_as_uint(x[e]);
+    } else {
+      load_words(src + u * C, A.vec, w[n]);
+    }
   }
   const int64_t at = token_of(K, P), token = max(at, (int64_t)0);  // the page's load beside the row's
   P.ok = P.ok && at >= 0;
@@ -347,6 +380,9 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, boo
         for (int j = 0; j < 4; ++j) x[j] = word_value<T>(w[n], 4 * k + j);
         c[k] = quantise4<FMT, T>(x, S);
       }
+    } else if constexpr (U::words == 8) {  // fp32 values of a bf16 cache
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = pack_bf16x2(__uint_as_float(w[n][2 * k]), __uint_as_float(w[n][2 * k + 1]));
     } else {
       c = u32x4_t{w[n][0], w[n][1], w[n][2], w[n][3]};
     }
@@ -428,7 +464,8 @@ __device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, co
 template <int FMT, class T>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_groups_kernel(KvArgs K, KvRows A) {
   Place P;
-  if (group_place(K, K.q_start, K.T, blockIdx.z && KvFormat<FMT>::bytes == 1, P)) write_rows<FMT, T, true>(K, A, blockIdx.z, P);
+  if (group_place(K, K.q_start, K.T, blockIdx.x, blockIdx.y, blockIdx.z && KvFormat<FMT>::bytes == 1, P))
+    write_rows<FMT, T, true, false>(K, A, KvTurn{}, blockIdx.z, P);
 }
 
 // Workgroups [0, for_v) take V, the others K.
@@ -441,7 +478,139 @@ __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_rows_kernel(KvArgs K,
     write_v_row<FMT, T>(K, A, P);
   } else {
     row_place(K, K.q_start, K.T, (((int)blockIdx.x - for_v) * RW_WAVES + wv) * 16 + (lane & 15), P);
-    write_rows<FMT, T, false>(K, A, false, P);
+    write_rows<FMT, T, false, false>(K, A, KvTurn{}, false, P);
+  }
+}
+
+constexpr int TURN_HEADS = 4;  // that a lane of the queries' waves takes
+
+// How the queries' rows are laid over waves: a lane takes one piece of a head, 16 values that make 8 pairs (of
+// neighbours 8, of what is not turned 8 to copy), of TURN_HEADS heads `side` apart.
+struct TurnGrid {
+  int turned, pieces;  // pieces of a head that are turned, and all (with those to copy)
+  int side;            // heads side by side in a wave
+  int waves;           // of a token
+};
+
+__host__ __device__ inline TurnGrid turn_grid(const KvTurn& R, int D) {
+  TurnGrid g;
+  g.turned = R.rotary / (R.interleaved ? 8 : 16);
+  const bool same = R.q == R.q_out && R.ldq_t == R.ldo_t && R.ldq_h == R.ldo_h;
+  g.pieces = g.turned + (same ? 0 : (D - R.rotary) / 8);
+  g.side = WAVE / g.pieces;
+  g.waves = (R.heads + g.side * TURN_HEADS - 1) / (g.side * TURN_HEADS);
+  return g;
+}
+
+// One wave of the queries. A lane reads all that it turns before it writes, so that rows may be turned in place.
+template <class T>
+__device__ __forceinline__ void turn_queries(const KvArgs& K, const KvTurn& R, int wave) {
+  constexpr int W = 2 * sizeof(T);  // words of 8 values
+  const int lane = threadIdx.x & (WAVE - 1);
+  const TurnGrid G = turn_grid(R, K.D);
+  const int token = wave / G.waves;
+  if (token >= K.T) return;
+  Place P;
+  row_place(K, K.q_start, K.T, token * K.H, P);  // (the same in all lanes)
+  if (!P.ok || P.pos < 0) return;
+  const int at = lane / G.pieces, piece = lane - at * G.pieces;
+  const int head0 = (wave - token * G.waves) * G.side * TURN_HEADS + at;
+  if (at >= G.side) return;
+  const T* q = static_cast<const T*>(R.q) + token * R.ldq_t;
+  T* out = static_cast<T*>(R.q_out) + token * R.ldo_t;
+  const bool copy = piece >= G.turned;
+  const int half = R.rotary / 2;
+  // the lane's values: d, and of pairs half a rotation apart d + half
+  const int d = copy ? R.rotary + 8 * (piece - G.turned) : 8 * piece;
+  const bool two = !copy && !R.interleaved;
+  uint32_t a[TURN_HEADS][W], b[TURN_HEADS][W];
+#pragma unroll
+  for (int n = 0; n < TURN_HEADS; ++n) {
+    const int head = head0 + n * G.side;
+    if (head >= R.heads) break;
+    load_words(q + head * R.ldq_h + d, R.q_vec, a[n]);
+    if (two) load_words(q + head * R.ldq_h + d + half, R.q_vec, b[n]);
+  }
+  float c[8], s[8];
+  if (two) {
+    angles(R, P.pos, d, c, s);
+  } else if (!copy) {
+    float c4[4], s4[4];
+    angles(R, P.pos, d / 2, c4, s4);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      c[e] = c4[e];
+      s[e] = s4[e];
+    }
+  }
+  const auto words = [](const float (&y)[8], uint32_t (&w)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(y[i]);
+      else w[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+    }
+  };
+#pragma unroll
+  for (int n = 0; n < TURN_HEADS; ++n) {
+    const int head = head0 + n * G.side;
+    if (head >= R.heads) break;
+    T* to = out + head * R.ldo_h + d;
+    if (copy) {
+      store_words(to, R.q_vec, a[n]);
+      continue;
+    }
+    float x[8], o[8], y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = word_value<T>(a[n], e);
+    uint32_t w[W];
+    if (R.interleaved) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[2 * e] = turn_low(x[2 * e], x[2 * e + 1], c[e], s[e]);
+        y[2 * e + 1] = turn_high(x[2 * e], x[2 * e + 1], c[e], s[e]);
+      }
+      words(y, w);
+      store_words(to, R.q_vec, w);
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      o[e] = word_value<T>(b[n], e);
+      y[e] = turn_low(x[e], o[e], c[e], s[e]);
+    }
+    words(y, w);
+    store_words(to, R.q_vec, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = turn_high(x[e], o[e], c[e], s[e]);
+    words(y, w);
+    store_words(to + half, R.q_vec, w);
+  }
+}
+
+// As the write kernels, with K turned; workgroups from `rest` on take the queries.
+template <int FMT, class T>
+__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_groups_kernel(KvArgs K, KvRows A, KvTurn R, int slots, int rest) {
+  const int at = blockIdx.x;
+  if (at >= rest) return turn_queries<T>(K, R, (at - rest) * RW_WAVES + threadIdx.x / WAVE);
+  const bool is_v = at >= rest / 2;
+  const int of = is_v ? at - rest / 2 : at, head = of / slots;
+  Place P;
+  if (!group_place(K, K.q_start, K.T, of - head * slots, head, is_v && KvFormat<FMT>::bytes == 1, P)) return;
+  if (is_v) write_rows<FMT, T, true, false>(K, A, R, true, P);
+  else write_rows<FMT, T, true, true>(K, A, R, false, P);
+}
+
+template <int FMT, class T>
+__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_rows_kernel(KvArgs K, KvRows A, KvTurn R, int for_v, int rest) {
+  const int wv = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1), at = blockIdx.x;
+  if (at >= rest) return turn_queries<T>(K, R, (at - rest) * RW_WAVES + wv);
+  Place P;
+  if (at < for_v) {
+    row_place(K, K.q_start, K.T, at * RW_WAVES + wv, P);
+    write_v_row<FMT, T>(K, A, P);
+  } else {
+    row_place(K, K.q_start, K.T, ((at - for_v) * RW_WAVES + wv) * 16 + (lane & 15), P);
+    write_rows<FMT, T, false, true>(K, A, R, false, P);
   }
 }
 
@@ -563,7 +732,7 @@ __device__ __forceinline__ void read_v_row(const KvArgs& K, const KvRows& A, con
 template <int FMT, class T>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_read_groups_kernel(KvArgs K, KvRows A) {
   Place P;
-  if (group_place(K, A.out_start, A.rows, blockIdx.z && KvFormat<FMT>::bytes == 1, P)) read_rows<FMT, T, true>(K, A, blockIdx.z, P);
+  if (group_place(K, A.out_start, A.rows, blockIdx.x, blockIdx.y, blockIdx.z && KvFormat<FMT>::bytes == 1, P)) read_rows<FMT, T, true>(K, A, blockIdx.z, P);
 }
 
 template <int FMT, class T>
@@ -604,6 +773,19 @@ void launch_write(const KvArgs& K, const KvRows& R, int max_q, hipStream_t strea
 }
 
 template <int FMT, class T>
+void launch_append(const KvArgs& K, const KvRows& A, const KvTurn& R, int max_q, hipStream_t stream) {
+  const unsigned for_q = R.heads ? (unsigned)(((int64_t)K.T * turn_grid(R, K.D).waves + RW_WAVES - 1) / RW_WAVES) : 0u;
+  const RowGrid g = row_grid(K, K.T, max_q <= 8);
+  if (g.all) {
+    kv_append_rows_kernel<FMT, T><<<g.all + for_q, RW_WAVES * WAVE, 0, stream>>>(K, A, R, g.for_v, (int)g.all);
+  } else {
+    const dim3 d = group_grid(K, K.T);
+    const unsigned rest = 2 * d.x * d.y;
+    kv_append_groups_kernel<FMT, T><<<rest + for_q, RW_WAVES * WAVE, 0, stream>>>(K, A, R, (int)d.x, (int)rest);
+  }
+}
+
+template <int FMT, class T>
 void launch_read(const KvArgs& K, const KvRows& R, hipStream_t stream) {
   const RowGrid g = row_grid(K, R.rows, R.rows <= 4 * (int64_t)K.B);
   if (g.all) kv_read_rows_kernel<FMT, T><<<g.all, RW_WAVES * WAVE, 0, stream>>>(K, R, g.for_v);
@@ -619,6 +801,23 @@ hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, int max_q,
   else if (fmt == SGMV_KV_E4M3) launch_write<SGMV_KV_E4M3, uint16_t>(K, R, max_q, stream);
   else if (R.f32) launch_write<SGMV_KV_I8, float>(K, R, max_q, stream);
   else launch_write<SGMV_KV_I8, uint16_t>(K, R, max_q, stream);
+  return hipGetLastError();
+}
+
+// Waves of an append's launch, at most.
+int64_t kv_append_waves(const KvArgs& K, const KvTurn& R) {
+  const dim3 g = group_grid(K, K.T);
+  const RowGrid r = row_grid(K, K.T, true);
+  return std::max<int64_t>((int64_t)2 * g.x * g.y, r.all) * RW_WAVES + (R.heads ? (int64_t)K.T * turn_grid(R, K.D).waves + RW_WAVES : 0);
+}
+
+hipError_t launch_kv_append(const KvArgs& K, const KvRows& A, const KvTurn& R, int fmt, int max_q, hipStream_t stream) {
+  if (fmt == SGMV_KV_F32) launch_append<SGMV_KV_F32, float>(K, A, R, max_q, stream);
+  else if (fmt == SGMV_KV_BF16) launch_append<SGMV_KV_BF16, uint16_t>(K, A, R, max_q, stream);
+  else if (fmt == SGMV_KV_E4M3 && A.f32) launch_append<SGMV_KV_E4M3, float>(K, A, R, max_q, stream);
+  else if (fmt == SGMV_KV_E4M3) launch_append<SGMV_KV_E4M3, uint16_t>(K, A, R, max_q, stream);
+  else if (A.f32) launch_append<SGMV_KV_I8, float>(K, A, R, max_q, stream);
+  else launch_append<SGMV_KV_I8, uint16_t>(K, A, R, max_q, stream);
   return hipGetLastError();
 }
 

@@ -44,6 +44,19 @@ struct KvRows {
   int32_t vec;               // rows may be accessed 16 bytes at a time
 };
 
+// Rotation of an append: the cosines and sines of each position, and the step's queries [T][heads][D].
+struct KvTurn {
+  const float* cos_sin;  // [positions][ld]: rotary / 2 cosines, then as many sines
+  int64_t ld;
+  int32_t positions, rotary, interleaved;
+  int32_t vec;           // rows of the table may be read 16 bytes at a time
+  const void* q;
+  void* q_out;
+  int64_t ldq_t, ldq_h, ldo_t, ldo_h;
+  int32_t heads;         // 0: no queries
+  int32_t q_vec;         // their rows may be accessed 16 bytes at a time
+};
+
 // One sequence of the batch, whatever the arrays hold: its first new token, its new tokens and
 // its length, clamped so that nothing they lead to lies outside the arrays.
 struct KvSeq {

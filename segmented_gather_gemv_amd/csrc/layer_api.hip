@@ -1,0 +1,154 @@
+// C-ABI of the norm and of the base product: argument validation and launch geometry. Stateless; every call runs on
+// the caller's stream. Declarations and contracts are in include/sgmv.h.
+#include <algorithm>
+#include <cmath>
+
+#include "base.h"
+#include "norm.h"
+
+namespace sgmv {
+
+namespace {
+
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool row_type_ok(int dtype) { return dtype == SGMV_F32 || dtype == SGMV_BF16; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline sgmv_status launched(hipError_t e) { return e == hipSuccess ? SGMV_OK : SGMV_EHIP; }
+constexpr int64_t MOST_WAVES = 0xffffffffll / 64;  // of a launch: it takes fewer than 2^32 work items
+
+// Rows [T][heads][W] with a token and a head stride: rows must not overlap one another.
+bool rows_ok(const void* p, const sgmv_norm* n, int64_t ld_t, int64_t ld_h) {
+  return p && (n->heads == 1 || ld_h >= n->width) &&
+         (n->T == 1 || ld_t >= (n->heads - 1) * (n->heads == 1 ? 0 : ld_h) + n->width);
+}
+
+// The sizes of a weight's parts.
+struct BaseShape {
+  int64_t tiles, blocks, groups, s, scale_rows, per_group;
+};
+
+BaseShape base_shape(const sgmv_base& b) {
+  BaseShape h;
+  h.tiles = ceil_div(b.N, BASE_N);
+  h.blocks = ceil_div(b.K, BASE_K);
+  h.groups = ceil_div(b.K, b.group);
+  h.s = b.group < BASE_K ? BASE_K / b.group : 1;
+  h.scale_rows = b.group < BASE_K ? h.blocks : h.groups;
+  h.per_group = b.group < BASE_K ? 1 : b.group / BASE_K;
+  return h;
+}
+
+sgmv_status base_shape_ok(int32_t N, int32_t K, int32_t group, int32_t format, int32_t dtype, int32_t has_zero) {
+  if (N < 1 || K < 1 || group < 1 || (format != SGMV_BASE_I4 && format != SGMV_BASE_E2M1) || !row_type_ok(dtype) ||
+      (has_zero != 0 && has_zero != 1))
+    return SGMV_EINVAL;
+  if (format == SGMV_BASE_E2M1 && (has_zero || group != 32)) return SGMV_EINVAL;
+  if ((group != 32 && group != 64 && group % BASE_K) || N > SGMV_BASE_MAX_SIZE || K > SGMV_BASE_MAX_SIZE)
+    return SGMV_EUNSUPPORTED;
+  return SGMV_OK;
+}
+
+sgmv_status base_ok(const sgmv_base* b) {
+  if (!b || !b->codes || !b->scale) return SGMV_EINVAL;
+  const sgmv_status s = base_shape_ok(b->N, b->K, b->group, b->format, b->dtype, b->has_zero);
+  if (s != SGMV_OK) return s;
+  if ((b->has_zero != 0) != (b->zero != nullptr)) return SGMV_EINVAL;
+  if (!aligned_to(b->codes, 16) || !aligned_to(b->scale, 16) || !aligned_to(b->zero, 16)) return SGMV_EINVAL;
+  return SGMV_OK;
+}
+
+inline int scale_size(int format, int dtype) { return format == SGMV_BASE_E2M1 ? 1 : dtype == SGMV_F32 ? 4 : 2; }
+
+}  // namespace
+}  // namespace sgmv
+
+using namespace sgmv;
+
+extern "C" {
+
+sgmv_status sgmv_rms_norm(const sgmv_norm* n, void* stream) {
+  if (!n || n->T < 0 || n->heads < 1 || n->width < 1 || !row_type_ok(n->dtype) || !std::isfinite(n->eps) || n->eps <= 0.f)
+    return SGMV_EINVAL;
+  if (n->codes && n->format != SGMV_KV_E4M3 && n->format != SGMV_KV_I8) return SGMV_EINVAL;
+  if (n->width > SGMV_MAX_NORM_WIDTH) return SGMV_EUNSUPPORTED;
+  if (n->T == 0) return SGMV_OK;
+  if (!n->weight || !rows_ok(n->x, n, n->ldx_token, n->ldx_head) || (n->codes != nullptr) != (n->scale != nullptr) ||
+      (!n->out && !n->codes) || (n->residual_out && !n->residual))
+    return SGMV_EINVAL;
+  if ((n->residual && !rows_ok(n->residual, n, n->ldr_token, n->ldr_head)) ||
+      (n->residual_out && !rows_ok(n->residual_out, n, n->lds_token, n->lds_head)) ||
+      (n->out && !rows_ok(n->out, n, n->ldo_token, n->ldo_head)) ||
+      (n->codes && !rows_ok(n->codes, n, n->ldc_token, n->ldc_head)))
+    return SGMV_EINVAL;
+  const int E = n->dtype == SGMV_F32 ? 4 : 8;
+  const auto vec = [&](const void* p, int64_t ld_t, int64_t ld_h, int bytes) {
+    return !p || (aligned_to(p, bytes) && (n->T == 1 || ld_t % E == 0) && (n->heads == 1 || ld_h % E == 0));
+  };
+  const NormArgs A{n->x, n->residual, n->weight, n->residual_out, n->out, n->codes, n->scale,
+                   n->ldx_token, n->ldx_head, n->ldr_token, n->ldr_head, n->lds_token, n->lds_head,
+                   n->ldo_token, n->ldo_head, n->ldc_token, n->ldc_head, (int64_t)n->T * n->heads, n->heads, n->width,
+                   n->eps,
+                   vec(n->x, n->ldx_token, n->ldx_head, 16) && vec(n->residual, n->ldr_token, n->ldr_head, 16) &&
+                       aligned_to(n->weight, 16) && vec(n->residual_out, n->lds_token, n->lds_head, 16) &&
+                       vec(n->out, n->ldo_token, n->ldo_head, 16) && vec(n->codes, n->ldc_token, n->ldc_head, E)};
+  const NormShape s = norm_shape(A.rows, (int)ceil_div(n->width, E));
+  if (ceil_div(A.rows * s.group, 64) + 16 > MOST_WAVES) return SGMV_EUNSUPPORTED;
+  return launched(launch_norm(A, n->dtype, n->format, static_cast<hipStream_t>(stream)));
+}
+
+sgmv_status sgmv_base_init(int32_t N, int32_t K, int32_t group, int32_t format, int32_t dtype, int32_t has_zero,
+                           sgmv_base* base, size_t* code_bytes, size_t* scale_bytes, size_t* zero_bytes) {
+  if (!base || !code_bytes || !scale_bytes || !zero_bytes) return SGMV_EINVAL;
+  const sgmv_status st = base_shape_ok(N, K, group, format, dtype, has_zero);
+  if (st != SGMV_OK) return st;
+  *base = sgmv_base{nullptr, nullptr, nullptr, N, K, group, format, dtype, has_zero};
+  const BaseShape h = base_shape(*base);
+  const size_t scales = (size_t)h.tiles * h.scale_rows * BASE_N * h.s;
+  *code_bytes = (size_t)h.tiles * h.blocks * BASE_N * BASE_K / 2;
+  *scale_bytes = scales * scale_size(format, dtype);
+  *zero_bytes = has_zero ? scales : 0;
+  return SGMV_OK;
+}
+
+sgmv_status sgmv_base_pack(const uint8_t* codes, int64_t ldc, const void* scale, const uint8_t* zero,
+                           const sgmv_base* b, void* stream) {
+  const sgmv_status st = base_ok(b);
+  if (st != SGMV_OK) return st;
+  if (!codes || ldc < (b->K + 1) / 2 || !scale || (zero != nullptr) != (b->has_zero != 0)) return SGMV_EINVAL;
+  const BaseShape h = base_shape(*b);
+  if (h.tiles * h.blocks * 4 > MOST_WAVES || h.tiles * h.scale_rows * BASE_N * h.s / 64 + 4 > MOST_WAVES) return SGMV_EUNSUPPORTED;
+  const BasePackArgs A{codes, ldc, scale, zero, b->codes, b->scale, b->zero, b->N, b->K, (int32_t)h.groups,
+                       (int32_t)h.blocks, (int32_t)h.scale_rows, (int32_t)h.s, b->format == SGMV_BASE_E2M1,
+                       scale_size(b->format, b->dtype)};
+  return launched(launch_base_pack(A, static_cast<hipStream_t>(stream)));
+}
+
+sgmv_status sgmv_base_product_workspace(int32_t T, const sgmv_base* b, size_t* bytes) {
+  if (!bytes || T < 0) return SGMV_EINVAL;
+  const sgmv_status st = base_ok(b);
+  if (st != SGMV_OK) return st;
+  *bytes = 0;
+  return SGMV_OK;
+}
+
+sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, const sgmv_base* b, void* y, int64_t ldy,
+                              void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  const sgmv_status st = sgmv_base_product_workspace(T, b, &need);
+  if (st != SGMV_OK) return st;
+  if (T == 0) return SGMV_OK;
+  if (!x || !y || ldx < b->K || ldy < b->N) return SGMV_EINVAL;
+  if (need) {
+    if (!workspace || !aligned_to(workspace, 16)) return SGMV_EINVAL;
+    if (workspace_bytes < need) return SGMV_ECAPACITY;
+  }
+  const BaseShape h = base_shape(*b);
+  const int f32 = b->dtype == SGMV_F32, e = f32 ? 4 : 2;
+  const BaseArgs A{b->codes, b->scale, b->zero, x, y, ldx, ldy, T, b->N, b->K, (int32_t)h.blocks, (int32_t)h.scale_rows,
+                   (int32_t)h.per_group, aligned_to(x, 16) && (T == 1 || ldx * e % 16 == 0)};
+  if (ceil_div(T, 16) * h.tiles * 8 > MOST_WAVES) return SGMV_EUNSUPPORTED;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  return launched(f32 ? launch_base_direct_f32(A, b->format, (int)h.s, s) : launch_base_direct_bf16(A, b->format, (int)h.s, s));
+}
+
+}  // extern "C"
