@@ -246,6 +246,8 @@ def sgmv_base_product(x: torch.Tensor, base: BaseWeight, y: Optional[torch.Tenso
             base.N > 1 and y.stride(1) != 1):
         raise ValueError(f"y must be row-major [{T}, {base.N}] of {base.dtype} on the weight's device")
     _int32("T", T)
+    if base.index < 0:
+        raise ValueError("the kernels run on GPU tensors")
     need = ctypes.c_size_t()
     st = _lib.sgmv_base_product_workspace(T, base.ref, ctypes.byref(need))
     if st != SGMV_OK:
