@@ -555,7 +555,7 @@ from ._serving import (  # noqa: E402
     sgmv_kv_read, sgmv_kv_attention, sgmv_kv_attention_workspace, sgmv_verify_drafts)
 # the norm, the 4-bit base product and the rotated append
 from ._layer import (  # noqa: E402
-    MAX_NORM_WIDTH, BASE_MAX_SIZE, BASE_I4, BASE_E2M1, Normed, BaseWeight, sgmv_rms_norm, sgmv_base_pack,
+    MAX_NORM_WIDTH, BASE_MAX_SIZE, BASE_MAX_SPLITS, BASE_I4, BASE_E2M1, Normed, BaseWeight, sgmv_rms_norm, sgmv_base_pack,
     sgmv_base_product, sgmv_base_product_workspace, sgmv_kv_append)
 
 __all__ = [

@@ -16,10 +16,11 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import SGMV_OK, _check, _dtype_code, _lib, _raw_stream
-from ._serving import KV_E4M3, KV_I8, KvBatch, KvCache, _dense3, _int32, _KvBatch, _KvCache, _on_gpu, _rows3
+from ._serving import KV_E4M3, KV_I8, KvBatch, KvCache, _MOST, _dense3, _int32, _KvBatch, _KvCache, _on_gpu, _rows3
 
 MAX_NORM_WIDTH = 32768
 BASE_MAX_SIZE = 4194304
+BASE_MAX_SPLITS = 16
 BASE_I4, BASE_E2M1 = range(2)
 _CODES = {torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_I8}
 
@@ -50,8 +51,8 @@ def _bind():
         "sgmv_rms_norm": [P(_Norm), vp],
         "sgmv_base_init": [i32, i32, i32, i32, i32, i32, B, P(sz), P(sz), P(sz)],
         "sgmv_base_pack": [vp, i64, vp, vp, B, vp],
-        "sgmv_base_product_workspace": [i32, B, P(sz)],
-        "sgmv_base_product": [vp, i64, i32, B, vp, i64, vp, sz, vp],
+        "sgmv_base_product_workspace": [i32, B, i32, P(sz)],
+        "sgmv_base_product": [vp, i64, i32, B, vp, i64, i32, vp, sz, vp],
         "sgmv_kv_append": [P(_Rotation), vp, i64, i64, vp, i64, i64, i32, P(_KvBatch), P(_KvCache), vp],
     }.items():
         f = getattr(_lib, name)
@@ -232,44 +233,50 @@ def sgmv_base_pack(codes: torch.Tensor, scale: torch.Tensor, zero: Optional[torc
 
 
 def sgmv_base_product(x: torch.Tensor, base: BaseWeight, y: Optional[torch.Tensor] = None,
-                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+                      workspace: Optional[torch.Tensor] = None, n_split: int = 0) -> torch.Tensor:
     """y = x W^T for rows x [T, K] of the weight's dtype (strided rows are fine), into ``y`` [T, N] if given; the
-    delta is then added to it. A workspace (uint8) is allocated on the current stream unless one is given."""
-    if x.dim() != 2 or x.shape[1] != base.K or (base.K > 1 and x.stride(1) != 1):
-        raise ValueError(f"x must be row-major [T, {base.K}], got {list(x.shape)}")
-    if x.dtype != base.dtype or x.get_device() != base.index:
-        raise TypeError(f"x must be {base.dtype} on the weight's device")
-    T = x.shape[0]
+    delta is then added to it. A workspace (uint8) is allocated on the current stream unless one is given;
+    ``n_split`` > 0 asks for the kernel of many rows, with K split into that many ranges."""
+    T, N, K, dtype, index = x.shape[0], base.N, base.K, base.dtype, base.index
+    if x.dim() != 2 or x.shape[1] != K or (K > 1 and x.stride(1) != 1):
+        raise ValueError(f"x must be row-major [T, {K}], got {list(x.shape)}")
+    if x.dtype != dtype or x.get_device() != index:
+        raise TypeError(f"x must be {dtype} on the weight's device")
+    if T > _MOST or abs(n_split) > _MOST:
+        _int32("T and n_split", T, n_split)
     if y is None:
-        y = torch.empty((T, base.N), dtype=base.dtype, device=x.device)
-    elif tuple(y.shape) != (T, base.N) or y.dtype != base.dtype or y.get_device() != base.index or (
-            base.N > 1 and y.stride(1) != 1):
-        raise ValueError(f"y must be row-major [{T}, {base.N}] of {base.dtype} on the weight's device")
-    _int32("T", T)
-    if base.index < 0:
+        y, ldy = torch.empty((T, N), dtype=dtype, device=x.device), N
+    else:
+        if tuple(y.shape) != (T, N) or y.dtype != dtype or y.get_device() != index or (N > 1 and y.stride(1) != 1):
+            raise ValueError(f"y must be row-major [{T}, {N}] of {dtype} on the weight's device")
+        ldy = y.stride(0) if T > 1 else N
+    if index < 0:
         raise ValueError("the kernels run on GPU tensors")
-    need = ctypes.c_size_t()
-    st = _lib.sgmv_base_product_workspace(T, base.ref, ctypes.byref(need))
-    if st != SGMV_OK:
-        _check(st, "sgmv_base_product")
-    size, ptr = need.value, None
+    size, ptr = 0, None
+    if T > 32 or n_split:  # (none for fewer rows)
+        need = ctypes.c_size_t()
+        st = _lib.sgmv_base_product_workspace(T, base.ref, n_split, ctypes.byref(need))
+        if st != SGMV_OK:
+            _check(st, "sgmv_base_product")
+        size = need.value
     if workspace is not None:
-        if workspace.get_device() != base.index or not workspace.is_contiguous():
+        if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on x's device")
         size, ptr = workspace.numel() * workspace.element_size(), workspace.data_ptr()
     elif size:
         workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
         ptr = workspace.data_ptr()
-    _launch("sgmv_base_product", base.index, _lib.sgmv_base_product, x.data_ptr(),
-            x.stride(0) if T > 1 else base.K, T, base.ref, y.data_ptr(), y.stride(0) if T > 1 else base.N, ptr, size)
+    _launch("sgmv_base_product", index, _lib.sgmv_base_product, x.data_ptr(), x.stride(0) if T > 1 else K, T,
+            base.ref, y.data_ptr(), ldy, n_split, ptr, size)
     return y
 
 
-def sgmv_base_product_workspace(T: int, base: BaseWeight) -> int:
+def sgmv_base_product_workspace(T: int, base: BaseWeight, n_split: int = 0) -> int:
     """Bytes of workspace that sgmv_base_product takes for T rows."""
-    _int32("T", T)
+    _int32("T and n_split", T, n_split)
     need = ctypes.c_size_t()
-    _check(_lib.sgmv_base_product_workspace(int(T), base.ref, ctypes.byref(need)), "sgmv_base_product_workspace")
+    _check(_lib.sgmv_base_product_workspace(int(T), base.ref, int(n_split), ctypes.byref(need)),
+           "sgmv_base_product_workspace")
     return int(need.value)
 
 

@@ -10,6 +10,8 @@
 // fp32 rows are split into three bf16 (24 bits), of I4 with c - z as the operand.
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace sgmv {
@@ -28,7 +30,11 @@ struct BaseArgs {
   int32_t blocks;      // of 128 k
   int32_t scale_rows;  // [16][s] rows of scales of 16 n
   int32_t per_group;   // blocks of a group (1 for short ones)
-  int32_t x_vec;       // rows of x may be read 16 bytes at a time
+  // tiled kernel
+  char* rows;          // x in blocks of a tile's rows and 128 k, with their sums (base_tiled.hip)
+  int32_t y_vec;       // rows of y may be written 16 bytes at a time
+  int32_t splits, split_blocks;  // ranges of K, and their blocks
+  float* parts;        // their sums, where there are several
 };
 
 struct BasePackArgs {
@@ -41,8 +47,15 @@ struct BasePackArgs {
   int32_t N, K, groups, blocks, scale_rows, s, e2m1, scale_bytes;
 };
 
+// Rows and columns of a workgroup of the tiled kernel.
+constexpr int TILE_T = 64;
+constexpr int TILE_N = 256;
+
+hipError_t launch_base_tiled(const BaseArgs& A, int format, int s, hipStream_t stream);
 hipError_t launch_base_pack(const BasePackArgs& A, hipStream_t stream);
-hipError_t launch_base_direct_bf16(const BaseArgs& A, int format, int s, hipStream_t stream);
+hipError_t launch_base_direct_i4(const BaseArgs& A, int s, hipStream_t stream);
+hipError_t launch_base_direct_i4z(const BaseArgs& A, int s, hipStream_t stream);
+hipError_t launch_base_direct_e2m1(const BaseArgs& A, hipStream_t stream);
 hipError_t launch_base_direct_f32(const BaseArgs& A, int format, int s, hipStream_t stream);
 
 // Eight I4 codes as bf16.
@@ -73,59 +86,71 @@ __device__ __forceinline__ u32x4_t base_less(u32x4_t c, float zero) {
   return r;
 }
 
-// The scales of one row of 16 n, or E2M1's as what the conversion takes.
+// The scales of one row of 16 n, kept as they were loaded (what converts them waits for them); E2M1's as what the
+// conversion takes.
 template <bool E2M1, bool F32, int S>
 struct BaseScale {
-  float f[S];
+  static constexpr int BITS = E2M1 ? 8 : F32 ? 32 : 16, WORDS = (S * BITS + 31) / 32;
+  uint32_t w[WORDS];
   static __device__ __forceinline__ BaseScale load(const void* p, int64_t row, int n) {
     BaseScale r;
-    const int64_t at = (row * BASE_N + n) * S;
-    if constexpr (E2M1) {
-      static_assert(S == 4, "groups of 32");
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(p) + at);
-#pragma unroll
-      for (int i = 0; i < S; ++i) r.f[i] = __uint_as_float((w >> (8 * i) & 255u) << 23);
-    } else if constexpr (F32) {
-#pragma unroll
-      for (int i = 0; i < S; ++i) r.f[i] = static_cast<const float*>(p)[at + i];
+    const char* q = static_cast<const char*>(p) + (row * BASE_N + n) * (S * BITS / 8);
+    if constexpr (S * BITS == 16) {
+      r.w[0] = *reinterpret_cast<const uint16_t*>(q);
+    } else if constexpr (WORDS == 2) {
+      const u32x2_t v = *reinterpret_cast<const u32x2_t*>(q);
+      r.w[0] = v.x;
+      r.w[1] = v.y;
     } else {
-      const uint16_t* q = static_cast<const uint16_t*>(p) + at;
-      if constexpr (S == 1) {
-        r.f[0] = bf16_bits_to_f32(*q);
-      } else {
 #pragma unroll
-        for (int i = 0; i < S / 2; ++i) {
-          const uint32_t w = reinterpret_cast<const uint32_t*>(q)[i];
-          r.f[2 * i] = __uint_as_float(w << 16);
-          r.f[2 * i + 1] = __uint_as_float(w & 0xffff0000u);
-        }
-      }
+      for (int i = 0; i < WORDS; ++i) r.w[i] = reinterpret_cast<const uint32_t*>(q)[i];
     }
     return r;
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (E2M1) return __uint_as_float((w[0] >> (8 * i) & 255u) << 23);
+    else if constexpr (F32) return __uint_as_float(w[i]);
+    else return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
 };
 
 // Zero points of one row of 16 n (8 where there are none).
 template <bool ZERO, int S>
 struct BaseZero {
-  float f[S];
+  uint32_t w;
   static __device__ __forceinline__ BaseZero load(const uint8_t* p, int64_t row, int n) {
-    BaseZero r;
-    if constexpr (!ZERO) {
-#pragma unroll
-      for (int i = 0; i < S; ++i) r.f[i] = 8.f;
-    } else {
+    BaseZero r{0u};
+    if constexpr (ZERO) {
       const uint8_t* q = p + (row * BASE_N + n) * S;
-      uint32_t w;
-      if constexpr (S == 4) w = *reinterpret_cast<const uint32_t*>(q);
-      else if constexpr (S == 2) w = *reinterpret_cast<const uint16_t*>(q);
-      else w = *q;
-#pragma unroll
-      for (int i = 0; i < S; ++i) r.f[i] = (float)(w >> (8 * i) & 255u);
+      if constexpr (S == 4) r.w = *reinterpret_cast<const uint32_t*>(q);
+      else if constexpr (S == 2) r.w = *reinterpret_cast<const uint16_t*>(q);
+      else r.w = *q;
     }
     return r;
   }
+  __device__ __forceinline__ float get(int i) const { return ZERO ? (float)(w >> (8 * i) & 255u) : 8.f; }
 };
+
+// 16 bytes of a row, wherever it starts.
+template <bool F32>
+__device__ __forceinline__ u32x4_t load_row(const char* p) {
+  typedef u32x4_t by_4_t __attribute__((aligned(4)));
+  typedef u32x4_t by_2_t __attribute__((aligned(2)));
+  return *reinterpret_cast<const std::conditional_t<F32, by_4_t, by_2_t>*>(p);
+}
+
+// The same, of a piece that ends n values on, zeros behind them.
+template <bool F32>
+__device__ __forceinline__ u32x4_t load_rest(const char* p, int n) {
+  u32x4_t v = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int i = 0; i < (F32 ? 4 : 8); ++i)
+    if (i < n) {
+      if constexpr (F32) v[i] = reinterpret_cast<const uint32_t*>(p)[i];
+      else v[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+    }
+  return v;
+}
 
 // fp32 values as three bf16 each that add up to them: their leading 8 bits, the next 8, the last (numbers below
 // 2^-110 lose bits that bf16 does not hold).

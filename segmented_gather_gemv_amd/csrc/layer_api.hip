@@ -57,6 +57,33 @@ sgmv_status base_ok(const sgmv_base* b) {
   return SGMV_OK;
 }
 
+// How a product is computed.
+struct BasePlan {
+  bool tiled;
+  int32_t splits, split_blocks;
+  size_t rows, parts;  // floats of workspace
+};
+
+// The tiled kernel from 1e10 products on: it converts each code for 64 rows, not 16 or 32, and has its rows prepared in a
+// launch of its own (128 rows, 8192 x 8192, I4: 36 us in 4 ranges, direct 35; 256: 52 and 67; 512: 89 and 130; 128
+// over 4096 x 4096: 25 and 11). Its tiles fill the card from 256 on; of fewer, K is split into up to 8 ranges of 8
+// blocks and more (256 rows: 81 us in 1, 56 in 2, 52 in 4, 64 in 8; 1024 over 4096 x 4096, 256 tiles: 49 us in 1, 54 in 2).
+BasePlan base_plan(int32_t T, const sgmv_base& b, int32_t n_split) {
+  const BaseShape h = base_shape(b);
+  BasePlan p{};
+  p.splits = 1;
+  if (b.dtype != SGMV_BF16 || (!n_split && (T <= 32 || (double)T * b.N * b.K < 1e10))) return p;
+  p.tiled = true;
+  const int64_t bands = ceil_div(T, TILE_T), tiles = bands * ceil_div(b.N, TILE_N);
+  if (n_split) p.splits = n_split;
+  else if (tiles < 256) p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, 8, h.blocks / 8}));
+  p.split_blocks = (int32_t)ceil_div(h.blocks, p.splits);
+  p.splits = (int32_t)ceil_div(h.blocks, p.split_blocks);
+  p.rows = (size_t)bands * TILE_T * h.blocks * (BASE_K / 2 + (b.format == SGMV_BASE_I4 ? h.s : 0));
+  if (p.splits > 1) p.parts = (size_t)p.splits * tiles * TILE_T * TILE_N;
+  return p;
+}
+
 inline int scale_size(int format, int dtype) { return format == SGMV_BASE_E2M1 ? 1 : dtype == SGMV_F32 ? 4 : 2; }
 
 }  // namespace
@@ -123,32 +150,46 @@ sgmv_status sgmv_base_pack(const uint8_t* codes, int64_t ldc, const void* scale,
   return launched(launch_base_pack(A, static_cast<hipStream_t>(stream)));
 }
 
-sgmv_status sgmv_base_product_workspace(int32_t T, const sgmv_base* b, size_t* bytes) {
-  if (!bytes || T < 0) return SGMV_EINVAL;
+sgmv_status sgmv_base_product_workspace(int32_t T, const sgmv_base* b, int32_t n_split, size_t* bytes) {
+  if (!bytes || T < 0 || n_split < 0 || n_split > SGMV_BASE_MAX_SPLITS) return SGMV_EINVAL;
   const sgmv_status st = base_ok(b);
   if (st != SGMV_OK) return st;
-  *bytes = 0;
+  if (n_split && b->dtype == SGMV_F32) return SGMV_EUNSUPPORTED;
+  const BasePlan p = base_plan(T, *b, n_split);
+  *bytes = (p.rows + p.parts) * sizeof(float);
   return SGMV_OK;
 }
 
 sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, const sgmv_base* b, void* y, int64_t ldy,
-                              void* workspace, size_t workspace_bytes, void* stream) {
+                              int32_t n_split, void* workspace, size_t workspace_bytes, void* stream) {
   size_t need = 0;
-  const sgmv_status st = sgmv_base_product_workspace(T, b, &need);
+  const sgmv_status st = sgmv_base_product_workspace(T, b, n_split, &need);
   if (st != SGMV_OK) return st;
   if (T == 0) return SGMV_OK;
-  if (!x || !y || ldx < b->K || ldy < b->N) return SGMV_EINVAL;
+  if (!x || !y || (T > 1 && (ldx < b->K || ldy < b->N))) return SGMV_EINVAL;
   if (need) {
     if (!workspace || !aligned_to(workspace, 16)) return SGMV_EINVAL;
     if (workspace_bytes < need) return SGMV_ECAPACITY;
   }
   const BaseShape h = base_shape(*b);
-  const int f32 = b->dtype == SGMV_F32, e = f32 ? 4 : 2;
+  const BasePlan p = base_plan(T, *b, n_split);
+  const int f32 = b->dtype == SGMV_F32;
   const BaseArgs A{b->codes, b->scale, b->zero, x, y, ldx, ldy, T, b->N, b->K, (int32_t)h.blocks, (int32_t)h.scale_rows,
-                   (int32_t)h.per_group, aligned_to(x, 16) && (T == 1 || ldx * e % 16 == 0)};
-  if (ceil_div(T, 16) * h.tiles * 8 > MOST_WAVES) return SGMV_EUNSUPPORTED;
+                   (int32_t)h.per_group, static_cast<char*>(workspace), aligned_to(y, 16) && (T == 1 || ldy % 8 == 0), p.splits, p.split_blocks,
+                   static_cast<float*>(workspace) + p.rows};
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return launched(f32 ? launch_base_direct_f32(A, b->format, (int)h.s, s) : launch_base_direct_bf16(A, b->format, (int)h.s, s));
+  if (p.tiled) {
+    const int64_t bands = ceil_div(T, TILE_T);
+    if ((bands * ceil_div(b->N, TILE_N) + 8) * 4 * std::max(p.splits, TILE_T / 16) > MOST_WAVES ||
+        bands * h.blocks * (TILE_T / 4) > MOST_WAVES)
+      return SGMV_EUNSUPPORTED;
+    return launched(launch_base_tiled(A, b->format, (int)h.s, s));
+  }
+  if (ceil_div(T, 16) * h.tiles * 16 > MOST_WAVES) return SGMV_EUNSUPPORTED;
+  return launched(f32                           ? launch_base_direct_f32(A, b->format, (int)h.s, s)
+                  : b->format == SGMV_BASE_E2M1 ? launch_base_direct_e2m1(A, s)
+                  : b->zero                     ? launch_base_direct_i4z(A, (int)h.s, s)
+                                                : launch_base_direct_i4(A, (int)h.s, s));
 }
 
 }  // extern "C"

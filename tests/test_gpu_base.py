@@ -65,6 +65,8 @@ def test_product_against_oracle(sg, N, K, fmt, group, zero, dtype):
     for T in (1, 2, 16, 17, 40):
         x = torch.randn(T, K, generator=g).to(dtype)
         w.check(sg.sgmv_base_product(x.to(DEV), w.packed), x)
+        for n in (1, 3) if dtype == BF16 and T in (1, 40) else ():  # in tiles, K in ranges
+            w.check(sg.sgmv_base_product(x.to(DEV), w.packed, n_split=n), x)
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
@@ -74,6 +76,50 @@ def test_product_of_many_rows(sg, T, fmt, group, zero, dtype):
     N, K = (331, 700) if T % 2 else (384, 640)
     w = Weight(sg, N, K, fmt, dtype, group, zero)
     x = torch.randn(T, K, generator=torch.Generator().manual_seed(T)).to(dtype)
+    for n in (0, 1, 2, 16) if dtype == BF16 else (0,):
+        w.check(sg.sgmv_base_product(x.to(DEV), w.packed, n_split=n), x)
+
+
+@pytest.mark.parametrize("T,N,K,fmt,group,zero", [(200, 5000, 10050, "e2m1", 32, False), (260, 8200, 4700, "i4", 128, True),
+                                                  (2100, 2048, 2400, "i4", 64, False)])
+def test_product_as_the_library_chooses(sg, T, N, K, fmt, group, zero):
+    """Sizes that go to the tiles by themselves, with and without ranges."""
+    w = Weight(sg, N, K, fmt, BF16, group, zero)
+    assert sg.sgmv_base_product_workspace(T, w.packed) > 0
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(T)).to(BF16)
+    y = sg.sgmv_base_product(x.to(DEV), w.packed)
+    w.check(y, x)
+    need = sg.sgmv_base_product_workspace(T, w.packed)
+    space = torch.full((need + 64,), 7, dtype=torch.uint8, device=DEV)
+    assert torch.equal(sg.sgmv_base_product(x.to(DEV), w.packed, workspace=space[:need]), y)
+    assert (space[need:] == 7).all()
+
+
+@pytest.mark.parametrize("N", [256, 272, 500])
+@pytest.mark.parametrize("T", [64, 67, 700])
+def test_every_launch_shape_gives_the_same_sums(sg, T, N):
+    """Whole numbers, so that sums are exact and every kernel's results are equal."""
+    K = 900
+    g = torch.Generator().manual_seed(N + T)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, dtype=torch.uint8)
+    for zero in (None, torch.randint(0, 16, (N, 15), generator=g, dtype=torch.uint8)):
+        w = sg.sgmv_base_pack(codes.to(DEV), torch.ones(N, 15).to(BF16).to(DEV), None if zero is None else zero.to(DEV),
+                              K=K, group=64)
+        x = torch.randint(-3, 4, (T, K), generator=g).to(BF16).to(DEV)
+        want = sg.sgmv_base_product(x, w)
+        for n in (1, 2, 5, 8):
+            assert torch.equal(sg.sgmv_base_product(x, w, n_split=n), want)
+        for rows in (1, 4, 5, 16, 17, 32, 33):  # other instances of the kernel of few rows
+            assert torch.equal(sg.sgmv_base_product(x[:rows], w), want[:rows])
+
+
+@pytest.mark.parametrize("N,T", [(4096, 16), (8192, 3), (8208, 5), (16384, 9), (16400, 16), (8192, 40), (16384, 33)])
+def test_wide_weights_of_few_rows(sg, N, T):
+    """The instances that take several tiles of columns and rows."""
+    w = Weight(sg, N, 200, "i4", BF16, 128, True)
+    x = torch.randn(T, 200, generator=torch.Generator().manual_seed(T)).to(BF16)
+    w.check(sg.sgmv_base_product(x.to(DEV), w.packed), x)
+    w = Weight(sg, N, 200, "e2m1", BF16, 32, False)
     w.check(sg.sgmv_base_product(x.to(DEV), w.packed), x)
 
 
@@ -90,6 +136,11 @@ def test_product_of_strided_unaligned_rows(sg, T, dtype):
         w.check(y[:, 9:79], x)
         assert (y[:, :9] == 7).all() and (y[:, 79:] == 7).all()
         assert torch.equal(sg.sgmv_base_product(xd, w.packed), y[:, 9:79])
+        if dtype == BF16:
+            y.fill_(7.0)
+            sg.sgmv_base_product(xd, w.packed, y=y[:, 9:79], n_split=2)
+            w.check(y[:, 9:79], x)
+            assert (y[:, :9] == 7).all() and (y[:, 79:] == 7).all()
 
 
 @pytest.mark.parametrize("fmt,zero", [("i4", True), ("e2m1", False)])
@@ -97,14 +148,16 @@ def test_product_of_strided_unaligned_rows(sg, T, dtype):
 @pytest.mark.parametrize("T", [6, 90, 200])
 def test_rows_that_are_not_finite_spoil_their_own_results_only(sg, fmt, zero, dtype, T):
     w = Weight(sg, 48, 384, fmt, dtype, 32, zero)
-    x = torch.randn(T, 384, generator=torch.Generator().manual_seed(2)).to(dtype)
-    clean = sg.sgmv_base_product(x.to(DEV), w.packed)
+    clean = torch.randn(T, 384, generator=torch.Generator().manual_seed(2)).to(dtype)
+    x = clean.clone()
     x[1, 7], x[3, 383], x[T - 2, 200] = float("nan"), float("inf"), float("-inf")
-    y = sg.sgmv_base_product(x.to(DEV), w.packed)
     bad = [1, 3, T - 2]
     good = [t for t in range(T) if t not in bad]
-    assert torch.equal(y[good], clean[good])
-    assert torch.isnan(y[1]).all() and not torch.isfinite(y[3]).any() and not torch.isfinite(y[T - 2]).any()
+    for n in (0, 2) if dtype == BF16 else (0,):
+        want = sg.sgmv_base_product(clean.to(DEV), w.packed, n_split=n)
+        y = sg.sgmv_base_product(x.to(DEV), w.packed, n_split=n)
+        assert torch.equal(y[good], want[good])
+        assert torch.isnan(y[1]).all() and not torch.isfinite(y[3]).any() and not torch.isfinite(y[T - 2]).any()
 
 
 @pytest.mark.parametrize("T", [1, 30, 200])
@@ -164,21 +217,21 @@ def test_no_rows_and_captured_calls(sg):
     w = Weight(sg, 256, 512, "i4", BF16, 128, True)
     assert sg.sgmv_base_product(torch.empty(0, 512, dtype=BF16, device=DEV), w.packed).shape == (0, 256)
     g = torch.Generator().manual_seed(5)
-    for T in (3, 150):
+    for T, n in ((3, 0), (150, 0), (150, 3)):
         x = torch.randn(T, 512, generator=g).to(BF16).to(DEV)
         side = torch.cuda.Stream()
         torch.cuda.synchronize()
         with torch.cuda.stream(side):
-            first = sg.sgmv_base_product(x, w.packed)
+            first = sg.sgmv_base_product(x, w.packed, n_split=n)
         side.synchronize()
         w.check(first, x)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
-            y = sg.sgmv_base_product(x, w.packed)
+            y = sg.sgmv_base_product(x, w.packed, n_split=n)
         for _ in range(3):
             x.copy_(torch.randn(T, 512, generator=g))
             graph.replay()
-            want = sg.sgmv_base_product(x, w.packed)
+            want = sg.sgmv_base_product(x, w.packed, n_split=n)
             torch.cuda.synchronize()
             assert torch.equal(y, want)
             w.check(y, x)

@@ -57,7 +57,7 @@ def test_rotate_by_hand_and_as_complex_numbers():
 def test_constants_match_the_header():
     text = open(os.path.join(os.path.dirname(os.path.dirname(sg.__file__)), "include", "sgmv.h")).read()
     defs = dict(re.findall(r"#define SGMV_([A-Z_0-9]+) (\d+)", text))
-    for name in ("MAX_NORM_WIDTH", "BASE_MAX_SIZE"):
+    for name in ("MAX_NORM_WIDTH", "BASE_MAX_SIZE", "BASE_MAX_SPLITS"):
         assert int(defs[name]) == getattr(sg, name)
     for name in ("BASE_I4", "BASE_E2M1"):
         assert re.search(r"SGMV_%s = %d\b" % (name, getattr(sg, name)), text)
@@ -110,8 +110,8 @@ def test_base_calls_refuse():
     def pack(b=None, codes=0x1000, ldc=150, scale=0x2000, zero=0x3000):
         return lib.sgmv_base_pack(codes, ldc, scale, zero, ctypes.byref(b or _base()), None)
 
-    def product(b=None, x=0x1000, ldx=300, T=3, y=0x9000, ldy=40, ws=None, size=0):
-        return lib.sgmv_base_product(x, ldx, T, ctypes.byref(b or _base()), y, ldy, ws, size, None)
+    def product(b=None, x=0x1000, ldx=300, T=3, y=0x9000, ldy=40, n_split=0, ws=None, size=0):
+        return lib.sgmv_base_product(x, ldx, T, ctypes.byref(b or _base()), y, ldy, n_split, ws, size, None)
 
     for kw in (dict(codes=None), dict(ldc=149), dict(scale=None), dict(zero=None), dict(b=_base(has_zero=0, zero=0))):
         assert pack(**kw) == E, kw
@@ -121,21 +121,43 @@ def test_base_calls_refuse():
     for kw, status in bad:
         b = _base(**kw)
         assert pack(b) == status and product(b) == status, kw
-        assert lib.sgmv_base_product_workspace(3, ctypes.byref(b), ctypes.byref(need)) == status
+        assert lib.sgmv_base_product_workspace(3, ctypes.byref(b), 0, ctypes.byref(need)) == status
     assert lib.sgmv_base_pack(0x1000, 150, 0x2000, 0x3000, None, None) == E
-    assert lib.sgmv_base_product(0x1000, 300, 3, None, 0x9000, 40, None, 0, None) == E
-    assert lib.sgmv_base_product_workspace(3, None, ctypes.byref(need)) == E
-    assert lib.sgmv_base_product_workspace(3, ctypes.byref(_base()), None) == E
-    for kw in (dict(x=None), dict(y=None), dict(ldx=299), dict(ldy=39), dict(T=-1)):
+    assert lib.sgmv_base_product(0x1000, 300, 3, None, 0x9000, 40, 0, None, 0, None) == E
+    assert lib.sgmv_base_product_workspace(3, None, 0, ctypes.byref(need)) == E
+    assert lib.sgmv_base_product_workspace(3, ctypes.byref(_base()), 0, None) == E
+    for kw in (dict(x=None), dict(y=None), dict(ldx=299), dict(ldy=39), dict(T=-1), dict(n_split=-1), dict(n_split=17)):
         assert product(**kw) == E, kw
+    assert product(b=_base(dtype=sg.SGMV_F32), n_split=1) == UNS
     assert product(T=0, x=None, y=None) == OK
-    assert lib.sgmv_base_product_workspace(0, ctypes.byref(_base()), ctypes.byref(need)) == OK and need.value == 0
+    assert lib.sgmv_base_product_workspace(0, ctypes.byref(_base()), 0, ctypes.byref(need)) == OK and need.value == 0
+
+
+def test_base_workspace():
+    """Rows in blocks of 64 x 128 (16 KB, for I4 with the sums of their groups behind them), and the ranges' sums."""
+    lib, need = sg.library(), ctypes.c_size_t()
+
+    def size(T, n_split=0, **kw):
+        assert lib.sgmv_base_product_workspace(T, ctypes.byref(_base(**kw)), n_split, ctypes.byref(need)) == OK
+        return need.value
+
+    assert size(64) == 0 and size(64, 1) == 3 * (16384 + 64 * 2 * 4)
+    assert size(65, 3) == 2 * 3 * (16384 + 64 * 2 * 4) + 3 * 2 * 64 * 256 * 4
+    assert size(65, 2, N=257) == 2 * 3 * (16384 + 64 * 2 * 4) + 2 * 2 * 2 * 64 * 256 * 4
+    assert size(65, 16) == size(65, 3)  # three blocks of K
+    assert size(64, 1, format=sg.BASE_E2M1, group=32, has_zero=0, zero=0) == 3 * 16384
+    big = dict(N=8192, K=8192, group=128)
+    assert size(32, **big) == 0 and size(128, **big) == 0 and size(1024, **big) == 16 * 64 * (16384 + 64 * 4)
+    assert size(256, **big) == 4 * 64 * (16384 + 64 * 4) + 4 * 128 * 64 * 256 * 4
+    call = lambda ws, n: lib.sgmv_base_product(0x1000, 300, 65, ctypes.byref(_base()), 0x9000, 40, 3, ws, n, None)
+    n = size(65, 3)
+    assert call(None, n) == E and call(0x10008, n) == E and call(0x10000, n - 1) == sg.SGMV_ECAPACITY
 
 
 def test_launches_past_the_limit_are_refused():
     b = _base(N=4194304, K=4194304, group=128)
-    assert sg.library().sgmv_base_product(0x1000, 1 << 23, 2 ** 31 - 1, ctypes.byref(b), 0x9000, 1 << 23, 0x10, 1 << 62,
-                                          None) == UNS
+    assert sg.library().sgmv_base_product(0x1000, 1 << 23, 2 ** 31 - 1, ctypes.byref(b), 0x9000, 1 << 23, 0, 0x10,
+                                          1 << 62, None) == UNS
 
 
 def _norm(**kw):
@@ -248,6 +270,8 @@ def test_base_binding_refuses():
             sg.sgmv_base_product(base=w, **kw)
     with pytest.raises(TypeError):
         sg.sgmv_base_product(x.bfloat16(), w)
+    with pytest.raises(ValueError):
+        sg.sgmv_base_product(x, w, n_split=2 ** 40)
     with pytest.raises(ValueError, match="GPU"):
         sg.sgmv_base_product(x, w)
 
