@@ -15,7 +15,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from . import SGMV_OK, _check, _dtype_code, _lib, _raw_stream
+from . import SGMV_OK, _check, _dtype_code, _lib
 from ._serving import KV_E4M3, KV_I8, KvBatch, KvCache, _MOST, _dense3, _int32, _KvBatch, _KvCache, _on_gpu, _rows3
 
 MAX_NORM_WIDTH = 32768
@@ -62,16 +62,15 @@ def _bind():
 _bind()
 
 
-def _launch(where: str, index: int, call, *args):
-    """The call on the current stream of GPU `index`, which is made the current one if it is not (the default
-    stream's handle is that of the current GPU)."""
-    if index == torch._C._cuda_getDevice():
-        st = call(*args, _raw_stream(index))
-    else:
-        with torch.cuda.device(index):
-            st = call(*args, _raw_stream(index))
-    if st != SGMV_OK:
-        _check(st, where)
+_current = torch._C._cuda_getDevice  # (the calls behind torch.cuda's, which take longer than they)
+_stream = torch._C._cuda_getCurrentRawStream
+_ROWS = {torch.float32: _dtype_code(torch.float32), torch.bfloat16: _dtype_code(torch.bfloat16)}
+
+
+def _elsewhere(index: int, call, *args) -> int:
+    """The call with GPU `index` made the current one (the default stream's handle is that of the current GPU)."""
+    with torch.cuda.device(index):
+        return call(*args, _stream(index))
 
 
 # ---------------------------------------------------------------------------------------
@@ -84,19 +83,26 @@ class Normed(NamedTuple):
     scale: Optional[torch.Tensor]     # float32, of each row
 
 
-def _strides(t: torch.Tensor, shape, index: int, what: str):
-    """Token and head strides of rows [T, width] or [T, heads, width]."""
+def _refuse(t: torch.Tensor, shape, dtype: torch.dtype, index: int, what: str):
     if t.shape != shape:
         raise ValueError(f"{what} must be {list(shape)}, got {list(t.shape)}")
-    st = t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"{what} must be contiguous over the last dimension")
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if t.get_device() != index:
         raise ValueError(f"{what} must be on x's device")
-    T, W, heads = shape[0], shape[-1], shape[1] if len(shape) == 3 else 1
-    head = st[1] if heads > 1 else W
-    # a stride of a single token says nothing
-    return (st[0] if T > 1 else heads * head), head
+    raise ValueError(f"{what} must be contiguous over the last dimension")
+
+
+def _strides(t: torch.Tensor, shape, dtype: torch.dtype, index: int, what: str):
+    """Token and head strides of rows [T, width] or [T, heads, width]."""
+    st = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index or (st[-1] != 1 and shape[-1] > 1):
+        _refuse(t, shape, dtype, index, what)
+    # a stride of a single token or head says nothing
+    if len(st) == 2:
+        return (st[0] if shape[0] > 1 else shape[1]), shape[1]
+    head = st[1] if shape[1] > 1 else shape[2]
+    return (st[0] if shape[0] > 1 else shape[1] * head), head
 
 
 def sgmv_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
@@ -110,64 +116,69 @@ def sgmv_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     for those alone. Outputs are allocated unless given; ``out`` and ``residual_out`` may be x or residual
     themselves."""
     shape, dtype, index = x.shape, x.dtype, x.get_device()
-    if len(shape) not in (2, 3):
+    if len(shape) == 2:
+        T, W = shape
+        heads = 1
+    elif len(shape) == 3:
+        T, heads, W = shape
+    else:
         raise ValueError(f"x must be [T, width] or [T, heads, width], got {list(shape)}")
-    code = _dtype_code(dtype)
-    W, heads = shape[-1], shape[1] if len(shape) == 3 else 1
-    _int32("T, heads and width", *shape)
-    if weight.shape != (W,) or weight.dtype != dtype or weight.get_device() != index or (W > 1 and weight.stride(0) != 1):
+    code = _ROWS.get(dtype)
+    if code is None:
+        _dtype_code(dtype)  # says which
+    if T > _MOST or heads > _MOST or W > _MOST:
+        _int32("T, heads and width", T, heads, W)
+    if weight.numel() != W or weight.dtype is not dtype or weight.get_device() != index or weight.dim() != 1 or (
+            not weight.is_contiguous()):
         raise TypeError(f"weight must be {W} contiguous {dtype} entries on x's device")
-    a = _Norm(x=x.data_ptr(), weight=weight.data_ptr(), T=shape[0], heads=heads, width=W, dtype=code, eps=eps)
-    a.ldx_token, a.ldx_head = _strides(x, shape, index, "x")
-    dense = (heads * W, W)
+    xt, xh = _strides(x, shape, dtype, index, "x")
+    rp = sp = op = cp = fp = None
+    dense = heads * W
+    rt = st = ot = ct = dense
+    rh = sh = oh = ch = W
+    fmt = 0
     if residual is not None:
-        if residual.dtype != dtype:
-            raise TypeError("residual must have x's dtype")
-        a.ldr_token, a.ldr_head = _strides(residual, shape, index, "residual")
-        a.residual = residual.data_ptr()
-        a.lds_token, a.lds_head = dense
+        rt, rh = _strides(residual, shape, dtype, index, "residual")
+        rp = residual.data_ptr()
         if residual_out is None:
-            residual_out = torch.empty(shape, dtype=dtype, device=x.device)
+            residual_out = x.new_empty(shape)
         else:
-            if residual_out.dtype != dtype:
-                raise TypeError("residual_out must have x's dtype")
-            a.lds_token, a.lds_head = _strides(residual_out, shape, index, "residual_out")
-        a.residual_out = residual_out.data_ptr()
+            st, sh = _strides(residual_out, shape, dtype, index, "residual_out")
+        sp = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out goes with a residual")
     if out is not None:
-        if out.dtype != dtype:
-            raise TypeError("out must have x's dtype")
-        a.ldo_token, a.ldo_head = _strides(out, shape, index, "out")
-        a.out = out.data_ptr()
+        ot, oh = _strides(out, shape, dtype, index, "out")
+        op = out.data_ptr()
     elif want_out:
-        out = torch.empty(shape, dtype=dtype, device=x.device)
-        a.ldo_token, a.ldo_head = dense
-        a.out = out.data_ptr()
+        out = x.new_empty(shape)
+        op = out.data_ptr()
     if quantise is not None:
-        if quantise not in _CODES:
+        fmt = _CODES.get(quantise)
+        if fmt is None:
             raise TypeError(f"codes are float8_e4m3fn or int8, got {quantise}")
-        a.format = _CODES[quantise]
-        a.ldc_token, a.ldc_head = dense
         if codes is None:
-            codes = torch.empty(shape, dtype=quantise, device=x.device)
+            codes = x.new_empty(shape, dtype=quantise)
         else:
-            if codes.dtype != quantise:
-                raise TypeError(f"codes must be {quantise}")
-            a.ldc_token, a.ldc_head = _strides(codes, shape, index, "codes")
+            ct, ch = _strides(codes, shape, quantise, index, "codes")
         if scale is None:
-            scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+            scale = x.new_empty(shape[:-1], dtype=torch.float32)
         elif scale.shape != shape[:-1] or scale.dtype != torch.float32 or not scale.is_contiguous() or (
                 scale.get_device() != index):
             raise TypeError("scale must be a contiguous float32 tensor of one entry per row on x's device")
-        a.codes, a.scale = codes.data_ptr(), scale.data_ptr()
+        cp, fp = codes.data_ptr(), scale.data_ptr()
     elif codes is not None or scale is not None:
         raise ValueError("codes and scale go with quantise")
     elif out is None:
         raise ValueError("nothing to compute: neither out nor codes are wanted")
     if index < 0:
         raise ValueError("the kernels run on GPU tensors")
-    _launch("sgmv_rms_norm", index, _lib.sgmv_rms_norm, ctypes.byref(a))
+    a = _Norm(x.data_ptr(), rp, weight.data_ptr(), sp, op, cp, fp, xt, xh, rt, rh, st, sh, ot, oh, ct, ch, T, heads, W,
+              code, fmt, eps)
+    call, ref = _lib.sgmv_rms_norm, ctypes.byref(a)
+    status = call(ref, _stream(index)) if index == _current() else _elsewhere(index, call, ref)
+    if status != SGMV_OK:
+        _check(status, "sgmv_rms_norm")
     return Normed(out, residual_out, codes, scale)
 
 
@@ -226,9 +237,8 @@ def sgmv_base_pack(codes: torch.Tensor, scale: torch.Tensor, zero: Optional[torc
     desc.codes, desc.scale = parts[0].data_ptr(), parts[1].data_ptr()
     desc.zero = parts[2].data_ptr() if parts[2] is not None else None
     base = BaseWeight(parts[0], parts[1] if format == BASE_E2M1 else parts[1].view(dtype), parts[2], desc, dtype)
-    _launch("sgmv_base_pack", index, _lib.sgmv_base_pack, codes.data_ptr(),
-            codes.stride(0) if N > 1 else codes.shape[1], scale.data_ptr(),
-            None if zero is None else zero.data_ptr(), base.ref)
+    _check(_elsewhere(index, _lib.sgmv_base_pack, codes.data_ptr(), codes.stride(0) if N > 1 else codes.shape[1],
+                      scale.data_ptr(), None if zero is None else zero.data_ptr(), base.ref), "sgmv_base_pack")
     return base
 
 
@@ -240,12 +250,12 @@ def sgmv_base_product(x: torch.Tensor, base: BaseWeight, y: Optional[torch.Tenso
     T, N, K, dtype, index = x.shape[0], base.N, base.K, base.dtype, base.index
     if x.dim() != 2 or x.shape[1] != K or (K > 1 and x.stride(1) != 1):
         raise ValueError(f"x must be row-major [T, {K}], got {list(x.shape)}")
-    if x.dtype != dtype or x.get_device() != index:
+    if x.dtype is not dtype or x.get_device() != index:
         raise TypeError(f"x must be {dtype} on the weight's device")
     if T > _MOST or abs(n_split) > _MOST:
         _int32("T and n_split", T, n_split)
     if y is None:
-        y, ldy = torch.empty((T, N), dtype=dtype, device=x.device), N
+        y, ldy = x.new_empty((T, N)), N
     else:
         if tuple(y.shape) != (T, N) or y.dtype != dtype or y.get_device() != index or (N > 1 and y.stride(1) != 1):
             raise ValueError(f"y must be row-major [{T}, {N}] of {dtype} on the weight's device")
@@ -266,8 +276,11 @@ def sgmv_base_product(x: torch.Tensor, base: BaseWeight, y: Optional[torch.Tenso
     elif size:
         workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
         ptr = workspace.data_ptr()
-    _launch("sgmv_base_product", index, _lib.sgmv_base_product, x.data_ptr(), x.stride(0) if T > 1 else K, T,
-            base.ref, y.data_ptr(), ldy, n_split, ptr, size)
+    args = (x.data_ptr(), x.stride(0) if T > 1 else K, T, base.ref, y.data_ptr(), ldy, n_split, ptr, size)
+    call = _lib.sgmv_base_product
+    st = call(*args, _stream(index)) if index == _current() else _elsewhere(index, call, *args)
+    if st != SGMV_OK:
+        _check(st, "sgmv_base_product")
     return y
 
 
@@ -291,35 +304,43 @@ def sgmv_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
     ``q_out`` if given (q itself: in place). ``cos_sin`` float32 [positions, rotary]: rotary / 2 cosines and then as
     many sines of each position's angles; the first ``rotary`` values of a row are turned, in pairs (i,
     i + rotary / 2) or, ``interleaved``, (2 i, 2 i + 1)."""
-    kt, kh = _rows3(k, batch.T, cache.heads, cache, "k")
-    vt, vh = _rows3(v, batch.T, cache.heads, cache, "v")
-    dtype = k.dtype
-    if v.dtype != dtype:
+    T, index, dtype = batch.T, cache.index, k.dtype
+    kt, kh = _rows3(k, T, cache.heads, cache, "k")
+    vt, vh = _rows3(v, T, cache.heads, cache, "v")
+    if v.dtype is not dtype:
         raise TypeError("k and v must share a dtype")
-    code = _dtype_code(dtype)
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.stride(1) != 1 or (
-            cos_sin.get_device() != cache.index):
+    code = _ROWS.get(dtype)
+    if code is None:
+        _dtype_code(dtype)  # says which
+    if cos_sin.dim() != 2 or cos_sin.dtype is not torch.float32 or cos_sin.get_device() != index or (
+            cos_sin.stride(1) != 1):
         raise TypeError("cos_sin must be row-major float32 [positions, rotary] on the cache's device")
     positions, rotary = cos_sin.shape
-    _int32("positions and rotary", positions, rotary)
-    r = _Rotation(cos_sin.data_ptr(), cos_sin.stride(0) if positions > 1 else rotary, positions, rotary,
-                  1 if interleaved else 0)
+    if positions > _MOST or rotary > _MOST:
+        _int32("positions and rotary", positions, rotary)
+    heads = qt = qh = ot = oh = 0
+    qp = op = None
     if q is not None:
-        r.ldq_token, r.ldq_head = _rows3(q, batch.T, None, cache, "q")
-        if q.dtype != dtype:
+        qt, qh = _rows3(q, T, None, cache, "q")
+        if q.dtype is not dtype:
             raise TypeError("q must have k's dtype")
-        r.heads, r.q = q.shape[1], q.data_ptr()
+        heads, qp = q.shape[1], q.data_ptr()
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
-            r.ldo_token, r.ldo_head = _dense3(r.heads, cache)
+            q_out = q.new_empty(q.shape)
+            ot, oh = _dense3(heads, cache)
         else:
-            r.ldo_token, r.ldo_head = _rows3(q_out, batch.T, r.heads, cache, "q_out")
-            if q_out.dtype != dtype:
+            ot, oh = _rows3(q_out, T, heads, cache, "q_out")
+            if q_out.dtype is not dtype:
                 raise TypeError("q_out must have q's dtype")
-        r.q_out = q_out.data_ptr()
+        op = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out goes with q")
     _on_gpu(batch, cache)
-    _launch("sgmv_kv_append", cache.index, _lib.sgmv_kv_append, ctypes.byref(r), k.data_ptr(), kt, kh, v.data_ptr(),
-            vt, vh, code, batch.ref, cache.ref)
+    r = _Rotation(cos_sin.data_ptr(), cos_sin.stride(0) if positions > 1 else rotary, positions, rotary,
+                  1 if interleaved else 0, heads, qp, op, qt, qh, ot, oh)
+    args = (ctypes.byref(r), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, code, batch.ref, cache.ref)
+    call = _lib.sgmv_kv_append
+    st = call(*args, _stream(index)) if index == _current() else _elsewhere(index, call, *args)
+    if st != SGMV_OK:
+        _check(st, "sgmv_kv_append")
     return q_out
