@@ -278,8 +278,12 @@ __device__ __forceinline__ float turn_high(float a, float b, float c, float s) {
   return b * c + a * s;
 }
 
+// What write_rows turns: nothing, pairs half a rotation apart, pairs of neighbours. (Kernels of their own for the last
+// two: the registers of the one would cost the other waves in flight, 56 us and not 52 in the interleaved form.)
+enum Turn { AS_IT_IS, HALVES, NEIGHBOURS };
+
 // Values d .. d + N - 1 (d a multiple of N, N of 4 and a divisor of 8) of a row at a position, turned.
-template <class T, int N>
+template <class T, int N, Turn TURN>
 __device__ __forceinline__ void turned(const KvTurn& R, const T* row, bool vec, int pos, int d, float* y) {
   constexpr int W = N * sizeof(T) / 4;
   uint32_t own[W];
@@ -296,7 +300,7 @@ __device__ __forceinline__ void turned(const KvTurn& R, const T* row, bool vec, 
   if (d >= R.rotary) {
 #pragma unroll
     for (int e = 0; e < N; ++e) y[e] = x[e];
-  } else if (R.interleaved) {
+  } else if constexpr (TURN == NEIGHBOURS) {
     float c[N / 2], s[N / 2];
     angles(R, pos, d / 2, c, s);
 #pragma unroll
@@ -318,10 +322,32 @@ __device__ __forceinline__ void turned(const KvTurn& R, const T* row, bool vec, 
   }
 }
 
+// A row's units (values 16 n quads of lanes apart, C each) whose pairs lie P units of one lane apart: turned where they
+// are, so that cosines, sines and values are loaded once.
+template <int P, int MOST, int C>
+__device__ __forceinline__ void turn_units(const KvTurn& R, int pos, int quad, uint32_t (&w)[MOST][C]) {
+  constexpr int N = C < 8 ? C : 8;
+  if constexpr (2 * P <= MOST) {
+#pragma unroll
+    for (int n = 0; n < P; ++n)
+#pragma unroll
+      for (int e = 0; e < C; e += N) {
+        float c[N], s[N];
+        angles(R, pos, (quad + 4 * n) * C + e, c, s);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          const float a = __uint_as_float(w[n][e + j]), b = __uint_as_float(w[n + P][e + j]);
+          w[n][e + j] = __float_as_uint(turn_low(a, b, c[j], s[j]));
+          w[n + P][e + j] = __float_as_uint(turn_high(a, b, c[j], s[j]));
+        }
+      }
+  }
+}
+
 // 16 rows of K (or, grouped, of V) per wave. TURN: of K, turned by their positions on the way.
-template <int FMT, class ROW, bool GROUPED, bool TURN>
+template <int FMT, class ROW, bool GROUPED, Turn TURN>
 __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, const KvTurn& R, bool is_v, const Place& place16) {
-  using T = std::conditional_t<TURN, float, ROW>;  // of the values in registers
+  using T = std::conditional_t<TURN != AS_IT_IS, float, ROW>;  // of the values in registers
   using U = Unit<FMT, T>;
   constexpr int BYTES = U::bytes, C = U::C;
   constexpr bool SCALED = KvFormat<FMT>::scaled;
@@ -332,6 +358,12 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, con
   const ROW* src = static_cast<const ROW*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) +
                    P.head * (is_v ? A.ldv_h : A.ldk_h);
   uint32_t w[U::most][U::words];
+  int apart = 0;  // units of a lane from one of a pair to the other, 0: they are not in one lane
+  if constexpr (TURN == HALVES) {
+    const int half = R.rotary / 2;
+    apart = half % (4 * C) == 0 ? half / (4 * C) : 0;
+    if (apart != 1 && apart != 2 && apart != 4) apart = 0;
+  }
 #pragma unroll
   for (int n = 0; n < U::most; ++n) {
     if (4 * n >= units) break;
@@ -339,15 +371,29 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, con
 #pragma unroll
     for (int i = 0; i < U::words; ++i) w[n][i] = 0u;
     if (!P.ok || u >= units) continue;
-    if constexpr (TURN) {
+    if constexpr (TURN != AS_IT_IS) {
+      if (apart) {
+        uint32_t raw[C * sizeof(ROW) / 4];
+        load_words(src + u * C, A.vec, raw);
+#pragma unroll
+        for (int e = 0; e < C; ++e) w[n][e] = __float_as_uint(word_value<ROW>(raw, e));
+        continue;
+      }
       constexpr int N = C < 8 ? C : 8;
       float x[C];
 #pragma unroll
-      for (int e = 0; e < C; e += N) turned<ROW, N>(R, src, A.vec, P.pos, u * C + e, x + e);
+      for (int e = 0; e < C; e += N) turned<ROW, N, TURN>(R, src, A.vec, P.pos, u * C + e, x + e);
 #pragma unroll
       for (int e = 0; e < C; ++e) w[n][e] = __float_as_uint(x[e]);
     } else {
       load_words(src + u * C, A.vec, w[n]);
+    }
+  }
+  if constexpr (TURN == HALVES) {
+    if (P.ok) {
+      if (apart == 1) turn_units<1>(R, P.pos, quad, w);
+      else if (apart == 2) turn_units<2>(R, P.pos, quad, w);
+      else if (apart == 4) turn_units<4>(R, P.pos, quad, w);
     }
   }
   const int64_t at = token_of(K, P), token = max(at, (int64_t)0);  // the page's load beside the row's
@@ -465,7 +511,7 @@ template <int FMT, class T>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_groups_kernel(KvArgs K, KvRows A) {
   Place P;
   if (group_place(K, K.q_start, K.T, blockIdx.x, blockIdx.y, blockIdx.z && KvFormat<FMT>::bytes == 1, P))
-    write_rows<FMT, T, true, false>(K, A, KvTurn{}, blockIdx.z, P);
+    write_rows<FMT, T, true, AS_IT_IS>(K, A, KvTurn{}, blockIdx.z, P);
 }
 
 // Workgroups [0, for_v) take V, the others K.
@@ -478,7 +524,7 @@ __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_rows_kernel(KvArgs K,
     write_v_row<FMT, T>(K, A, P);
   } else {
     row_place(K, K.q_start, K.T, (((int)blockIdx.x - for_v) * RW_WAVES + wv) * 16 + (lane & 15), P);
-    write_rows<FMT, T, false, false>(K, A, KvTurn{}, false, P);
+    write_rows<FMT, T, false, AS_IT_IS>(K, A, KvTurn{}, false, P);
   }
 }
 
@@ -588,7 +634,7 @@ __device__ __forceinline__ void turn_queries(const KvArgs& K, const KvTurn& R, i
 }
 
 // As the write kernels, with K turned; workgroups from `rest` on take the queries.
-template <int FMT, class T>
+template <int FMT, class T, Turn TURN>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_groups_kernel(KvArgs K, KvRows A, KvTurn R, int slots, int rest) {
   const int at = blockIdx.x;
   if (at >= rest) return turn_queries<T>(K, R, (at - rest) * RW_WAVES + threadIdx.x / WAVE);
@@ -596,11 +642,11 @@ __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_groups_kernel(KvArgs
   const int of = is_v ? at - rest / 2 : at, head = of / slots;
   Place P;
   if (!group_place(K, K.q_start, K.T, of - head * slots, head, is_v && KvFormat<FMT>::bytes == 1, P)) return;
-  if (is_v) write_rows<FMT, T, true, false>(K, A, R, true, P);
-  else write_rows<FMT, T, true, true>(K, A, R, false, P);
+  if (is_v) write_rows<FMT, T, true, AS_IT_IS>(K, A, R, true, P);
+  else write_rows<FMT, T, true, TURN>(K, A, R, false, P);
 }
 
-template <int FMT, class T>
+template <int FMT, class T, Turn TURN>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_rows_kernel(KvArgs K, KvRows A, KvTurn R, int for_v, int rest) {
   const int wv = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1), at = blockIdx.x;
   if (at >= rest) return turn_queries<T>(K, R, (at - rest) * RW_WAVES + wv);
@@ -610,7 +656,7 @@ __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_rows_kernel(KvArgs K
     write_v_row<FMT, T>(K, A, P);
   } else {
     row_place(K, K.q_start, K.T, ((at - for_v) * RW_WAVES + wv) * 16 + (lane & 15), P);
-    write_rows<FMT, T, false, true>(K, A, R, false, P);
+    write_rows<FMT, T, false, TURN>(K, A, R, false, P);
   }
 }
 
@@ -777,11 +823,13 @@ void launch_append(const KvArgs& K, const KvRows& A, const KvTurn& R, int max_q,
   const unsigned for_q = R.heads ? (unsigned)(((int64_t)K.T * turn_grid(R, K.D).waves + RW_WAVES - 1) / RW_WAVES) : 0u;
   const RowGrid g = row_grid(K, K.T, max_q <= 8);
   if (g.all) {
-    kv_append_rows_kernel<FMT, T><<<g.all + for_q, RW_WAVES * WAVE, 0, stream>>>(K, A, R, g.for_v, (int)g.all);
+    const auto kernel = R.interleaved ? kv_append_rows_kernel<FMT, T, NEIGHBOURS> : kv_append_rows_kernel<FMT, T, HALVES>;
+    kernel<<<g.all + for_q, RW_WAVES * WAVE, 0, stream>>>(K, A, R, g.for_v, (int)g.all);
   } else {
     const dim3 d = group_grid(K, K.T);
     const unsigned rest = 2 * d.x * d.y;
-    kv_append_groups_kernel<FMT, T><<<rest + for_q, RW_WAVES * WAVE, 0, stream>>>(K, A, R, (int)d.x, (int)rest);
+    const auto kernel = R.interleaved ? kv_append_groups_kernel<FMT, T, NEIGHBOURS> : kv_append_groups_kernel<FMT, T, HALVES>;
+    kernel<<<rest + for_q, RW_WAVES * WAVE, 0, stream>>>(K, A, R, (int)d.x, (int)rest);
   }
 }
 
