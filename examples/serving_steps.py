@@ -11,12 +11,17 @@ sequence: a chunk of its prompt, or its last token and a few drafted ones behind
      Rejected drafts leave the cache by leaving the sequence's length: the next write takes
      their places.
 
+With --base i4 or e2m1 the base weights are held in 4 bits and the layer is a whole one: a root-mean-square norm
+before the projection and one after it that adds the residual (sgmv_rms_norm), both projections from the packed
+weights (sgmv_base_product), queries and keys norm'd head by head and then turned by their positions, the keys on
+their way into the cache (sgmv_kv_append in place of step 2).
+
 The drafter looks a sequence's last token up in its past and proposes what followed (its drafts are
 certain, so it has no probabilities of its own). Weights are random; the point is the calls. Every step,
 that of the prompts too, is compared with plain attention in torch, in 64 bits on the CPU, over the values
 that the cache holds.
 
-    python examples/serving_steps.py [--cache e4m3|i8|bf16] [--steps 12]
+    python examples/serving_steps.py [--cache e4m3|i8|bf16] [--base bf16|i4|e2m1] [--steps 12]
 """
 import argparse
 import math
@@ -48,14 +53,69 @@ class Layer:
     def project(self, tokens, adapters):
         """Queries, keys and values of the tokens, as views of one projection."""
         x = self.embed[tokens.long()]
-        y = x @ self.qkv.T
+        return self.adapted(x, x @ self.qkv.T, adapters)
+
+    def adapted(self, x, y, adapters):
+        """The base product y of rows x with the adapters' deltas added, as queries, keys and values."""
         seg = sg.sgmv_segments_alloc(x.shape[0], ADAPTERS, 0, x.device)
         sg.sgmv_lora_delta_ids(adapters, x, self.pool, seg, y)
         q, k, v = y.split([HEADS * DIM, KV_HEADS * DIM, KV_HEADS * DIM], 1)
         return q.unflatten(1, (HEADS, DIM)), k.unflatten(1, (KV_HEADS, DIM)), v.unflatten(1, (KV_HEADS, DIM))
 
+    def store(self, q, k, v, batch, cache):
+        """Keys and values into the cache; the queries that attend."""
+        sg.sgmv_kv_write(k, v, batch, cache)
+        return q
+
     def probabilities(self, attended):
         return torch.softmax((attended.flatten(1) @ self.out.T).float(), 1)
+
+
+def in_4_bits(weight, form):
+    """A weight packed from its values, each group's largest at the end of the codes' range."""
+    n, group = weight.shape[0], 32 if form == "e2m1" else 64
+    w = weight.float().unflatten(1, (-1, group))
+    top = w.abs().amax(2)
+    if form == "e2m1":
+        e = torch.ceil(torch.log2(top / 6))
+        values = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], device=w.device)
+        at = (w.abs() / torch.exp2(e)[:, :, None]).unsqueeze(3).sub(values).abs().argmin(3)
+        codes, scale, format = torch.where(w < 0, at + 8, at), (e + 127).to(torch.uint8), sg.BASE_E2M1
+    else:
+        scale = (top / 7).to(torch.bfloat16)
+        codes, format = (w / scale.float()[:, :, None]).round().clamp(-8, 7) + 8, sg.BASE_I4
+    codes = codes.to(torch.uint8).reshape(n, -1, 2)
+    return sg.sgmv_base_pack(codes[:, :, 0] | codes[:, :, 1] << 4, scale, group=group, format=format, dtype=torch.bfloat16)
+
+
+class WholeLayer(Layer):
+    """Norms, projections from weights of 4 bits, rotated positions and the residual."""
+
+    def __init__(self, device, form, seed=0):
+        super().__init__(device, seed)
+        g = torch.Generator().manual_seed(seed + 1)
+        bf16 = lambda *s, std: (torch.randn(*s, generator=g) * std).to(torch.bfloat16).to(device)
+        self.qkv = in_4_bits(self.qkv, form)
+        self.proj = in_4_bits(bf16(WIDTH, HEADS * DIM, std=(HEADS * DIM) ** -0.5), form)
+        self.unembed = bf16(VOCAB, WIDTH, std=2 * WIDTH ** -0.5)
+        self.norm_in, self.norm_out, self.norm_q, self.norm_k = (1 + bf16(n, std=0.1) for n in (WIDTH, WIDTH, DIM, DIM))
+        angle = torch.arange(512)[:, None] * 10000.0 ** (-torch.arange(0, DIM, 2) / DIM)
+        self.cos_sin = torch.cat([torch.cos(angle), torch.sin(angle)], 1).to(device)
+
+    def project(self, tokens, adapters):
+        self.hidden = self.embed[tokens.long()]
+        x = sg.sgmv_rms_norm(self.hidden, self.norm_in).out
+        q, k, v = self.adapted(x, sg.sgmv_base_product(x, self.qkv), adapters)
+        sg.sgmv_rms_norm(q, self.norm_q, out=q)  # head by head, where they are
+        sg.sgmv_rms_norm(k, self.norm_k, out=k)
+        return q, k, v
+
+    def store(self, q, k, v, batch, cache):
+        return sg.sgmv_kv_append(q, k, v, batch, cache, self.cos_sin)
+
+    def probabilities(self, attended):
+        y = sg.sgmv_base_product(attended.flatten(1), self.proj)
+        return torch.softmax((sg.sgmv_rms_norm(y, self.norm_out, residual=self.hidden).out @ self.unembed.T).float(), 1)
 
 
 class Sequence:
@@ -84,7 +144,7 @@ def step(layer, cache, seqs, new, device):
     batch = sg.sgmv_kv_batch(i32(start), i32(lens), table.to(device), start[-1], max(map(len, new)), max(lens))
     adapters = [s.adapter for s, n in zip(seqs, new) for _ in n]
     q, k, v = layer.project(i32([t for n in new for t in n]), i32(adapters))
-    sg.sgmv_kv_write(k, v, batch, cache)
+    q = layer.store(q, k, v, batch, cache)
     out, _ = sg.sgmv_kv_attention(q, batch, cache)
     return q, out, batch, lens
 
@@ -114,12 +174,13 @@ def check(q, out, batch, lens, cache):
 def main(argv=None):
     parser = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     parser.add_argument("--cache", choices=sorted(FORMATS), default="e4m3")
+    parser.add_argument("--base", choices=["bf16", "i4", "e2m1"], default="bf16")
     parser.add_argument("--steps", type=int, default=12)
     args = parser.parse_args(argv)
     if args.steps < 1:
         parser.error("--steps must be at least 1")
     device = torch.device("cuda:0")
-    layer = Layer(device)
+    layer = Layer(device) if args.base == "bf16" else WholeLayer(device, args.base)
     g = torch.Generator().manual_seed(1)
     free = torch.randperm(64, generator=g).tolist()
     cache = sg.sgmv_kv_init(64, PAGE, KV_HEADS, DIM, FORMATS[args.cache], device)
