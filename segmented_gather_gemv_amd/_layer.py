@@ -64,6 +64,7 @@ _bind()
 
 _current = torch._C._cuda_getDevice  # (the calls behind torch.cuda's, which take longer than they)
 _stream = torch._C._cuda_getCurrentRawStream
+_like, _dense = torch.empty_like, torch.contiguous_format  # (allocates faster than new_empty of a shape)
 _ROWS = {torch.float32: _dtype_code(torch.float32), torch.bfloat16: _dtype_code(torch.bfloat16)}
 
 
@@ -141,7 +142,7 @@ def sgmv_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         rt, rh = _strides(residual, shape, dtype, index, "residual")
         rp = residual.data_ptr()
         if residual_out is None:
-            residual_out = x.new_empty(shape)
+            residual_out = _like(x, memory_format=_dense)
         else:
             st, sh = _strides(residual_out, shape, dtype, index, "residual_out")
         sp = residual_out.data_ptr()
@@ -151,18 +152,18 @@ def sgmv_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         ot, oh = _strides(out, shape, dtype, index, "out")
         op = out.data_ptr()
     elif want_out:
-        out = x.new_empty(shape)
+        out = _like(x, memory_format=_dense)
         op = out.data_ptr()
     if quantise is not None:
         fmt = _CODES.get(quantise)
         if fmt is None:
             raise TypeError(f"codes are float8_e4m3fn or int8, got {quantise}")
         if codes is None:
-            codes = x.new_empty(shape, dtype=quantise)
+            codes = _like(x, dtype=quantise, memory_format=_dense)
         else:
             ct, ch = _strides(codes, shape, quantise, index, "codes")
         if scale is None:
-            scale = x.new_empty(shape[:-1], dtype=torch.float32)
+            scale = x.new_empty((T,) if len(shape) == 2 else (T, heads), dtype=torch.float32)
         elif scale.shape != shape[:-1] or scale.dtype != torch.float32 or not scale.is_contiguous() or (
                 scale.get_device() != index):
             raise TypeError("scale must be a contiguous float32 tensor of one entry per row on x's device")
@@ -326,7 +327,7 @@ def sgmv_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
             raise TypeError("q must have k's dtype")
         heads, qp = q.shape[1], q.data_ptr()
         if q_out is None:
-            q_out = q.new_empty(q.shape)
+            q_out = _like(q, memory_format=_dense)
             ot, oh = _dense3(heads, cache)
         else:
             ot, oh = _rows3(q_out, T, heads, cache, "q_out")

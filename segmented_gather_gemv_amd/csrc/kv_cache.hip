@@ -161,11 +161,19 @@ struct Place {
   int head;
 };
 
-// [pages][H][page size] index of a place, or -1: no page.
-__device__ __forceinline__ int64_t token_of(const KvArgs& K, const Place& P) {
-  const int page = kv_page(K, K.table + (int64_t)P.b * K.ldp, P.pos);
-  return page < 0 ? -1 : ((int64_t)page * K.H + P.head) * (1 << K.lps) + (P.pos & ((1 << K.lps) - 1));
+// The page table's entry of a place, whatever it is (-1: the table has none).
+__device__ __forceinline__ int page_entry(const KvArgs& K, const Place& P) {
+  const int i = P.pos >> K.lps;
+  return P.pos < 0 || i >= K.table_pages ? -1 : K.table[(int64_t)P.b * K.ldp + i];
 }
+
+// [pages][H][page size] index of a place in the page of an entry, or -1: no page.
+__device__ __forceinline__ int64_t token_in(const KvArgs& K, const Place& P, int page) {
+  if ((uint32_t)page >= (uint32_t)K.pages) return -1;
+  return ((int64_t)page * K.H + P.head) * (1 << K.lps) + (P.pos & ((1 << K.lps) - 1));
+}
+
+__device__ __forceinline__ int64_t token_of(const KvArgs& K, const Place& P) { return token_in(K, P, page_entry(K, P)); }
 
 // Place of token r of a group, and token at place r.
 __device__ __forceinline__ int place_of(int r) { return 8 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
@@ -358,6 +366,7 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, con
   const ROW* src = static_cast<const ROW*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) +
                    P.head * (is_v ? A.ldv_h : A.ldk_h);
   uint32_t w[U::most][U::words];
+  const int page = page_entry(K, P);  // (loaded beside the row)
   int apart = 0;  // units of a lane from one of a pair to the other, 0: they are not in one lane
   if constexpr (TURN == HALVES) {
     const int half = R.rotary / 2;
@@ -396,7 +405,7 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, con
       else if (apart == 4) turn_units<4>(R, P.pos, quad, w);
     }
   }
-  const int64_t at = token_of(K, P), token = max(at, (int64_t)0);  // the page's load beside the row's
+  const int64_t at = token_in(K, P, page), token = max(at, (int64_t)0);
   P.ok = P.ok && at >= 0;
   const int r = (int)(token & 15);
   char* dst = static_cast<char*>(const_cast<void*>(is_v ? K.v : K.k)) + (token & ~(int64_t)15) * D * BYTES;
