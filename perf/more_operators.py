@@ -245,7 +245,8 @@ def _own(st, kind):
     if kind == "product":
         if "plan" not in st:  # the weight as a serving program keeps it
             st["plan"] = sg.sgmv_base_pack(st["codes"], st["scale"], st["zero"], K=case["K"], group=case["group"],
-                                           format=sg.BASE_I4 if case["form"] == "i4" else sg.BASE_E2M1)
+                                           format=sg.BASE_I4 if case["form"] == "i4" else sg.BASE_E2M1,
+                                           dtype=st["x"].dtype)
         return {"y": sg.sgmv_base_product(st["x"], st["plan"])}
     if "plan" not in st:  # the handles a serving loop keeps beside its cache and its batch
         st["plan"] = (sg.sgmv_kv_wrap(st["k"], st["v"], st.get("k_scale"), st.get("v_scale")),
