@@ -108,16 +108,10 @@ sgmv_status sgmv_rms_norm(const sgmv_norm* n, void* stream) {
       (n->codes && !rows_ok(n->codes, n, n->ldc_token, n->ldc_head)))
     return SGMV_EINVAL;
   const int E = n->dtype == SGMV_F32 ? 4 : 8;
-  const auto vec = [&](const void* p, int64_t ld_t, int64_t ld_h, int bytes) {
-    return !p || (aligned_to(p, bytes) && (n->T == 1 || ld_t % E == 0) && (n->heads == 1 || ld_h % E == 0));
-  };
   const NormArgs A{n->x, n->residual, n->weight, n->residual_out, n->out, n->codes, n->scale,
                    n->ldx_token, n->ldx_head, n->ldr_token, n->ldr_head, n->lds_token, n->lds_head,
                    n->ldo_token, n->ldo_head, n->ldc_token, n->ldc_head, (int64_t)n->T * n->heads, n->heads, n->width,
-                   n->eps,
-                   vec(n->x, n->ldx_token, n->ldx_head, 16) && vec(n->residual, n->ldr_token, n->ldr_head, 16) &&
-                       aligned_to(n->weight, 16) && vec(n->residual_out, n->lds_token, n->lds_head, 16) &&
-                       vec(n->out, n->ldo_token, n->ldo_head, 16) && vec(n->codes, n->ldc_token, n->ldc_head, E)};
+                   n->eps};
   const NormShape s = norm_shape(A.rows, (int)ceil_div(n->width, E));
   if (ceil_div(A.rows * s.group, 64) + 16 > MOST_WAVES) return SGMV_EUNSUPPORTED;
   return launched(launch_norm(A, n->dtype, n->format, static_cast<hipStream_t>(stream)));

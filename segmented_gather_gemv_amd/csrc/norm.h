@@ -17,7 +17,6 @@ struct NormArgs {
   int64_t rows;          // T * heads
   int32_t H, W;
   float eps;
-  int32_t vec;           // rows may be accessed 16 bytes of x (and as many codes) at a time
 };
 
 // Threads that share a row, and its 16-byte pieces that each of them takes.

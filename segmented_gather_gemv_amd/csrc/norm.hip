@@ -15,36 +15,68 @@ namespace {
 
 constexpr int NONE = -1;  // no codes
 
-// 16 bytes of a row, n of its values inside it; element by element where `whole` is not set.
+// 16, 8, 4 and 2 bytes, wherever they start.
+typedef u32x4_t any16_t __attribute__((aligned(1)));
+typedef u32x2_t any8_t __attribute__((aligned(1)));
+typedef uint32_t any4_t __attribute__((aligned(1)));
+typedef uint16_t any2_t __attribute__((aligned(1)));
+
+// 16 bytes of a row, n of its values inside it. Rows start anywhere (a load of 16 bytes takes no longer off its
+// alignment); of a piece that the row ends in, 8, 4 and 2 bytes as its length has them, at once and in their places.
 template <class T>
-__device__ __forceinline__ u32x4_t load_piece(const T* p, bool whole, int n) {
-  constexpr int E = 16 / sizeof(T);
-  if (whole) return load_u32x4(p);
-  u32x4_t v = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (e < n) {
-      if constexpr (sizeof(T) == 4) v[e] = reinterpret_cast<const uint32_t*>(p)[e];
-      else v[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
-    }
-  return v;
+__device__ __forceinline__ u32x4_t load_piece(const T* p, int n) {
+  constexpr int E = 16 / sizeof(T), HALF = E / 2;
+  if (n >= E) return *reinterpret_cast<const any16_t*>(p);
+  u32x2_t front = {0u, 0u}, back = {0u, 0u};
+  if (n & HALF) front = *reinterpret_cast<const any8_t*>(p);
+  if constexpr (sizeof(T) == 4) {
+    if (n & 1) back[0] = *reinterpret_cast<const any4_t*>(p + (n & 2));
+  } else {
+    uint32_t pair = 0u, one = 0u;
+    if (n & 2) pair = *reinterpret_cast<const any4_t*>(p + (n & 4));
+    if (n & 1) one = p[n & 6];
+    back = n & 2 ? u32x2_t{pair, one} : u32x2_t{one, 0u};
+  }
+  return n & HALF ? u32x4_t{front[0], front[1], back[0], back[1]} : u32x4_t{back[0], back[1], 0u, 0u};
 }
 
 template <class T, int E>
-__device__ __forceinline__ void store_piece(T* p, bool whole, int n, const float (&y)[E]) {
+__device__ __forceinline__ void store_piece(T* p, int n, const float (&y)[E]) {
+  constexpr int HALF = E / 2;
   u32x4_t v;
   if constexpr (sizeof(T) == 4) v = u32x4_t{__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3])};
   else v = u32x4_t{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7])};
-  if (whole) {
-    *reinterpret_cast<u32x4_t*>(p) = v;
+  if (n >= E) {
+    *reinterpret_cast<any16_t*>(p) = v;
     return;
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (e < n) {
-      if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[e] = v[e];
-      else p[e] = (T)(v[e / 2] >> (16 * (e & 1)));
+  if (n & HALF) *reinterpret_cast<any8_t*>(p) = u32x2_t{v[0], v[1]};
+  const u32x2_t back = n & HALF ? u32x2_t{v[2], v[3]} : u32x2_t{v[0], v[1]};
+  if constexpr (sizeof(T) == 4) {
+    if (n & 1) *reinterpret_cast<any4_t*>(p + (n & 2)) = back[0];
+  } else {
+    if (n & 2) *reinterpret_cast<any4_t*>(p + (n & 4)) = back[0];
+    if (n & 1) p[n & 6] = (T)(n & 2 ? back[1] : back[0]);
+  }
+}
+
+// Codes of a piece.
+template <int E>
+__device__ __forceinline__ void store_codes(char* p, int n, const uint32_t (&c)[E / 4]) {
+  if (n >= E) {
+    if constexpr (E == 8) *reinterpret_cast<any8_t*>(p) = u32x2_t{c[0], c[1]};
+    else *reinterpret_cast<any4_t*>(p) = c[0];
+    return;
+  }
+  uint32_t back = c[0];
+  if constexpr (E == 8) {
+    if (n & 4) {
+      *reinterpret_cast<any4_t*>(p) = c[0];
+      back = c[1];
     }
+  }
+  if (n & 2) *reinterpret_cast<any2_t*>(p + (n & 4)) = (uint16_t)back;
+  if (n & 1) p[n & 6] = (char)(n & 2 ? back >> 16 : back);
 }
 
 // Value e of a piece.
@@ -79,26 +111,25 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void norm_kernel(NormArg
   const T* x = static_cast<const T*>(A.x) + t * A.ldx_t + head * A.ldx_h;
   const T* w = static_cast<const T*>(A.weight);
   const auto left = [&](int p) { return A.W - p * E; };  // values of the row from piece p on
-  const auto whole = [&](int p) { return A.vec && left(p) >= E; };
 
   u32x4_t xw[PER], rw[PER], ww[PER];
 #pragma unroll
   for (int n = 0; n < PER; ++n) {
     const int p = i + n * GROUP;
-    xw[n] = left(p) > 0 ? load_piece<T>(x + p * E, whole(p), left(p)) : u32x4_t{0u, 0u, 0u, 0u};
+    xw[n] = left(p) > 0 ? load_piece<T>(x + p * E, left(p)) : u32x4_t{0u, 0u, 0u, 0u};
   }
   if (A.residual) {
     const T* r = static_cast<const T*>(A.residual) + t * A.ldr_t + head * A.ldr_h;
 #pragma unroll
     for (int n = 0; n < PER; ++n) {
       const int p = i + n * GROUP;
-      rw[n] = left(p) > 0 ? load_piece<T>(r + p * E, whole(p), left(p)) : u32x4_t{0u, 0u, 0u, 0u};
+      rw[n] = left(p) > 0 ? load_piece<T>(r + p * E, left(p)) : u32x4_t{0u, 0u, 0u, 0u};
     }
   }
 #pragma unroll
   for (int n = 0; n < PER; ++n) {
     const int p = i + n * GROUP;
-    ww[n] = left(p) > 0 ? load_piece<T>(w + p * E, whole(p), left(p)) : u32x4_t{0u, 0u, 0u, 0u};
+    ww[n] = left(p) > 0 ? load_piece<T>(w + p * E, left(p)) : u32x4_t{0u, 0u, 0u, 0u};
   }
 
   float h[PER][E];
@@ -113,7 +144,7 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void norm_kernel(NormArg
       const int p = i + n * GROUP;
 #pragma unroll
       for (int e = 0; e < E; ++e) h[n][e] += piece_value<T>(rw[n], e);
-      if (A.residual_out && left(p) > 0) store_piece<T, E>(s + p * E, whole(p), left(p), h[n]);
+      if (A.residual_out && left(p) > 0) store_piece<T, E>(s + p * E, left(p), h[n]);
     }
   }
   const auto g = [&](int n, int e) { return h[n][e] * piece_value<T>(ww[n], e); };
@@ -175,7 +206,7 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void norm_kernel(NormArg
       float y[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) y[e] = g(n, e) * down * root;
-      if (left(p) > 0) store_piece<T, E>(out + p * E, whole(p), left(p), y);
+      if (left(p) > 0) store_piece<T, E>(out + p * E, left(p), y);
     }
   }
   if constexpr (FMT != NONE) {
@@ -193,16 +224,7 @@ __global__ __launch_bounds__(GROUP > 256 ? GROUP : 256) void norm_kernel(NormArg
         const float q[4] = {g(n, 4 * k), g(n, 4 * k + 1), g(n, 4 * k + 2), g(n, 4 * k + 3)};
         c[k] = quantise4<FMT, float>(q, S);
       }
-      if (left(p) <= 0) continue;
-      char* to = codes + p * E;
-      if (whole(p)) {
-        if constexpr (E == 8) *reinterpret_cast<u32x2_t*>(to) = u32x2_t{c[0], c[1]};
-        else *reinterpret_cast<uint32_t*>(to) = c[0];
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-          if (e < left(p)) to[e] = (char)(c[e / 4] >> (8 * (e % 4)));
-      }
+      if (left(p) > 0) store_codes<E>(codes + p * E, left(p), c);
     }
   }
 }
