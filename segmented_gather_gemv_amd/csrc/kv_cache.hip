@@ -244,20 +244,19 @@ template <int FMT, class T> struct Unit {
 template <int BYTES>
 __device__ __forceinline__ int64_t v_at(int d, int place) { return (int64_t)(d * 16 + place) * BYTES; }
 
-// N floats of the table of cosines and sines.
+// N floats of the table of cosines and sines, whose rows start anywhere.
 template <int N>
-__device__ __forceinline__ void load_angles(const float* p, bool vec, float (&f)[N]) {
-  if (!vec) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = p[i];
-  } else if constexpr (N == 2) {
-    const f32x2_t v = *reinterpret_cast<const f32x2_t*>(p);
+__device__ __forceinline__ void load_angles(const float* p, float (&f)[N]) {
+  typedef f32x2_t any8_t __attribute__((aligned(4)));
+  typedef f32x4_t any16_t __attribute__((aligned(4)));
+  if constexpr (N == 2) {
+    const f32x2_t v = *reinterpret_cast<const any8_t*>(p);
     f[0] = v.x;
     f[1] = v.y;
   } else {
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-      const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + i);
+      const f32x4_t v = *reinterpret_cast<const any16_t*>(p + i);
 #pragma unroll
       for (int j = 0; j < 4; ++j) f[i + j] = v[j];
     }
@@ -269,8 +268,8 @@ template <int N>
 __device__ __forceinline__ void angles(const KvTurn& R, int pos, int i, float (&c)[N], float (&s)[N]) {
   const bool in = (uint32_t)pos < (uint32_t)R.positions;  // (a row before the first token is not written anyway)
   const float* row = R.cos_sin + (in ? pos : 0) * R.ld + i;
-  load_angles(row, R.vec, c);
-  load_angles(row + R.rotary / 2, R.vec, s);
+  load_angles(row, c);
+  load_angles(row + R.rotary / 2, s);
   if (!in)
 #pragma unroll
     for (int j = 0; j < N; ++j) c[j] = s[j] = __uint_as_float(0x7fc00000u);
@@ -294,13 +293,18 @@ enum Turn { AS_IT_IS, HALVES, NEIGHBOURS };
 template <class T, int N, Turn TURN>
 __device__ __forceinline__ void turned(const KvTurn& R, const T* row, bool vec, int pos, int d, float* y) {
   constexpr int W = N * sizeof(T) / 4;
+  const auto load = [&](const T* p, uint32_t (&w)[W]) {
+    if constexpr (W >= 4) {
+      load_words(p, vec, w);
+    } else {
+      typedef u32x2_t any8_t __attribute__((aligned(2)));
+      const u32x2_t v = *reinterpret_cast<const any8_t*>(p);
+      w[0] = v[0];
+      w[1] = v[1];
+    }
+  };
   uint32_t own[W];
-  if constexpr (W >= 4) {
-    load_words(row + d, vec, own);
-  } else {  // 4 values of 16 bits
-#pragma unroll
-    for (int i = 0; i < W; ++i) own[i] = row[d + 2 * i] | (uint32_t)row[d + 2 * i + 1] << 16;
-  }
+  load(row + d, own);
   float x[N];
 #pragma unroll
   for (int e = 0; e < N; ++e) x[e] = word_value<T>(own, e);
@@ -319,7 +323,7 @@ __device__ __forceinline__ void turned(const KvTurn& R, const T* row, bool vec, 
   } else {  // the other half's values (the same lines of the row)
     const bool low = d < half;
     uint32_t other[W];
-    load_words(row + (low ? d + half : d - half), vec, other);
+    load(row + (low ? d + half : d - half), other);
     float c[N], s[N];
     angles(R, pos, low ? d : d - half, c, s);
 #pragma unroll
@@ -516,6 +520,38 @@ __device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, co
   }
 }
 
+// One row of K per wave, turned on the way: 4 values a lane, with those that they are paired with and their angles
+// loaded at once. (16 rows a wave load the units of a row one after another: 256 tokens of 8 heads of 128 took 7.7 us.)
+template <int FMT, class T, Turn TURN>
+__device__ __forceinline__ void write_turned_row(const KvArgs& K, const KvRows& A, const KvTurn& R, const Place& P) {
+  constexpr int BYTES = KvFormat<FMT>::bytes, C = 16 / BYTES;
+  const int lane = threadIdx.x & (WAVE - 1), D = K.D, d = 4 * lane;
+  if (!P.ok) return;
+  const T* src = static_cast<const T*>(A.k) + P.row * A.ldk_t + P.head * A.ldk_h;
+  const int page = page_entry(K, P);
+  float x[4] = {};
+  if (d < D) turned<T, 4, TURN>(R, src, A.vec, P.pos, d, x);
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = word_top<float>(top, __float_as_uint(x[i]));
+  const int64_t token = token_in(K, P, page);
+  if (token < 0) return;
+  char* dst = static_cast<char*>(const_cast<void*>(K.k)) + (token & ~(int64_t)15) * D * BYTES +
+              ((d / C * 16 + (int)(token & 15)) * C + d % C) * BYTES;
+  uint32_t c = 0;
+  if constexpr (KvFormat<FMT>::scaled) {
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+    const RowScale S = row_scale<FMT>(quad_top<float>(top));
+    c = quantise4<FMT, float>(x, S);
+    if (lane == 0) const_cast<float*>(K.k_scale)[token] = S.scale;
+  }
+  if (d >= D) return;
+  if constexpr (BYTES == 1) *reinterpret_cast<uint32_t*>(dst) = c;
+  else if constexpr (BYTES == 2) *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+  else *reinterpret_cast<f32x4_t*>(dst) = f32x4_t{x[0], x[1], x[2], x[3]};
+}
+
 template <int FMT, class T>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_groups_kernel(KvArgs K, KvRows A) {
   Place P;
@@ -656,17 +692,14 @@ __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_groups_kernel(KvArgs
 }
 
 template <int FMT, class T, Turn TURN>
-__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_rows_kernel(KvArgs K, KvRows A, KvTurn R, int for_v, int rest) {
-  const int wv = threadIdx.x / WAVE, lane = threadIdx.x & (WAVE - 1), at = blockIdx.x;
+__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_rows_kernel(KvArgs K, KvRows A, KvTurn R, int rest) {
+  const int wv = threadIdx.x / WAVE, at = blockIdx.x;
   if (at >= rest) return turn_queries<T>(K, R, (at - rest) * RW_WAVES + wv);
+  const bool is_v = at >= rest / 2;
   Place P;
-  if (at < for_v) {
-    row_place(K, K.q_start, K.T, at * RW_WAVES + wv, P);
-    write_v_row<FMT, T>(K, A, P);
-  } else {
-    row_place(K, K.q_start, K.T, ((at - for_v) * RW_WAVES + wv) * 16 + (lane & 15), P);
-    write_rows<FMT, T, false, TURN>(K, A, R, false, P);
-  }
+  row_place(K, K.q_start, K.T, (is_v ? at - rest / 2 : at) * RW_WAVES + wv, P);
+  if (is_v) write_v_row<FMT, T>(K, A, P);
+  else write_turned_row<FMT, T, TURN>(K, A, R, P);
 }
 
 // 16 rows of K (or, grouped, of V) per wave.
@@ -827,18 +860,33 @@ void launch_write(const KvArgs& K, const KvRows& R, int max_q, hipStream_t strea
   else kv_write_groups_kernel<FMT, T><<<group_grid(K, K.T), RW_WAVES * WAVE, 0, stream>>>(K, R);
 }
 
+// Workgroups of an append: of K and V, rows of their own (few new tokens a sequence) or in groups, and of the queries.
+struct AppendGrid {
+  bool rows;
+  int slots;  // of groups, a head
+  int64_t rest, for_q;
+};
+AppendGrid append_grid(const KvArgs& K, const KvTurn& R, int max_q) {
+  AppendGrid g{};
+  const int64_t rows = (int64_t)K.T * K.H;
+  g.rows = max_q <= 8 && rows <= 0x1000000;
+  const dim3 d = group_grid(K, K.T);
+  g.slots = (int)d.x;
+  g.rest = 2 * (g.rows ? (rows + RW_WAVES - 1) / RW_WAVES : (int64_t)d.x * d.y);
+  g.for_q = R.heads ? ((int64_t)K.T * turn_grid(R, K.D).waves + RW_WAVES - 1) / RW_WAVES : 0;
+  return g;
+}
+
 template <int FMT, class T>
 void launch_append(const KvArgs& K, const KvRows& A, const KvTurn& R, int max_q, hipStream_t stream) {
-  const unsigned for_q = R.heads ? (unsigned)(((int64_t)K.T * turn_grid(R, K.D).waves + RW_WAVES - 1) / RW_WAVES) : 0u;
-  const RowGrid g = row_grid(K, K.T, max_q <= 8);
-  if (g.all) {
+  const AppendGrid g = append_grid(K, R, max_q);
+  const unsigned all = (unsigned)(g.rest + g.for_q);
+  if (g.rows) {
     const auto kernel = R.interleaved ? kv_append_rows_kernel<FMT, T, NEIGHBOURS> : kv_append_rows_kernel<FMT, T, HALVES>;
-    kernel<<<g.all + for_q, RW_WAVES * WAVE, 0, stream>>>(K, A, R, g.for_v, (int)g.all);
+    kernel<<<all, RW_WAVES * WAVE, 0, stream>>>(K, A, R, (int)g.rest);
   } else {
-    const dim3 d = group_grid(K, K.T);
-    const unsigned rest = 2 * d.x * d.y;
     const auto kernel = R.interleaved ? kv_append_groups_kernel<FMT, T, NEIGHBOURS> : kv_append_groups_kernel<FMT, T, HALVES>;
-    kernel<<<rest + for_q, RW_WAVES * WAVE, 0, stream>>>(K, A, R, (int)d.x, (int)rest);
+    kernel<<<all, RW_WAVES * WAVE, 0, stream>>>(K, A, R, g.slots, (int)g.rest);
   }
 }
 
@@ -861,11 +909,10 @@ hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, int max_q,
   return hipGetLastError();
 }
 
-// Waves of an append's launch, at most.
-int64_t kv_append_waves(const KvArgs& K, const KvTurn& R) {
-  const dim3 g = group_grid(K, K.T);
-  const RowGrid r = row_grid(K, K.T, true);
-  return std::max<int64_t>((int64_t)2 * g.x * g.y, r.all) * RW_WAVES + (R.heads ? (int64_t)K.T * turn_grid(R, K.D).waves + RW_WAVES : 0);
+// Waves of an append's launch.
+int64_t kv_append_waves(const KvArgs& K, const KvTurn& R, int max_q) {
+  const AppendGrid g = append_grid(K, R, max_q);
+  return (g.rest + g.for_q) * RW_WAVES;
 }
 
 hipError_t launch_kv_append(const KvArgs& K, const KvRows& A, const KvTurn& R, int fmt, int max_q, hipStream_t stream) {

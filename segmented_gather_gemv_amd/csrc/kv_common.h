@@ -49,7 +49,6 @@ struct KvTurn {
   const float* cos_sin;  // [positions][ld]: rotary / 2 cosines, then as many sines
   int64_t ld;
   int32_t positions, rotary, interleaved;
-  int32_t vec;           // rows of the table may be read 16 bytes at a time
   const void* q;
   void* q_out;
   int64_t ldq_t, ldq_h, ldo_t, ldo_h;

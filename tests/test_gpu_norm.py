@@ -73,6 +73,22 @@ def test_norm_against_oracle(sg, T, heads, W, dtype, quantise):
     _check(got, x, w, 1e-5, r, quantise)
 
 
+@pytest.mark.parametrize("T,W,dtype,quantise", [(2100, 1099, BF16, E4M3), (700, 1501, BF16, I8), (1030, 16001, BF16, I8),
+                                                (1030, 9000, BF16, None), (2100, 777, F32, I8), (1030, 8001, F32, E4M3)])
+def test_norm_of_many_rows(sg, T, W, dtype, quantise):
+    """Shapes that many rows take; every eighth row is the same."""
+    g = torch.Generator().manual_seed(T + W)
+    x, r = (torch.randn(8, W, generator=g).to(dtype) for _ in range(2))
+    w = torch.randn(W, generator=g).to(dtype)
+    many = lambda t: t.repeat(-(-T // 8), 1)[:T].to(DEV)
+    got = sg.sgmv_rms_norm(many(x), w.to(DEV), residual=many(r), quantise=quantise)
+    _check(sg.Normed(*(None if t is None else t[:8] for t in got)), x, w, 1e-6, r, quantise)
+    for t in got:
+        if t is not None:
+            t = t.view(torch.uint8) if t.element_size() == 1 else t
+            assert torch.equal(t, t[:8].repeat(-(-T // 8), *[1] * (t.dim() - 1))[:T])
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("W", [48, 300, 2056])
 def test_norm_of_zeros_extremes_and_rows_that_are_not_finite(sg, dtype, W):
