@@ -12,7 +12,7 @@ namespace sgmv {
 hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, int max_q, hipStream_t stream);
 hipError_t launch_kv_read(const KvArgs& K, const KvRows& R, int fmt, hipStream_t stream);
 hipError_t launch_kv_append(const KvArgs& K, const KvRows& R, const KvTurn& turn, int fmt, int max_q, hipStream_t stream);
-int64_t kv_append_waves(const KvArgs& K, const KvTurn& turn, int max_q);
+int64_t kv_append_waves(const KvArgs& K, const KvTurn& turn, int fmt, int max_q);
 hipError_t launch_attn_direct_bf16(const AttnArgs& A, hipStream_t stream);
 hipError_t launch_attn_direct_e4m3(const AttnArgs& A, hipStream_t stream);
 hipError_t launch_attn_direct_i8(const AttnArgs& A, hipStream_t stream);
@@ -263,7 +263,7 @@ sgmv_status sgmv_kv_append(const sgmv_kv_rotation* turn, const void* k, int64_t 
   const KvTurn t{turn->cos_sin, turn->ld, turn->positions, turn->rotary, turn->interleaved,
                  turn->q, turn->q_out, turn->ldq_token, turn->ldq_head, turn->ldo_token, turn->ldo_head, turn->heads,
                  rows_vec(turn->q, turn->q_out, turn->ldq_token, turn->ldq_head, turn->ldo_token, turn->ldo_head, dtype)};
-  if (kv_append_waves(K, t, batch->max_q) > MOST_WAVES) return SGMV_EUNSUPPORTED;
+  if (kv_append_waves(K, t, cache->format, batch->max_q) > MOST_WAVES) return SGMV_EUNSUPPORTED;
   return launched(launch_kv_append(K, R, t, cache->format, batch->max_q, static_cast<hipStream_t>(stream)));
 }
 

@@ -30,7 +30,6 @@
 // 4.5 TB/s; a large copy: 5.1). Fp32 rows written as e4m3 or int8 19.4 us (floor 17.9), read back 143 (84); rows that
 // are held as they are: bf16 written in 13.9 us (14.2), read in 75 (67), fp32 25 (28) and 181 (133).
 #include <algorithm>
-#include <type_traits>
 
 #include "quantise.h"
 
@@ -178,29 +177,48 @@ __device__ __forceinline__ int64_t token_of(const KvArgs& K, const Place& P) { r
 // Place of token r of a group, and token at place r.
 __device__ __forceinline__ int place_of(int r) { return 8 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
 
+// A group of 16 tokens, the first at a multiple of 16: those of its rows that are there.
+struct Group {
+  int b, head;
+  int t0, lo, hi;  // position of the first token, and those of the first row and behind the last
+  int64_t row;     // row of position 0
+};
+
 // GROUPED: slot `w` of 16 tokens: the groups of sequence b take the slots from first(b) = (rows
 // before b) / 16 + 2 b on; n rows touch at most (n + 14) / 16 + 1 groups. start: rows of each sequence,
 // the last ones of it.
-// by_place: lane r of 16 has the token at place r, not token r.
-__device__ __forceinline__ bool group_place(const KvArgs& K, const int32_t* start, int total, int slots, int head,
-                                            bool by_place, Place& P) {
-  const int lane = threadIdx.x & (WAVE - 1), r = by_place ? place_of(lane & 15) : lane & 15;
+__device__ __forceinline__ bool find_group(const KvArgs& K, const int32_t* start, int total, int slots, int head, Group& G) {
   const int slot = slots * RW_WAVES + threadIdx.x / WAVE;
   const int b = wave_find(K.B, slot, [&](int i) { return min(max(start[i], 0), total) / 16 + 2 * i; });
   const int r0 = min(max(start[b], 0), total), r1 = min(max(start[b + 1], 0), total);
   const int n = max(r1 - r0, 0), kv_len = kv_seq(K, b).kv_len;
   const int first = kv_len - n;  // position of the first row; may be negative
   const int g0 = (first >> 4) + (slot - (r0 / 16 + 2 * b));
-  const int t_lo = max(16 * g0, first), t_hi = min(16 * g0 + 16, kv_len);
-  if (t_lo >= t_hi) return false;
-  const int t = 16 * g0 + r, t4 = t & ~3;
-  P.head = head;
-  P.ok = t >= t_lo && t < t_hi;
-  P.quad_ok = t4 >= t_lo && t4 + 4 <= t_hi;
-  P.whole = t_lo == 16 * g0 && t_hi == 16 * g0 + 16;
-  P.row = P.ok ? r0 + (t - first) : r0;
-  P.b = b;
+  G = {b, head, 16 * g0, max(16 * g0, first), min(16 * g0 + 16, kv_len), (int64_t)r0 - first};
+  return G.lo < G.hi;
+}
+
+// Token r of a group.
+__device__ __forceinline__ Place place_in(const Group& G, int r) {
+  const int t = G.t0 + r, t4 = t & ~3;
+  Place P;
+  P.head = G.head;
+  P.ok = t >= G.lo && t < G.hi;
+  P.quad_ok = t4 >= G.lo && t4 + 4 <= G.hi;
+  P.whole = G.lo == G.t0 && G.hi == G.t0 + 16;
+  P.row = G.row + (P.ok ? t : G.lo);
+  P.b = G.b;
   P.pos = t;
+  return P;
+}
+
+// by_place: lane r of 16 has the token at place r, not token r.
+__device__ __forceinline__ bool group_place(const KvArgs& K, const int32_t* start, int total, int slots, int head,
+                                            bool by_place, Place& P) {
+  const int lane = threadIdx.x & (WAVE - 1);
+  Group G;
+  if (!find_group(K, start, total, slots, head, G)) return false;
+  P = place_in(G, by_place ? place_of(lane & 15) : lane & 15);
   return true;
 }
 
@@ -266,13 +284,12 @@ __device__ __forceinline__ void load_angles(const float* p, float (&f)[N]) {
 // Cosines and sines i .. i + N - 1 of a position; past the table they are NaN, so that what they turn is.
 template <int N>
 __device__ __forceinline__ void angles(const KvTurn& R, int pos, int i, float (&c)[N], float (&s)[N]) {
-  const bool in = (uint32_t)pos < (uint32_t)R.positions;  // (a row before the first token is not written anyway)
-  const float* row = R.cos_sin + (in ? pos : 0) * R.ld + i;
+#pragma unroll
+  for (int j = 0; j < N; ++j) c[j] = s[j] = __uint_as_float(0x7fc00000u);
+  if ((uint32_t)pos >= (uint32_t)R.positions) return;  // (a row before the first token is not written anyway)
+  const float* row = R.cos_sin + pos * R.ld + i;       // (nothing waits for the loads here)
   load_angles(row, c);
   load_angles(row + R.rotary / 2, s);
-  if (!in)
-#pragma unroll
-    for (int j = 0; j < N; ++j) c[j] = s[j] = __uint_as_float(0x7fc00000u);
 }
 
 // A pair turned by its angle: two products and their sum, each rounded to fp32.
@@ -285,81 +302,9 @@ __device__ __forceinline__ float turn_high(float a, float b, float c, float s) {
   return b * c + a * s;
 }
 
-// What write_rows turns: nothing, pairs half a rotation apart, pairs of neighbours. (Kernels of their own for the last
-// two: the registers of the one would cost the other waves in flight, 56 us and not 52 in the interleaved form.)
-enum Turn { AS_IT_IS, HALVES, NEIGHBOURS };
-
-// Values d .. d + N - 1 (d a multiple of N, N of 4 and a divisor of 8) of a row at a position, turned.
-template <class T, int N, Turn TURN>
-__device__ __forceinline__ void turned(const KvTurn& R, const T* row, bool vec, int pos, int d, float* y) {
-  constexpr int W = N * sizeof(T) / 4;
-  const auto load = [&](const T* p, uint32_t (&w)[W]) {
-    if constexpr (W >= 4) {
-      load_words(p, vec, w);
-    } else {
-      typedef u32x2_t any8_t __attribute__((aligned(2)));
-      const u32x2_t v = *reinterpret_cast<const any8_t*>(p);
-      w[0] = v[0];
-      w[1] = v[1];
-    }
-  };
-  uint32_t own[W];
-  load(row + d, own);
-  float x[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) x[e] = word_value<T>(own, e);
-  const int half = R.rotary / 2;
-  if (d >= R.rotary) {
-#pragma unroll
-    for (int e = 0; e < N; ++e) y[e] = x[e];
-  } else if constexpr (TURN == NEIGHBOURS) {
-    float c[N / 2], s[N / 2];
-    angles(R, pos, d / 2, c, s);
-#pragma unroll
-    for (int e = 0; e < N / 2; ++e) {
-      y[2 * e] = turn_low(x[2 * e], x[2 * e + 1], c[e], s[e]);
-      y[2 * e + 1] = turn_high(x[2 * e], x[2 * e + 1], c[e], s[e]);
-    }
-  } else {  // the other half's values (the same lines of the row)
-    const bool low = d < half;
-    uint32_t other[W];
-    load(row + (low ? d + half : d - half), other);
-    float c[N], s[N];
-    angles(R, pos, low ? d : d - half, c, s);
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float o = word_value<T>(other, e);
-      y[e] = low ? turn_low(x[e], o, c[e], s[e]) : turn_high(o, x[e], c[e], s[e]);
-    }
-  }
-}
-
-// A row's units (values 16 n quads of lanes apart, C each) whose pairs lie P units of one lane apart: turned where they
-// are, so that cosines, sines and values are loaded once.
-template <int P, int MOST, int C>
-__device__ __forceinline__ void turn_units(const KvTurn& R, int pos, int quad, uint32_t (&w)[MOST][C]) {
-  constexpr int N = C < 8 ? C : 8;
-  if constexpr (2 * P <= MOST) {
-#pragma unroll
-    for (int n = 0; n < P; ++n)
-#pragma unroll
-      for (int e = 0; e < C; e += N) {
-        float c[N], s[N];
-        angles(R, pos, (quad + 4 * n) * C + e, c, s);
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-          const float a = __uint_as_float(w[n][e + j]), b = __uint_as_float(w[n + P][e + j]);
-          w[n][e + j] = __float_as_uint(turn_low(a, b, c[j], s[j]));
-          w[n + P][e + j] = __float_as_uint(turn_high(a, b, c[j], s[j]));
-        }
-      }
-  }
-}
-
-// 16 rows of K (or, grouped, of V) per wave. TURN: of K, turned by their positions on the way.
-template <int FMT, class ROW, bool GROUPED, Turn TURN>
-__device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, const KvTurn& R, bool is_v, const Place& place16) {
-  using T = std::conditional_t<TURN != AS_IT_IS, float, ROW>;  // of the values in registers
+// 16 rows of K (or, grouped, of V) per wave.
+template <int FMT, class T, bool GROUPED>
+__device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, bool is_v, const Place& place16) {
   using U = Unit<FMT, T>;
   constexpr int BYTES = U::bytes, C = U::C;
   constexpr bool SCALED = KvFormat<FMT>::scaled;
@@ -367,47 +312,17 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, con
   Place P = place16;
   if (!__any(P.ok)) return;
   const int D = K.D, units = D / C;
-  const ROW* src = static_cast<const ROW*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) +
-                   P.head * (is_v ? A.ldv_h : A.ldk_h);
-  uint32_t w[U::most][U::words];
+  const T* src = static_cast<const T*>(is_v ? A.v : A.k) + P.row * (is_v ? A.ldv_t : A.ldk_t) +
+                 P.head * (is_v ? A.ldv_h : A.ldk_h);
   const int page = page_entry(K, P);  // (loaded beside the row)
-  int apart = 0;  // units of a lane from one of a pair to the other, 0: they are not in one lane
-  if constexpr (TURN == HALVES) {
-    const int half = R.rotary / 2;
-    apart = half % (4 * C) == 0 ? half / (4 * C) : 0;
-    if (apart != 1 && apart != 2 && apart != 4) apart = 0;
-  }
+  uint32_t w[U::most][U::words];
 #pragma unroll
   for (int n = 0; n < U::most; ++n) {
     if (4 * n >= units) break;
     const int u = quad + 4 * n;
 #pragma unroll
     for (int i = 0; i < U::words; ++i) w[n][i] = 0u;
-    if (!P.ok || u >= units) continue;
-    if constexpr (TURN != AS_IT_IS) {
-      if (apart) {
-        uint32_t raw[C * sizeof(ROW) / 4];
-        load_words(src + u * C, A.vec, raw);
-#pragma unroll
-        for (int e = 0; e < C; ++e) w[n][e] = __float_as_uint(word_value<ROW>(raw, e));
-        continue;
-      }
-      constexpr int N = C < 8 ? C : 8;
-      float x[C];
-#pragma unroll
-      for (int e = 0; e < C; e += N) turned<ROW, N, TURN>(R, src, A.vec, P.pos, u * C + e, x + e);
-#pragma unroll
-      for (int e = 0; e < C; ++e) w[n][e] = __float_as_uint(x[e]);
-    } else {
-      load_words(src + u * C, A.vec, w[n]);
-    }
-  }
-  if constexpr (TURN == HALVES) {
-    if (P.ok) {
-      if (apart == 1) turn_units<1>(R, P.pos, quad, w);
-      else if (apart == 2) turn_units<2>(R, P.pos, quad, w);
-      else if (apart == 4) turn_units<4>(R, P.pos, quad, w);
-    }
+    if (P.ok && u < units) load_words(src + u * C, A.vec, w[n]);
   }
   const int64_t at = token_in(K, P, page), token = max(at, (int64_t)0);
   P.ok = P.ok && at >= 0;
@@ -439,9 +354,6 @@ __device__ __forceinline__ void write_rows(const KvArgs& K, const KvRows& A, con
         for (int j = 0; j < 4; ++j) x[j] = word_value<T>(w[n], 4 * k + j);
         c[k] = quantise4<FMT, T>(x, S);
       }
-    } else if constexpr (U::words == 8) {  // fp32 values of a bf16 cache
-#pragma unroll
-      for (int k = 0; k < 4; ++k) c[k] = pack_bf16x2(__uint_as_float(w[n][2 * k]), __uint_as_float(w[n][2 * k + 1]));
     } else {
       c = u32x4_t{w[n][0], w[n][1], w[n][2], w[n][3]};
     }
@@ -520,43 +432,154 @@ __device__ __forceinline__ void write_v_row(const KvArgs& K, const KvRows& A, co
   }
 }
 
-// One row of K per wave, turned on the way: 4 values a lane, with those that they are paired with and their angles
-// loaded at once. (16 rows a wave load the units of a row one after another: 256 tokens of 8 heads of 128 took 7.7 us.)
-template <int FMT, class T, Turn TURN>
-__device__ __forceinline__ void write_turned_row(const KvArgs& K, const KvRows& A, const KvTurn& R, const Place& P) {
-  constexpr int BYTES = KvFormat<FMT>::bytes, C = 16 / BYTES;
-  const int lane = threadIdx.x & (WAVE - 1), D = K.D, d = 4 * lane;
-  if (!P.ok) return;
-  const T* src = static_cast<const T*>(A.k) + P.row * A.ldk_t + P.head * A.ldk_h;
-  const int page = page_entry(K, P);
-  float x[4] = {};
-  if (d < D) turned<T, 4, TURN>(R, src, A.vec, P.pos, d, x);
-  uint32_t top = 0;
+// Rows of K that are turned, side by side in a wave: a lane takes 8 values of one, two times 4 that are each other's
+// pairs (of neighbours, and of what is not turned, 8 in a row), so that values, cosines and sines are loaded once.
+// turned_lanes: of a row, as many as a power of two.
+__host__ __device__ inline int turned_lanes(int D) {
+  int lanes = 2;
+  while (lanes * 8 < D) lanes *= 2;
+  return lanes;
+}
+
+template <class T>
+struct TurnedPiece {
+  uint32_t a[sizeof(T)], b[sizeof(T)];  // 4 values each
+  float c[4], s[4];
+};
+
+template <class T, bool NEIGHBOURS>
+__device__ __forceinline__ void piece_places(const KvTurn& R, int piece, int& d0, int& d1) {
+  const bool halves = !NEIGHBOURS && 8 * piece < R.rotary;
+  d0 = halves ? 4 * piece : 8 * piece;
+  d1 = d0 + (halves ? R.rotary / 2 : 4);
+}
+
+template <class T>
+__device__ __forceinline__ void load4(const T* p, uint32_t (&w)[sizeof(T)]) {
+  typedef u32x2_t any8_t __attribute__((aligned(2)));
+  typedef u32x4_t any16_t __attribute__((aligned(4)));
+  if constexpr (sizeof(T) == 2) {
+    const u32x2_t v = *reinterpret_cast<const any8_t*>(p);
+    w[0] = v[0], w[1] = v[1];
+  } else {
+    const u32x4_t v = *reinterpret_cast<const any16_t*>(p);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) top = word_top<float>(top, __float_as_uint(x[i]));
-  const int64_t token = token_in(K, P, page);
-  if (token < 0) return;
-  char* dst = static_cast<char*>(const_cast<void*>(K.k)) + (token & ~(int64_t)15) * D * BYTES +
-              ((d / C * 16 + (int)(token & 15)) * C + d % C) * BYTES;
-  uint32_t c = 0;
-  if constexpr (KvFormat<FMT>::scaled) {
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-    const RowScale S = row_scale<FMT>(quad_top<float>(top));
-    c = quantise4<FMT, float>(x, S);
-    if (lane == 0) const_cast<float*>(K.k_scale)[token] = S.scale;
+    for (int i = 0; i < 4; ++i) w[i] = v[i];
   }
-  if (d >= D) return;
-  if constexpr (BYTES == 1) *reinterpret_cast<uint32_t*>(dst) = c;
-  else if constexpr (BYTES == 2) *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
-  else *reinterpret_cast<f32x4_t*>(dst) = f32x4_t{x[0], x[1], x[2], x[3]};
+}
+
+template <class T, bool NEIGHBOURS>
+__device__ __forceinline__ void load_turned(const KvArgs& K, const KvRows& A, const KvTurn& R, const Place& P, int piece,
+                                            TurnedPiece<T>& t) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T); ++i) t.a[i] = t.b[i] = 0u;
+  if (!P.ok || 8 * piece >= K.D) return;
+  const T* src = static_cast<const T*>(A.k) + P.row * A.ldk_t + P.head * A.ldk_h;
+  int d0, d1;
+  piece_places<T, NEIGHBOURS>(R, piece, d0, d1);
+  load4(src + d0, t.a);
+  load4(src + d1, t.b);
+  if (8 * piece < R.rotary) angles(R, P.pos, 4 * piece, t.c, t.s);
+}
+
+// The largest of 2, 4, 8, 16 or 32 lanes side by side, in all of them.
+__device__ __forceinline__ uint32_t side_top(uint32_t top, int lanes) {
+  top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp(top, 0xb1, 0xf, 0xf, true));                 // lane ^ 1
+  if (lanes > 2) top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp(top, 0x4e, 0xf, 0xf, true));   // lane ^ 2
+  if (lanes > 4) top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp(top, 0x141, 0xf, 0xf, true));  // 8 lanes reversed
+  if (lanes > 8) top = max(top, (uint32_t)__builtin_amdgcn_mov_dpp(top, 0x140, 0xf, 0xf, true));  // 16 lanes reversed
+  if (lanes > 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+    top = max(r[0], r[1]);
+  }
+  return top;
+}
+
+// All lanes of a wave call it; `token` negative: the row is not written.
+template <int FMT, class T, bool NEIGHBOURS>
+__device__ __forceinline__ void write_turned(const KvArgs& K, const KvTurn& R, int64_t token, int lanes, int piece,
+                                             const TurnedPiece<T>& t) {
+  constexpr int BYTES = KvFormat<FMT>::bytes, C = 16 / BYTES;
+  float x[4], y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[i] = word_value<T>(t.a, i);
+    y[i] = word_value<T>(t.b, i);
+  }
+  if (8 * piece < R.rotary) {
+    if constexpr (NEIGHBOURS) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float a = x[2 * i], b = y[2 * i];
+        x[2 * i] = turn_low(a, x[2 * i + 1], t.c[i], t.s[i]);
+        x[2 * i + 1] = turn_high(a, x[2 * i + 1], t.c[i], t.s[i]);
+        y[2 * i] = turn_low(b, y[2 * i + 1], t.c[2 + i], t.s[2 + i]);
+        y[2 * i + 1] = turn_high(b, y[2 * i + 1], t.c[2 + i], t.s[2 + i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = x[i];
+        x[i] = turn_low(a, y[i], t.c[i], t.s[i]);
+        y[i] = turn_high(a, y[i], t.c[i], t.s[i]);
+      }
+    }
+  }
+  uint32_t cx = 0, cy = 0;
+  if constexpr (KvFormat<FMT>::scaled) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = word_top<float>(word_top<float>(top, __float_as_uint(x[i])), __float_as_uint(y[i]));
+    const RowScale S = row_scale<FMT>(side_top(top, lanes));
+    cx = quantise4<FMT, float>(x, S);
+    cy = quantise4<FMT, float>(y, S);
+    if (piece == 0 && token >= 0) const_cast<float*>(K.k_scale)[token] = S.scale;
+  }
+  if (token < 0 || 8 * piece >= K.D) return;
+  char* dst = static_cast<char*>(const_cast<void*>(K.k)) + (token & ~(int64_t)15) * K.D * BYTES;
+  const auto store = [&](int d, uint32_t c, const float (&v)[4]) {
+    char* to = dst + ((d / C * 16 + (int)(token & 15)) * C + d % C) * BYTES;
+    if constexpr (BYTES == 1) *reinterpret_cast<uint32_t*>(to) = c;
+    else if constexpr (BYTES == 2) *reinterpret_cast<u32x2_t*>(to) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    else *reinterpret_cast<f32x4_t*>(to) = f32x4_t{v[0], v[1], v[2], v[3]};
+  };
+  int d0, d1;
+  piece_places<T, NEIGHBOURS>(R, piece, d0, d1);
+  store(d0, cx, x);
+  store(d1, cy, y);
+}
+
+// The rows of a group; all of its loads are in flight at once but for long rows'.
+template <int FMT, class T, bool NEIGHBOURS>
+__device__ __forceinline__ void write_turned_group(const KvArgs& K, const KvRows& A, const KvTurn& R, const Group& G) {
+  const int lane = threadIdx.x & (WAVE - 1), lanes = turned_lanes(K.D);
+  const int piece = lane & (lanes - 1), first = lane / lanes, step = WAVE / lanes;
+  Place at = place_in(G, 0);
+  const int page = page_entry(K, at);
+  for (int r0 = 0; r0 < 16; r0 += 4 * step) {
+    TurnedPiece<T> t[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + i * step + first;
+      Place P = place_in(G, r);
+      P.ok = P.ok && r < 16;
+      load_turned<T, NEIGHBOURS>(K, A, R, P, piece, t[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (r0 + i * step >= 16) break;
+      const int r = r0 + i * step + first;
+      const Place P = place_in(G, r);
+      write_turned<FMT, T, NEIGHBOURS>(K, R, P.ok && r < 16 ? token_in(K, P, page) : -1, lanes, piece, t[i]);
+    }
+  }
 }
 
 template <int FMT, class T>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_groups_kernel(KvArgs K, KvRows A) {
   Place P;
   if (group_place(K, K.q_start, K.T, blockIdx.x, blockIdx.y, blockIdx.z && KvFormat<FMT>::bytes == 1, P))
-    write_rows<FMT, T, true, AS_IT_IS>(K, A, KvTurn{}, blockIdx.z, P);
+    write_rows<FMT, T, true>(K, A, blockIdx.z, P);
 }
 
 // Workgroups [0, for_v) take V, the others K.
@@ -569,27 +592,30 @@ __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_write_rows_kernel(KvArgs K,
     write_v_row<FMT, T>(K, A, P);
   } else {
     row_place(K, K.q_start, K.T, (((int)blockIdx.x - for_v) * RW_WAVES + wv) * 16 + (lane & 15), P);
-    write_rows<FMT, T, false, AS_IT_IS>(K, A, KvTurn{}, false, P);
+    write_rows<FMT, T, false>(K, A, false, P);
   }
 }
 
-constexpr int TURN_HEADS = 4;  // that a lane of the queries' waves takes
+constexpr int TURN_HEADS = 4;  // that a lane of the queries' waves takes, at most
 
 // How the queries' rows are laid over waves: a lane takes one piece of a head, 16 values that make 8 pairs (of
-// neighbours 8, of what is not turned 8 to copy), of TURN_HEADS heads `side` apart.
+// neighbours 8, of what is not turned 8 to copy), of `each` heads `side` apart.
 struct TurnGrid {
   int turned, pieces;  // pieces of a head that are turned, and all (with those to copy)
-  int side;            // heads side by side in a wave
+  int side, each;      // heads side by side in a wave, and of a lane
   int waves;           // of a token
 };
 
-__host__ __device__ inline TurnGrid turn_grid(const KvTurn& R, int D) {
+__host__ __device__ inline TurnGrid turn_grid(const KvTurn& R, int T, int D) {
   TurnGrid g;
   g.turned = R.rotary / (R.interleaved ? 8 : 16);
   const bool same = R.q == R.q_out && R.ldq_t == R.ldo_t && R.ldq_h == R.ldo_h;
   g.pieces = g.turned + (same ? 0 : (D - R.rotary) / 8);
   g.side = WAVE / g.pieces;
-  g.waves = (R.heads + g.side * TURN_HEADS - 1) / (g.side * TURN_HEADS);
+  // few tokens do not fill the card with waves of several heads a lane
+  const int waves = (R.heads + g.side - 1) / g.side;
+  g.each = (int64_t)waves * T <= 4096 ? 1 : TURN_HEADS;
+  g.waves = (waves + g.each - 1) / g.each;
   return g;
 }
 
@@ -598,14 +624,14 @@ template <class T>
 __device__ __forceinline__ void turn_queries(const KvArgs& K, const KvTurn& R, int wave) {
   constexpr int W = 2 * sizeof(T);  // words of 8 values
   const int lane = threadIdx.x & (WAVE - 1);
-  const TurnGrid G = turn_grid(R, K.D);
+  const TurnGrid G = turn_grid(R, K.T, K.D);
   const int token = wave / G.waves;
   if (token >= K.T) return;
   Place P;
   row_place(K, K.q_start, K.T, token * K.H, P);  // (the same in all lanes)
   if (!P.ok || P.pos < 0) return;
   const int at = lane / G.pieces, piece = lane - at * G.pieces;
-  const int head0 = (wave - token * G.waves) * G.side * TURN_HEADS + at;
+  const int head0 = (wave - token * G.waves) * G.side * G.each + at;
   if (at >= G.side) return;
   const T* q = static_cast<const T*>(R.q) + token * R.ldq_t;
   T* out = static_cast<T*>(R.q_out) + token * R.ldo_t;
@@ -618,7 +644,7 @@ __device__ __forceinline__ void turn_queries(const KvArgs& K, const KvTurn& R, i
 #pragma unroll
   for (int n = 0; n < TURN_HEADS; ++n) {
     const int head = head0 + n * G.side;
-    if (head >= R.heads) break;
+    if (n >= G.each || head >= R.heads) break;
     load_words(q + head * R.ldq_h + d, R.q_vec, a[n]);
     if (two) load_words(q + head * R.ldq_h + d + half, R.q_vec, b[n]);
   }
@@ -644,7 +670,7 @@ __device__ __forceinline__ void turn_queries(const KvArgs& K, const KvTurn& R, i
 #pragma unroll
   for (int n = 0; n < TURN_HEADS; ++n) {
     const int head = head0 + n * G.side;
-    if (head >= R.heads) break;
+    if (n >= G.each || head >= R.heads) break;
     T* to = out + head * R.ldo_h + d;
     if (copy) {
       store_words(to, R.q_vec, a[n]);
@@ -679,27 +705,36 @@ __device__ __forceinline__ void turn_queries(const KvArgs& K, const KvTurn& R, i
 }
 
 // As the write kernels, with K turned; workgroups from `rest` on take the queries.
-template <int FMT, class T, Turn TURN>
+template <int FMT, class T, bool NEIGHBOURS>
 __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_groups_kernel(KvArgs K, KvRows A, KvTurn R, int slots, int rest) {
   const int at = blockIdx.x;
   if (at >= rest) return turn_queries<T>(K, R, (at - rest) * RW_WAVES + threadIdx.x / WAVE);
   const bool is_v = at >= rest / 2;
   const int of = is_v ? at - rest / 2 : at, head = of / slots;
-  Place P;
-  if (!group_place(K, K.q_start, K.T, of - head * slots, head, is_v && KvFormat<FMT>::bytes == 1, P)) return;
-  if (is_v) write_rows<FMT, T, true, AS_IT_IS>(K, A, R, true, P);
-  else write_rows<FMT, T, true, TURN>(K, A, R, false, P);
+  Group G;
+  if (!find_group(K, K.q_start, K.T, of - head * slots, head, G)) return;
+  if (!is_v) return write_turned_group<FMT, T, NEIGHBOURS>(K, A, R, G);
+  const int r = threadIdx.x & 15;
+  write_rows<FMT, T, true>(K, A, true, place_in(G, KvFormat<FMT>::bytes == 1 ? place_of(r) : r));
 }
 
-template <int FMT, class T, Turn TURN>
-__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_rows_kernel(KvArgs K, KvRows A, KvTurn R, int rest) {
-  const int wv = threadIdx.x / WAVE, at = blockIdx.x;
+template <int FMT, class T, bool NEIGHBOURS>
+__global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_rows_kernel(KvArgs K, KvRows A, KvTurn R, int for_v, int rest, int side) {
+  const int lane = threadIdx.x & (WAVE - 1), wv = threadIdx.x / WAVE, at = blockIdx.x;
   if (at >= rest) return turn_queries<T>(K, R, (at - rest) * RW_WAVES + wv);
-  const bool is_v = at >= rest / 2;
   Place P;
-  row_place(K, K.q_start, K.T, (is_v ? at - rest / 2 : at) * RW_WAVES + wv, P);
-  if (is_v) write_v_row<FMT, T>(K, A, P);
-  else write_turned_row<FMT, T, TURN>(K, A, R, P);
+  if (at < for_v) {
+    row_place(K, K.q_start, K.T, at * RW_WAVES + wv, P);
+    write_v_row<FMT, T>(K, A, P);
+  } else {
+    const int lanes = turned_lanes(K.D), piece = lane & (lanes - 1), of = lane / lanes;
+    row_place(K, K.q_start, K.T, ((at - for_v) * RW_WAVES + wv) * side + min(of, side - 1), P);
+    P.ok = P.ok && of < side;
+    TurnedPiece<T> t;
+    const int page = P.ok ? page_entry(K, P) : -1;
+    load_turned<T, NEIGHBOURS>(K, A, R, P, piece, t);
+    write_turned<FMT, T, NEIGHBOURS>(K, R, token_in(K, P, page), lanes, piece, t);
+  }
 }
 
 // 16 rows of K (or, grouped, of V) per wave.
@@ -861,31 +896,38 @@ void launch_write(const KvArgs& K, const KvRows& R, int max_q, hipStream_t strea
 }
 
 // Workgroups of an append: of K and V, rows of their own (few new tokens a sequence) or in groups, and of the queries.
+//
+// Rows or groups, measured at 512 sequences of 8 heads of 128 with 32 query heads, us: one new token each bf16 9.5 and
+// 16.7, int8 7.9 and 20.1; two 14.7 and 18.2, 12.7 and 20.8; four 29.7 and 25.8, 22.3 and 26.3; six 34 and 33, 33 and
+// 32. Rows of K one or several a wave: one token 3.1 and 4.1, 225 of 4 heads into e4m3 4.8 and 4.7.
 struct AppendGrid {
   bool rows;
   int slots;  // of groups, a head
-  int64_t rest, for_q;
+  int side;   // rows of K side by side in a wave
+  int64_t for_v, rest, for_q;  // (of rows: those of V, then K's)
 };
-AppendGrid append_grid(const KvArgs& K, const KvTurn& R, int max_q) {
+AppendGrid append_grid(const KvArgs& K, const KvTurn& R, int fmt, int max_q) {
   AppendGrid g{};
   const int64_t rows = (int64_t)K.T * K.H;
-  g.rows = max_q <= 8 && rows <= 0x1000000;
+  g.rows = max_q <= (fmt == SGMV_KV_E4M3 || fmt == SGMV_KV_I8 ? 4 : 2) && rows <= 0x1000000;
   const dim3 d = group_grid(K, K.T);
+  g.side = rows <= 256 ? 1 : WAVE / turned_lanes(K.D);
   g.slots = (int)d.x;
-  g.rest = 2 * (g.rows ? (rows + RW_WAVES - 1) / RW_WAVES : (int64_t)d.x * d.y);
-  g.for_q = R.heads ? ((int64_t)K.T * turn_grid(R, K.D).waves + RW_WAVES - 1) / RW_WAVES : 0;
+  g.for_v = g.rows ? (rows + RW_WAVES - 1) / RW_WAVES : (int64_t)d.x * d.y;
+  g.rest = g.for_v + (g.rows ? (rows + RW_WAVES * g.side - 1) / (RW_WAVES * g.side) : g.for_v);
+  g.for_q = R.heads ? ((int64_t)K.T * turn_grid(R, K.T, K.D).waves + RW_WAVES - 1) / RW_WAVES : 0;
   return g;
 }
 
 template <int FMT, class T>
 void launch_append(const KvArgs& K, const KvRows& A, const KvTurn& R, int max_q, hipStream_t stream) {
-  const AppendGrid g = append_grid(K, R, max_q);
+  const AppendGrid g = append_grid(K, R, FMT, max_q);
   const unsigned all = (unsigned)(g.rest + g.for_q);
   if (g.rows) {
-    const auto kernel = R.interleaved ? kv_append_rows_kernel<FMT, T, NEIGHBOURS> : kv_append_rows_kernel<FMT, T, HALVES>;
-    kernel<<<all, RW_WAVES * WAVE, 0, stream>>>(K, A, R, (int)g.rest);
+    const auto kernel = R.interleaved ? kv_append_rows_kernel<FMT, T, true> : kv_append_rows_kernel<FMT, T, false>;
+    kernel<<<all, RW_WAVES * WAVE, 0, stream>>>(K, A, R, (int)g.for_v, (int)g.rest, g.side);
   } else {
-    const auto kernel = R.interleaved ? kv_append_groups_kernel<FMT, T, NEIGHBOURS> : kv_append_groups_kernel<FMT, T, HALVES>;
+    const auto kernel = R.interleaved ? kv_append_groups_kernel<FMT, T, true> : kv_append_groups_kernel<FMT, T, false>;
     kernel<<<all, RW_WAVES * WAVE, 0, stream>>>(K, A, R, g.slots, (int)g.rest);
   }
 }
@@ -910,8 +952,8 @@ hipError_t launch_kv_write(const KvArgs& K, const KvRows& R, int fmt, int max_q,
 }
 
 // Waves of an append's launch.
-int64_t kv_append_waves(const KvArgs& K, const KvTurn& R, int max_q) {
-  const AppendGrid g = append_grid(K, R, max_q);
+int64_t kv_append_waves(const KvArgs& K, const KvTurn& R, int fmt, int max_q) {
+  const AppendGrid g = append_grid(K, R, fmt, max_q);
   return (g.rest + g.for_q) * RW_WAVES;
 }
 

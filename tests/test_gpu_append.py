@@ -55,6 +55,12 @@ APPENDS = {
     "more_new_than_tokens": ([6, 4], [2, 0], 16, 2, 4, 64, 32, E4M3, BF16),
     "more_new_than_tokens_chunk": ([60, 40], [20, 0], 16, 2, 4, 64, 64, I8, BF16),
     "many_sequences": ([1, 0, 2] * 50, [9, 4, 40] * 50, 16, 1, 3, 32, 32, I8, BF16),
+    "chunk_16_i8": ([9, 33], [20, 33], 16, 2, 3, 16, 16, I8, BF16),
+    "chunk_32_e4m3": ([30, 5, 1], [64, 5, 9], 32, 3, 3, 32, 16, E4M3, F32),
+    "four_new_i8": ([4, 3, 1, 4] * 9, [4, 40, 17, 19] * 9, 16, 8, 8, 128, 96, I8, BF16),
+    "two_new_bf16": ([2, 1] * 20, [40, 3] * 20, 16, 7, 14, 48, 32, BF16, BF16),
+    "many_rows_f32_256": ([1] * 90, [19, 64, 5] * 30, 16, 3, 3, 256, 240, F32, F32),
+    "many_tokens": ([700, 500], [700, 800], 64, 1, 32, 128, 128, E4M3, BF16),
     "no_queries": ([1, 20], [9, 40], 16, 2, 0, 64, 64, BF16, BF16),
 }
 
