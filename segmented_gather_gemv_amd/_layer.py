@@ -195,10 +195,12 @@ class BaseWeight:
     dtype: torch.dtype            # of x and y
     ref: object = field(init=False, repr=False)  # what the library takes
     index: int = field(init=False, repr=False)   # of the GPU, -1: not on one
+    few: int = field(init=False, repr=False)     # rows that take no workspace
 
     def __post_init__(self):
         self.N, self.K, self.group, self.format = self.desc.N, self.desc.K, self.desc.group, self.desc.format
         self.ref, self.index = ctypes.byref(self.desc), self.codes.get_device()
+        self.few = 16 if self.dtype is torch.float32 else 32
 
 
 def sgmv_base_pack(codes: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor] = None,
@@ -264,7 +266,7 @@ def sgmv_base_product(x: torch.Tensor, base: BaseWeight, y: Optional[torch.Tenso
     if index < 0:
         raise ValueError("the kernels run on GPU tensors")
     size, ptr = 0, None
-    if T > 32 or n_split:  # (none for fewer rows)
+    if T > base.few or n_split:
         need = ctypes.c_size_t()
         st = _lib.sgmv_base_product_workspace(T, base.ref, n_split, ctypes.byref(need))
         if st != SGMV_OK:

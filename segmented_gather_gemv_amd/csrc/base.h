@@ -7,7 +7,7 @@
 //   I4    c is an e4m3 code as it stands (a number below 16 in the low bits of a byte is c 2^-9), so that two codes
 //         become two exact bf16 by one instruction: y += s (sum c x - z sum x), with sum x from a product by ones.
 //   E2M1  the scale is a power of two, which the conversion applies: the operand is the weight itself, exact.
-// fp32 rows are split into three bf16 (24 bits), of I4 with c - z as the operand.
+// fp32 rows are split into three bf16 (24 bits); of few rows and I4 with c - z as the operand.
 #pragma once
 
 #include <type_traits>
@@ -51,7 +51,7 @@ struct BasePackArgs {
 constexpr int TILE_T = 64;
 constexpr int TILE_N = 256;
 
-hipError_t launch_base_tiled(const BaseArgs& A, int format, int s, hipStream_t stream);
+hipError_t launch_base_tiled(const BaseArgs& A, int format, int dtype, int s, hipStream_t stream);
 hipError_t launch_base_pack(const BasePackArgs& A, hipStream_t stream);
 hipError_t launch_base_direct_i4(const BaseArgs& A, int s, hipStream_t stream);
 hipError_t launch_base_direct_i4z(const BaseArgs& A, int s, hipStream_t stream);

@@ -9,6 +9,8 @@
 //   I4    a group's sum is kept apart and scaled at its end: part = c x - z sum x, y += s part; sum x over the groups
 //         comes from a first launch (of each wave by products with ones, it would be a fifth of all products).
 //   E2M1  sums go straight on.
+//   fp32  rows are three bf16 parts, small ones first, each a block of its own over the same codes: three times the
+//         products, and the same kernel.
 // Where that leaves compute units without a tile, K is split into ranges whose sums a last launch adds up.
 #include "base.h"
 
@@ -26,9 +28,9 @@ constexpr int block_bytes(int sums) { return TILE_T * (BASE_K * 2 + sums * 4); }
 // Rows of x as the tiles stage them: blocks of 64 rows and 128 k, 256 bytes a row whose pieces of 16 are exchanged
 // within it, zeros past the last row and the last k; and behind them the sums over each 128 / S values of the rows. Four
 // rows of a block per wave.
-template <bool SUMS, int S>
+template <bool F32, bool SUMS, int S>
 __global__ __launch_bounds__(256) void base_rows_kernel(BaseArgs A) {
-  constexpr int BLOCK_BYTES = block_bytes(SUMS ? S : 0);
+  constexpr int BLOCK_BYTES = block_bytes(SUMS ? S : 0), PARTS = F32 ? 3 : 1, E = F32 ? 4 : 2;
   const int lane = threadIdx.x & (WAVE - 1), r = lane & 15;
   const int64_t rows = (int64_t)((A.T + TILE_T - 1) / TILE_T) * TILE_T;
   const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / WAVE;  // of a tile, block by block its 16 quads of rows
@@ -37,19 +39,35 @@ __global__ __launch_bounds__(256) void base_rows_kernel(BaseArgs A) {
   if (band * TILE_T >= rows) return;
   const int64_t row = band * TILE_T + t;
   const int k = kb * BASE_K + 8 * r, left = row < A.T ? A.K - k : 0;
-  const char* p = static_cast<const char*>(A.x) + (row * A.ldx + k) * 2;
-  u32x4_t v = {0u, 0u, 0u, 0u};
-  if (left >= 8) v = load_row<false>(p);
-  else if (left > 0) v = load_rest<false>(p, left);
-  *reinterpret_cast<u32x4_t*>(A.rows + block * BLOCK_BYTES + t * 256 + (r ^ (t & 15)) * 16) = v;
-  if constexpr (SUMS) {
+  const char* p = static_cast<const char*>(A.x) + (row * A.ldx + k) * E;
+  u32x4_t v[E / 2];
+#pragma unroll
+  for (int h = 0; h < E / 2; ++h) {
+    const int n = left - 4 * h;  // (of fp32 4 values a piece)
+    v[h] = u32x4_t{0u, 0u, 0u, 0u};
+    if (n >= (F32 ? 4 : 8)) v[h] = load_row<F32>(p + 16 * h);
+    else if (n > 0) v[h] = load_rest<F32>(p + 16 * h, n);
+  }
+  char* to = A.rows + block * PARTS * BLOCK_BYTES;
+  bf16x8_t part[PARTS];
+  if constexpr (F32) split3(v, part);
+  else part[0] = as_bf16x8(v[0]);
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i)
+    *reinterpret_cast<u32x4_t*>(to + i * BLOCK_BYTES + t * 256 + (r ^ (t & 15)) * 16) = __builtin_bit_cast(u32x4_t, part[PARTS - 1 - i]);
+  if constexpr (SUMS) {  // with the last part
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) sum += __uint_as_float(v[i] << 16) + __uint_as_float(v[i] & 0xffff0000u);
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (F32) sum += __uint_as_float(v[i / 4][i % 4]);
+      else sum += __uint_as_float(i & 1 ? v[0][i / 2] & 0xffff0000u : v[0][i / 2] << 16);
+    }
 #pragma unroll
     for (int o = 1; o < 16 / S; o <<= 1) sum += __shfl_xor(sum, o);
     if (r % (16 / S) == 0)
-      *reinterpret_cast<float*>(A.rows + block * BLOCK_BYTES + TILE_T * BASE_K * 2 + ((r / (16 / S)) * TILE_T + t) * 4) = sum;
+#pragma unroll
+      for (int i = 0; i < PARTS; ++i)
+        *reinterpret_cast<float*>(to + i * BLOCK_BYTES + TILE_T * BASE_K * 2 + ((r / (16 / S)) * TILE_T + t) * 4) = i == PARTS - 1 ? sum : 0.f;
   }
 }
 
@@ -70,10 +88,23 @@ __device__ __forceinline__ bool tile_place(const BaseArgs& A, int block, TilePla
   return true;
 }
 
-// 16 rows and 64 columns of a wave's results as rows of y, through its 2 KB of LDS (16-byte pieces exchanged within the
+// 16 rows and 64 columns of a wave's results as rows of y: fp32 straight from its registers (64 bytes a row at once),
+// bf16 through its 2 KB of LDS (16-byte pieces exchanged within the
 // rows of 128, as above).
+template <bool F32>
 __device__ __forceinline__ void store_tile(const BaseArgs& A, char* own, int t0, int n0, const f32x4_t (&acc)[TN]) {
   const int lane = threadIdx.x & (WAVE - 1), r = lane & 15, quad = lane >> 4;
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + 4 * quad + i;
+      float* y = static_cast<float*>(A.y) + (int64_t)t * A.ldy + n0 + r;
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+        if (t < A.T && n0 + 16 * n + r < A.N) y[16 * n] = acc[n][i];
+    }
+    return;
+  }
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int n = 0; n < TN; ++n)
@@ -106,6 +137,7 @@ __device__ __forceinline__ float* part_of(const BaseArgs& A, int tiles, int spli
 }
 
 // Sum of the parts of 16 rows and 64 columns, in the splits' order.
+template <bool F32>
 __global__ __launch_bounds__(TW* WAVE) void base_join_kernel(BaseArgs A) {
   __shared__ alignas(16) char s_y[TW][16 * 128];
   const int lane = threadIdx.x & (WAVE - 1), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
@@ -132,14 +164,15 @@ __global__ __launch_bounds__(TW* WAVE) void base_join_kernel(BaseArgs A) {
 #pragma unroll
         for (int n = 0; n < TN; ++n) acc[n] += v[i][n];
   }
-  store_tile(A, s_y[wv], p.t0 + 16 * m, p.n0 + wv * (16 * TN), acc);
+  store_tile<F32>(A, s_y[wv], p.t0 + 16 * m, p.n0 + wv * (16 * TN), acc);
 }
 
 // Workgroup barrier behind this wave's LDS accesses, with its loads from memory left in flight.
 __device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <bool E2M1, bool ZERO, int S>
+template <bool E2M1, bool F32, bool ZERO, int S>
 __global__ __launch_bounds__(TW* WAVE, 2) void base_tiled_kernel(BaseArgs A) {
+  constexpr int PARTS = F32 ? 3 : 1;  // steps of a block
   constexpr int BLOCK_BYTES = block_bytes(E2M1 ? 0 : S), ROW_BYTES = TILE_T * BASE_K * 2;
   __shared__ alignas(16) char s_x[2][BLOCK_BYTES];
   const int lane = threadIdx.x & (WAVE - 1), wv = __builtin_amdgcn_readfirstlane(threadIdx.x / WAVE);
@@ -150,25 +183,25 @@ __global__ __launch_bounds__(TW* WAVE, 2) void base_tiled_kernel(BaseArgs A) {
   TilePlace place;
   if (!tile_place(A, blockIdx.x - split * run, place)) return;
   const int t0 = place.t0, n0 = place.n0 + wv * (16 * TN);
-  const int kb0 = split * A.split_blocks, kb1 = min(kb0 + A.split_blocks, A.blocks);
+  const int kb0 = split * A.split_blocks * PARTS, kb1 = min((split + 1) * A.split_blocks, A.blocks) * PARTS;
 
   int64_t tile[TN];  // (columns past the last ones are those again, and not stored)
 #pragma unroll
   for (int n = 0; n < TN; ++n) tile[n] = min(n0 / 16 + n, tiles - 1);
-  const char* const x = A.rows + (int64_t)(t0 / TILE_T) * A.blocks * BLOCK_BYTES;
+  const char* const x = A.rows + (int64_t)(t0 / TILE_T) * A.blocks * PARTS * BLOCK_BYTES;
 
   struct Weights {
     u32x4_t w[TN];
-    BaseScale<E2M1, false, S> s[TN];
+    BaseScale<E2M1, F32, S> s[TN];
     BaseZero<ZERO, S> z[TN];
   };
-  const auto load_weights = [&](int kb, Weights& b) {
-    const int row = kb / A.per_group;
+  const auto load_weights = [&](int step, Weights& b) {
+    const int kb = step / PARTS, row = kb / A.per_group;
 #pragma unroll
     for (int n = 0; n < TN; ++n) b.w[n] = static_cast<const u32x4_t*>(A.codes)[(tile[n] * A.blocks + kb) * WAVE + lane];
 #pragma unroll
     for (int n = 0; n < TN; ++n) {
-      b.s[n] = BaseScale<E2M1, false, S>::load(A.scale, tile[n] * A.scale_rows + row, r);
+      b.s[n] = BaseScale<E2M1, F32, S>::load(A.scale, tile[n] * A.scale_rows + row, r);
       if constexpr (!E2M1) b.z[n] = BaseZero<ZERO, S>::load(A.zero, tile[n] * A.scale_rows + row, r);
     }
   };
@@ -279,39 +312,40 @@ __global__ __launch_bounds__(TW* WAVE, 2) void base_tiled_kernel(BaseArgs A) {
     f32x4_t out[TN];
 #pragma unroll
     for (int n = 0; n < TN; ++n) out[n] = acc[n][m];
-    store_tile(A, s_x[0] + (wv * TT + m) * (16 * 128), t0 + 16 * m, n0, out);
+    store_tile<F32>(A, s_x[0] + (wv * TT + m) * (16 * 128), t0 + 16 * m, n0, out);
   }
 }
 
-template <bool E2M1, bool ZERO, int S>
+template <bool E2M1, bool F32, bool ZERO, int S>
 hipError_t launch(const BaseArgs& A, hipStream_t stream) {
-  const int64_t n = ((int64_t)((A.T + TILE_T - 1) / TILE_T) * ((A.N + TILE_N - 1) / TILE_N) + 7) / 8 * 8;
-  base_tiled_kernel<E2M1, ZERO, S><<<(unsigned)(n * A.splits), TW * WAVE, 0, stream>>>(A);
-  if (A.splits > 1) base_join_kernel<<<(unsigned)(n * TT), TW * WAVE, 0, stream>>>(A);
+  const int64_t bands = (A.T + TILE_T - 1) / TILE_T, n = (bands * ((A.N + TILE_N - 1) / TILE_N) + 7) / 8 * 8;
+  base_rows_kernel<F32, !E2M1, S><<<(unsigned)(bands * A.blocks * TT), 256, 0, stream>>>(A);
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  base_tiled_kernel<E2M1, F32, ZERO, S><<<(unsigned)(n * A.splits), TW * WAVE, 0, stream>>>(A);
+  err = hipGetLastError();
+  if (err != hipSuccess || A.splits == 1) return err;
+  base_join_kernel<F32><<<(unsigned)(n * TT), TW * WAVE, 0, stream>>>(A);
   return hipGetLastError();
 }
 
-template <bool ZERO>
+template <bool F32, bool ZERO>
 hipError_t launch_i4(const BaseArgs& A, int s, hipStream_t stream) {
-  return s == 4 ? launch<false, ZERO, 4>(A, stream) : s == 2 ? launch<false, ZERO, 2>(A, stream) : launch<false, ZERO, 1>(A, stream);
+  return s == 4   ? launch<false, F32, ZERO, 4>(A, stream)
+         : s == 2 ? launch<false, F32, ZERO, 2>(A, stream)
+                  : launch<false, F32, ZERO, 1>(A, stream);
 }
 
-hipError_t launch_rows(const BaseArgs& A, int format, int s, hipStream_t stream) {
-  const unsigned g = (unsigned)((A.T + TILE_T - 1) / TILE_T) * (unsigned)A.blocks * TT;
-  if (format == SGMV_BASE_E2M1) base_rows_kernel<false, 4><<<g, 256, 0, stream>>>(A);
-  else if (s == 4) base_rows_kernel<true, 4><<<g, 256, 0, stream>>>(A);
-  else if (s == 2) base_rows_kernel<true, 2><<<g, 256, 0, stream>>>(A);
-  else base_rows_kernel<true, 1><<<g, 256, 0, stream>>>(A);
-  return hipGetLastError();
+template <bool F32>
+hipError_t launch_format(const BaseArgs& A, int format, int s, hipStream_t stream) {
+  if (format == SGMV_BASE_E2M1) return launch<true, F32, false, 4>(A, stream);
+  return A.zero ? launch_i4<F32, true>(A, s, stream) : launch_i4<F32, false>(A, s, stream);
 }
 
 }  // namespace
 
-hipError_t launch_base_tiled(const BaseArgs& A, int format, int s, hipStream_t stream) {
-  const hipError_t err = launch_rows(A, format, s, stream);
-  if (err != hipSuccess) return err;
-  if (format == SGMV_BASE_E2M1) return launch<true, false, 4>(A, stream);
-  return A.zero ? launch_i4<true>(A, s, stream) : launch_i4<false>(A, s, stream);
+hipError_t launch_base_tiled(const BaseArgs& A, int format, int dtype, int s, hipStream_t stream) {
+  return dtype == SGMV_F32 ? launch_format<true>(A, format, s, stream) : launch_format<false>(A, format, s, stream);
 }
 
 }  // namespace sgmv

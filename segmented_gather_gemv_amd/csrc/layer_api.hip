@@ -64,22 +64,30 @@ struct BasePlan {
   size_t rows, parts;  // floats of workspace
 };
 
-// The tiled kernel from 1e10 products on: it converts each code for 64 rows, not 16 or 32, and has its rows prepared in a
-// launch of its own (128 rows, 8192 x 8192, I4: 36 us in 4 ranges, direct 35; 256: 52 and 67; 512: 89 and 130; 128
-// over 4096 x 4096: 25 and 11). Its tiles fill the card from 256 on; of fewer, K is split into up to 8 ranges of 8
-// blocks and more (256 rows: 81 us in 1, 56 in 2, 52 in 4, 64 in 8; 1024 over 4096 x 4096, 256 tiles: 49 us in 1, 54 in 2).
+// The tiled kernel converts each code for 64 rows, not 16 or 32, but has its rows prepared in a launch of its own and
+// takes few workgroups: for bf16 rows, from 160 full tiles or 1e10 products on, for fp32 ones from 32 or 1.2e9. Measured
+// (tiles in their best number of ranges, direct; us): bf16, I4: 1000 rows, 4096 x 1024: 20 and 31, 3008 x 1408: 23 and 29,
+// 400 rows, 4096 x 1024: 17 and 16, 2000 rows, 1024 x 4096: 40 and 37, 128 rows, 8192 x 8192: 36 and 35, 256: 52 and 67,
+// 512: 89 and 130; fp32: 1000 rows, 4096 x 1024: 39 and 184, 200 rows, 2527 x 313: 17 and 20, 4096 x 4096: 100 rows 35
+// and 60, 64 rows 33 and 37, 32 rows 31 and 20; 24 rows, 11136 x 14592: 98 and 144, 16: 97 and 85.
+//
+// Tiles fill the card from 256 on; of fewer, K is split into up to 8 ranges of 8 steps and more (256 rows, 8192 x 8192:
+// 81 us in 1, 56 in 2, 52 in 4, 64 in 8; 1024 over 4096 x 4096, 256 tiles: 49 us in 1, 54 in 2).
 BasePlan base_plan(int32_t T, const sgmv_base& b, int32_t n_split) {
   const BaseShape h = base_shape(b);
   BasePlan p{};
   p.splits = 1;
-  if (b.dtype != SGMV_BF16 || (!n_split && (T <= 32 || (double)T * b.N * b.K < 1e10))) return p;
+  const bool f32 = b.dtype == SGMV_F32;
+  const double area = (double)T * b.N, full = (double)TILE_T * TILE_N;
+  if (!n_split && (f32 ? T <= 16 || (area < 32 * full && area * b.K < 1.2e9) : T <= 32 || (area < 160 * full && area * b.K < 1e10)))
+    return p;
   p.tiled = true;
-  const int64_t bands = ceil_div(T, TILE_T), tiles = bands * ceil_div(b.N, TILE_N);
+  const int64_t bands = ceil_div(T, TILE_T), tiles = bands * ceil_div(b.N, TILE_N), steps = h.blocks * (f32 ? 3 : 1);
   if (n_split) p.splits = n_split;
-  else if (tiles < 256) p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, 8, h.blocks / 8}));
+  else if (tiles < 256) p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, 8, steps / 8}));
   p.split_blocks = (int32_t)ceil_div(h.blocks, p.splits);
   p.splits = (int32_t)ceil_div(h.blocks, p.split_blocks);
-  p.rows = (size_t)bands * TILE_T * h.blocks * (BASE_K / 2 + (b.format == SGMV_BASE_I4 ? h.s : 0));
+  p.rows = (size_t)bands * TILE_T * h.blocks * (f32 ? 3 : 1) * (BASE_K / 2 + (b.format == SGMV_BASE_I4 ? h.s : 0));
   if (p.splits > 1) p.parts = (size_t)p.splits * tiles * TILE_T * TILE_N;
   return p;
 }
@@ -148,7 +156,6 @@ sgmv_status sgmv_base_product_workspace(int32_t T, const sgmv_base* b, int32_t n
   if (!bytes || T < 0 || n_split < 0 || n_split > SGMV_BASE_MAX_SPLITS) return SGMV_EINVAL;
   const sgmv_status st = base_ok(b);
   if (st != SGMV_OK) return st;
-  if (n_split && b->dtype == SGMV_F32) return SGMV_EUNSUPPORTED;
   const BasePlan p = base_plan(T, *b, n_split);
   *bytes = (p.rows + p.parts) * sizeof(float);
   return SGMV_OK;
@@ -177,7 +184,7 @@ sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, const sgmv_
     if ((bands * ceil_div(b->N, TILE_N) + 8) * 4 * std::max(p.splits, TILE_T / 16) > MOST_WAVES ||
         bands * h.blocks * (TILE_T / 4) > MOST_WAVES)
       return SGMV_EUNSUPPORTED;
-    return launched(launch_base_tiled(A, b->format, (int)h.s, s));
+    return launched(launch_base_tiled(A, b->format, b->dtype, (int)h.s, s));
   }
   if (ceil_div(T, 16) * h.tiles * 16 > MOST_WAVES) return SGMV_EUNSUPPORTED;
   return launched(f32                           ? launch_base_direct_f32(A, b->format, (int)h.s, s)

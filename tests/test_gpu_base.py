@@ -65,7 +65,7 @@ def test_product_against_oracle(sg, N, K, fmt, group, zero, dtype):
     for T in (1, 2, 16, 17, 40):
         x = torch.randn(T, K, generator=g).to(dtype)
         w.check(sg.sgmv_base_product(x.to(DEV), w.packed), x)
-        for n in (1, 3) if dtype == BF16 and T in (1, 40) else ():  # in tiles, K in ranges
+        for n in (1, 3) if T in (1, 40) else ():  # in tiles, K in ranges
             w.check(sg.sgmv_base_product(x.to(DEV), w.packed, n_split=n), x)
 
 
@@ -76,17 +76,20 @@ def test_product_of_many_rows(sg, T, fmt, group, zero, dtype):
     N, K = (331, 700) if T % 2 else (384, 640)
     w = Weight(sg, N, K, fmt, dtype, group, zero)
     x = torch.randn(T, K, generator=torch.Generator().manual_seed(T)).to(dtype)
-    for n in (0, 1, 2, 16) if dtype == BF16 else (0,):
+    for n in (0, 1, 2, 16):
         w.check(sg.sgmv_base_product(x.to(DEV), w.packed, n_split=n), x)
 
 
 @pytest.mark.parametrize("T,N,K,fmt,group,zero", [(200, 5000, 10050, "e2m1", 32, False), (260, 8200, 4700, "i4", 128, True),
-                                                  (2100, 2048, 2400, "i4", 64, False)])
+                                                  (2100, 2048, 2400, "i4", 64, False), (1500, 1790, 300, "i4", 32, True),
+                                                  (300, 1801, 1100, "i4f32", 64, True), (600, 900, 333, "e2m1f32", 32, False),
+                                                  (17, 9000, 8000, "i4f32", 128, False)])
 def test_product_as_the_library_chooses(sg, T, N, K, fmt, group, zero):
     """Sizes that go to the tiles by themselves, with and without ranges."""
-    w = Weight(sg, N, K, fmt, BF16, group, zero)
+    dtype, fmt = F32 if fmt.endswith("f32") else BF16, fmt.replace("f32", "")
+    w = Weight(sg, N, K, fmt, dtype, group, zero)
     assert sg.sgmv_base_product_workspace(T, w.packed) > 0
-    x = torch.randn(T, K, generator=torch.Generator().manual_seed(T)).to(BF16)
+    x = torch.randn(T, K, generator=torch.Generator().manual_seed(T)).to(dtype)
     y = sg.sgmv_base_product(x.to(DEV), w.packed)
     w.check(y, x)
     need = sg.sgmv_base_product_workspace(T, w.packed)

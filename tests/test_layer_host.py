@@ -128,7 +128,6 @@ def test_base_calls_refuse():
     assert lib.sgmv_base_product_workspace(3, ctypes.byref(_base()), 0, None) == E
     for kw in (dict(x=None), dict(y=None), dict(ldx=299), dict(ldy=39), dict(T=-1), dict(n_split=-1), dict(n_split=17)):
         assert product(**kw) == E, kw
-    assert product(b=_base(dtype=sg.SGMV_F32), n_split=1) == UNS
     assert product(T=0, x=None, y=None) == OK
     assert lib.sgmv_base_product_workspace(0, ctypes.byref(_base()), 0, ctypes.byref(need)) == OK and need.value == 0
 
@@ -146,6 +145,7 @@ def test_base_workspace():
     assert size(65, 2, N=257) == 2 * 3 * (16384 + 64 * 2 * 4) + 2 * 2 * 2 * 64 * 256 * 4
     assert size(65, 16) == size(65, 3)  # three blocks of K
     assert size(64, 1, format=sg.BASE_E2M1, group=32, has_zero=0, zero=0) == 3 * 16384
+    assert size(64, 1, dtype=sg.SGMV_F32) == 3 * 3 * (16384 + 64 * 2 * 4)  # in three parts each
     big = dict(N=8192, K=8192, group=128)
     assert size(32, **big) == 0 and size(128, **big) == 0 and size(1024, **big) == 16 * 64 * (16384 + 64 * 4)
     assert size(256, **big) == 4 * 64 * (16384 + 64 * 4) + 4 * 128 * 64 * 256 * 4
