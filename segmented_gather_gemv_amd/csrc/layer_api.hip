@@ -72,7 +72,8 @@ struct BasePlan {
 // and 60, 64 rows 33 and 37, 32 rows 31 and 20; 24 rows, 11136 x 14592: 98 and 144, 16: 97 and 85.
 //
 // Tiles fill the card from 256 on; of fewer, K is split into up to 8 ranges of 8 steps and more (256 rows, 8192 x 8192:
-// 81 us in 1, 56 in 2, 52 in 4, 64 in 8; 1024 over 4096 x 4096, 256 tiles: 49 us in 1, 54 in 2).
+// 81 us in 1, 56 in 2, 52 in 4, 64 in 8; 1024 over 4096 x 4096, 256 tiles: 49 us in 1, 54 in 2); of fp32 rows into up to
+// 16 of 12 steps (202 rows, 732 x 15403: 113 us in 8, 75 in 16; 100 rows, 4096 x 4096: 34 in 8, 37 in 16).
 BasePlan base_plan(int32_t T, const sgmv_base& b, int32_t n_split) {
   const BaseShape h = base_shape(b);
   BasePlan p{};
@@ -84,7 +85,10 @@ BasePlan base_plan(int32_t T, const sgmv_base& b, int32_t n_split) {
   p.tiled = true;
   const int64_t bands = ceil_div(T, TILE_T), tiles = bands * ceil_div(b.N, TILE_N), steps = h.blocks * (f32 ? 3 : 1);
   if (n_split) p.splits = n_split;
-  else if (tiles < 256) p.splits = (int32_t)std::max<int64_t>(1, std::min<int64_t>({512 / tiles, 8, steps / 8}));
+  else if (tiles < 256) {
+    const int64_t most = std::max(std::min<int64_t>(8, steps / 8), f32 ? std::min<int64_t>(SGMV_BASE_MAX_SPLITS, steps / 12) : 1);
+    p.splits = (int32_t)std::max<int64_t>(1, std::min(512 / tiles, most));
+  }
   p.split_blocks = (int32_t)ceil_div(h.blocks, p.splits);
   p.splits = (int32_t)ceil_div(h.blocks, p.split_blocks);
   p.rows = (size_t)bands * TILE_T * h.blocks * (f32 ? 3 : 1) * (BASE_K / 2 + (b.format == SGMV_BASE_I4 ? h.s : 0));
