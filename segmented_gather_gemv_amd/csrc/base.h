@@ -7,7 +7,7 @@
 //   I4    c is an e4m3 code as it stands (a number below 16 in the low bits of a byte is c 2^-9), so that two codes
 //         become two exact bf16 by one instruction: y += s (sum c x - z sum x), with sum x from a product by ones.
 //   E2M1  the scale is a power of two, which the conversion applies: the operand is the weight itself, exact.
-// fp32 rows are split into three bf16 (24 bits); of few rows and I4 with c - z as the operand.
+// fp32 rows are split into three bf16 (24 bits).
 #pragma once
 
 #include <type_traits>
@@ -73,17 +73,6 @@ __device__ __forceinline__ u32x4_t base_floats(uint32_t w, float scale) {
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2)),
                  __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3))};
-}
-
-// Eight codes less their zero point, as bf16 (exact: whole numbers below 16).
-__device__ __forceinline__ u32x4_t base_less(u32x4_t c, float zero) {
-  u32x4_t r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = __uint_as_float(c[i] << 16) - zero, b = __uint_as_float(c[i] & 0xffff0000u) - zero;
-    r[i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
-  }
-  return r;
 }
 
 // The scales of one row of 16 n, kept as they were loaded (what converts them waits for them); E2M1's as what the

@@ -12,7 +12,7 @@ namespace sgmv {
 // Waves per SIMD to allocate registers for: two workgroups per compute unit where their rows' registers leave room.
 constexpr int base_occupancy(bool zero, bool f32, int nt, int tm, int waves, bool staged) {
   if (f32) return waves / 4;
-  return !staged && !zero ? 8 : waves / 4;
+  return !staged && !zero ? 8 : waves >= 8 ? waves / 4 : 2;
 }
 
 template <bool E2M1, bool F32, bool ZERO, int S, int NT, int TM, int WAVES, bool STAGED>
@@ -106,13 +106,14 @@ __global__ __launch_bounds__(WAVES* WAVE, base_occupancy(ZERO, F32, NT, TM, WAVE
           if constexpr (F32) split3(rows.x[m][j], p[m]);
           else if constexpr (STAGED) p[m][0] = as_bf16x8(load_u32x4(own + (16 * m + r) * 256 + ((4 * j + quad) ^ r) * 16));
           else p[m][0] = as_bf16x8(rows.x[m][j][0]);
-          if constexpr (!E2M1 && !F32) sum[m] = mfma_16x16x32_bf16(p[m][0], ones, sum[m]);
+          if constexpr (!E2M1)
+#pragma unroll
+            for (int k = (F32 ? 3 : 1) - 1; k >= 0; --k) sum[m] = mfma_16x16x32_bf16(p[m][k], ones, sum[m]);
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           u32x4_t w;
           if constexpr (E2M1) w = base_floats(b.w[n][j], b.s[n].get(g));
-          else if constexpr (F32) w = base_less(base_codes(b.w[n][j]), b.z[n].get(g));
           else w = base_codes(b.w[n][j]);
 #pragma unroll
           for (int m = 0; m < TM; ++m)
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(WAVES* WAVE, base_occupancy(ZERO, F32, NT, TM, WAVE
           for (int m = 0; m < TM; ++m)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float v = F32 ? part[n][m][i] : fmaf(-b.z[n].get(g), sum[m][i], part[n][m][i]);
+              const float v = fmaf(-b.z[n].get(g), sum[m][i], part[n][m][i]);
               acc[n][m][i] = fmaf(b.s[n].get(g), v, acc[n][m][i]);
             }
     }
@@ -208,25 +209,25 @@ hipError_t launch_base(const BaseArgs& A, hipStream_t stream) {
 
 // The instance of a call: the more columns and rows a workgroup takes, the less often rows of x are read and codes
 // converted; but each compute unit wants a workgroup of its own, the weight's bytes having to be in flight. So the
-// most that leaves 256 of them: 16 columns and rows where nothing does.
+// smallest whose workgroups run at once, one on each of 256 units, or the largest.
 template <bool E2M1, bool F32, bool ZERO, int S>
 hipError_t launch_base_rows(const BaseArgs& A, hipStream_t stream) {
   const int64_t tiles = (A.N + BASE_N - 1) / BASE_N;
+  const auto at_once = [&](int nt, int tm) { return (tiles + nt - 1) / nt * ((A.T + 16 * tm - 1) / (16 * tm)) <= 256; };
   if constexpr (F32) {
-    return launch_base<E2M1, F32, ZERO, S, 1, 1, 16, false>(A, stream);
+    if (at_once(1, 1)) return launch_base<E2M1, F32, ZERO, S, 1, 1, 16, false>(A, stream);
+    if (at_once(2, 1)) return launch_base<E2M1, F32, ZERO, S, 2, 1, 16, false>(A, stream);
+    return launch_base<E2M1, F32, ZERO, S, 4, 1, 8, false>(A, stream);
   } else if (A.T <= 4) {
     if (tiles >= 512) return launch_base<E2M1, F32, ZERO, S, 2, 1, 16, false>(A, stream);
     return launch_base<E2M1, F32, ZERO, S, 1, 1, 16, false>(A, stream);
   } else {
-    const int64_t by_16 = (A.T + 15) / 16, by_32 = (A.T + 31) / 32;
-    if (A.T > 16) {
-      if (tiles / 4 * by_32 >= 256) return launch_base<E2M1, F32, ZERO, S, 4, 2, 8, true>(A, stream);
-      if (tiles / 2 * by_32 >= 256) return launch_base<E2M1, F32, ZERO, S, 2, 2, 8, true>(A, stream);
-    } else if (tiles >= 1024) {
-      return launch_base<E2M1, F32, ZERO, S, 4, 1, 8, true>(A, stream);
-    }
-    if (tiles / 2 * by_16 >= 256) return launch_base<E2M1, F32, ZERO, S, 2, 1, 16, true>(A, stream);
-    return launch_base<E2M1, F32, ZERO, S, 1, 1, 16, true>(A, stream);
+    if (at_once(1, 1)) return launch_base<E2M1, F32, ZERO, S, 1, 1, 16, true>(A, stream);
+    if (at_once(2, 1)) return launch_base<E2M1, F32, ZERO, S, 2, 1, 16, true>(A, stream);
+    if (A.T <= 16) return launch_base<E2M1, F32, ZERO, S, 4, 1, 8, true>(A, stream);
+    if (at_once(2, 2)) return launch_base<E2M1, F32, ZERO, S, 2, 2, 8, true>(A, stream);
+    if (at_once(4, 2)) return launch_base<E2M1, F32, ZERO, S, 4, 2, 8, true>(A, stream);
+    return launch_base<E2M1, F32, ZERO, S, 4, 2, 4, true>(A, stream);
   }
 }
 

@@ -65,11 +65,11 @@ struct BasePlan {
 };
 
 // The tiled kernel converts each code for 64 rows, not 16 or 32, but has its rows prepared in a launch of its own and
-// takes few workgroups: for bf16 rows, from 160 full tiles or 1e10 products on, for fp32 ones from 32 or 1.2e9. Measured
-// (tiles in their best number of ranges, direct; us): bf16, I4: 1000 rows, 4096 x 1024: 20 and 31, 3008 x 1408: 23 and 29,
-// 400 rows, 4096 x 1024: 17 and 16, 2000 rows, 1024 x 4096: 40 and 37, 128 rows, 8192 x 8192: 36 and 35, 256: 52 and 67,
-// 512: 89 and 130; fp32: 1000 rows, 4096 x 1024: 39 and 184, 200 rows, 2527 x 313: 17 and 20, 4096 x 4096: 100 rows 35
-// and 60, 64 rows 33 and 37, 32 rows 31 and 20; 24 rows, 11136 x 14592: 98 and 144, 16: 97 and 85.
+// takes few workgroups: for bf16 rows, from 160 full tiles or 1e10 products on, for fp32 ones from 128 or 5e9. Measured
+// (tiles in their best number of ranges, direct; us): bf16, I4: 850 rows, 3008 x 1408: 24 and 21, 600 rows, 4096 x 1024:
+// 19 and 16, 1000 rows: 20 and 31 (of an earlier instance), 64 rows, 28672 x 5000: 38 and 41, 150 rows, 8192 x 8000: 46
+// and 44, 256 rows, 8192 x 8192: 52 and 67; fp32: 800 rows, 2527 x 313: 27 and 28, 400 rows, 4096 x 1024: 32 and 22, 170
+// rows, 4096 x 4096: 40 and 31, 200 rows, 1088 x 12096: 62 and 33.
 //
 // Tiles fill the card from 256 on; of fewer, K is split into up to 8 ranges of 8 steps and more (256 rows, 8192 x 8192:
 // 81 us in 1, 56 in 2, 52 in 4, 64 in 8; 1024 over 4096 x 4096, 256 tiles: 49 us in 1, 54 in 2); of fp32 rows into up to
@@ -80,7 +80,7 @@ BasePlan base_plan(int32_t T, const sgmv_base& b, int32_t n_split) {
   p.splits = 1;
   const bool f32 = b.dtype == SGMV_F32;
   const double area = (double)T * b.N, full = (double)TILE_T * TILE_N;
-  if (!n_split && (f32 ? T <= 16 || (area < 32 * full && area * b.K < 1.2e9) : T <= 32 || (area < 160 * full && area * b.K < 1e10)))
+  if (!n_split && (f32 ? T <= 16 || (area < 128 * full && area * b.K < 5e9) : T <= 32 || (area < 160 * full && area * b.K < 1e10)))
     return p;
   p.tiled = true;
   const int64_t bands = ceil_div(T, TILE_T), tiles = bands * ceil_div(b.N, TILE_N), steps = h.blocks * (f32 ? 3 : 1);

@@ -82,8 +82,8 @@ def test_product_of_many_rows(sg, T, fmt, group, zero, dtype):
 
 @pytest.mark.parametrize("T,N,K,fmt,group,zero", [(200, 5000, 10050, "e2m1", 32, False), (260, 8200, 4700, "i4", 128, True),
                                                   (2100, 2048, 2400, "i4", 64, False), (1500, 1790, 300, "i4", 32, True),
-                                                  (300, 1801, 1100, "i4f32", 64, True), (600, 900, 333, "e2m1f32", 32, False),
-                                                  (17, 9000, 8000, "i4f32", 128, False), (130, 700, 15403, "i4f32", 32, True)])
+                                                  (1200, 1801, 1100, "i4f32", 64, True), (2400, 900, 333, "e2m1f32", 32, False),
+                                                  (340, 1500, 10050, "i4f32", 128, False), (480, 700, 15403, "i4f32", 32, True)])
 def test_product_as_the_library_chooses(sg, T, N, K, fmt, group, zero):
     """Sizes that go to the tiles by themselves, with and without ranges."""
     dtype, fmt = F32 if fmt.endswith("f32") else BF16, fmt.replace("f32", "")
