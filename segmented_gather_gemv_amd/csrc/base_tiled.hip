@@ -26,48 +26,51 @@ constexpr int TN = TILE_N / 16 / TW;  // tiles of columns of a wave
 constexpr int block_bytes(int sums) { return TILE_T * (BASE_K * 2 + sums * 4); }
 
 // Rows of x as the tiles stage them: blocks of 64 rows and 128 k, 256 bytes a row whose pieces of 16 are exchanged
-// within it, zeros past the last row and the last k; and behind them the sums over each 128 / S values of the rows. Four
-// rows of a block per wave.
+// within it, zeros past the last row and the last k; and behind them the sums over each 128 / S values of the rows. A block
+// per workgroup, 16 rows of it per wave, their loads in flight together.
 template <bool F32, bool SUMS, int S>
 __global__ __launch_bounds__(256) void base_rows_kernel(BaseArgs A) {
   constexpr int BLOCK_BYTES = block_bytes(SUMS ? S : 0), PARTS = F32 ? 3 : 1, E = F32 ? 4 : 2;
   const int lane = threadIdx.x & (WAVE - 1), r = lane & 15;
-  const int64_t rows = (int64_t)((A.T + TILE_T - 1) / TILE_T) * TILE_T;
-  const int64_t at = (int64_t)blockIdx.x * 4 + threadIdx.x / WAVE;  // of a tile, block by block its 16 quads of rows
-  const int64_t block = at / (4 * TT), band = block / A.blocks;
-  const int kb = (int)(block - band * A.blocks), t = 4 * (int)(at % (4 * TT)) + lane / 16;
-  if (band * TILE_T >= rows) return;
-  const int64_t row = band * TILE_T + t;
-  const int k = kb * BASE_K + 8 * r, left = row < A.T ? A.K - k : 0;
-  const char* p = static_cast<const char*>(A.x) + (row * A.ldx + k) * E;
-  u32x4_t v[E / 2];
+  const int band = (int)blockIdx.x / A.blocks, kb = (int)blockIdx.x - band * A.blocks, k = kb * BASE_K + 8 * r;
+  u32x4_t v[4][E / 2];
 #pragma unroll
-  for (int h = 0; h < E / 2; ++h) {
-    const int n = left - 4 * h;  // (of fp32 4 values a piece)
-    v[h] = u32x4_t{0u, 0u, 0u, 0u};
-    if (n >= (F32 ? 4 : 8)) v[h] = load_row<F32>(p + 16 * h);
-    else if (n > 0) v[h] = load_rest<F32>(p + 16 * h, n);
-  }
-  char* to = A.rows + block * PARTS * BLOCK_BYTES;
-  bf16x8_t part[PARTS];
-  if constexpr (F32) split3(v, part);
-  else part[0] = as_bf16x8(v[0]);
+  for (int q = 0; q < 4; ++q) {
+    const int64_t row = (int64_t)band * TILE_T + threadIdx.x / WAVE * 16 + 4 * q + lane / 16;
+    const int left = row < A.T ? A.K - k : 0;
+    const char* p = static_cast<const char*>(A.x) + (row * A.ldx + k) * E;
 #pragma unroll
-  for (int i = 0; i < PARTS; ++i)
-    *reinterpret_cast<u32x4_t*>(to + i * BLOCK_BYTES + t * 256 + (r ^ (t & 15)) * 16) = __builtin_bit_cast(u32x4_t, part[PARTS - 1 - i]);
-  if constexpr (SUMS) {  // with the last part
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if constexpr (F32) sum += __uint_as_float(v[i / 4][i % 4]);
-      else sum += __uint_as_float(i & 1 ? v[0][i / 2] & 0xffff0000u : v[0][i / 2] << 16);
+    for (int h = 0; h < E / 2; ++h) {
+      const int n = left - 4 * h;  // (of fp32 4 values a piece)
+      v[q][h] = u32x4_t{0u, 0u, 0u, 0u};
+      if (n >= (F32 ? 4 : 8)) v[q][h] = load_row<F32>(p + 16 * h);
+      else if (n > 0) v[q][h] = load_rest<F32>(p + 16 * h, n);
     }
+  }
+  char* to = A.rows + (int64_t)blockIdx.x * PARTS * BLOCK_BYTES;
 #pragma unroll
-    for (int o = 1; o < 16 / S; o <<= 1) sum += __shfl_xor(sum, o);
-    if (r % (16 / S) == 0)
+  for (int q = 0; q < 4; ++q) {
+    const int t = threadIdx.x / WAVE * 16 + 4 * q + lane / 16;
+    bf16x8_t part[PARTS];
+    if constexpr (F32) split3(v[q], part);
+    else part[0] = as_bf16x8(v[q][0]);
 #pragma unroll
-      for (int i = 0; i < PARTS; ++i)
-        *reinterpret_cast<float*>(to + i * BLOCK_BYTES + TILE_T * BASE_K * 2 + ((r / (16 / S)) * TILE_T + t) * 4) = i == PARTS - 1 ? sum : 0.f;
+    for (int i = 0; i < PARTS; ++i)
+      *reinterpret_cast<u32x4_t*>(to + i * BLOCK_BYTES + t * 256 + (r ^ (t & 15)) * 16) = __builtin_bit_cast(u32x4_t, part[PARTS - 1 - i]);
+    if constexpr (SUMS) {  // with the last part
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (F32) sum += __uint_as_float(v[q][i / 4][i % 4]);
+        else sum += __uint_as_float(i & 1 ? v[q][0][i / 2] & 0xffff0000u : v[q][0][i / 2] << 16);
+      }
+#pragma unroll
+      for (int o = 1; o < 16 / S; o <<= 1) sum += __shfl_xor(sum, o);
+      if (r % (16 / S) == 0)
+#pragma unroll
+        for (int i = 0; i < PARTS; ++i)
+          *reinterpret_cast<float*>(to + i * BLOCK_BYTES + TILE_T * BASE_K * 2 + ((r / (16 / S)) * TILE_T + t) * 4) = i == PARTS - 1 ? sum : 0.f;
+    }
   }
 }
 
@@ -319,7 +322,7 @@ __global__ __launch_bounds__(TW* WAVE, 2) void base_tiled_kernel(BaseArgs A) {
 template <bool E2M1, bool F32, bool ZERO, int S>
 hipError_t launch(const BaseArgs& A, hipStream_t stream) {
   const int64_t bands = (A.T + TILE_T - 1) / TILE_T, n = (bands * ((A.N + TILE_N - 1) / TILE_N) + 7) / 8 * 8;
-  base_rows_kernel<F32, !E2M1, S><<<(unsigned)(bands * A.blocks * TT), 256, 0, stream>>>(A);
+  base_rows_kernel<F32, !E2M1, S><<<(unsigned)(bands * A.blocks), 256, 0, stream>>>(A);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   base_tiled_kernel<E2M1, F32, ZERO, S><<<(unsigned)(n * A.splits), TW * WAVE, 0, stream>>>(A);

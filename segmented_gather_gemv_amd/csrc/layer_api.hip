@@ -186,7 +186,7 @@ sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, const sgmv_
   if (p.tiled) {
     const int64_t bands = ceil_div(T, TILE_T);
     if ((bands * ceil_div(b->N, TILE_N) + 8) * 4 * std::max(p.splits, TILE_T / 16) > MOST_WAVES ||
-        bands * h.blocks * (TILE_T / 4) > MOST_WAVES)
+        bands * h.blocks * 4 > MOST_WAVES)
       return SGMV_EUNSUPPORTED;
     return launched(launch_base_tiled(A, b->format, b->dtype, (int)h.s, s));
   }
