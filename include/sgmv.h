@@ -689,11 +689,10 @@ sgmv_status sgmv_base_pack(const uint8_t* codes, int64_t ldc, const void* scale,
  * is not finite spoils its own row of y only. I4 sums codes as they are and takes the zero points' share off
  * after: sums of 16 |x| have to stay in fp32.
  *   x  device [T][ldx >= K], y device [T][ldy >= N], of base->dtype; y must not overlap x
- *   n_split  0 = the library's choice, else 1..SGMV_BASE_MAX_SPLITS: as of many rows, in tiles (of bf16 rows
- *            only) with K split into that many ranges
+ *   n_split  0 = the library's choice, else 1..SGMV_BASE_MAX_SPLITS: as of many rows, in tiles with K split
+ *            into that many ranges
  *   workspace  device, 16-byte aligned, of sgmv_base_product_workspace bytes (0: may be NULL)
- * Errors: EINVAL; EUNSUPPORTED (n_split with fp32 rows; a launch past 2^32 work items); ECAPACITY (workspace);
- * EHIP. */
+ * Errors: EINVAL; EUNSUPPORTED (a launch past 2^32 work items); ECAPACITY (workspace); EHIP. */
 #define SGMV_BASE_MAX_SPLITS 16
 sgmv_status sgmv_base_product_workspace(int32_t T, const sgmv_base* base, int32_t n_split, size_t* bytes);
 sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, const sgmv_base* base, void* y,

@@ -1,5 +1,6 @@
 // Packing a 4-bit base weight (load time): rows of codes into blocks of 16 n and 128 k in the order of the matrix
-// cores' operands (base.h), scales and zero points beside them.
+// cores' operands (base.h), scales and zero points beside them. Bound: eight bytes read one by one for each word
+// written, from lines that a wave shares; 8192 x 8192 in 121 us, once.
 #include "base.h"
 
 namespace sgmv {

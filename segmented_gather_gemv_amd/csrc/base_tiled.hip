@@ -12,6 +12,14 @@
 //   fp32  rows are three bf16 parts, small ones first, each a block of its own over the same codes: three times the
 //         products, and the same kernel.
 // Where that leaves compute units without a tile, K is split into ranges whose sums a last launch adds up.
+//
+// Bound: the matrix cores and the conversions beside them: per block a wave converts 128 words and scales 64 sums while it
+// makes 64 products, which 2 waves a SIMD overlap in part (2048 rows over 11008 x 4096 with zero points: matrix cores
+// busy 38% of the cycles, vector units 51%, at 2.06 GHz). Measured, bf16 rows: that 214 us (865 TFLOP/s; the
+// library's bf16 product alone runs at 1197), 9 of them preparing rows; without zero points 196, groups of 64 217, groups
+// of 32 with zero points 307, E2M1 166 (1115 TFLOP/s); 1000 rows over 8192 x 28672 460 us (1020). fp32 rows: 2048 over 8192 x
+// 8192 with zero points 833 us, E2M1 639 (a library product of fp32: 1785). Not kept: 128 rows a workgroup (one wave a
+// SIMD: 329 us), 192 columns (224), loads straight to LDS (the compiler waits for all loads before each LDS read).
 #include "base.h"
 
 namespace sgmv {
@@ -92,8 +100,7 @@ __device__ __forceinline__ bool tile_place(const BaseArgs& A, int block, TilePla
 }
 
 // 16 rows and 64 columns of a wave's results as rows of y: fp32 straight from its registers (64 bytes a row at once),
-// bf16 through its 2 KB of LDS (16-byte pieces exchanged within the
-// rows of 128, as above).
+// bf16 through its 2 KB of LDS (16-byte pieces exchanged within the rows of 128, as above).
 template <bool F32>
 __device__ __forceinline__ void store_tile(const BaseArgs& A, char* own, int t0, int n0, const f32x4_t (&acc)[TN]) {
   const int lane = threadIdx.x & (WAVE - 1), r = lane & 15, quad = lane >> 4;

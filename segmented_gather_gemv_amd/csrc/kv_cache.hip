@@ -24,11 +24,22 @@
 // separate waves.
 //
 // Bound: the rows' bytes; one token per sequence: the chain of loads from the sequence to its page.
-// Measured, 8 heads of 128: 256 sequences' new tokens written as e4m3 5.6 us and read back 4.2 us; 16 prompts'
-// chunks (8.9 thousand tokens) written as int8 16.0 us (55 MB, 11 us of a large copy: all waves are resident at once,
-// so that loads, quantising and stores follow each other), 41 thousand tokens read back as bf16 57 us (258 MB,
+// Measured, 8 heads of 128: 256 sequences' new tokens written as e4m3 5.3 us and read back 4.2 us; 16 prompts'
+// chunks (8.9 thousand tokens) written as int8 13.4 us (55 MB, 11 us of a large copy: all waves are resident at once,
+// so that loads, quantising and stores follow each other; with the page asked for behind the row 16.0), 41 thousand tokens read back as bf16 57 us (258 MB,
 // 4.5 TB/s; a large copy: 5.1). Fp32 rows written as e4m3 or int8 19.4 us (floor 17.9), read back 143 (84); rows that
 // are held as they are: bf16 written in 13.9 us (14.2), read in 75 (67), fp32 25 (28) and 181 (133).
+//
+// The append turns K on its way, (a, b) -> (a c - b s, b c + a s) with the cosine and sine of the token's position, every
+// product and sum rounded to fp32, and the queries, which it writes as rows. V goes as above. K takes lanes of its
+// own: 4 values and the 4 that they are paired with in one lane, rows side by side in a wave, so that values and
+// angles are loaded once whatever the rotation and the head size; a group's 16 rows are four loads in flight and four
+// stores (16 rows a wave in pieces of 16 bytes, as above, needs the pairs' other halves and the angles of 16 values at
+// once: 150 registers, or each loaded twice; the chunks below took 54 us, and tokens of D = 256 that bring one each 9.4
+// us, now 4.0). The queries are workgroups of the same launch, behind the others (between them, 55 us).
+// Bound: the rows' bytes; of few tokens, the chain of loads. Measured with 32 query and 8 key heads of 128: one token 3.2
+// us, 16 prompts' chunks (8.6 thousand tokens) into int8 48 us (206 MB, 4.2 TB/s), the queries' part alone 30 (as
+// long as a copy of them), K and V 20 (floor 11); 256 tokens of 64 and 8 heads into e4m3 6.4.
 #include <algorithm>
 
 #include "quantise.h"
