@@ -220,7 +220,9 @@ hipError_t launch_base(const BaseArgs& A, hipStream_t stream) {
 template <bool E2M1, bool F32, bool ZERO, int S>
 hipError_t launch_base_rows(const BaseArgs& A, hipStream_t stream) {
   const int64_t tiles = (A.N + BASE_N - 1) / BASE_N;
-  const auto at_once = [&](int nt, int tm) { return (tiles + nt - 1) / nt * ((A.T + 16 * tm - 1) / (16 * tm)) <= 256; };
+  const auto at_once = [&](int nt, int tm) {  // (and of narrow weights no more columns than they have)
+    return tiles <= nt || (tiles + nt - 1) / nt * ((A.T + 16 * tm - 1) / (16 * tm)) <= 256;
+  };
   if constexpr (F32) {
     if (at_once(1, 1)) return launch_base<E2M1, F32, ZERO, S, 1, 1, 16, false>(A, stream);
     if (at_once(2, 1)) return launch_base<E2M1, F32, ZERO, S, 2, 1, 16, false>(A, stream);

@@ -139,6 +139,64 @@ def test_two_steps_at_once_on_two_streams(sg):
             layer.check(*inputs[i], g, other)
 
 
+def _far(rows, width, dtype):
+    """Rows 2^27 elements apart: the last ones lie past 2^32 elements."""
+    step = 1 << 27
+    return torch.empty((rows - 1) * step + width, dtype=dtype, device=DEV).as_strided((rows, width), (step, 1))
+
+
+def test_rows_past_32_bits(sg):
+    T, K, N = 36, 300, 272
+    g = torch.Generator().manual_seed(5)
+    w = Weight(sg, N, K, "i4", BF16, 64, True)
+    x, y = _far(T, K, BF16), _far(T, N, BF16)
+    x.copy_(torch.randn(T, K, generator=g).to(BF16))
+    for n in (0, 1, 2):
+        y.fill_(7.0)
+        sg.sgmv_base_product(x, w.packed, y, n_split=n)
+        w.check(y.contiguous(), x.cpu())
+    weight = torch.randn(K, generator=g).to(BF16)
+    keep, W = x.cpu(), N - 7
+    got = sg.sgmv_rms_norm(x[:, :W], weight[:W].to(DEV), residual=x[:, 8:8 + W], out=y[:, 3:3 + W], quantise=I8)
+    _check(got._replace(out=got.out.contiguous()), keep[:, :W], weight[:W], 1e-6, keep[:, 8:8 + W], I8)
+
+
+@pytest.mark.parametrize("new", [[1, 2, 1], [40, 3, 17]])
+@pytest.mark.parametrize("fmt", [BF16, I8])
+def test_append_into_pages_past_32_bits(sg, fmt, new):
+    H, D, ps, pages = 8, 256, 64, 20000 if fmt == BF16 else 36000
+    lens = [n + 50 for n in new]
+    cache = sg.sgmv_kv_init(pages, ps, H, D, fmt, DEV)
+    small = Step(sg, new, lens, ps, H, D, fmt, seed=9)
+    start = small.batch.q_start
+    far = torch.from_numpy(small.table).to(DEV)
+    far = torch.where(far >= 0, far + (pages - small.pages), far)
+    batch = sg.sgmv_kv_batch(start, small.batch.kv_len, far, small.T, max(new), max(lens))
+    g = torch.Generator().manual_seed(6)
+    k, v, q = (torch.randn(small.T, h, D, generator=g).to(BF16).to(DEV) for h in (H, H, 16))
+    table = _table(max(lens), 192).to(DEV)
+    for c in (cache, small.cache):
+        for t in (c.k, c.v):
+            _raw(t)[-small.pages:].zero_()
+        for t in (c.k_scale, c.v_scale) if fmt == I8 else ():
+            t[-small.pages:].fill_(1.0)
+    a = sg.sgmv_kv_append(q, k, v, batch, cache, table)
+    b = sg.sgmv_kv_append(q, k, v, small.batch, small.cache, table)
+    assert torch.equal(a, b)
+    for far_part, part in ((cache.k, small.cache.k), (cache.v, small.cache.v)):
+        assert torch.equal(_raw(far_part)[-small.pages:], _raw(part))
+    out = [sg.sgmv_kv_attention(a, x, c)[0] for x, c in ((batch, cache), (small.batch, small.cache))]
+    assert torch.equal(*out)
+
+
+@pytest.mark.parametrize("N", [1, 16, 20, 48])
+def test_narrow_weights_of_many_rows(sg, N):
+    for dtype in (BF16, F32):
+        w = Weight(sg, N, 200, "i4", dtype, 128, True)
+        x = torch.randn(9000, 200, generator=torch.Generator().manual_seed(N)).to(dtype)
+        w.check(sg.sgmv_base_product(x.to(DEV), w.packed), x)
+
+
 @pytest.mark.parametrize("base,fmt", [("i4", "bf16"), ("i4", "i8"), ("e2m1", "e4m3")])
 def test_serving_steps_of_a_whole_layer(sg, base, fmt, capsys):
     spec = importlib.util.spec_from_file_location("serving_steps", PATH)
