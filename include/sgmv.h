@@ -510,7 +510,7 @@ sgmv_status sgmv_kv_write(const void* k, int64_t ldk_token, int64_t ldk_head, co
  *   cos_sin  device [positions][ld >= rotary] fp32
  *   rotary   a multiple of 16 up to head_dim
  *   q, q_out device rows [T][heads][head_dim] of `dtype`; q_out may be q itself (with the same
- *            strides), must not overlap it otherwise. heads = 0: no queries
+ *            strides, which is checked), must not overlap it otherwise. heads = 0: no queries
  * Errors: EINVAL; EUNSUPPORTED; EHIP. */
 typedef struct {
   const float* cos_sin;
@@ -617,8 +617,8 @@ sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draf
  *   x, residual, residual_out, out  device, row of token t and head j at t * ld_token + j * ld_head,
  *            `width` contiguous elements of `dtype`; residual may be NULL (h = x), and then
  *            residual_out is NULL; residual_out may be NULL, and so may out where codes are asked for.
- *            residual_out and out may be x or residual themselves (with the same strides, each another
- *            one), none of the outputs may overlap anything otherwise
+ *            residual_out and out may be x or residual themselves (with the same strides; each another
+ *            one, which is checked), none of the outputs may overlap anything otherwise
  *   weight   device [width] of `dtype`
  *   codes    device bytes, rows as above, with strides ldc, or NULL;  scale  device [T][heads] fp32
  *   eps      finite and > 0;  width up to SGMV_MAX_NORM_WIDTH

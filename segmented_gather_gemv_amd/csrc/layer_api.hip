@@ -112,7 +112,7 @@ sgmv_status sgmv_rms_norm(const sgmv_norm* n, void* stream) {
   if (n->width > SGMV_MAX_NORM_WIDTH) return SGMV_EUNSUPPORTED;
   if (n->T == 0) return SGMV_OK;
   if (!n->weight || !rows_ok(n->x, n, n->ldx_token, n->ldx_head) || (n->codes != nullptr) != (n->scale != nullptr) ||
-      (!n->out && !n->codes) || (n->residual_out && !n->residual))
+      (!n->out && !n->codes) || (n->residual_out && !n->residual) || (n->out && n->out == n->residual_out))
     return SGMV_EINVAL;
   if ((n->residual && !rows_ok(n->residual, n, n->ldr_token, n->ldr_head)) ||
       (n->residual_out && !rows_ok(n->residual_out, n, n->lds_token, n->lds_head)) ||
@@ -171,7 +171,7 @@ sgmv_status sgmv_base_product(const void* x, int64_t ldx, int32_t T, const sgmv_
   const sgmv_status st = sgmv_base_product_workspace(T, b, n_split, &need);
   if (st != SGMV_OK) return st;
   if (T == 0) return SGMV_OK;
-  if (!x || !y || (T > 1 && (ldx < b->K || ldy < b->N))) return SGMV_EINVAL;
+  if (!x || !y || x == y || (T > 1 && (ldx < b->K || ldy < b->N))) return SGMV_EINVAL;
   if (need) {
     if (!workspace || !aligned_to(workspace, 16)) return SGMV_EINVAL;
     if (workspace_bytes < need) return SGMV_ECAPACITY;

@@ -126,7 +126,7 @@ def test_base_calls_refuse():
     assert lib.sgmv_base_product(0x1000, 300, 3, None, 0x9000, 40, 0, None, 0, None) == E
     assert lib.sgmv_base_product_workspace(3, None, 0, ctypes.byref(need)) == E
     assert lib.sgmv_base_product_workspace(3, ctypes.byref(_base()), 0, None) == E
-    for kw in (dict(x=None), dict(y=None), dict(ldx=299), dict(ldy=39), dict(T=-1), dict(n_split=-1), dict(n_split=17)):
+    for kw in (dict(x=None), dict(y=None), dict(y=0x1000), dict(ldx=299), dict(ldy=39), dict(T=-1), dict(n_split=-1), dict(n_split=17)):
         assert product(**kw) == E, kw
     assert product(T=0, x=None, y=None) == OK
     assert lib.sgmv_base_product_workspace(0, ctypes.byref(_base()), 0, ctypes.byref(need)) == OK and need.value == 0
@@ -174,7 +174,7 @@ def test_norm_refuses():
     call = lambda **kw: lib.sgmv_rms_norm(ctypes.byref(_norm(**kw)), None)
     bad = [dict(x=0), dict(weight=0), dict(T=-1), dict(heads=0), dict(width=0), dict(dtype=2), dict(eps=0.0),
            dict(eps=-1.0), dict(eps=float("nan")), dict(eps=float("inf")), dict(format=sg.KV_BF16), dict(scale=0),
-           dict(codes=0), dict(residual=0), dict(out=0, codes=0, scale=0)]
+           dict(codes=0), dict(residual=0), dict(out=0, codes=0, scale=0), dict(out=0x4000)]
     bad += [{f"ld{a}_token": 127} for a in "xrsoc"] + [{f"ld{a}_head": 63} for a in "xrsoc"]
     for kw in bad:
         assert call(**kw) == E, kw
@@ -211,6 +211,7 @@ def test_append_refuses():
     for kw in (dict(k=None), dict(v=None), dict(kt=127), dict(vt=127), dict(kh=63), dict(vh=0), dict(dtype=2),
                dict(cos_sin=0), dict(cos_sin=0x1002), dict(ld=63), dict(positions=0), dict(rotary=0), dict(rotary=80),
                dict(rotary=-16), dict(interleaved=2), dict(interleaved=-1), dict(heads=-1), dict(q=0), dict(q_out=0),
+               dict(q_out=0xa0000, ldo_token=512), dict(q_out=0xa0000, ldo_head=60 + 8, ldo_token=512),
                dict(ldq_token=255), dict(ldq_head=63), dict(ldo_token=255), dict(ldo_head=1),
                dict(cache=_cache(k=0)), dict(cache=_cache(format=9)), dict(batch=_batch(T=-1)), dict(batch=_batch(ldp=1))):
         assert _append(**kw) == E, kw
