@@ -4,7 +4,7 @@
 // summing all of its tiles in fp32, and their sums are added in LDS in the waves' order. The weight's next blocks and the
 // rows of x that go with them are in flight while one is multiplied. Up to 4 rows go straight into operands (16 rows of the
 // product's, the last of them again); more are read as whole lines and pass through the wave's part of LDS (16 rows over
-// 8192 x 8192: 12 us without). 16 waves and two workgroups a unit keep 128 KB of the weight in flight.
+// 8192 x 8192: 12 us without), but for fp32, whose parts are made in registers. 16 waves and two workgroups a unit keep 128 KB of the weight in flight.
 //
 // Bound: the weight's bytes, from some 16 rows on the conversions and products. Measured (I4, groups of 128, bf16 rows;
 // floors by a large copy's 5.14 TB/s): one row over 8192 x 8192 8.0 us (35 MB, 4.3 TB/s; floor 6.8), over 28672 x 8192
@@ -16,14 +16,15 @@
 
 namespace sgmv {
 
-// Waves per SIMD to allocate registers for: two workgroups per compute unit where their rows' registers leave room.
-constexpr int base_occupancy(bool zero, bool f32, int nt, int tm, int waves, bool staged) {
-  if (f32) return waves / 4;
-  return !staged && !zero ? 8 : waves >= 8 ? waves / 4 : 2;
+// Waves per SIMD to allocate registers for: one workgroup per compute unit, two where the registers of rows and zero
+// points leave room or it has four waves (three of those a unit: 36 to 93 spilled registers, 10 to 200% slower).
+constexpr int base_occupancy(bool zero, bool f32, int waves, bool staged) {
+  if (!f32 && !staged && !zero) return 8;
+  return waves >= 8 ? waves / 4 : 2;
 }
 
 template <bool E2M1, bool F32, bool ZERO, int S, int NT, int TM, int WAVES, bool STAGED>
-__global__ __launch_bounds__(WAVES* WAVE, base_occupancy(ZERO, F32, NT, TM, WAVES, STAGED)) void base_direct_kernel(BaseArgs A) {
+__global__ __launch_bounds__(WAVES* WAVE, base_occupancy(ZERO, F32, WAVES, STAGED)) void base_direct_kernel(BaseArgs A) {
   constexpr int XW = F32 ? 2 : 1, ROWS = 16 * TM, COLS = 16 * NT, LD = COLS + 4;
   static_assert(!(STAGED && F32), "rows of bf16 are staged");
   constexpr int X_BYTES = STAGED ? ROWS * BASE_K * 2 : 0, SUM_BYTES = ROWS * LD * 4;
