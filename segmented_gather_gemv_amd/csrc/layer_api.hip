@@ -16,10 +16,13 @@ inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline sgmv_status launched(hipError_t e) { return e == hipSuccess ? SGMV_OK : SGMV_EHIP; }
 constexpr int64_t MOST_WAVES = 0xffffffffll / 64;  // of a launch: it takes fewer than 2^32 work items
 
-// Rows [T][heads][W] with a token and a head stride: rows must not overlap one another.
+// Rows [T][heads][W] with a token and a head stride: rows must not overlap one another, tokens or heads outermost.
 bool rows_ok(const void* p, const sgmv_norm* n, int64_t ld_t, int64_t ld_h) {
-  return p && (n->heads == 1 || ld_h >= n->width) &&
-         (n->T == 1 || ld_t >= (n->heads - 1) * (n->heads == 1 ? 0 : ld_h) + n->width);
+  const int64_t T = n->T, H = n->heads, W = n->width;
+  const auto nested = [W](int64_t inner, int64_t ld_in, int64_t outer, int64_t ld_out) {
+    return (inner == 1 || ld_in >= W) && (outer == 1 || (__int128)ld_out >= (inner == 1 ? 0 : (__int128)(inner - 1) * ld_in) + W);
+  };
+  return p && (nested(H, ld_h, T, ld_t) || nested(T, ld_t, H, ld_h));
 }
 
 // The sizes of a weight's parts.

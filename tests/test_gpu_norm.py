@@ -162,6 +162,19 @@ def test_norm_in_place_and_into_strided_rows(sg, dtype, W):
     assert only.out is None and torch.equal(only.codes, want.codes) and torch.equal(only.scale, want.scale)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_norm_of_rows_with_heads_outermost(sg, dtype):
+    g = torch.Generator().manual_seed(3)
+    x, r = (torch.randn(5, 33, 80, generator=g).to(dtype) for _ in range(2))
+    w = torch.randn(80, generator=g).to(dtype)
+    dx, dr = x.to(DEV).transpose(0, 1), r.to(DEV).transpose(0, 1)
+    got = sg.sgmv_rms_norm(dx, w.to(DEV), residual=dr, quantise=I8)
+    assert got.out.is_contiguous() and got.codes.is_contiguous()
+    _check(got, x.transpose(0, 1), w, 1e-6, r.transpose(0, 1), I8)
+    again = sg.sgmv_rms_norm(dx, w.to(DEV), residual=dr, out=dx, residual_out=dr)  # where they are
+    assert torch.equal(again.out, got.out) and torch.equal(dx, got.out) and torch.equal(dr, got.residual)
+
+
 def test_norm_of_no_rows(sg):
     w = torch.ones(64, device=DEV)
     got = sg.sgmv_rms_norm(torch.empty(0, 64, device=DEV), w, quantise=E4M3)
