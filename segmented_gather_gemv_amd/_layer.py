@@ -10,6 +10,7 @@ Argument marshalling only; calls for serving, which autograd does not see.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass, field
 from typing import NamedTuple, Optional
 
@@ -43,17 +44,22 @@ class _Rotation(ctypes.Structure):
                 [(n, ctypes.c_int64) for n in ("ldq_token", "ldq_head", "ldo_token", "ldo_head")])
 
 
+# The same as bytes, which take a third of the time to fill (0: no pointer); calls take either.
+_pack_norm, _pack_rotation = (struct.Struct(f).pack for f in ("7P10q5if", "Pq4i2P4q"))
+assert struct.calcsize("7P10q5if") == ctypes.sizeof(_Norm) and struct.calcsize("Pq4i2P4q") == ctypes.sizeof(_Rotation)
+
+
 def _bind():
     i32, i64, vp, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t
     P = ctypes.POINTER
     B = P(_Base)
     for name, args in {
-        "sgmv_rms_norm": [P(_Norm), vp],
+        "sgmv_rms_norm": [vp, vp],
         "sgmv_base_init": [i32, i32, i32, i32, i32, i32, B, P(sz), P(sz), P(sz)],
         "sgmv_base_pack": [vp, i64, vp, vp, B, vp],
         "sgmv_base_product_workspace": [i32, B, i32, P(sz)],
         "sgmv_base_product": [vp, i64, i32, B, vp, i64, i32, vp, sz, vp],
-        "sgmv_kv_append": [P(_Rotation), vp, i64, i64, vp, i64, i64, i32, P(_KvBatch), P(_KvCache), vp],
+        "sgmv_kv_append": [vp, vp, i64, i64, vp, i64, i64, i32, P(_KvBatch), P(_KvCache), vp],
     }.items():
         f = getattr(_lib, name)
         f.argtypes, f.restype = args, ctypes.c_int
@@ -64,6 +70,7 @@ _bind()
 
 _current = torch._C._cuda_getDevice  # (the calls behind torch.cuda's, which take longer than they)
 _stream = torch._C._cuda_getCurrentRawStream
+_tuple = tuple.__new__
 _like, _dense = torch.empty_like, torch.contiguous_format  # (allocates faster than new_empty of a shape)
 _ROWS = {torch.float32: _dtype_code(torch.float32), torch.bfloat16: _dtype_code(torch.bfloat16)}
 
@@ -133,7 +140,7 @@ def sgmv_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
             not weight.is_contiguous()):
         raise TypeError(f"weight must be {W} contiguous {dtype} entries on x's device")
     xt, xh = _strides(x, shape, dtype, index, "x")
-    rp = sp = op = cp = fp = None
+    rp = sp = op = cp = fp = 0
     dense = heads * W
     rt = st = ot = ct = dense
     rh = sh = oh = ch = W
@@ -174,13 +181,13 @@ def sgmv_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
         raise ValueError("nothing to compute: neither out nor codes are wanted")
     if index < 0:
         raise ValueError("the kernels run on GPU tensors")
-    a = _Norm(x.data_ptr(), rp, weight.data_ptr(), sp, op, cp, fp, xt, xh, rt, rh, st, sh, ot, oh, ct, ch, T, heads, W,
+    a = _pack_norm(x.data_ptr(), rp, weight.data_ptr(), sp, op, cp, fp, xt, xh, rt, rh, st, sh, ot, oh, ct, ch, T, heads, W,
               code, fmt, eps)
-    call, ref = _lib.sgmv_rms_norm, ctypes.byref(a)
-    status = call(ref, _stream(index)) if index == _current() else _elsewhere(index, call, ref)
+    call = _lib.sgmv_rms_norm
+    status = call(a, _stream(index)) if index == _current() else _elsewhere(index, call, a)
     if status != SGMV_OK:
         _check(status, "sgmv_rms_norm")
-    return Normed(out, residual_out, codes, scale)
+    return _tuple(Normed, (out, residual_out, codes, scale))
 
 
 # ---------------------------------------------------------------------------------------
@@ -322,7 +329,7 @@ def sgmv_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
     if positions > _MOST or rotary > _MOST:
         _int32("positions and rotary", positions, rotary)
     heads = qt = qh = ot = oh = 0
-    qp = op = None
+    qp = op = 0
     if q is not None:
         qt, qh = _rows3(q, T, None, cache, "q")
         if q.dtype is not dtype:
@@ -339,9 +346,9 @@ def sgmv_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
     elif q_out is not None:
         raise ValueError("q_out goes with q")
     _on_gpu(batch, cache)
-    r = _Rotation(cos_sin.data_ptr(), cos_sin.stride(0) if positions > 1 else rotary, positions, rotary,
+    r = _pack_rotation(cos_sin.data_ptr(), cos_sin.stride(0) if positions > 1 else rotary, positions, rotary,
                   1 if interleaved else 0, heads, qp, op, qt, qh, ot, oh)
-    args = (ctypes.byref(r), k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, code, batch.ref, cache.ref)
+    args = (r, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, code, batch.ref, cache.ref)
     call = _lib.sgmv_kv_append
     st = call(*args, _stream(index)) if index == _current() else _elsewhere(index, call, *args)
     if st != SGMV_OK:
