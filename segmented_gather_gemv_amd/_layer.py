@@ -17,7 +17,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import SGMV_OK, _check, _dtype_code, _lib
-from ._serving import KV_E4M3, KV_I8, KvBatch, KvCache, _MOST, _dense3, _int32, _KvBatch, _KvCache, _on_gpu, _rows3
+from ._serving import KV_E4M3, KV_I8, KvBatch, KvCache, _MOST, _int32, _KvBatch, _KvCache, _on_gpu, _rows3
 
 MAX_NORM_WIDTH = 32768
 BASE_MAX_SIZE = 4194304
@@ -182,7 +182,7 @@ def sgmv_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     if index < 0:
         raise ValueError("the kernels run on GPU tensors")
     a = _pack_norm(x.data_ptr(), rp, weight.data_ptr(), sp, op, cp, fp, xt, xh, rt, rh, st, sh, ot, oh, ct, ch, T, heads, W,
-              code, fmt, eps)
+                   code, fmt, eps)
     call = _lib.sgmv_rms_norm
     status = call(a, _stream(index)) if index == _current() else _elsewhere(index, call, a)
     if status != SGMV_OK:
@@ -337,7 +337,7 @@ def sgmv_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
         heads, qp = q.shape[1], q.data_ptr()
         if q_out is None:
             q_out = _like(q, memory_format=_dense)
-            ot, oh = _dense3(heads, cache)
+            ot, oh = heads * cache.head_dim, cache.head_dim
         else:
             ot, oh = _rows3(q_out, T, heads, cache, "q_out")
             if q_out.dtype is not dtype:
@@ -345,9 +345,10 @@ def sgmv_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
         op = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out goes with q")
-    _on_gpu(batch, cache)
+    if batch.index != index or index < 0:
+        _on_gpu(batch, cache)  # says which
     r = _pack_rotation(cos_sin.data_ptr(), cos_sin.stride(0) if positions > 1 else rotary, positions, rotary,
-                  1 if interleaved else 0, heads, qp, op, qt, qh, ot, oh)
+                       1 if interleaved else 0, heads, qp, op, qt, qh, ot, oh)
     args = (r, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, code, batch.ref, cache.ref)
     call = _lib.sgmv_kv_append
     st = call(*args, _stream(index)) if index == _current() else _elsewhere(index, call, *args)
