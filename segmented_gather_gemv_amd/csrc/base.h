@@ -120,6 +120,14 @@ struct BaseZero {
   __device__ __forceinline__ float get(int i) const { return ZERO ? (float)(w >> (8 * i) & 255u) : 8.f; }
 };
 
+// Keeps a wave's LDS accesses before it in front of those behind it, for values that its lanes pass to each other there.
+// (The hardware carries out a wave's LDS accesses in order: this is for the compiler, and makes no instruction.)
+__device__ __forceinline__ void wave_lds_order() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // 16 bytes of a row, wherever it starts.
 template <bool F32>
 __device__ __forceinline__ u32x4_t load_row(const char* p) {

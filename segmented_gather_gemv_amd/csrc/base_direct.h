@@ -80,6 +80,7 @@ __global__ __launch_bounds__(WAVES* WAVE, base_occupancy(ZERO, F32, WAVES, STAGE
   // that 16 rows' pieces of the same k lie in different banks.
   char* const own = s_all + wv * X_BYTES;
   const auto stage = [&](const Rows& b) {
+    wave_lds_order();  // behind the reads of the block before
 #pragma unroll
     for (int m = 0; m < TM; ++m)
 #pragma unroll
@@ -87,6 +88,7 @@ __global__ __launch_bounds__(WAVES* WAVE, base_occupancy(ZERO, F32, WAVES, STAGE
         const int row = 4 * j + quad;
         *reinterpret_cast<u32x4_t*>(own + (16 * m + row) * 256 + (r ^ row) * 16) = b.x[m][j][0];
       }
+    wave_lds_order();  // other lanes read them
   };
 
   f32x4_t acc[NT][TM];

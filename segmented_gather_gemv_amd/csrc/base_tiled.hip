@@ -115,7 +115,7 @@ __device__ __forceinline__ void store_tile(const BaseArgs& A, char* own, int t0,
     }
     return;
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_order();
 #pragma unroll
   for (int n = 0; n < TN; ++n)
 #pragma unroll
@@ -123,7 +123,7 @@ __device__ __forceinline__ void store_tile(const BaseArgs& A, char* own, int t0,
       const int t = 4 * quad + i, c = 2 * n + (r >> 3);
       *reinterpret_cast<uint16_t*>(own + t * 128 + (c ^ (t & 7)) * 16 + (r & 7) * 2) = (uint16_t)pack_bf16x2(acc[n][i], 0.f);
     }
-  __builtin_amdgcn_wave_barrier();
+  wave_lds_order();
   constexpr int PIECES = 2 * TN;  // of a row
 #pragma unroll
   for (int i = 0; i < (16 * PIECES + WAVE - 1) / WAVE; ++i) {
