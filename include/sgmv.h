@@ -615,10 +615,11 @@ sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draf
  * h and g are fp32, each rounded once; h and out are then rounded once to `dtype`, codes as in the
  * cache above: zeros give scale 0 and codes 0, a row with a g that is not finite scale NaN and codes 0.
  *   x, residual, residual_out, out  device, row of token t and head j at t * ld_token + j * ld_head,
- *            `width` contiguous elements of `dtype`, tokens or heads outermost, each row its own; residual may be NULL (h = x), and then
- *            residual_out is NULL; residual_out may be NULL, and so may out where codes are asked for.
- *            residual_out and out may be x or residual themselves (with the same strides; each another
- *            one, which is checked), none of the outputs may overlap anything otherwise
+ *            `width` contiguous elements of `dtype`, tokens or heads outermost, each row its own;
+ *            residual may be NULL (h = x), and then residual_out is NULL; residual_out may be NULL,
+ *            and so may out where codes are asked for. residual_out and out may be x or residual
+ *            themselves, with the same strides and not both the same one; no output may overlap
+ *            anything otherwise. (Checked: equal addresses; not parts of rows that overlap.)
  *   weight   device [width] of `dtype`
  *   codes    device bytes, rows as above, with strides ldc, or NULL;  scale  device [T][heads] fp32
  *   eps      finite and > 0;  width up to SGMV_MAX_NORM_WIDTH

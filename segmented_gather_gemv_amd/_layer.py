@@ -122,7 +122,8 @@ def sgmv_rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6,
     times ``weight``; of x + ``residual`` where one is given, which is returned too. ``quantise``
     (float8_e4m3fn or int8) asks for the normed rows as codes with one scale per row as well, ``want_out=False``
     for those alone. Outputs are allocated unless given; ``out`` and ``residual_out`` may be x or residual
-    themselves."""
+    themselves (views of the same strides, each another one). The norm is that of the fp32 sum: ``residual``
+    of the result is that sum rounded."""
     shape, dtype, index = x.shape, x.dtype, x.get_device()
     if len(shape) == 2:
         T, W = shape

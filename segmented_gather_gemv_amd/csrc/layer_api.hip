@@ -25,6 +25,25 @@ bool rows_ok(const void* p, const sgmv_norm* n, int64_t ld_t, int64_t ld_h) {
   return p && (nested(H, ld_h, T, ld_t) || nested(T, ld_t, H, ld_h));
 }
 
+// Whether outputs may stand where they do. Rows are read whole before they are written, each by the threads that write
+// it: an output may be x or the residual row for row, and nothing else may be in two places of a call.
+bool places_ok(const sgmv_norm* n) {
+  const auto row_for_row = [n](const void* out, int64_t out_t, int64_t out_h, const void* in, int64_t in_t, int64_t in_h) {
+    return !out || out != in || ((n->T == 1 || out_t == in_t) && (n->heads == 1 || out_h == in_h));
+  };
+  const void* const outs[] = {n->residual_out, n->out, n->codes, n->scale};
+  for (int i = 0; i < 4; ++i) {
+    if (!outs[i]) continue;
+    for (int k = 0; k < i; ++k)
+      if (outs[i] == outs[k]) return false;
+    if (outs[i] == n->weight || (i >= 2 && (outs[i] == n->x || outs[i] == n->residual))) return false;
+  }
+  return row_for_row(n->out, n->ldo_token, n->ldo_head, n->x, n->ldx_token, n->ldx_head) &&
+         row_for_row(n->out, n->ldo_token, n->ldo_head, n->residual, n->ldr_token, n->ldr_head) &&
+         row_for_row(n->residual_out, n->lds_token, n->lds_head, n->x, n->ldx_token, n->ldx_head) &&
+         row_for_row(n->residual_out, n->lds_token, n->lds_head, n->residual, n->ldr_token, n->ldr_head);
+}
+
 // The sizes of a weight's parts.
 struct BaseShape {
   int64_t tiles, blocks, groups, s, scale_rows, per_group;
@@ -115,12 +134,12 @@ sgmv_status sgmv_rms_norm(const sgmv_norm* n, void* stream) {
   if (n->width > SGMV_MAX_NORM_WIDTH) return SGMV_EUNSUPPORTED;
   if (n->T == 0) return SGMV_OK;
   if (!n->weight || !rows_ok(n->x, n, n->ldx_token, n->ldx_head) || (n->codes != nullptr) != (n->scale != nullptr) ||
-      (!n->out && !n->codes) || (n->residual_out && !n->residual) || (n->out && n->out == n->residual_out))
+      (!n->out && !n->codes) || (n->residual_out && !n->residual))
     return SGMV_EINVAL;
   if ((n->residual && !rows_ok(n->residual, n, n->ldr_token, n->ldr_head)) ||
       (n->residual_out && !rows_ok(n->residual_out, n, n->lds_token, n->lds_head)) ||
       (n->out && !rows_ok(n->out, n, n->ldo_token, n->ldo_head)) ||
-      (n->codes && !rows_ok(n->codes, n, n->ldc_token, n->ldc_head)))
+      (n->codes && !rows_ok(n->codes, n, n->ldc_token, n->ldc_head)) || !places_ok(n))
     return SGMV_EINVAL;
   const int E = n->dtype == SGMV_F32 ? 4 : 8;
   const NormArgs A{n->x, n->residual, n->weight, n->residual_out, n->out, n->codes, n->scale,

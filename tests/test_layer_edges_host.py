@@ -1,0 +1,34 @@
+"""CPU tests of the norm, the base product and the rotated append at the edges of what they take. Nothing is launched."""
+import ctypes
+
+import pytest
+
+import segmented_gather_gemv_amd as sg
+from test_layer_host import _norm
+
+E, OK = sg.SGMV_EINVAL, sg.SGMV_OK
+# where _norm has its rows
+AT = dict(x=0x1000, residual=0x2000, weight=0x3000, residual_out=0x4000, out=0x5000, codes=0x6000, scale=0x7000)
+LD = dict(x="x", residual="r", residual_out="s", out="o")
+
+
+def _call(**kw):
+    return sg.library().sgmv_rms_norm(ctypes.byref(_norm(**kw)), None)
+
+
+@pytest.mark.parametrize("out", ["out", "residual_out"])
+@pytest.mark.parametrize("of", ["x", "residual"])
+def test_norm_refuses_rows_in_place_with_other_strides(out, of):
+    """Rows of an output over other rows of an input, which other workgroups have not read yet."""
+    for ld in ("ld%s_token", "ld%s_head"):
+        for wider in (out, of):
+            kw = {f"ld{a}_{b}": n for a in "xrsoc" for b, n in (("token", 4096), ("head", 64))}
+            kw[ld % LD[wider]] *= 2
+            assert _call(**kw, **{out: AT[of]}) == E, (ld, wider)
+
+
+def test_norm_refuses_outputs_in_each_others_or_an_inputs_place():
+    for out in ("residual_out", "out", "codes", "scale"):
+        others = [n for n in AT if n != out and not (out in ("residual_out", "out") and n in ("x", "residual"))]
+        for other in others:
+            assert _call(**{out: AT[other]}) == E, (out, other)
