@@ -723,7 +723,7 @@ __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_groups_kernel(KvArgs
   const bool is_v = at >= rest / 2;
   const int of = is_v ? at - rest / 2 : at, head = of / slots;
   Group G;
-  if (!find_group(K, K.q_start, K.T, of - head * slots, head, G)) return;
+  if (!find_group(K, K.q_start, K.T, of - head * slots, head, G) || G.t0 < 0) return;  // (no row before position 0 is read)
   if (!is_v) return write_turned_group<FMT, T, NEIGHBOURS>(K, A, R, G);
   const int r = threadIdx.x & 15;
   write_rows<FMT, T, true>(K, A, true, place_in(G, KvFormat<FMT>::bytes == 1 ? place_of(r) : r));
@@ -736,11 +736,12 @@ __global__ __launch_bounds__(RW_WAVES* WAVE) void kv_append_rows_kernel(KvArgs K
   Place P;
   if (at < for_v) {
     row_place(K, K.q_start, K.T, at * RW_WAVES + wv, P);
+    P.ok = P.ok && P.pos >= 0;
     write_v_row<FMT, T>(K, A, P);
   } else {
     const int lanes = turned_lanes(K.D), piece = lane & (lanes - 1), of = lane / lanes;
     row_place(K, K.q_start, K.T, ((at - for_v) * RW_WAVES + wv) * side + min(of, side - 1), P);
-    P.ok = P.ok && of < side;
+    P.ok = P.ok && P.pos >= 0 && of < side;
     TurnedPiece<T> t;
     const int page = P.ok ? page_entry(K, P) : -1;
     load_turned<T, NEIGHBOURS>(K, A, R, P, piece, t);
