@@ -509,8 +509,9 @@ sgmv_status sgmv_kv_write(const void* k, int64_t ldk_token, int64_t ldk_head, co
  * keys and values but not the queries.
  *   cos_sin  device [positions][ld >= rotary] fp32
  *   rotary   a multiple of 16 up to head_dim
- *   q, q_out device rows [T][heads][head_dim] of `dtype`; q_out may be q itself (with the same
- *            strides, which is checked), must not overlap it otherwise. heads = 0: no queries
+ *   q, q_out device rows [T][heads][head_dim] of `dtype`; q_out may be q itself, with the same
+ *            strides, and must not overlap q, k or v otherwise (checked: equal addresses). heads = 0:
+ *            no queries
  * Errors: EINVAL; EUNSUPPORTED; EHIP. */
 typedef struct {
   const float* cos_sin;

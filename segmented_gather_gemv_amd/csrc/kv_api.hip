@@ -257,6 +257,7 @@ sgmv_status sgmv_kv_append(const sgmv_kv_rotation* turn, const void* k, int64_t 
   if (turn->heads > 0 && (!rows_ok(turn->q, K.T, turn->ldq_token, turn->ldq_head, turn->heads, K.D) ||
                           !rows_ok(turn->q_out, K.T, turn->ldo_token, turn->ldo_head, turn->heads, K.D)))
     return SGMV_EINVAL;
+  if (turn->heads > 0 && (turn->q_out == k || turn->q_out == v)) return SGMV_EINVAL;
   if (turn->heads > 0 && turn->q == turn->q_out && ((K.T > 1 && turn->ldq_token != turn->ldo_token) ||
                                                     (turn->heads > 1 && turn->ldq_head != turn->ldo_head)))
     return SGMV_EINVAL;

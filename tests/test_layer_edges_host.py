@@ -4,7 +4,7 @@ import ctypes
 import pytest
 
 import segmented_gather_gemv_amd as sg
-from test_layer_host import _norm
+from test_layer_host import _append, _norm
 
 E, OK = sg.SGMV_EINVAL, sg.SGMV_OK
 # where _norm has its rows
@@ -32,3 +32,8 @@ def test_norm_refuses_outputs_in_each_others_or_an_inputs_place():
         others = [n for n in AT if n != out and not (out in ("residual_out", "out") and n in ("x", "residual"))]
         for other in others:
             assert _call(**{out: AT[other]}) == E, (out, other)
+
+
+def test_append_refuses_queries_over_its_keys_or_values():
+    for part in (0x80000, 0x90000):  # k and v
+        assert _append(q_out=part) == E
