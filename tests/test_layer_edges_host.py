@@ -2,9 +2,10 @@
 import ctypes
 
 import pytest
+import torch
 
 import segmented_gather_gemv_amd as sg
-from test_layer_host import _append, _norm
+from test_layer_host import _append, _base, _norm
 
 E, OK = sg.SGMV_EINVAL, sg.SGMV_OK
 # where _norm has its rows
@@ -37,3 +38,15 @@ def test_norm_refuses_outputs_in_each_others_or_an_inputs_place():
 def test_append_refuses_queries_over_its_keys_or_values():
     for part in (0x80000, 0x90000):  # k and v
         assert _append(q_out=part) == E
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_that_the_binding_takes_without_a_workspace_need_none(dtype):
+    """BaseWeight.few asks the library only past it: as many rows of any weight take none there, one more of a large one does."""
+    for kw in (dict(group=128), dict(group=32), dict(group=64, has_zero=0, zero=0), dict(format=sg.BASE_E2M1, group=32, has_zero=0, zero=0)):
+        for N, K in ((1, 1), (40, 300), (4194304, 4194304), (4194304, 1), (1, 4194304)):
+            desc = _base(N=N, K=K, dtype=sg.SGMV_F32 if dtype is torch.float32 else sg.SGMV_BF16, **kw)
+            w = sg.BaseWeight(torch.empty(0, dtype=torch.uint8), torch.empty(0), None, desc, dtype)
+            assert all(sg.sgmv_base_product_workspace(T, w) == 0 for T in range(w.few + 1)), (N, K)
+            if N == K == 4194304:
+                assert sg.sgmv_base_product_workspace(w.few + 1, w) > 0
