@@ -24,11 +24,13 @@
 // separate waves.
 //
 // Bound: the rows' bytes; one token per sequence: the chain of loads from the sequence to its page.
-// Measured, 8 heads of 128: 256 sequences' new tokens written as e4m3 5.3 us and read back 4.2 us; 16 prompts'
-// chunks (8.9 thousand tokens) written as int8 13.4 us (55 MB, 11 us of a large copy: all waves are resident at once,
-// so that loads, quantising and stores follow each other; with the page asked for behind the row 16.0), 41 thousand tokens read back as bf16 57 us (258 MB,
-// 4.5 TB/s; a large copy: 5.1). Fp32 rows written as e4m3 or int8 19.4 us (floor 17.9), read back 143 (84); rows that
-// are held as they are: bf16 written in 13.9 us (14.2), read in 75 (67), fp32 25 (28) and 181 (133).
+// Measured, 8 heads of 128, passes over one set of tensors and over eight in turn, which the memory-side cache does not
+// hold (floors by a large copy's 5.1 TB/s): 256 sequences' new tokens written as e4m3 5.0 and 5.5 us; 16 prompts' chunks
+// (8.9 thousand tokens) of bf16 as int8 or e4m3 13.1 and 17.2 us (55 MB, floor 11: all waves are resident at once, so
+// that loads, quantising and stores follow each other; with the page asked for behind the row 14.1 and 19.0), as they
+// are 14.1 and 20.6 (14); of fp32 as 8 bits 18.9 and 26.5 (18), as they are 24.9 and 39.9 (28). Read back, over one set
+// and over four: the new tokens 4.2 and 4.8 us; 41 thousand tokens of int8 as bf16 46 and 53 us (258 MB, 50), of bf16
+// 75 and 75 (67), of e4m3 as fp32 142 and 147 (84), of fp32 188 and 178 (133).
 //
 // The append turns K on its way, (a, b) -> (a c - b s, b c + a s) with the cosine and sine of the token's position, every
 // product and sum rounded to fp32, and the queries, which it writes as rows. V goes as above. K takes lanes of its
