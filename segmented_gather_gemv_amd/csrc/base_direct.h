@@ -1,15 +1,19 @@
 // Product of few rows with a 4-bit base weight: the weight read once, straight into matrix-core operands.
 //
 // A workgroup takes NT * 16 columns n and 16 TM rows of x; its waves take every WAVES-th block of 128 k, each
-// summing all of its tiles in fp32, and their sums are added in LDS in the waves' order. The weight's next blocks and the
-// rows of x that go with them are in flight while one is multiplied. Up to 4 rows go straight into operands (16 rows of the
-// product's, the last of them again); more are read as whole lines and pass through the wave's part of LDS (16 rows over
-// 8192 x 8192: 12 us without), but for fp32, whose parts are made in registers. 16 waves and two workgroups a unit keep 128 KB of the weight in flight.
+// summing all of its tiles in fp32, and their sums are added in LDS in the waves' order. Up to 4 rows go straight into
+// operands (16 rows of the product's, the last of them again), and so do fp32 rows, whose parts are made in registers: a
+// wave asks for its next block behind the products of one, and other waves' blocks are in flight meanwhile. More rows of
+// bf16 are read as whole lines and pass through the wave's part of LDS (16 rows over 8192 x 8192: 12 us without); there
+// the next block is in flight while one is multiplied. A wave's block is NT KB of the weight, so that 16 waves of one or
+// two tiles have up to 16 or 32 KB of it in flight and 8 waves of four 32 KB; a unit holds two workgroups of unstaged bf16
+// rows without zero points, and twice that.
 //
 // Bound: the weight's bytes, from some 16 rows on the conversions and products. Measured (I4, groups of 128, bf16 rows;
 // floors by a large copy's 5.14 TB/s): one row over 8192 x 8192 8.0 us (35 MB, 4.3 TB/s; floor 6.8), over 28672 x 8192
 // 26 (23.6); 16 rows 10.0 (6.8), 64 rows 18 (7.2); E2M1, 16 rows over 28672 x 8192 29 (24.7); fp32, one row over 8192 x
-// 8192 12.9 (6.9), 64 over 4096 x 4096 12.8.
+// 8192 12.8 (6.9), 64 over 4096 x 4096 12.9. 128 over 8192 x 8192 30 to 34 (14.4), 256 over 4096 x 4096 18 (7.2): each
+// 16 or 32 rows convert the whole weight again.
 #pragma once
 
 #include "base.h"
@@ -17,7 +21,8 @@
 namespace sgmv {
 
 // Waves per SIMD to allocate registers for: one workgroup per compute unit, two where the registers of rows and zero
-// points leave room or it has four waves (three of those a unit: 36 to 93 spilled registers, 10 to 200% slower).
+// points leave room or it has four waves (three of those a unit: 36 to 93 spilled registers, 10 to 200% slower). Of the instances here one spills: fp32, groups of 32 without zero points,
+// one tile of columns, 2 registers.
 constexpr int base_occupancy(bool zero, bool f32, int waves, bool staged) {
   if (!f32 && !staged && !zero) return 8;
   return waves >= 8 ? waves / 4 : 2;

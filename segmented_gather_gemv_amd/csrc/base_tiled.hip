@@ -18,7 +18,8 @@
 // busy 38% of the cycles, vector units 51%, at 2.06 GHz). Measured, bf16 rows: that 214 us (865 TFLOP/s; the
 // library's bf16 product alone runs at 1197), 9 of them preparing rows; without zero points 196, groups of 64 217, groups
 // of 32 with zero points 307, E2M1 166 (1115 TFLOP/s); 1000 rows over 8192 x 28672 460 us (1020). fp32 rows: 2048 over 8192 x
-// 8192 with zero points 833 us, E2M1 639 (a library product of fp32: 1785). Not kept: 128 rows a workgroup (one wave a
+// 8192 with zero points 833 us, E2M1 639 (a library product of fp32: 1785). The instances of short groups with zero points
+// spill: fp32 rows 11 registers (groups of 32) and 14 (64), bf16 rows 3 (64). Not kept: 128 rows a workgroup (one wave a
 // SIMD: 329 us), 192 columns (224), loads straight to LDS (the compiler waits for all loads before each LDS read).
 #include "base.h"
 

@@ -88,14 +88,16 @@ struct BasePlan {
 
 // The tiled kernel converts each code for 64 rows, not 16 or 32, but has its rows prepared in a launch of its own and
 // takes few workgroups: for bf16 rows, from 160 full tiles or 1e10 products on, for fp32 ones from 128 or 5e9. Measured
-// (tiles in their best number of ranges, direct; us): bf16, I4: 850 rows, 3008 x 1408: 24 and 21, 600 rows, 4096 x 1024:
-// 19 and 16, 1000 rows: 20 and 31 (of an earlier instance), 64 rows, 28672 x 5000: 38 and 41, 150 rows, 8192 x 8000: 46
-// and 44, 256 rows, 8192 x 8192: 52 and 67; fp32: 800 rows, 2527 x 313: 27 and 28, 400 rows, 4096 x 1024: 32 and 22, 170
-// rows, 4096 x 4096: 40 and 31, 200 rows, 1088 x 12096: 62 and 33.
+// (in tiles by the ranges below, direct; us): bf16, I4: 850 rows, 3008 x 1408: 24 and 20, 600 rows, 4096 x 1024: 19 and
+// 16, 1000 rows: 20 and 23, 256 rows, 4096 x 4096: 27 and 18, 128 rows, 8192 x 8192: 36 and 30, 150 rows, 8192 x 8000: 43
+// and 43, 256 rows, 8192 x 8192: 52 and 55, 64 rows, 28672 x 8192: 53 and 62, x 5000 (which the rule leaves direct): 38
+// and 40; fp32: 800 rows, 2527 x 313: 21 and 16, 400 rows, 4096 x 1024: 32 and 22, 170 rows, 4096 x 4096: 40 and 30, 200
+// rows, 1088 x 12096: 57 and 30, 1000 rows, 4096 x 1024: 41 and 43, 128 rows, 8192 x 8192: 65 and 71, 340 rows, 4096 x
+// 4096: 57 and 53.
 //
 // Tiles fill the card from 256 on; of fewer, K is split into up to 8 ranges of 8 steps and more (256 rows, 8192 x 8192:
-// 81 us in 1, 56 in 2, 52 in 4, 64 in 8; 1024 over 4096 x 4096, 256 tiles: 49 us in 1, 54 in 2); of fp32 rows into up to
-// 16 of 12 steps (202 rows, 732 x 15403: 113 us in 8, 75 in 16; 100 rows, 4096 x 4096: 34 in 8, 37 in 16).
+// 82 us in 1, 54 in 2, 51 in 4, 60 in 8; 1024 over 4096 x 4096, 256 tiles: 49 us in 1, 53 in 2); of fp32 rows into up to
+// 16 of 12 steps (202 rows, 732 x 15403: 72 us in 8, 53 in 16; 100 rows, 4096 x 4096: 33 in 8, 37 in 16).
 BasePlan base_plan(int32_t T, const sgmv_base& b, int32_t n_split) {
   const BaseShape h = base_shape(b);
   BasePlan p{};
