@@ -505,10 +505,12 @@ sgmv_status sgmv_kv_write(const void* k, int64_t ldk_token, int64_t ldk_head, co
  * each product and each sum rounded to fp32; the others stay as they are. Queries are then
  * rounded once to `dtype`, keys once to the cache's format (the 8-bit formats: quantised from the
  * fp32 values). Rows of no sequence and those at negative positions are neither read nor written;
- * queries and keys at positions past the table come out as NaN, and a missing page leaves out its
- * keys and values but not the queries.
+ * at positions past the table the turned values of queries and keys come out as NaN (in an 8-bit
+ * cache that is the whole row: scale NaN, codes 0), and a missing page leaves out its keys and
+ * values but not the queries.
  *   cos_sin  device [positions][ld >= rotary] fp32
- *   rotary   a multiple of 16 up to head_dim
+ *   rotary   a multiple of 16 up to head_dim (a lane turns 8 pairs, in whole pieces of rows; other
+ *            multiples of 2 are EUNSUPPORTED)
  *   q, q_out device rows [T][heads][head_dim] of `dtype`; q_out may be q itself, with the same
  *            strides, and must not overlap q, k or v otherwise (checked: equal addresses). heads = 0:
  *            no queries
@@ -610,11 +612,13 @@ sgmv_status sgmv_verify_drafts(const void* target, int64_t ldt, const void* draf
 
 /* Root-mean-square norm of rows [T][heads][width] (heads = 1: of a layer's input; heads > 1: of
  * each head's queries or keys), with the residual's addition before it and codes of 8 bits beside
- * its output (for a base product of such rows, where the delta takes `out`):
+ * its output (for a caller's own product of 8-bit rows, the library has none; the delta and
+ * sgmv_base_product take `out`):
  *   h = x + residual, residual_out = h,  g = h * weight,  root = sqrt(sum h^2 / width + eps),
  *   out = g / root,   scale = max |g| / root / F,   code = g * F / max |g|, F = 448 (E4M3) or 127 (I8)
  * h and g are fp32, each rounded once; h and out are then rounded once to `dtype`, codes as in the
  * cache above: zeros give scale 0 and codes 0, a row with a g that is not finite scale NaN and codes 0.
+ * out is the norm of h before that rounding, not of residual_out.
  *   x, residual, residual_out, out  device, row of token t and head j at t * ld_token + j * ld_head,
  *            `width` contiguous elements of `dtype`, tokens or heads outermost, each row its own;
  *            residual may be NULL (h = x), and then residual_out is NULL; residual_out may be NULL,
@@ -650,7 +654,8 @@ sgmv_status sgmv_rms_norm(const sgmv_norm* norm, void* stream);
  *   I4    w[n][k] = scale[n][k / group] * (code - zero[n][k / group]), codes and zeros 0..15, zero 8
  *         where there are none; scales of the product's `dtype`
  *   E2M1  w[n][k] = 2^(scale[n][k / 32] - 127) * value(code): codes of sign, 2 exponent bits and 1 of
- *         mantissa (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), scales one byte (255: NaN), group 32
+ *         mantissa (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), scales one byte (255: NaN), group 32;
+ *         a weight past fp32's range is infinite
  * Packed once, when weights are loaded, into the library's layout:
  *   codes        [N / 16][K / 128][64][4] words: word j of lane l holds, of row 16 (n / 16) + l % 16, the 8
  *                values from k = 128 (k / 128) + 32 j + 8 (l / 16) on, value i in the four bits from
@@ -682,14 +687,17 @@ sgmv_status sgmv_base_init(int32_t N, int32_t K, int32_t group, int32_t format, 
 /* Pack a weight: codes device [N][ldc >= (K + 1) / 2] bytes, k even in the low four bits; scale device
  * [N][groups] (groups = K / group rounded up) of base->dtype (E2M1: bytes); zero [N][groups] bytes, or NULL
  * without zero points. base's pointers are 16-byte aligned.
- * Errors: EINVAL; EHIP. */
+ * Errors: EINVAL; EUNSUPPORTED (a launch past 2^32 work items); EHIP. */
 sgmv_status sgmv_base_pack(const uint8_t* codes, int64_t ldc, const void* scale, const uint8_t* zero,
                            const sgmv_base* base, void* stream);
 
-/* y[t][n] = sum_k w[n][k] x[t][k] for T rows (0 is allowed), products and sums in fp32 (of fp32 rows all
- * their bits enter), scales applied to the fp32 sums of their groups, rounded once to dtype. A row of x that
- * is not finite spoils its own row of y only. I4 sums codes as they are and takes the zero points' share off
- * after: sums of 16 |x| have to stay in fp32.
+/* y[t][n] = sum_k w[n][k] x[t][k] for T rows (0 is allowed), products and sums in fp32 (of fp32 rows all 24
+ * bits enter, of values below 2^-110 those from 2^-133 on; products below 2^-126 may count as 0), scales
+ * applied to the fp32 sums of their groups, rounded once to dtype. A row of x that is not finite spoils its
+ * own row of y only. I4 sums codes as they are and takes the zero points' share off after: sums of 16 |x|
+ * have to stay in fp32, and roundings are relative to sum |scale| (code + zero) |x|, not to sum |w x|, so
+ * that fp32 results of rows with a large mean lose some two bits that weights dequantised first would keep
+ * (zeros of 8, codes spread evenly: 15.5 against 4 on average). bf16 results round far more coarsely.
  *   x  device [T][ldx >= K], y device [T][ldy >= N], of base->dtype; y must not overlap x
  *   n_split  0 = the library's choice, else 1..SGMV_BASE_MAX_SPLITS: as of many rows, in tiles with K split
  *            into that many ranges

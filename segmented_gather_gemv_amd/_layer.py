@@ -313,8 +313,9 @@ def sgmv_kv_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, 
     """Write the step's keys and values [T, heads, head_dim] into the cache as sgmv_kv_write does, the keys turned
     by their positions, and turn the queries q [T, query heads, head_dim] (None: none), which are returned, in
     ``q_out`` if given (q itself: in place). ``cos_sin`` float32 [positions, rotary]: rotary / 2 cosines and then as
-    many sines of each position's angles; the first ``rotary`` values of a row are turned, in pairs (i,
-    i + rotary / 2) or, ``interleaved``, (2 i, 2 i + 1)."""
+    many sines of each position's angles; the first ``rotary`` values of a row (a multiple of 16) are turned, in
+    pairs (i, i + rotary / 2) or, ``interleaved``, (2 i, 2 i + 1). Rows of no sequence and those at negative
+    positions are not written: in a ``q_out`` that the call allocates they are whatever the memory held."""
     T, index, dtype = batch.T, cache.index, k.dtype
     kt, kh = _rows3(k, T, cache.heads, cache, "k")
     vt, vh = _rows3(v, T, cache.heads, cache, "v")

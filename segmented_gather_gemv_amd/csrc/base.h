@@ -6,6 +6,7 @@
 // group's scale and zero point are one value of the lane.
 //   I4    c is an e4m3 code as it stands (a number below 16 in the low bits of a byte is c 2^-9), so that two codes
 //         become two exact bf16 by one instruction: y += s (sum c x - z sum x), with sum x from a product by ones.
+//         (Both sums are of one sign where x is, and cancel: roundings count against s (c + z) |x|.)
 //   E2M1  the scale is a power of two, which the conversion applies: the operand is the weight itself, exact.
 // fp32 rows are split into three bf16 (24 bits).
 #pragma once
