@@ -70,8 +70,13 @@ __global__ __launch_bounds__(256) void base_rows_kernel(BaseArgs A) {
       float sum = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        if constexpr (F32) sum += __uint_as_float(v[q][i / 4][i % 4]);
-        else sum += __uint_as_float(i & 1 ? v[q][0][i / 2] & 0xffff0000u : v[q][0][i / 2] << 16);
+        float value = 0.f;  // (of its parts: what they lack of one below 2^-110 is missing here too)
+#pragma unroll
+        for (int k = PARTS - 1; k >= 0; --k) {
+          const uint32_t w = __builtin_bit_cast(u32x4_t, part[k])[i / 2];
+          value += __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+        }
+        sum += value;
       }
 #pragma unroll
       for (int o = 1; o < 16 / S; o <<= 1) sum += __shfl_xor(sum, o);

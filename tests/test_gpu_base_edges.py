@@ -87,3 +87,23 @@ def test_every_bit_of_fp32_rows(sg, T, N, K, splits, fmt, group, zero):
     assert torch.equal(want.float().double(), want)
     for n in splits:
         assert torch.equal(sg.sgmv_base_product(x.to(DEV), base, n_split=n).cpu(), want.float()), n
+
+
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("T", [3, 70])
+def test_values_below_what_the_parts_hold(sg, T, zero):
+    """Bits below 2^-133 do not enter, in the products and in the zero points' share alike: with weights of 1 (codes
+    9, zeros 8) a row is off by less than 2^-133 for its one value, and its result's own rounding."""
+    K, N = 300, 40
+    g = torch.Generator().manual_seed(T)
+    codes = torch.full((N, K // 2), 0x99, dtype=torch.uint8, device=DEV)
+    z = torch.full((N, 5), 8, dtype=torch.uint8, device=DEV) if zero else None
+    base = sg.sgmv_base_pack(codes, torch.ones(N, 5, device=DEV), z, group=64)
+    x = torch.zeros(T, K)
+    v = torch.ldexp(1 + torch.rand(T, generator=g, dtype=torch.float64), -(13 * torch.arange(T) % 30) - 110).float()
+    x[torch.arange(T), torch.randint(0, K, (T,), generator=g)] = v
+    v = v.double()[:, None]
+    for n in (0, 1, 2):
+        y = sg.sgmv_base_product(x.to(DEV), base, n_split=n).cpu().double()
+        # (9 x and 8 x are rounded before they are subtracted: 2^-24 of each)
+        assert ((y - v).abs() <= 2.0 ** -133 + 18 * 2.0 ** -24 * v).all(), n
