@@ -692,9 +692,8 @@ sgmv_status sgmv_base_pack(const uint8_t* codes, int64_t ldc, const void* scale,
                            const sgmv_base* base, void* stream);
 
 /* y[t][n] = sum_k w[n][k] x[t][k] for T rows (0 is allowed), products and sums in fp32 (of fp32 rows all 24
- * bits enter, of values below 2^-110 those from 2^-133 on; products below 2^-126 may count as 0), scales
- * applied to the fp32 sums of their groups, rounded once to dtype. A row of x that is not finite spoils its
- * own row of y only. I4 sums codes as they are and takes the zero points' share off after: sums of 16 |x|
+ * bits enter, of values below 2^-110 those from 2^-133 on), scales applied to the fp32 sums of their groups,
+ * rounded once to dtype. A row of x that is not finite spoils its own row of y only. I4 sums codes as they are and takes the zero points' share off after: sums of 16 |x|
  * have to stay in fp32, and roundings are relative to sum |scale| (code + zero) |x|, not to sum |w x|, so
  * that fp32 results of rows with a large mean lose some two bits that weights dequantised first would keep
  * (zeros of 8, codes spread evenly: 15.5 against 4 on average). bf16 results round far more coarsely.

@@ -1,6 +1,6 @@
-"""GPU tests of the base product at the edges of what it states: all 24 bits of fp32 rows.
+"""GPU tests of the base product at the edges of what it states: all 24 bits of fp32 rows, the smallest values and weights.
 
-Rows of x have one value that is not zero, a whole number with bits in the first, the second and the last eight of its 24, so
+In the first, rows of x have one value that is not zero, a whole number with bits in the first, the second and the last eight of its 24, so
 that each of the three bf16 parts that the kernels make of it counts. Codes and zero points are such that every sum
 on the way is a whole multiple of the code's power of two below 2^24 of it, whatever the order of the parts (z a power of two
 and codes 0, z and 2 z, or 0 and z / 2; z = 0 and codes powers of two), and scales are powers of two: results are equal to the
@@ -107,3 +107,23 @@ def test_values_below_what_the_parts_hold(sg, T, zero):
         y = sg.sgmv_base_product(x.to(DEV), base, n_split=n).cpu().double()
         # (9 x and 8 x are rounded before they are subtracted: 2^-24 of each)
         assert ((y - v).abs() <= 2.0 ** -133 + 18 * 2.0 ** -24 * v).all(), n
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, F32])
+@pytest.mark.parametrize("T", [1, 20, 70])
+def test_every_weight_of_e2m1(sg, T, dtype):
+    """All codes with all scales against single values that are powers of two: exact, weights and results below 2^-126
+    among them; weights past fp32 are infinite (here met by zeros too: NaN), and so for scales of 255, NaN."""
+    K, i = 32, torch.arange(16 * 256)
+    code, scale = (i % 16).to(torch.uint8), (i // 16).to(torch.uint8)
+    packed = (code | code << 4)[:, None].expand(len(i), K // 2).contiguous()
+    base = sg.sgmv_base_pack(packed.to(DEV), scale[:, None].to(DEV), group=32, format=sg.BASE_E2M1, dtype=dtype)
+    value = torch.from_numpy(np.concatenate([lo.E2M1, -lo.E2M1]))[code.long()] * torch.exp2(scale.double() - 127)
+    lost = (value.abs() >= 2.0 ** 128) | (scale == 255)
+    assert lost.sum() == 12 + 16
+    for e in (0, -20, 20):
+        x = torch.zeros(T, K)
+        x[:, 3] = 2.0 ** e
+        y = sg.sgmv_base_product(x.to(dtype).to(DEV), base).cpu()
+        assert torch.isnan(y[:, lost]).all()
+        assert torch.equal(y[:, ~lost], (value * 2.0 ** e).to(dtype)[None, ~lost].expand(T, -1))
