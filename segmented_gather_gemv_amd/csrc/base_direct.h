@@ -21,8 +21,8 @@
 namespace sgmv {
 
 // Waves per SIMD to allocate registers for: one workgroup per compute unit, two where the registers of rows and zero
-// points leave room or it has four waves (three of those a unit: 36 to 93 spilled registers, 10 to 200% slower). Of the instances here one spills: fp32, groups of 32 without zero points,
-// one tile of columns, 2 registers.
+// points leave room or it has four waves (three of those a unit: 36 to 93 spilled registers, 10 to 200% slower). Of the
+// instances below one spills: fp32, groups of 32 without zero points, one tile of columns, 2 registers.
 constexpr int base_occupancy(bool zero, bool f32, int waves, bool staged) {
   if (!f32 && !staged && !zero) return 8;
   return waves >= 8 ? waves / 4 : 2;
